@@ -161,6 +161,32 @@ MOE_API int moe_layer_launches(const moe_shape* shape);
 MOE_API int moe_route_topk(const moe_shape* shape, const float* logits, int32_t* ids, float* weights,
                    moe_stream_t stream);
 
+/* Router variants: what moe_route_grouped selects by and how it weights the selection. */
+typedef enum moe_dtype { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_FP16 = 2 } moe_dtype;
+typedef struct moe_routing {
+  int32_t E, k;        /* experts and experts per token: 1 <= k <= 32, k <= E <= 1024 */
+  int32_t softmax;     /* scores: 0 sigmoid of every logit, 1 softmax of the row */
+  int32_t groups;      /* consecutive groups of E / groups experts; 1 <= groups <= 32, divides E */
+  int32_t keep_groups; /* groups that stay, 1 <= keep_groups <= groups, keep_groups * (E / groups) >= k */
+  int32_t top2;        /* a group's score: 0 its largest key, 1 the sum of its two largest */
+  int32_t renormalise; /* 1: weights are the selected scores divided by their sum, times scale */
+  float scale;         /* factor of the weights */
+} moe_routing;
+
+/* Step 1 in its grouped form.  Every expert has a score s_e (sigmoid or softmax of the logits) and
+ * a key s_e + bias_e that only selects; the keep_groups groups with the largest group scores stay,
+ * and the k largest keys among their experts are selected (larger first; equal values go to the
+ * lower index, of groups and of experts).  With softmax and no bias the key is the logit itself.
+ * The weights are the selected experts' scores, without the bias.
+ *   logits     [T, E] of `dtype` (moe_dtype), rows row_stride elements apart, aligned to an element;
+ *              NaN counts as -infinity
+ *   bias       [E] float32 or NULL; a NaN sum counts as -infinity
+ *   ids        [T, k] int32 out, in selection order;  weights [T, k] float32 out (0 where the
+ *              selected scores sum to 0)
+ * 0 <= T <= 65536.  The ids and weights are what moe_plan takes. */
+MOE_API int moe_route_grouped(const moe_routing* routing, int T, const void* logits, int64_t row_stride, int dtype,
+                              const float* bias, int32_t* ids, float* weights, moe_stream_t stream);
+
 /* Step 2, bucketing ("First implementation boundary", step 1): per-expert route counts,
  * their exclusive prefix sum, the ascending list of touched experts, each route's
  * position in expert-major order, the per-expert task prefix sums used by the expert

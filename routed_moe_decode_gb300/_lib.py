@@ -45,7 +45,24 @@ class Shape(ctypes.Structure):
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32)]
 
 
+class RoutingArgs(ctypes.Structure):
+    """moe_routing (include/moe.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("E", "k", "softmax", "groups", "keep_groups", "top2", "renormalise")] + \
+        [("scale", _F)]
+
+
+class Kv4Args(ctypes.Structure):
+    """moe_kv4_cache (include/moe_kv4.h)."""
+    _fields_ = [(n, _P) for n in ("pool", "table", "lens", "refs", "workspace")] + \
+        [("workspace_bytes", ctypes.c_size_t)] + \
+        [(n, ctypes.c_int32) for n in ("layers", "pages", "kv_heads", "head_dim", "page_size", "seqs", "max_pages")] + \
+        [("k_scale", _F), ("v_scale", _F)]
+
+
 _SP = ctypes.POINTER(Shape)
+_RP = ctypes.POINTER(RoutingArgs)
+_KP = ctypes.POINTER(Kv4Args)
+_L = ctypes.c_int64
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
@@ -81,6 +98,20 @@ SIGNATURES = {
     "moe_read_device_status": (_I, [_P, _I, ctypes.POINTER(ctypes.c_uint32), _P]),
     "moe_plan_summary": (_I, [_SP, _P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), _P]),
     "moe_plan_views": (_I, [_SP, _P] + [ctypes.POINTER(ctypes.c_void_p)] * 5),
+    "moe_route_grouped": (_I, [_RP, _I, _P, _L, _I, _P, _P, _P, _P]),
+    # include/moe_kv4.h
+    "moe_kv4_page_bytes": (ctypes.c_size_t, [_KP]),
+    "moe_kv4_workspace_bytes": (ctypes.c_size_t, [_KP]),
+    "moe_kv4_check": (_I, [_KP]),
+    "moe_kv4_workspace_init": (_I, [_KP, _P]),
+    "moe_kv4_append": (_I, [_KP, _I, _P, _L, _L, _P, _L, _L, _I, _P, _I, _P]),
+    "moe_kv4_read": (_I, [_KP, _I, _P, _P, _I, _P, _I, _P]),
+    "moe_kv4_attend": (_I, [_KP, _I, _P, _L, _L, _I, _I, _P, _I, _I, _F, _I, _P, _P, _P, _P]),
+    "moe_kv4_reserve": (_I, [_KP, _P, _P]),
+    "moe_kv4_fork": (_I, [_KP, _P, _P, _I, _P]),
+    "moe_kv4_trim": (_I, [_KP, _P, _P]),
+    "moe_kv4_compact": (_I, [_KP, _P, _P, _I, _I, _P]),
+    "moe_kv4_read_status": (_I, [_KP, _I, ctypes.POINTER(ctypes.c_uint32), _P]),
     # include/moe_selftest.h
     "moe_selftest_expert_timeout": (_I, [_SP, _P, _P, _F, _P, _P, _F, _P, _P, _P, ctypes.c_size_t, _I, _I,
                                          ctypes.c_longlong, _P]),

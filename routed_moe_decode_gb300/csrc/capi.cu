@@ -2,6 +2,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -129,6 +130,15 @@ int encode_f16_rows_map(CUtensorMap* tm, const void* base, uint64_t cols, uint64
 }
 
 void set_last_error_message(const char* msg) { snprintf(g_last_error, sizeof g_last_error, "%s", msg); }
+
+void set_last_cuda_error(const char* where, cudaError_t e) { set_error(where, e); }
+
+int device_sms(int* sms) {
+  DeviceInfo info;
+  const int rc = device_info(&info);
+  if (rc == MOE_OK) *sms = info.num_sms;
+  return rc;
+}
 
 }  // namespace moe
 
@@ -276,6 +286,30 @@ int moe_route_topk(const moe_shape* shape, const float* logits, int32_t* ids, fl
     return MOE_ERR_INVALID_ARG;
   cudaError_t e = moe::launch_route_topk(logits, shape->T, shape->E, shape->k, ids, weights, stream);
   if (e != cudaSuccess) { set_error("route_topk launch", e); return MOE_ERR_CUDA; }
+  return MOE_OK;
+}
+
+int moe_route_grouped(const moe_routing* r, int T, const void* logits, int64_t row_stride, int dtype,
+                      const float* bias, int32_t* ids, float* weights, moe_stream_t stream) {
+  if (!r || T < 0 || r->E <= 0 || r->k <= 0 || r->k > r->E || row_stride < r->E) return MOE_ERR_INVALID_ARG;
+  if (r->groups <= 0 || r->E % r->groups || r->keep_groups < 1 || r->keep_groups > r->groups ||
+      static_cast<int64_t>(r->keep_groups) * (r->E / r->groups) < r->k || !(fabsf(r->scale) <= 3.4e38f))
+    return MOE_ERR_INVALID_ARG;
+  if (dtype < MOE_DTYPE_FP32 || dtype > MOE_DTYPE_FP16) return MOE_ERR_INVALID_ARG;
+  if (T > 65536 || r->k > 32 || r->E > 1024 || r->groups > 32) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const size_t size = dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (!logits || !ids || !weights || !aligned(logits, size) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(bias, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe::RouteGroupedArgs a{};
+  a.logits = logits; a.row_stride = row_stride; a.bias = bias; a.ids = ids; a.weights = weights;
+  a.T = T; a.E = r->E; a.k = r->k; a.groups = r->groups; a.keep_groups = r->keep_groups; a.dtype = dtype;
+  a.softmax = r->softmax != 0; a.top2 = r->top2 != 0; a.renormalise = r->renormalise != 0;
+  a.vec = aligned(logits, 16) && (row_stride * size) % 16 == 0;
+  a.scale = r->scale;
+  const cudaError_t e = moe::launch_route_grouped(a, stream);
+  if (e != cudaSuccess) { set_error("grouped router launch", e); return MOE_ERR_CUDA; }
   return MOE_OK;
 }
 

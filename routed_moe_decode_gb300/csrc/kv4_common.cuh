@@ -1,0 +1,161 @@
+// Shared definitions of the 4-bit K/V cache kernels: the page format, the workspace and the
+// lookup of a step's rows.
+#pragma once
+
+#include "../../include/moe_kv4.h"
+#include "moe_kernels.cuh"
+
+namespace moe {
+namespace kv4 {
+
+constexpr int kTile = 16;       // tokens of a tile
+constexpr int kMaxGrid = 1024;  // CTAs of an attention launch at most
+constexpr int kStepRows = 64;   // rows of a sequence's step with a tree or in a compaction
+
+// A cache as the kernels see it.
+struct Cache {
+  uint8_t* pool;  // of the layer (append, read, attend) or of layer 0 (pages)
+  int* table;
+  int* lens;
+  int* refs;
+  int* status;
+  int layers, pages, heads, dim, page_size, seqs, max_pages;
+  int tile_bytes;       // 18 * dim
+  int tiles_per_page;   // page_size / 16
+  size_t page_bytes;    // heads * tiles_per_page * tile_bytes
+};
+
+struct WsLayout {
+  size_t status, counters, copies, need, part, total;
+  size_t part_floats;  // floats of one partial result of the attention
+};
+
+// A partial result holds up to 4096 / dim ... rows of dim + 2 floats; the widest row block of
+// every head size is kept at or below 4096 sums, so that one partial is 4096 + 2 * 64 floats.
+constexpr int kPartSums = 4096;
+constexpr int kPartRows = 64;
+
+inline WsLayout ws_layout(const moe_kv4_cache& c) {
+  WsLayout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
+  L.status = take(64);
+  L.counters = take(size_t(kMaxGrid) * 4);
+  // moe_kv4_reserve: copies [1 + 2 * seqs] (their number, then page pairs), need [seqs + 1]
+  L.copies = take((1 + 2 * size_t(c.seqs)) * 4);
+  L.need = take((1 + size_t(c.seqs)) * 8);
+  L.part_floats = kPartSums + 2 * kPartRows;
+  L.part = take(size_t(2) * kMaxGrid * L.part_floats * 4);
+  L.total = o;
+  return L;
+}
+
+// A load of what an earlier kernel wrote (lengths, tables, counts): volatile, so that it stays
+// behind the wait for that kernel.
+template <typename T>
+MOE_DEVICE T ld(const T* p) {
+  return *reinterpret_cast<const volatile T*>(p);
+}
+
+// Rows [first, first + n) of the step and sequence s, cut to the `rows` that exist.
+struct StepRows {
+  int first, n;
+};
+MOE_DEVICE StepRows step_rows(const int* __restrict__ cu, int s, int rows) {
+  const int a = min(max(ld(cu + s), 0), rows);
+  const int b = min(max(ld(cu + s + 1), a), rows);
+  return {a, b - a};
+}
+
+// The sequence that row r belongs to: the last s with cu[s] <= r (binary search; empty
+// sequences share a start and are passed over).
+MOE_DEVICE int seq_of_row(const int* __restrict__ cu, int seqs, int r) {
+  int lo = 0, hi = seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (ld(cu + mid) <= r) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The tile that holds token `pos` of sequence s and head h, or nullptr where it has no page.
+MOE_DEVICE uint8_t* tile_of(const Cache& c, int s, int pos, int h) {
+  if (pos < 0) return nullptr;
+  const int pi = pos / c.page_size;
+  if (pi >= c.max_pages) return nullptr;
+  const int page = ld(c.table + static_cast<size_t>(s) * c.max_pages + pi);
+  if (page < 0 || page >= c.pages) return nullptr;
+  return c.pool + static_cast<size_t>(page) * c.page_bytes +
+         (static_cast<size_t>(h) * c.tiles_per_page + (pos - pi * c.page_size) / kTile) * c.tile_bytes;
+}
+
+// Two BF16 or FP16 values of one word as floats.
+MOE_DEVICE float2 unpack2(uint32_t w, bool fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+MOE_DEVICE uint32_t pack2(float a, float b, bool fp16) {
+  uint32_t o;
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    o = *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    o = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return o;
+}
+
+struct RowArgs {
+  Cache c;
+  const void* k;
+  const void* v;
+  int64_t k_row, k_head, v_row, v_head;  // strides in elements
+  void* k_out;
+  void* v_out;
+  const int* cu;
+  int rows;
+  bool fp16;
+  float k_ts, v_ts;
+};
+
+struct AttendArgs {
+  Cache c;
+  const void* q;
+  int64_t q_row, q_head;
+  int group;   // query heads per K/V head
+  const int* cu;
+  int rows;
+  bool fp16;
+  float scale2;  // scale * k tensor scale * log2(e)
+  float v_ts;
+  int window;
+  const unsigned long long* tree;
+  void* out;
+  float* lse;
+  float* part;
+  size_t part_floats;
+  uint32_t* counters;
+};
+
+struct PageArgs {
+  Cache c;
+  const int* a;  // new_tokens / to_tokens / src
+  const int* b;  // dst
+  const uint8_t* keep;
+  const int* cu;
+  int n, rows;
+  int* copies;
+  unsigned long long* need;
+};
+
+cudaError_t launch_append(const RowArgs& a, cudaStream_t stream);
+cudaError_t launch_read(const RowArgs& a, cudaStream_t stream);
+cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream);
+cudaError_t launch_reserve(const PageArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_fork(const PageArgs& a, cudaStream_t stream);
+cudaError_t launch_trim(const PageArgs& a, cudaStream_t stream);
+cudaError_t launch_compact(const PageArgs& a, cudaStream_t stream);
+
+}  // namespace kv4
+}  // namespace moe

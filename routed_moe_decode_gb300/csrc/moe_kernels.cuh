@@ -308,6 +308,19 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
 
 cudaError_t launch_route_topk(const float* logits, int T, int E, int k, int32_t* ids, float* weights,
                               cudaStream_t stream);
+
+// Grouped router (route_grouped.cu); vec: rows can be read 16 bytes at a time.
+struct RouteGroupedArgs {
+  const void* logits;
+  int64_t row_stride;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  int T, E, k, groups, keep_groups, dtype;
+  bool softmax, top2, renormalise, vec;
+  float scale;
+};
+cudaError_t launch_route_grouped(const RouteGroupedArgs& a, cudaStream_t stream);
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream);
 cudaError_t launch_front(FrontArgs f, cudaStream_t stream);
 cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream);
@@ -406,5 +419,8 @@ cudaError_t launch_gated_unroute(const ExpertArgs& a, int G, const __nv_bfloat16
                                  __nv_bfloat16* normed, cudaStream_t stream);
 // Record a message for moe_last_cuda_error on the calling host thread.
 void set_last_error_message(const char* msg);
+void set_last_cuda_error(const char* where, cudaError_t e);
+// SMs of the current device (MOE_OK or a status).
+int device_sms(int* sms);
 
 }  // namespace moe

@@ -1,0 +1,471 @@
+"""The 4-bit K/V cache on the GPU against the plain 64-bit implementation (tests/kv4_plain.py)."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_plain as P
+from gpu_helpers import BF16_HALF_ULP_REL
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import __graft_entry__
+    __graft_entry__.build()
+    import routed_moe_decode_gb300 as m
+    return m
+
+
+def dev(x, dtype=torch.int32):
+    return torch.tensor(np.asarray(x), dtype=dtype, device="cuda")
+
+
+def make_cache(moe, lens, heads, D, page, layers=1, extra_pages=3, max_pages=None, k_scale=1.0, v_scale=1.0, seed=0,
+               fill=True):
+    """A cache whose sequences hold `lens` tokens of random K and V in pages of random order, and the
+    same as numpy arrays.  Bytes that belong to no token are 0x7f (scales there are NaN)."""
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens, dtype=np.int32)
+    need = [-(-int(n) // page) for n in lens]
+    per = max_pages or max(max(need), 1)
+    pages = sum(need) + extra_pages
+    table = np.full((len(lens), per), -1, dtype=np.int32)
+    refs = np.zeros(pages, dtype=np.int32)
+    order = rng.permutation(pages)[:sum(need)]
+    at = 0
+    for s, n in enumerate(need):
+        table[s, :n] = order[at:at + n]
+        at += n
+    refs[order] = 1
+    nbytes = heads * (page // 16) * 18 * D
+    pool = np.full((layers, pages, nbytes), 0x7f, dtype=np.uint8)
+    if fill:
+        for layer in range(layers):
+            for s, n in enumerate(lens):
+                for t in range(0, int(n), 16):
+                    for h in range(heads):
+                        kv = rng.standard_normal((2, 16, D)) * np.where(rng.random(D) < 0.05, 4.0, 1.0)
+                        (kc, ks), (vc, vs) = (P.quantise(x, 1.0) for x in kv)
+                        m = min(16, int(n) - t)
+                        tile = P.tile_at(pool[layer], table, s, t, h, heads, D, page)
+                        new = [np.full_like(c, 15) for c in (kc, vc)] + [np.full_like(c, 0x7f) for c in (ks, vs)]
+                        for a, b in zip(new, (kc, vc, ks, vs)):
+                            a[:m] = b[:m]
+                        tile[:] = P.make_tile(*new)
+    cache = moe.Kv4Cache(layers, pages, heads, D, page, len(lens), per, pool=dev(pool, torch.uint8), table=dev(table),
+                         lens=dev(lens), refs=dev(refs), k_scale=k_scale, v_scale=v_scale)
+    return cache, pool, table, lens.copy(), refs
+
+
+def cu_of(rows):
+    return np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+
+
+def check_attend(moe, lens, rows, heads, group, D, page, dtype="bf16", window=0, trees=None, scale=None, q_std=1.0,
+                 k_scale=1.0, v_scale=1.0, strided=False, max_rows=None, layers=1, layer=0, seed=0, cache=None):
+    cache, pool, table, lens, _ = cache or make_cache(moe, lens, heads, D, page, layers=layers, k_scale=k_scale,
+                                                      v_scale=v_scale, seed=seed)
+    rng = np.random.default_rng(seed + 1)
+    cu, total, hq = cu_of(rows), int(sum(rows)), heads * group
+    dt = DT[dtype]
+    if strided:  # the queries as a slice of a wider projection, heads further apart than head_dim
+        wide = torch.randn((total, hq + 3, D + 8), generator=torch.Generator().manual_seed(seed)).to(dt).cuda() * q_std
+        q = wide[:, 1:hq + 1, :D]
+    else:
+        q = (dev(rng.standard_normal((total, hq, D)), torch.float32) * q_std).to(dt)
+    lse = torch.full((total, hq), 7.0, dtype=torch.float32, device="cuda")
+    out = torch.full((total, hq, D), 7.0, dtype=dt, device="cuda")
+    tree = None if trees is None else dev(trees, torch.int64)
+    cache.attend(layer, q, dev(cu), max_rows=max_rows or max(max(rows), 1), scale=scale, window=window, tree=tree, out=out,
+                 lse=lse)
+    assert cache.status() == 0
+    got, got_lse, qd = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
+    scale = D ** -0.5 if scale is None else scale
+    half = BF16_HALF_ULP_REL if dtype == "bf16" else 2.0 ** -11
+    tiny = 2.0 ** -134 if dtype == "bf16" else 2.0 ** -25  # half the spacing of the smallest outputs
+    for s in range(len(lens)):
+        n, first = int(rows[s]), int(lens[s]) - int(rows[s])
+        for h in range(heads):
+            k, v = P.kv_of(pool[layer], table, s, int(lens[s]), h, heads, D, page, k_scale, v_scale)
+            for r in range(n):
+                see = P.visible(int(lens[s]), first, r, window, None if trees is None else trees[cu[s] + r])
+                for j in range(group):
+                    at = (cu[s] + r, h * group + j)
+                    ref, ref_lse, spread, qk, vmax = P.attend_row(qd[at], k, v, see, scale)
+                    N = int(see.sum())
+                    # FP32 scores: D products summed, error at most D 2^-23 of sum |q k|; exp2 to 2^-21; p
+                    # rounded to FP16 (2^-11, and 2^-25 where it is subnormal; the largest p is at
+                    # least 1); FP32 sums over N tokens, 16 a step
+                    z = D * 2.0 ** -23 * qk
+                    sums = (N / 16 + 64) * 2.0 ** -22
+                    bound = spread * (2.0 ** -11 + 2 * z + 2.0 ** -20 + sums) + N * 2.0 ** -25 * vmax
+                    bound = bound + np.abs(ref) * half * 1.01 + bound * half + tiny
+                    err = np.abs(got[at] - ref)
+                    assert (err <= bound).all(), (s, h, r, j, float((err / bound).max()))
+                    if N == 0:
+                        assert got_lse[at] == -np.inf and (got[at] == 0).all()
+                    else:
+                        assert abs(got_lse[at] - ref_lse) <= z + sums + 2.0 ** -20 + abs(ref_lse) * 2.0 ** -22, (s, h, r, j)
+    return got
+
+
+# ---- attention ----
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 48, 128])
+@pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 129, 300])
+def test_attend_one_token(moe, D, page, length):
+    check_attend(moe, [length], [1], heads=2, group=3, D=D, page=page, seed=length)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group,rows", [(1, 1), (1, 5), (4, 4), (7, 3), (8, 1), (8, 2), (16, 4), (5, 13), (12, 64)])
+def test_attend_groups_and_rows(moe, D, group, rows):
+    check_attend(moe, [rows + 70, rows + 1, rows + 17], [rows, rows, max(rows // 2, 1)], heads=2, group=group, D=D, page=32,
+                 seed=group * 100 + rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_ragged_batch(moe, D, dtype):
+    lens = [1, 700, 33, 5, 64, 257, 0, 16, 1000]
+    rows = [1, 4, 2, 3, 1, 4, 0, 0, 2]
+    check_attend(moe, lens, rows, heads=3, group=4, D=D, page=64, dtype=dtype, seed=5)
+
+
+@pytest.mark.parametrize("window", [1, 7, 16, 40, 1000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_window(moe, D, window):
+    check_attend(moe, [200, 31, 3], [5, 3, 2], heads=2, group=4, D=D, page=16, window=window, seed=window)
+
+
+def test_attend_rows_that_see_nothing(moe):
+    # more rows than tokens: the first rows lie before the sequence's start; and an empty sequence
+    check_attend(moe, [3, 0, 20], [6, 2, 1], heads=2, group=4, D=128, page=32)
+    # tree rows without a bit and without a prefix
+    check_attend(moe, [4, 3], [4, 3], heads=2, group=2, D=64, page=16, trees=[0, 1, 0, 0xf, 0, 2, 0])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_trees(moe, D):
+    rng = np.random.default_rng(3)
+    rows, lens = [16, 1, 64, 7, 33], [130, 1, 64, 300, 40]
+    trees = []
+    for n in rows:
+        for i in range(n):
+            bits = int(rng.integers(0, 2 ** 62)) & ((1 << (i + 1)) - 1) | (1 << i)
+            trees.append(bits - 2 ** 64 if bits >> 63 else bits)
+    trees[3] = -1  # every bit, the sign bit too: every token of the step
+    check_attend(moe, lens, rows, heads=2, group=3, D=D, page=32, trees=np.array(trees, dtype=np.int64))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_strided_queries_layers_and_scales(moe, D):
+    check_attend(moe, [150, 90], [3, 4], heads=2, group=4, D=D, page=32, strided=True, layers=3, layer=2, k_scale=0.37,
+                 v_scale=12.5, scale=0.21, seed=9)
+
+
+def test_attend_peaked_and_flat_scores(moe):
+    # scores of hundreds, where one token takes all, and of 0; queries far from 1
+    check_attend(moe, [400], [4], heads=2, group=4, D=128, page=64, q_std=60.0)
+    check_attend(moe, [400], [4], heads=2, group=4, D=128, page=64, q_std=0.0)
+    check_attend(moe, [400], [4], heads=2, group=4, D=128, page=64, q_std=1e-20)
+    check_attend(moe, [400], [4], heads=2, group=4, D=128, page=64, q_std=1e20, scale=1e-20)
+
+
+def test_attend_tile_hint_does_not_matter(moe):
+    # max_rows only chooses the tile: fewer rows than there are, or more, are computed all the same
+    for hint in (1, 2, 64, 1000):
+        check_attend(moe, [300, 120], [9, 5], heads=2, group=4, D=128, page=64, max_rows=hint)
+
+
+def test_attend_long_split_over_many_ctas_is_deterministic(moe):
+    cache = make_cache(moe, [6000, 50], 1, 64, 128, seed=2)
+    a = check_attend(moe, None, [2, 1], 1, 8, 64, 128, cache=cache)
+    b = check_attend(moe, None, [2, 1], 1, 8, 64, 128, cache=cache)
+    assert np.array_equal(a, b)
+
+
+def test_attend_repeated_calls_same_bits(moe):
+    cache, *_ = make_cache(moe, [9000, 30, 4000], 2, 64, 64, seed=4)
+    q = torch.randn((9, 16, 64), device="cuda").to(torch.bfloat16)
+    cu = dev([0, 4, 5, 9])
+    first = cache.attend(0, q, cu, max_rows=4)
+    for _ in range(20):
+        assert torch.equal(first, cache.attend(0, q, cu, max_rows=4))
+    assert cache.status() == 0
+
+
+def test_attend_bad_page_is_reported_and_skipped(moe):
+    cache, pool, table, lens, _ = make_cache(moe, [100, 40], 2, 64, 16, seed=6)
+    cache.table[0, 2] = 10 ** 6
+    q = torch.randn((2, 4, 64), device="cuda").to(torch.bfloat16)
+    out = cache.attend(0, q, dev([0, 1, 2]), max_rows=1)
+    assert torch.isfinite(out.float()).all()
+    assert cache.status() == moe.KV4_BAD_PAGE and cache.status() == 0
+
+
+def test_attend_on_another_stream_and_in_a_graph(moe):
+    cache, *_ = make_cache(moe, [500, 77], 2, 128, 64, seed=8)
+    q = torch.randn((4, 8, 128), device="cuda").to(torch.bfloat16)
+    cu = dev([0, 2, 4])
+    want = cache.attend(0, q, cu, max_rows=2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = torch.zeros_like(want)
+    with torch.cuda.stream(side):
+        cache.attend(0, q, cu, max_rows=2, out=out)
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(0, q, cu, max_rows=2, out=out)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+# ---- append and read ----
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,page,ts", [(1, 16, 1.0), (3, 48, 0.375), (8, 128, 2.5)])
+def test_append_and_read(moe, D, dtype, heads, page, ts):
+    lens, rows = [40, 1, 17, 300, 0], [5, 1, 17, 130, 0]
+    cache, pool, table, lens, _ = make_cache(moe, lens, heads, D, page, layers=2, k_scale=ts, v_scale=2 * ts, fill=False)
+    cu, total = cu_of(rows), sum(rows)
+    rng = np.random.default_rng(D + heads)
+    dt = DT[dtype]
+    x = rng.standard_normal((total, 2, heads, D)) * np.exp2(rng.integers(-6, 7, (total, 2, heads, 1)))
+    x[1] = 0.0
+    x[2, :, :, :16] = 0.0
+    kv = dev(x, torch.float64).to(dt)  # K and V interleaved: strided rows
+    k, v = kv[:, 0], kv[:, 1]
+    cache.append(1, k, v, dev(cu))
+    assert cache.status() == 0
+    kn, vn = k.double().cpu().numpy(), v.double().cpu().numpy()
+    want_k, want_v = [P.values(*P.quantise(a, t), t) for a, t in ((kn, ts), (vn, 2 * ts))]
+    after = cache.pool.cpu().numpy()
+    assert np.array_equal(after[0], pool[0])  # the other layer is untouched
+    touched = np.zeros_like(pool[1], dtype=bool)
+    for s, n in enumerate(rows):
+        for i in range(n):
+            pos = int(lens[s]) - n + i
+            for h in range(heads):
+                tile = P.tile_at(after[1], table, s, pos, h, heads, D, page)
+                kc, vc, ks, vs = (f[pos % 16] for f in P.tile_fields(tile, D))
+                assert np.array_equal(P.values(kc, ks, ts), want_k[cu[s] + i, h])
+                assert np.array_equal(P.values(vc, vs, 2 * ts), want_v[cu[s] + i, h])
+                mark = P.tile_at(touched, table, s, pos, h, heads, D, page)
+                mark[:8 * D].reshape(D // 32, 16, 16)[:, pos % 16] = True
+                mark[8 * D:16 * D].reshape(16, D // 2)[pos % 16] = True
+                mark[16 * D:17 * D].reshape(16, D // 16)[pos % 16] = True
+                mark[17 * D:].reshape(16, D // 16)[pos % 16] = True
+    assert np.array_equal(after[1][~touched], pool[1][~touched])
+    gk, gv = cache.read(1, dev(cu), rows=total, dtype=dt)
+    for got, want in ((gk, want_k), (gv, want_v)):
+        assert torch.equal(got.cpu(), torch.tensor(want).float().to(dt))
+
+
+def test_append_ties_go_to_even(moe):
+    # every tie of the code grid under a scale of 1 (largest value 6), and ties of the scale itself
+    x = np.zeros((3, 1, 64))
+    ties = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
+    x[0, 0, :15] = ties + [-t for t in ties] + [6.0]
+    x[1, 0, 0] = 6 * 1.0625  # halfway between the scales 1 and 1.125: to 1
+    x[1, 0, 16] = 6 * 1.1875  # halfway between 1.125 and 1.25: to 1.25
+    x[2, 0, 0] = 2.0 ** -10 * 6  # half the smallest scale: to 0
+    cache, *_ = make_cache(moe, [3], 1, 64, 16, fill=False)
+    t = dev(x, torch.float64).to(torch.bfloat16)
+    cache.append(0, t, t, dev([0, 3]))
+    k, v = cache.read(0, dev([0, 3]), rows=3)
+    want = P.values(*P.quantise(t.double().cpu().numpy(), 1.0), 1.0)
+    assert list(want[0, 0, :7]) == [0.0, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0]
+    assert want[1, 0, 0] == 6.0 and want[1, 0, 16] == 7.5 and want[2, 0, 0] == 0.0
+    for got in (k, v):
+        assert np.array_equal(got.double().cpu().numpy(), want)
+
+
+def held_one():
+    """The value that a block of ones is held as (the scale 1/6 is rounded to 1.375 / 8)."""
+    one = P.values(*P.quantise(np.ones(16), 1.0), 1.0)
+    assert (one == 6 * 1.375 / 8).all()
+    return float(one[0])
+
+
+def test_append_nonfinite(moe):
+    cache, *_ = make_cache(moe, [2], 1, 64, 16, fill=False)
+    x = torch.ones((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    x[0, 0, 3], x[0, 0, 4], x[0, 0, 20] = float("inf"), float("-inf"), float("nan")
+    cache.append(0, x, torch.ones_like(x), dev([0, 2]))
+    k, v = cache.read(0, dev([0, 2]), rows=2)
+    assert cache.status() == moe.KV4_NONFINITE
+    k = k.float().cpu()
+    assert k[0, 0, 3] == 2688 and k[0, 0, 4] == -2688 and k[0, 0, 0] == 0  # 1 is below half the smallest step at scale 448
+    one = held_one()
+    assert k[0, 0, 20] == 0 and k[0, 0, 21] == one and (k[1] == one).all() and (v.float() == one).all()
+
+
+def test_append_outside_the_sequence_is_reported(moe):
+    cache, pool, *_ = make_cache(moe, [2, 5], 1, 64, 16, fill=False)
+    x = torch.ones((8, 1, 64), dtype=torch.bfloat16, device="cuda")
+    cache.table[1, 0] = 99
+    cache.append(0, x, x, dev([0, 4, 8]))  # two rows before the start of sequence 0; a page that is none
+    assert cache.status() == moe.KV4_BAD_PAGE
+    k, _ = cache.read(0, dev([0, 4, 8]), rows=8)
+    assert (k[:2] == 0).all() and (k[2:4] == held_one()).all() and (k[4:] == 0).all()
+
+
+# ---- pages ----
+
+def same(cache, plain):
+    assert np.array_equal(cache.table.cpu().numpy(), plain.table)
+    assert np.array_equal(cache.lens.cpu().numpy(), plain.lens)
+    assert np.array_equal(cache.refs.cpu().numpy(), plain.refs)
+    assert np.array_equal(cache.pool.cpu().numpy(), plain.pool)
+
+
+def random_cache(moe, lens, heads, D, page, layers, extra, max_pages, seed):
+    cache, pool, table, lens, refs = make_cache(moe, lens, heads, D, page, layers=layers, extra_pages=extra, max_pages=max_pages,
+                                                seed=seed, fill=False)
+    rng = np.random.default_rng(seed)
+    pool[:] = rng.integers(0, 256, pool.shape, dtype=np.uint8)
+    cache.pool.copy_(dev(pool, torch.uint8))
+    return cache, P.PlainPages(pool, table, lens, refs, heads, D, page)
+
+
+@pytest.mark.parametrize("D,heads,page", [(64, 3, 16), (128, 2, 48), (256, 1, 32)])
+@pytest.mark.parametrize("seed", range(4))
+def test_pages_random_steps(moe, D, heads, page, seed):
+    rng = np.random.default_rng(seed)
+    n = 9
+    cache, plain = random_cache(moe, rng.integers(0, 70, n), heads, D, page, 3, 40, 12, seed)
+    for step in range(6):
+        if step % 2 == 0:
+            dst = rng.choice(n, 3, replace=False)
+            src = rng.choice([s for s in range(n) if s not in dst], 3)
+            cache.fork(dev(src), dev(dst))
+            plain.fork(src, dst)
+            same(cache, plain)
+        new = rng.integers(-1, 9, n)
+        cache.reserve(dev(new))
+        plain.reserve(new)
+        same(cache, plain)
+        assert not plain.no_page and cache.status() == 0
+        rows = np.maximum(new, 0)
+        cu = cu_of(rows)
+        keep = (rng.random(max(int(cu[-1]), 1)) < 0.5).astype(np.uint8)
+        cache.compact(dev(keep, torch.uint8), dev(cu), max_rows=8)
+        plain.compact(keep, cu)
+        same(cache, plain)
+        to = plain.lens - rng.integers(0, 20, n) * (rng.random(n) < 0.3)
+        cache.trim(dev(to))
+        plain.trim(to)
+        same(cache, plain)
+    assert cache.status() == 0
+    cache.trim(dev(np.zeros(n)))
+    assert (cache.refs == 0).all() and (cache.table == -1).all() and (cache.lens == 0).all()
+
+
+def test_reserve_out_of_pages(moe):
+    # 5 free pages of 16: sequence 0 takes two, 1 needs four and is refused, 2 (which needs none) still grows, 3 is
+    # refused although one page would do; 4 has no room in its table
+    cache, plain = random_cache(moe, [16, 32, 20, 16, 90], 1, 64, 16, 2, 5, 6, 1)
+    new = [32, 64, 3, 1, 7]
+    cache.reserve(dev(new))
+    plain.reserve(new)
+    same(cache, plain)
+    assert plain.no_page and cache.status() == moe.KV4_NO_PAGE
+    assert list(plain.lens) == [48, 32, 23, 16, 90]
+
+
+def test_reserve_shared_page_of_several_writers(moe):
+    # the last page of a sequence shared by three, two of which write: both copy; then all three
+    for writers in ([1, 2], [0, 1, 2]):
+        cache, plain = random_cache(moe, [21, 0, 0, 5], 2, 64, 16, 2, 12, 4, 2)
+        cache.fork(dev([0, 0]), dev([1, 2]))
+        plain.fork([0, 0], [1, 2])
+        new = [13 if s in writers else 0 for s in range(4)]
+        cache.reserve(dev(new))
+        plain.reserve(new)
+        same(cache, plain)
+        assert cache.status() == 0
+
+
+def test_reserve_many_sequences_and_pages(moe):
+    # more sequences than the allocation keeps in shared memory, pages over several rounds
+    rng = np.random.default_rng(5)
+    cache, plain = random_cache(moe, rng.integers(0, 20, 5000), 1, 64, 16, 1, 9000, 4, 3)
+    new = rng.integers(0, 20, 5000)
+    cache.reserve(dev(new))
+    plain.reserve(new)
+    same(cache, plain)
+    assert cache.status() == 0
+
+
+@pytest.mark.parametrize("kept", [[], [0], [0, 1, 2], [63], [5, 6, 7, 40], list(range(64)), list(range(0, 64, 2)), list(range(1, 64))])
+def test_compact_patterns(moe, kept):
+    cache, plain = random_cache(moe, [70, 64, 200], 2, 128, 16, 2, 4, 16, 4)
+    keep = np.zeros(3 * 64, dtype=np.uint8)
+    for s in range(3):
+        keep[64 * s + np.array(kept, dtype=int)] = 1 + 100 * s  # any value but 0 keeps a row
+    cu = [0, 64, 128, 192]
+    cache.compact(dev(keep, torch.uint8), dev(cu), max_rows=64)
+    plain.compact(keep, np.array(cu))
+    same(cache, plain)
+    assert cache.status() == 0
+
+
+def test_fork_bad_sequences_are_reported(moe):
+    cache, plain = random_cache(moe, [20, 0, 3], 1, 64, 16, 1, 4, 4, 1)
+    cache.fork(dev([0, 7, 2]), dev([1, 0, 2]))
+    plain.fork([0], [1])
+    same(cache, plain)
+    assert cache.status() == moe.KV4_BAD_SEQ
+
+
+def test_refusals(moe):
+    with pytest.raises(moe.MoeError):
+        moe.Kv4Cache(1, 4, 2, 96, 16, 2, 4)  # head size
+    with pytest.raises(moe.MoeError):
+        moe.Kv4Cache(1, 4, 2, 64, 24, 2, 4)  # page size
+    with pytest.raises(moe.MoeError):
+        moe.Kv4Cache(1, 4, 2, 64, 16, 2, 4, k_scale=0.0)
+    with pytest.raises(ValueError):
+        moe.Kv4Cache(1, 4, 2, 64, 16, 2, 4, lens=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    cache, *_ = make_cache(moe, [20, 30], 2, 64, 16)
+    cu = dev([0, 1, 2])
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    for bad in (q.float(), q[..., :32], q.transpose(1, 2).contiguous().transpose(1, 2)):
+        with pytest.raises(ValueError):
+            cache.attend(0, bad, cu, max_rows=1)
+    with pytest.raises(moe.MoeError):  # 5 query heads over 2
+        cache.attend(0, torch.zeros((2, 5, 64), dtype=torch.bfloat16, device="cuda"), cu, max_rows=1)
+    with pytest.raises(moe.MoeError):  # rows 4 elements off a 16-byte boundary
+        wide = torch.zeros((2, 4, 72), dtype=torch.bfloat16, device="cuda")
+        cache.attend(0, wide[..., 4:68], cu, max_rows=1)
+    with pytest.raises(moe.MoeError):
+        cache.attend(1, q, cu, max_rows=1)  # no such layer
+    with pytest.raises(moe.MoeError):
+        cache.attend(0, q, cu, max_rows=1, window=-1)
+    tree = torch.zeros(2, dtype=torch.int64, device="cuda")
+    with pytest.raises(moe.MoeError):
+        cache.attend(0, q, cu, max_rows=1, window=4, tree=tree)
+    with pytest.raises(moe.MoeError):
+        cache.attend(0, q, cu, max_rows=65, tree=tree)
+    with pytest.raises(ValueError):
+        cache.attend(0, q, cu[:2], max_rows=1)
+    with pytest.raises(ValueError):
+        cache.attend(0, q, cu.long(), max_rows=1)
+    with pytest.raises(ValueError):
+        cache.append(0, q[:, :2], q[:1, :2], cu)
+    with pytest.raises(ValueError):
+        cache.reserve(dev([1, 2, 3]))
+    with pytest.raises(moe.MoeError):
+        cache.compact(torch.zeros(2, dtype=torch.uint8, device="cuda"), cu, max_rows=65)
+    assert cache.attend(0, q[:0], dev([0, 0, 0]), max_rows=0).shape == (0, 4, 64)
+    assert cache.status() == 0
