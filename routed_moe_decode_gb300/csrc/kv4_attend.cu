@@ -29,8 +29,6 @@ namespace kv4 {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.69314718055994530942f;
 // A row's reference m moves only when a score exceeds it by more than this (in powers of two): p
 // stays below 2^8, far inside FP16, and the sums are rescaled a few times instead of at every tile.
@@ -71,44 +69,69 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, Bytes<BYTES>& o) {
   }
 }
 
-// A lane's share of one tile as it lies in memory.
+// N scale bytes (1, 2 or 4) in the low bytes of a word.
+template <int N>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
+  if constexpr (N == 4) {
+    uint32_t v;
+    asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+  } else if constexpr (N == 2) {
+    uint16_t v;
+    asm volatile("ld.global.L1::no_allocate.b16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+  } else {
+    uint32_t v;
+    asm volatile("ld.global.L1::no_allocate.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+  }
+}
+
+// A lane's share of the keys of one tile as they lie in memory: tokens g and g + 8, channels
+// [q D/4, +D/4) and their D / 64 scales; and of the values: tokens 2q, 2q + 1, 2q + 8, 2q + 9,
+// channels [g D/8, +D/8) and their scale (D = 256: two).
 template <int D>
-struct TileData {
-  Bytes<D / 8> k[2];     // tokens g, g + 8: channels [q D/4, +D/4)
-  Bytes<D / 16> v[4];    // tokens 2q, 2q + 1, 2q + 8, 2q + 9: channels [g D/8, +D/8)
-  uint32_t ks[2];        // D / 64 scales each
-  uint32_t vs[4];        // D = 256: 2 scales, else 1
+struct KeyData {
+  Bytes<D / 8> c[2];
+  uint32_t s[2];
+};
+template <int D>
+struct ValueData {
+  Bytes<D / 16> c[4];
+  uint32_t s[4];
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(const uint8_t* tile, int lane, TileData<D>& t) {
+__device__ __forceinline__ void load_keys(const uint8_t* tile, int lane, KeyData<D>& t) {
   const int g = lane >> 2, q = lane & 3;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int tok = g + 8 * i;
     if constexpr (D == 64) {
-      load_bytes<8>(tile + (q >> 1) * 256 + tok * 16 + (q & 1) * 8, t.k[i]);
-      t.ks[i] = tile[16 * D + tok * (D / 16) + q];
+      load_bytes<8>(tile + (q >> 1) * 256 + tok * 16 + (q & 1) * 8, t.c[i]);
+      t.s[i] = load_scales<1>(tile + 16 * D + tok * (D / 16) + q);
     } else if constexpr (D == 128) {
-      load_bytes<16>(tile + q * 256 + tok * 16, t.k[i]);
-      t.ks[i] = *reinterpret_cast<const uint16_t*>(tile + 16 * D + tok * (D / 16) + 2 * q);
+      load_bytes<16>(tile + q * 256 + tok * 16, t.c[i]);
+      t.s[i] = load_scales<2>(tile + 16 * D + tok * (D / 16) + 2 * q);
     } else {
       Bytes<16> a, b;
       load_bytes<16>(tile + (2 * q) * 256 + tok * 16, a);
       load_bytes<16>(tile + (2 * q + 1) * 256 + tok * 16, b);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) { t.k[i].w[j] = a.w[j]; t.k[i].w[4 + j] = b.w[j]; }
-      t.ks[i] = *reinterpret_cast<const uint32_t*>(tile + 16 * D + tok * (D / 16) + 4 * q);
+      for (int j = 0; j < 4; ++j) { t.c[i].w[j] = a.w[j]; t.c[i].w[4 + j] = b.w[j]; }
+      t.s[i] = load_scales<4>(tile + 16 * D + tok * (D / 16) + 4 * q);
     }
   }
+}
+template <int D>
+__device__ __forceinline__ void load_values(const uint8_t* tile, int lane, ValueData<D>& t) {
+  const int g = lane >> 2, q = lane & 3;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int tok = 2 * q + (i & 1) + 8 * (i >> 1);
-    load_bytes<D / 16>(tile + 8 * D + tok * (D / 2) + g * (D / 16), t.v[i]);
+    load_bytes<D / 16>(tile + 8 * D + tok * (D / 2) + g * (D / 16), t.c[i]);
     const uint8_t* sp = tile + 17 * D + tok * (D / 16);
-    if constexpr (D == 64) t.vs[i] = sp[g >> 1];
-    else if constexpr (D == 128) t.vs[i] = sp[g];
-    else t.vs[i] = *reinterpret_cast<const uint16_t*>(sp + 2 * g);
+    t.s[i] = D == 64 ? load_scales<1>(sp + (g >> 1)) : D == 128 ? load_scales<1>(sp + g) : load_scales<2>(sp + 2 * g);
   }
 }
 
@@ -123,6 +146,8 @@ struct Item {
   int items;     // heads * blocks (0: no rows)
 };
 
+constexpr long long kMaxTokens = 1ll << 30;
+
 template <int ROWS>
 __device__ __forceinline__ Item item_of(const AttendArgs& a, int s) {
   Item it;
@@ -133,7 +158,7 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, int s) {
   it.items = 0;
   it.tiles = 1;
   if (st.n == 0) return it;
-  const long long room = static_cast<long long>(a.c.max_pages) * a.c.page_size;
+  const long long room = min(static_cast<long long>(a.c.max_pages) * a.c.page_size, kMaxTokens);
   const int len = max(ld(a.c.lens + s), 0);
   it.len = static_cast<int>(min(static_cast<long long>(len), room));
   it.first = len - st.n;
@@ -147,6 +172,7 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, int s) {
 __device__ __forceinline__ long long work_of(const Item& it) { return static_cast<long long>(it.items) * it.tiles; }
 
 // Exclusive prefix sum of one value per thread over the block, and the block's sum.
+template <int W>
 __device__ __forceinline__ long long block_prefix(long long v, long long* sums, long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
@@ -159,33 +185,40 @@ __device__ __forceinline__ long long block_prefix(long long v, long long* sums, 
   __syncthreads();
   long long before = 0;
   total = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) before += sums[w];
     total += sums[w];
   }
   return before + x - v;
 }
 
-template <int D, int NT>
+// W warps, blocks of 8 NT rows; QS: the query rows' operands are kept in shared memory (one copy for
+// all warps) instead of registers.
+template <int D, int NT, int W, bool QS>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kSumBytes = kWarps * kRows * (D + 4) * 4;  // the warps' sums, rows padded by 4 floats
-  static constexpr int kStatBytes = kWarps * kRows * 2 * 4;       // their m and l
-  static constexpr int kSmem = kSumBytes + kStatBytes + kRows * 2 * 4;
+  static constexpr int kJoin = W / 2;  // warps whose sums lie in shared memory at a time
+  static constexpr int kSumBytes = kJoin * kRows * (D + 4) * 4;  // rows padded by 4 floats
+  static constexpr int kStatBytes = W * kRows * 2 * 4;           // the warps' m and l
+  static constexpr int kQBytes = QS ? kRows * D * 2 : 0;
+  static constexpr int kSmem = kSumBytes + kStatBytes + kRows * 2 * 4 + kQBytes;
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
+template <int D, int NT, int W, int CTAS, bool QS>
+__global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;   // k16 steps of a score, and m16 tiles of the output
   constexpr int PITCH = D + 4;
+  constexpr int kThreads = 32 * W;
+  constexpr int JOIN = W / 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* s_sum = reinterpret_cast<float*>(smem);                       // [warps][rows][PITCH]
-  float* s_m = s_sum + kWarps * ROWS * PITCH;                          // [warps][rows]
-  float* s_l = s_m + kWarps * ROWS;                                    // [warps][rows]
-  float* s_mt = s_l + kWarps * ROWS;                                   // [rows] joined m
+  float* s_sum = reinterpret_cast<float*>(smem);                       // [JOIN][rows][PITCH]
+  float* s_m = s_sum + JOIN * ROWS * PITCH;                            // [warps][rows]
+  float* s_l = s_m + W * ROWS;                                         // [warps][rows]
+  float* s_mt = s_l + W * ROWS;                                        // [rows] joined m
   float* s_lt = s_mt + ROWS;                                           // [rows] joined l
-  __shared__ long long s_scan[kWarps];
+  uint4* s_q = reinterpret_cast<uint4*>(s_lt + ROWS);                  // QS: [n-tile][word][lane]
+  __shared__ long long s_scan[W];
   __shared__ long long s_off;
   __shared__ int s_seq, s_last;
   pdl_wait();
@@ -198,8 +231,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
   long long mine = 0;
   for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS>(a, s));
   long long total;
-  const long long before = block_prefix(mine, s_scan, total);
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kWarps));
+  const long long before = block_prefix<W>(mine, s_scan, total);
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(W));
   long long pos = per * blockIdx.x;
   const long long end = min(pos + per, total);
   if (pos >= end) return;
@@ -226,9 +259,11 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
     const int r0 = blk * ROWS;  // first of the block's rows: row r is (step row r / group, query head r % group)
     const int nrows = min(ROWS, it.n * a.group - r0);
 
-    // the query rows as FP16, brought near 2^10 by a power of two that z's factor takes back
-    uint32_t qf[NT][2 * KS];
+    // the query rows as FP16, brought near 2^10 by a power of two that z's factor takes back; the
+    // sign of the scale goes to the rows, so that a larger product is a larger score
+    uint32_t qf[QS ? 1 : NT][QS ? 1 : 2 * KS];
     float factor[NT][2];  // of the rows 2q and 2q + 1 of each n-tile
+    const float sign = a.scale2 < 0.f ? -1.f : 1.f, size = fabsf(a.scale2);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = 8 * t + g;
@@ -253,16 +288,25 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
       // 2^shift: the exponent field of top, brought to that of 2^10
       const int e = static_cast<int>(__float_as_uint(top) >> 23);
       const int shift = e == 0 || e == 255 ? 0 : min(max(137 - e, -100), 100);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) * a.scale2;
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23) * sign;
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) * size;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const float2 f = unpack2(raw[i], a.fp16);
-        qf[t][i] = half2_bits(f.x * up, f.y * up);
+        raw[i] = half2_bits(f.x * up, f.y * up);
+        if constexpr (!QS) qf[t][i] = raw[i];
+      }
+      if constexpr (QS) {
+        if (t % W == warp) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            s_q[(t * (D / 32) + i) * 32 + lane] = make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+        }
       }
       factor[t][0] = __shfl_sync(0xffffffffu, down, 8 * q);      // lane of row 2q: g = 2q
       factor[t][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
     }
+    if constexpr (QS) __syncthreads();
 
     float acc[NT][KS][4];
     float m[NT][2], l[NT][2];
@@ -282,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
     const int* table = a.c.table + static_cast<size_t>(it.s) * a.c.max_pages;
     auto tile_ptr = [&](int t) -> const uint8_t* {  // nullptr: no token of it may be read
       if (t * kTile >= it.len) return nullptr;
-      const int pi = t / a.c.tiles_per_page;
+      const int pi = a.c.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), a.page_magic));
       const int page = ld(table + pi);
       if (page < 0 || page >= a.c.pages) {
         if (lane == 0) atomicOr(a.c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
@@ -291,28 +335,31 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
       return a.c.pool + static_cast<size_t>(page) * a.c.page_bytes +
              (static_cast<size_t>(h) * a.c.tiles_per_page + (t - pi * a.c.tiles_per_page)) * a.c.tile_bytes;
     };
-    TileData<D> cur, nxt;
+    KeyData<D> kd;
+    ValueData<D> vd;
     int t = t0 + warp;
     const uint8_t* p_cur = t < t1 ? tile_ptr(t) : nullptr;
-    if (p_cur) load_tile<D>(p_cur, lane, cur);
-    const uint8_t* p_nxt = t + kWarps < t1 ? tile_ptr(t + kWarps) : nullptr;
-    for (; t < t1; t += kWarps) {
-      if (p_nxt) load_tile<D>(p_nxt, lane, nxt);
-      const uint8_t* p_nxt2 = t + 2 * kWarps < t1 ? tile_ptr(t + 2 * kWarps) : nullptr;
-      if (p_cur) {
-        const int tok0 = t * kTile;
-        float sc[NT][4];
+    if (p_cur) {
+      load_keys<D>(p_cur, lane, kd);
+      load_values<D>(p_cur, lane, vd);
+    }
+    const uint8_t* p_nxt = t + W < t1 ? tile_ptr(t + W) : nullptr;
+    for (; t < t1; t += W) {
+      const uint8_t* p_nxt2 = t + 2 * W < t1 ? tile_ptr(t + 2 * W) : nullptr;
+      const int tok0 = t * kTile;
+      float sc[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+      for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+      if (p_cur) {
         // ---- S^T = K Q^T, one word (8 channels, half a scale block) of each token at a time ----
         uint32_t kscale[2][D / 64];  // broadcast pairs
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t s2 = e4m3x2_to_f16x2(cur.ks[i]);
+          const uint32_t s2 = e4m3x2_to_f16x2(kd.s[i]);
           kscale[i][0] = bcast_lo_half(s2);
           if constexpr (D >= 128) kscale[i][1] = bcast_hi_half(s2);
           if constexpr (D == 256) {
-            const uint32_t s3 = e4m3x2_to_f16x2(cur.ks[i] >> 16);
+            const uint32_t s3 = e4m3x2_to_f16x2(kd.s[i] >> 16);
             kscale[i][2] = bcast_lo_half(s3);
             kscale[i][3] = bcast_hi_half(s3);
           }
@@ -320,8 +367,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           uint32_t x[4], y[4];
-          e2m1x8_to_f16x2x4(cur.k[0].w[w], x[0], x[1], x[2], x[3]);
-          e2m1x8_to_f16x2x4(cur.k[1].w[w], y[0], y[1], y[2], y[3]);
+          e2m1x8_to_f16x2x4(kd.c[0].w[w], x[0], x[1], x[2], x[3]);
+          e2m1x8_to_f16x2x4(kd.c[1].w[w], y[0], y[1], y[2], y[3]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             x[i] = hmul2_bits(x[i], kscale[0][w / 2]);
@@ -329,18 +376,25 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mk::mma_16816(sc[n], x[0], y[0], x[1], y[1], qf[n][4 * w], qf[n][4 * w + 1]);
-            mk::mma_16816(sc[n], x[2], y[2], x[3], y[3], qf[n][4 * w + 2], qf[n][4 * w + 3]);
+            uint4 b;
+            if constexpr (QS) b = s_q[(n * (D / 32) + w) * 32 + lane];
+            else b = make_uint4(qf[n][4 * w], qf[n][4 * w + 1], qf[n][4 * w + 2], qf[n][4 * w + 3]);
+            mk::mma_16816(sc[n], x[0], y[0], x[1], y[1], b.x, b.y);
+            mk::mma_16816(sc[n], x[2], y[2], x[3], y[3], b.z, b.w);
           }
         }
+      }
+      if (p_nxt) load_keys<D>(p_nxt, lane, kd);  // the next tile's, in flight until it comes round
+      if (p_cur) {
         // ---- masks, running reference, p ----
         const bool open = tok0 >= open_lo && tok0 + kTile <= open_hi;
         uint32_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          float z[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float z = sc[n][i] * factor[n][i & 1];
+            z[i] = sc[n][i] * factor[n][i & 1];
             if (!open) {
               const int tok = tok0 + g + 8 * (i >> 1), r = 8 * n + 2 * q + (i & 1);
               const int row = (r0 + min(r, nrows - 1)) / a.group, x = it.first + row;
@@ -351,11 +405,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
               } else {
                 see = see && tok <= x && (a.window <= 0 || tok > x - a.window);
               }
-              if (!see) z = -INFINITY;
+              if (!see) z[i] = -INFINITY;
             }
-            sc[n][i] = z;
           }
-          const float hi0 = fmaxf(sc[n][0], sc[n][2]), hi1 = fmaxf(sc[n][1], sc[n][3]);
+          const float hi0 = fmaxf(z[0], z[2]), hi1 = fmaxf(z[1], z[3]);
           if (__any_sync(0xffffffffu, hi0 > m[n][0] + kSlack || hi1 > m[n][1] + kSlack)) {
             float n0 = fmaxf(hi0, m[n][0]), n1 = fmaxf(hi1, m[n][1]);
 #pragma unroll
@@ -375,8 +428,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
             }
           }
           const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-          const float p0 = exp2_approx(sc[n][0] - m0), p1 = exp2_approx(sc[n][1] - m1);
-          const float p2 = exp2_approx(sc[n][2] - m0), p3 = exp2_approx(sc[n][3] - m1);
+          const float p0 = exp2_approx(z[0] - m0), p1 = exp2_approx(z[1] - m1);
+          const float p2 = exp2_approx(z[2] - m0), p3 = exp2_approx(z[3] - m1);
           l[n][0] += p0 + p2;
           l[n][1] += p1 + p3;
           pf[n][0] = movmatrix(half2_bits(p0, p1));
@@ -386,12 +439,12 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
         if (tok0 + kTile > it.len) {  // scales past the end are not the sequence's: 0, so that 0 * p is 0
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (tok0 + 2 * q + (i & 1) + 8 * (i >> 1) >= it.len) cur.vs[i] = 0;
+            if (tok0 + 2 * q + (i & 1) + 8 * (i >> 1) >= it.len) vd.s[i] = 0;
         }
         uint32_t vscale[2][D == 256 ? 2 : 1];  // (token 2q, 2q + 1), (2q + 8, 2q + 9)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t u = cur.vs[2 * i], v = cur.vs[2 * i + 1];
+          const uint32_t u = vd.s[2 * i], v = vd.s[2 * i + 1];
           vscale[i][0] = e4m3x2_to_f16x2((u & 0xffu) | ((v & 0xffu) << 8));
           if constexpr (D == 256) vscale[i][1] = e4m3x2_to_f16x2((u >> 8) | (v & 0xff00u));
         }
@@ -400,7 +453,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
           uint32_t e[2][4], o[2][4];        // even and odd channels, (2q, 2q + 1) and (2q + 8, 2q + 9)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t u = cur.v[2 * i].w[w], v = cur.v[2 * i + 1].w[w];
+            const uint32_t u = vd.c[2 * i].w[w], v = vd.c[2 * i + 1].w[w];
             const uint32_t we = (u & 0x0f0f0f0fu) | ((v << 4) & 0xf0f0f0f0u);
             const uint32_t wo = ((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u);
             e2m1x8_to_f16x2x4(we, e[i][0], e[i][1], e[i][2], e[i][3]);
@@ -419,12 +472,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
               mk::mma_16816(acc[n][4 * w + j], e[0][j], o[0][j], e[1][j], o[1][j], pf[n][0], pf[n][1]);
         }
       }
-      cur = nxt;
+      if (p_nxt) load_values<D>(p_nxt, lane, vd);
       p_cur = p_nxt;
       p_nxt = p_nxt2;
     }
 
-    // ---- join the warps ----
+    // ---- join the warps: the second half's sums go to the first half's registers through shared
+    // memory, the first half's to all threads ----
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -439,25 +493,53 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
         s_l[warp * ROWS + r] = l[n][0];
         s_l[warp * ROWS + r + 1] = l[n][1];
       }
-      // accumulator i of m-tile t: channel g D/8 + 2t + (i >> 1), row 2q + (i & 1)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float* dst = s_sum + (warp * ROWS + 8 * n + 2 * q + i) * PITCH + g * (D / 8);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) *reinterpret_cast<float2*>(dst + 2 * k) = make_float2(acc[n][k][i], acc[n][k][2 + i]);
-      }
     }
     __syncthreads();
     if (tid < ROWS) {
       float mt = -INFINITY, lt = 0.f;
-      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_m[w * ROWS + tid]);
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < W; ++w) mt = fmaxf(mt, s_m[w * ROWS + tid]);
+      for (int w = 0; w < W; ++w) {
         const float c = s_m[w * ROWS + tid] == -INFINITY ? 0.f : exp2_approx(s_m[w * ROWS + tid] - mt);
         lt += c * s_l[w * ROWS + tid];
         s_m[w * ROWS + tid] = c;  // the warp's factor
       }
       s_mt[tid] = mt;
       s_lt[tid] = lt;
+    }
+    __syncthreads();
+    // accumulator i of m-tile k: channel g D/8 + 2k + (i >> 1), row 2q + (i & 1)
+    const int slot = warp % JOIN;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float c = s_m[warp * ROWS + 8 * n + 2 * q + i];
+#pragma unroll
+        for (int k = 0; k < KS; ++k) { acc[n][k][i] *= c; acc[n][k][2 + i] *= c; }
+      }
+    auto spot = [&](int n, int i, int k) {
+      return reinterpret_cast<float2*>(s_sum + (slot * ROWS + 8 * n + 2 * q + i) * PITCH + g * (D / 8) + 2 * k);
+    };
+    if (warp >= JOIN) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) *spot(n, i, k) = make_float2(acc[n][k][i], acc[n][k][2 + i]);
+    }
+    __syncthreads();
+    if (warp < JOIN) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            float2* p = spot(n, i, k);
+            const float2 x = *p;
+            *p = make_float2(acc[n][k][i] + x.x, acc[n][k][2 + i] + x.y);
+          }
     }
     __syncthreads();
 
@@ -478,10 +560,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
       const int r = i / (D / 4), d4 = i - r * (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float c = s_m[w * ROWS + r];
+      for (int w = 0; w < JOIN; ++w) {
         const float4 x = *reinterpret_cast<const float4*>(s_sum + (w * ROWS + r) * PITCH + 4 * d4);
-        v.x += c * x.x; v.y += c * x.y; v.z += c * x.z; v.w += c * x.w;
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
       if (whole) {
         if (r < nrows) finish(r, d4, v, s_mt[r], s_lt[r]);
@@ -551,25 +632,33 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
   }
 }
 
-template <int D, int NT>
-cudaError_t launch(const AttendArgs& a, int num_sms, cudaStream_t stream) {
-  constexpr int smem = Shape<D, NT>::kSmem;
-  static_assert(Shape<D, NT>::kRows * D <= kPartSums && Shape<D, NT>::kRows <= kPartRows, "a partial result holds a block");
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int D, int NT, int W, int CTAS, bool QS>
+cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
+  constexpr int smem = Shape<D, NT, W, QS>::kSmem;
+  static_assert(8 * NT * D <= kPartSums && 8 * NT <= kPartRows, "a partial result holds a block");
+  auto kernel = attend_kernel<D, NT, W, CTAS, QS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  int grid = 2 * num_sms;
-  if (grid > kMaxGrid) grid = kMaxGrid;
-  return launch_pdl(attend_kernel<D, NT>, dim3(grid), dim3(kThreads), smem, stream, a);
+  // t / tiles_per_page = umulhi(t, magic): exact for t below 2^26 (2^30 tokens) and up to 64 tiles a page
+  a.page_magic = static_cast<uint32_t>(((1ull << 32) + a.c.tiles_per_page - 1) / a.c.tiles_per_page);
+  const int grid = min(CTAS * num_sms, kMaxGrid);
+  return launch_pdl(kernel, dim3(grid), dim3(32 * W), smem, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream) {
-  const bool two = row_tile > 8;
   switch (a.c.dim) {
-    case 64: return two ? launch<64, 2>(a, num_sms, stream) : launch<64, 1>(a, num_sms, stream);
-    case 128: return two ? launch<128, 2>(a, num_sms, stream) : launch<128, 1>(a, num_sms, stream);
-    default: return two ? launch<256, 2>(a, num_sms, stream) : launch<256, 1>(a, num_sms, stream);
+    case 64:
+      return row_tile <= 8    ? launch<64, 1, 8, 2, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<64, 2, 8, 2, false>(a, num_sms, stream)
+                              : launch<64, 4, 12, 1, false>(a, num_sms, stream);
+    case 128:
+      return row_tile <= 8    ? launch<128, 1, 8, 2, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<128, 2, 12, 1, false>(a, num_sms, stream)
+                              : launch<128, 4, 8, 1, true>(a, num_sms, stream);
+    default:
+      return row_tile <= 8 ? launch<256, 1, 12, 1, false>(a, num_sms, stream) : launch<256, 2, 8, 1, true>(a, num_sms, stream);
   }
 }
 

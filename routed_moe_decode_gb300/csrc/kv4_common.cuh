@@ -133,6 +133,7 @@ struct AttendArgs {
   const unsigned long long* tree;
   void* out;
   float* lse;
+  uint32_t page_magic;  // set by the launcher
   float* part;
   size_t part_floats;
   uint32_t* counters;
