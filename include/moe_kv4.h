@@ -56,6 +56,8 @@ extern "C" {
 #define MOE_KV4_NONFINITE 0x4u /* moe_kv4_append met an infinity or a NaN */
 #define MOE_KV4_BAD_SEQ 0x8u   /* a sequence number outside [0, seqs) or forked onto itself: skipped */
 
+#define MOE_KV4_TIMEOUT 0x10u  /* a bounded wait in the attention kernel gave up: its results are not valid */
+
 typedef enum moe_kv4_dtype { MOE_KV4_BF16 = 0, MOE_KV4_FP16 = 1 } moe_kv4_dtype;
 
 /* One cache.  head_dim 64, 128 or 256; page_size a multiple of 16 up to 1024; kv_heads 1 to

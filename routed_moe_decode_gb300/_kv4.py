@@ -13,6 +13,7 @@ KV4_NO_PAGE = 0x1
 KV4_BAD_PAGE = 0x2
 KV4_NONFINITE = 0x4
 KV4_BAD_SEQ = 0x8
+KV4_TIMEOUT = 0x10
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
