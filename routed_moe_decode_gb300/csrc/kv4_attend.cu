@@ -125,41 +125,55 @@ __device__ __forceinline__ Words<N> shared_words(const uint8_t* p) {
   return o;
 }
 
-// The item that a position of the work lies in.
+// The work is counted in units of two tiles (32 tokens), each of which a warp takes as one step: two
+// independent chains of products, and one look at the masks and at the reference m for both.
+constexpr int kUnit = 2 * kTile;
+
+// A sequence's items.
 struct Item {
   int s;         // sequence
   int row0, n;   // its rows
   int len;       // its tokens
   int first;     // position of its first row
-  int lo, tiles; // first tile and number of tiles of each of its items
+  int lo, units; // first unit and number of units of each of its items
   int blocks;    // row blocks
   int items;     // heads * blocks (0: no rows)
 };
 
 constexpr long long kMaxTokens = 1ll << 30;
 
+// The step's rows and the lengths: of up to kSeqCache sequences they are kept in shared memory, so
+// that the step from one item to the next costs no trip to memory.
+constexpr int kSeqCache = 256;
+struct Steps {
+  const AttendArgs& a;
+  const int* cu;    // shared: [seqs + 1], [seqs]; nullptr past kSeqCache
+  const int* lens;
+  __device__ __forceinline__ int row(int s) const { return min(max(cu != nullptr ? cu[s] : ld(a.cu + s), 0), a.rows); }
+  __device__ __forceinline__ int len(int s) const { return max(lens != nullptr ? lens[s] : ld(a.c.lens + s), 0); }
+};
+
 template <int ROWS>
-__device__ __forceinline__ Item item_of(const AttendArgs& a, int s) {
+__device__ __forceinline__ Item item_of(const Steps& st, int s) {
+  const AttendArgs& a = st.a;
   Item it;
-  const StepRows st = step_rows(a.cu, s, a.rows);
   it.s = s;
-  it.row0 = st.first;
-  it.n = st.n;
+  it.row0 = st.row(s);
+  it.n = max(st.row(s + 1) - it.row0, 0);
   it.items = 0;
-  it.tiles = 1;
-  if (st.n == 0) return it;
+  it.units = 1;
+  if (it.n == 0) return it;
   const long long room = min(static_cast<long long>(a.c.max_pages) * a.c.page_size, kMaxTokens);
-  const int len = max(ld(a.c.lens + s), 0);
-  it.len = static_cast<int>(min(static_cast<long long>(len), room));
-  it.first = len - st.n;
+  it.len = static_cast<int>(min(static_cast<long long>(st.len(s)), room));
+  it.first = it.len - it.n;
   const int from = a.window > 0 ? max(it.first - a.window + 1, 0) : 0;
-  it.lo = min(from, max(it.len - 1, 0)) / kTile;
-  it.tiles = max((it.len + kTile - 1) / kTile - it.lo, 1);
-  it.blocks = static_cast<int>((static_cast<long long>(st.n) * a.group + ROWS - 1) / ROWS);
+  it.lo = min(from, max(it.len - 1, 0)) / kUnit;
+  it.units = max((it.len + kUnit - 1) / kUnit - it.lo, 1);
+  it.blocks = static_cast<int>((static_cast<long long>(it.n) * a.group + ROWS - 1) / ROWS);
   it.items = a.c.heads * it.blocks;
   return it;
 }
-__device__ __forceinline__ long long work_of(const Item& it) { return static_cast<long long>(it.items) * it.tiles; }
+__device__ __forceinline__ long long work_of(const Item& it) { return static_cast<long long>(it.items) * it.units; }
 
 // Exclusive prefix sum of one value per thread over the block, and the block's sum.
 template <int W>
@@ -182,155 +196,187 @@ __device__ __forceinline__ long long block_prefix(long long v, long long* sums, 
   return before + x - v;
 }
 
-// W warps, blocks of 8 NT rows, rings of S tiles; QS: the query rows' operands are kept in shared
-// memory (one copy for all warps) instead of registers.
-template <int D, int NT, int W, int S, bool QS>
+// Channels 4 d4 .. of row r (step row r / group, query head r % group of K/V head h) of the step that
+// begins at row0: from the sums v, their reference m and the sum l.
+template <int D>
+__device__ __forceinline__ void finish(const AttendArgs& a, int row0, int h, int r, int d4, float4 v, float m, float l) {
+  const int step_row = r / a.group, hq = h * a.group + r - step_row * a.group;
+  const int64_t at = static_cast<int64_t>(row0 + step_row) * (a.c.heads * a.group) + hq;
+  const bool seen = l > 0.f || l != l;
+  const float f = seen ? a.v_ts / l : 0.f;
+  uint2 o;
+  o.x = pack2(v.x * f, v.y * f, a.fp16);
+  o.y = pack2(v.z * f, v.w * f, a.fp16);
+  *reinterpret_cast<uint2*>(static_cast<char*>(a.out) + 2 * (at * D + 4 * d4)) = o;
+  if (d4 == 0 && a.lse != nullptr) a.lse[at] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// W warps, blocks of 8 NT rows, rings of S units; QS: the query rows' operands are read from shared
+// memory for every unit instead of being kept in registers.  The offsets in dynamic shared memory:
+template <int D, int NT, int W, int S>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kJoin = W / 2;  // warps whose sums lie in shared memory at a time
-  static constexpr int kRingBytes = W * S * 18 * D;
-  static constexpr int kSumBytes = kJoin * kRows * (D + 4) * 4;  // rows padded by 4 floats
-  static constexpr int kStatBytes = W * kRows * 2 * 4;           // the warps' m and l
-  static constexpr int kQBytes = QS ? kRows * D * 2 : 0;
-  static constexpr int kSmem = kRingBytes + kSumBytes + kStatBytes + kRows * 2 * 4 + kQBytes + W * S * 8;
+  static constexpr int kJoin = W / 2;                          // warps whose sums lie in shared memory
+  static constexpr int kRing = 0;                              // [W][S] units
+  static constexpr int kSums = kRing + W * S * 36 * D;         // [kJoin][rows][D + 4] floats
+  static constexpr int kQuery = kSums + kJoin * kRows * (D + 4) * 4;  // [rows][D] as they lie in memory; QS: then [NT][D / 32][32] uint4
+  static constexpr int kStats = kQuery + kRows * D * 2;        // [2][W][rows] floats: the warps' m and l
+  static constexpr int kFactors = kStats + 2 * W * kRows * 4;  // [rows]
+  static constexpr int kBars = kFactors + kRows * 4;
+  static constexpr int kSeqs = kBars + W * S * 8;              // cu [kSeqCache + 1], lens [kSeqCache]
+  static constexpr int kTotal = kSeqs + (2 * kSeqCache + 1) * 4;
 };
 
-// A CTA's place in the work: an item and the part of it that lies in the CTA's range.
+// A CTA's place in the work: an item and the part of it that lies in the CTA's chunk.
 struct Walk {
   Item it;
-  int idx, off, count;  // item of the sequence, first tile of the item, tiles
+  int idx, off, count;  // item of the sequence, first unit of the item, units
+  int more;             // 0: past the chunk
   long long pos;
 };
-template <int ROWS>
-__device__ __forceinline__ bool advance(const AttendArgs& a, Walk& w, long long end) {
-  w.pos += w.count;
-  if (w.pos >= end) return false;
-  w.off = 0;  // the range goes on past this item
-  if (++w.idx == w.it.items) {
-    w.idx = 0;
-    int s = w.it.s;
-    do w.it = item_of<ROWS>(a, ++s); while (w.it.items == 0);
-  }
-  w.count = static_cast<int>(min(end - w.pos, static_cast<long long>(w.it.tiles)));
-  return true;
-}
 
 template <int D, int NT, int W, int S, int CTAS, bool QS>
 __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
+  typedef Shape<D, NT, W, S> L;
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;   // k16 steps of a score, and m16 tiles of the output
   constexpr int PITCH = D + 4;
   constexpr int TILE = 18 * D;
+  constexpr int UNIT = 2 * TILE;
   constexpr int kThreads = 32 * W;
   constexpr int JOIN = W / 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_sum = reinterpret_cast<float*>(smem + W * S * TILE);        // [JOIN][rows][PITCH]
-  uint4* s_q = reinterpret_cast<uint4*>(s_sum + JOIN * ROWS * PITCH);  // QS: [n-tile][word][lane]
-  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_q + (QS ? ROWS * D / 8 : 0));  // [warps][S]
-  float* s_m = reinterpret_cast<float*>(s_bar + W * S);                // [warps][rows]
-  float* s_l = s_m + W * ROWS;                                         // [warps][rows]
-  float* s_mt = s_l + W * ROWS;                                        // [rows] joined m
-  float* s_lt = s_mt + ROWS;                                           // [rows] joined l
+  float* s_sum = reinterpret_cast<float*>(smem + L::kSums);
+  uint4* s_q = reinterpret_cast<uint4*>(smem + L::kQuery);
+  float* s_m = reinterpret_cast<float*>(smem + L::kStats);
+  float* s_l = s_m + W * ROWS;
+  float* s_factor = reinterpret_cast<float*>(smem + L::kFactors);
+  int* s_cu = reinterpret_cast<int*>(smem + L::kSeqs);
+  int* s_len = s_cu + kSeqCache + 1;
   __shared__ long long s_scan[W];
-  __shared__ long long s_off;
-  __shared__ int s_seq, s_last;
+  __shared__ Walk s_walk[2];  // this part, the next
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const uint8_t* ring = smem + warp * S * TILE;
-  const uint32_t ring_addr = smem_addr(ring), bar0 = smem_addr(s_bar + warp * S);
+  const uint8_t* ring = smem + L::kRing + warp * S * UNIT;
+  const uint32_t ring_addr = smem_addr(ring), bar0 = smem_addr(smem + L::kBars + warp * S * 8);
   if (lane < S) mbar_init(bar0 + 8 * lane, 1);
   fence_barrier_init();
-  __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
 
-  // this CTA's range [pos, end) of the work
+  // the work, cut into one chunk of `per` units per CTA: this one's is [pos, end)
+  const bool cached = a.c.seqs <= kSeqCache;
+  if (cached) {
+    for (int s = tid; s <= a.c.seqs; s += kThreads) {
+      s_cu[s] = ld(a.cu + s);
+      if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
+    }
+    __syncthreads();
+  }
+  const Steps steps{a, cached ? s_cu : nullptr, cached ? s_len : nullptr};
   const int per_thread = (a.c.seqs + kThreads - 1) / kThreads;
   const int sa = min(tid * per_thread, a.c.seqs), sb = min(sa + per_thread, a.c.seqs);
   long long mine = 0;
-  for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS>(a, s));
+  for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS>(steps, s));
   long long total;
   const long long before = block_prefix<W>(mine, s_scan, total);
   const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(W));
-  Walk cur;
-  cur.pos = per * blockIdx.x;
-  const long long end = min(cur.pos + per, total);
-  if (cur.pos >= end) return;
-  if (cur.pos >= before && cur.pos < before + mine) {
+  const long long begin = per * blockIdx.x, end = min(begin + per, total);
+  if (tid == 0) a.pieces[blockIdx.x].on = 0;
+  if (begin >= end) return;
+  if (begin >= before && begin < before + mine) {
+    Walk w;
     long long at = before;
     for (int s = sa; s < sb; ++s) {
-      const long long w = work_of(item_of<ROWS>(a, s));
-      if (cur.pos < at + w) {
-        s_seq = s;
-        s_off = cur.pos - at;
-        break;
-      }
-      at += w;
+      w.it = item_of<ROWS>(steps, s);
+      const long long n = work_of(w.it);
+      if (begin < at + n) break;
+      at += n;
     }
+    w.pos = begin;
+    w.idx = static_cast<int>((begin - at) / w.it.units);
+    w.off = static_cast<int>(begin - at - static_cast<long long>(w.idx) * w.it.units);
+    w.count = static_cast<int>(min(end - begin, static_cast<long long>(w.it.units - w.off)));
+    w.more = 1;
+    s_walk[0] = w;
   }
   __syncthreads();
-  cur.it = item_of<ROWS>(a, s_seq);
-  cur.idx = static_cast<int>(s_off / cur.it.tiles);
-  cur.off = static_cast<int>(s_off - static_cast<long long>(cur.idx) * cur.it.tiles);
-  cur.count = static_cast<int>(min(end - cur.pos, static_cast<long long>(cur.it.tiles - cur.off)));
 
-  // ---- this warp's ring.  Its i-th tile of an item's part is tile `warp + i W` of the part ----
+  // ---- this warp's ring.  Its i-th unit of an item's part is unit `warp + i W` of the part ----
   int stage = 0;            // next stage to be consumed; all stages are empty between items
-  uint32_t parity = 0;      // of that stage's phase
-  uint32_t invalid = 0;     // stages whose tile has no page
+  uint32_t parity = 0;      // bit st: of stage st's phase
+  uint32_t invalid = 0;     // bits 2 st, 2 st + 1: the unit's tile has no page
   bool dead = false;        // a copy did not arrive
-  int pids = 0, pids_next = 0;  // this lane's page numbers: of tiles 32 b + lane and the batch after
-  auto load_pids = [&](const Walk& w, int i) {
-    const int n = i * W + warp;  // tile of the part
-    const int t = w.it.lo + w.off + n;
+  int pids = 0, pids_next = 0;  // this lane's page numbers: of the warp's tiles 32 b + lane, and the batch after
+  auto page_slot = [&](int t) {
+    return a.c.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), a.page_magic));
+  };
+  auto load_pids = [&](const Walk& w, int i) {  // of the warp's i-th tile of the part
+    const int n = (i >> 1) * W + warp;
+    const int t = 2 * (w.it.lo + w.off + n) + (i & 1);
     if (n >= w.count || t * kTile >= w.it.len) return -1;
-    const int pi = a.c.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), a.page_magic));
-    const int page = ld(a.c.table + static_cast<size_t>(w.it.s) * a.c.max_pages + pi);
+    const int page = ld(a.c.table + static_cast<size_t>(w.it.s) * a.c.max_pages + page_slot(t));
     if (page < 0 || page >= a.c.pages) {
       atomicOr(a.c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
       return -1;
     }
     return page;
   };
-  // start the copy of the part's tile i (this warp's count) into stage st
+  // start the copies of the part's unit i (this warp's count) into stage st
   auto issue = [&](const Walk& w, int i, int st, int h) {
-    if (i > 0 && (i & 31) == 0) {
+    if (i > 0 && (i & 15) == 0) {
       pids = pids_next;
-      pids_next = load_pids(w, i + 32 + lane);
+      pids_next = load_pids(w, 2 * i + 32 + lane);
     }
-    const int page = __shfl_sync(0xffffffffu, pids, i & 31);
-    if (page < 0) {
-      invalid |= 1u << st;
-      return;
-    }
-    invalid &= ~(1u << st);
-    if (lane == 0) {
-      const int t = w.it.lo + w.off + i * W + warp;
-      const int pi = a.c.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), a.page_magic));
-      const uint8_t* src = a.c.pool + static_cast<size_t>(page) * a.c.page_bytes +
-                           static_cast<size_t>(h * a.c.tiles_per_page + (t - pi * a.c.tiles_per_page)) * TILE;
-      mbar_arrive_expect_tx(bar0 + 8 * st, TILE);
-      bulk_copy_g2s(ring_addr + st * TILE, src, TILE, bar0 + 8 * st);
+    const int p0 = __shfl_sync(0xffffffffu, pids, 2 * (i & 15)), p1 = __shfl_sync(0xffffffffu, pids, 2 * (i & 15) + 1);
+    const uint32_t bad = (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
+    invalid = (invalid & ~(3u << (2 * st))) | (bad << (2 * st));
+    if (lane == 0 && bad != 3u) {
+      const uint32_t bar = bar0 + 8 * st, dst = ring_addr + st * UNIT;
+      const int t = 2 * (w.it.lo + w.off + i * W + warp);
+      const int first = h * a.c.tiles_per_page;
+      mbar_arrive_expect_tx(bar, bad == 0 ? UNIT : TILE);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int page = u ? p1 : p0;
+        if (page < 0) continue;
+        const uint8_t* src = a.c.pool + static_cast<size_t>(page) * a.c.page_bytes +
+                             static_cast<size_t>(first + t + u - page_slot(t + u) * a.c.tiles_per_page) * TILE;
+        bulk_copy_g2s(dst + u * TILE, src, TILE, bar);
+      }
     }
   };
-  auto tiles_of = [&](const Walk& w) { return w.count > warp ? (w.count - warp + W - 1) / W : 0; };
-  auto start = [&](const Walk& w) {  // the first tiles of a part
+  auto units_of = [&](const Walk& w) { return w.count > warp ? (w.count - warp + W - 1) / W : 0; };
+  // the first units of a part, and its query rows
+  auto start = [&](const Walk& w) {
+    const int n = units_of(w), h = w.idx / w.it.blocks, r0 = (w.idx - h * w.it.blocks) * ROWS;
+    if (!dead) pids = load_pids(w, lane);
+    for (int i = tid; i < ROWS * (D / 8); i += kThreads) {
+      const int r = i / (D / 8), piece = i - r * (D / 8), x = r0 + r;
+      if (x < w.it.n * a.group) {
+        const int step_row = x / a.group, hq = h * a.group + x - step_row * a.group;
+        cp_async_16(smem_addr(smem + L::kQuery + 16 * i), static_cast<const char*>(a.q) +
+                    2 * ((w.it.row0 + step_row) * a.q_row + hq * a.q_head + 8 * piece));
+      } else {
+        *reinterpret_cast<uint4*>(smem + L::kQuery + 16 * i) = make_uint4(0, 0, 0, 0);
+      }
+    }
     if (dead) return;
-    const int n = tiles_of(w), h = w.idx / w.it.blocks;
-    pids = load_pids(w, lane);
-    pids_next = n > 32 ? load_pids(w, 32 + lane) : -1;
+    pids_next = n > 16 ? load_pids(w, 32 + lane) : -1;
     int st = stage;
     for (int i = 0; i < S && i < n; ++i) {
       issue(w, i, st, h);
       if (++st == S) st = 0;
     }
   };
-  start(cur);
+  start(s_walk[0]);
 
-  while (true) {
-    const Item& it = cur.it;
-    const int h = cur.idx / it.blocks, blk = cur.idx - h * it.blocks, off = cur.off, count = cur.count;
-    const int r0 = blk * ROWS;  // first of the block's rows: row r is (step row r / group, query head r % group)
-    const int nrows = min(ROWS, it.n * a.group - r0);
+  for (int turn = 0;; turn ^= 1) {
+    const Walk& cur = s_walk[turn];
+    cp_async_wait_all();
+    __syncthreads();  // the query rows are here; the last item's shared sums are done with
+    const int h = cur.idx / cur.it.blocks;
+    const int r0 = (cur.idx - h * cur.it.blocks) * ROWS;  // first of the block's rows: row r is (step row r / group, query head r % group)
+    const int nrows = min(ROWS, cur.it.n * a.group - r0);
 
     // the query rows as FP16, brought near 2^10 by a power of two that z's factor takes back; the
     // sign of the scale goes to the rows, so that a larger product is a larger score
@@ -340,15 +386,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
       const float sign = a.scale2 < 0.f ? -1.f : 1.f, size = fabsf(a.scale2);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int r = 8 * t + g;
-        const bool ok = r < nrows;
-        const int step_row = (r0 + r) / a.group, hq = h * a.group + (r0 + r) - step_row * a.group;
-        const char* src = static_cast<const char*>(a.q) +
-                          2 * ((it.row0 + (ok ? step_row : 0)) * a.q_row + (ok ? hq : 0) * a.q_head + 8 * q);
+        if (QS && t % W != warp) continue;
+        const uint8_t* src = smem + L::kQuery + (8 * t + g) * (2 * D) + 16 * q;
         uint32_t raw[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {  // channels 32 i + 8 q ..
-          const uint4 v = ok ? *reinterpret_cast<const uint4*>(src + 64 * i) : make_uint4(0, 0, 0, 0);
+          const uint4 v = *reinterpret_cast<const uint4*>(src + 64 * i);
           raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
         }
         float top = 0.f;
@@ -370,18 +413,26 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
           raw[i] = half2_bits(f.x * up, f.y * up);
           if constexpr (!QS) qf[t][i] = raw[i];
         }
-        if constexpr (QS) {
-          if (t % W == warp) {
+        if constexpr (QS) {  // in place: the tile's 8 rows are this warp's
+          __syncwarp();
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              s_q[(t * (D / 32) + i) * 32 + lane] = make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
-          }
+          for (int i = 0; i < D / 32; ++i)
+            s_q[(t * (D / 32) + i) * 32 + lane] = make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+          if (q == 0) s_factor[8 * t + g] = down;
+        } else {
+          factor[t][0] = __shfl_sync(0xffffffffu, down, 8 * q);      // lane of row 2q: g = 2q
+          factor[t][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
         }
-        factor[t][0] = __shfl_sync(0xffffffffu, down, 8 * q);      // lane of row 2q: g = 2q
-        factor[t][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
       }
     }
-    if constexpr (QS) __syncthreads();
+    if constexpr (QS) {
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        factor[t][0] = s_factor[8 * t + 2 * q];
+        factor[t][1] = s_factor[8 * t + 2 * q + 1];
+      }
+    }
 
     float acc[NT][KS][4];
     float m[NT][2], l[NT][2];
@@ -393,66 +444,79 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
       for (int i = 0; i < KS; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
     }
     // tokens that every row of the block sees without a look at the masks: from `open_lo`, before `open_hi`
-    const int open_hi = a.tree != nullptr ? it.first : min(it.first + r0 / a.group + 1, it.len);
-    const int open_lo = a.window > 0 ? max(it.first + (r0 + nrows - 1) / a.group - a.window + 1, 0) : 0;
+    const int first = cur.it.first, len = cur.it.len;
+    const int open_hi = a.tree != nullptr ? first : min(first + r0 / a.group + 1, len);
+    const int open_lo = a.window > 0 ? max(first + (r0 + nrows - 1) / a.group - a.window + 1, 0) : 0;
 
-    const int n_tiles = dead ? 0 : tiles_of(cur);
-    int tok0 = (it.lo + off + warp) * kTile;
-    for (int i = 0; i < n_tiles; ++i, tok0 += W * kTile) {
-      if (!((invalid >> stage) & 1u)) {
+    const int n_units = dead ? 0 : units_of(cur);
+    int tok0 = (cur.it.lo + cur.off + warp) * kUnit;
+    for (int i = 0; i < n_units; ++i, tok0 += W * kUnit) {
+      const uint32_t bad = invalid >> (2 * stage) & 3u;
+      if (bad != 3u) {
         if (!warp_wait(bar0 + 8 * stage, parity >> stage & 1u, kWaitCycles)) {
           if (lane == 0) atomicOr(a.c.status, kStatusTimeout);
           dead = true;
           break;
         }
         parity ^= 1u << stage;
-        const uint8_t* tile = ring + stage * TILE;
+        const uint8_t* unit = ring + stage * UNIT;
         const int tok_g = (g >> 1) + 4 * (g & 1);
         // ---- S^T = K Q^T, one word (8 channels, half a scale block) of each token at a time ----
-        float sc[NT][4];
+        float sc[2][NT][4];
+        uint32_t ks[4][D / 64];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-        uint32_t ks0[D / 64], ks1[D / 64];
-        key_scales<D>(tile + 16 * D + tok_g * (D / 16), q, ks0);
-        key_scales<D>(tile + 16 * D + (tok_g + 8) * (D / 16), q, ks1);
-        const uint8_t* kp = tile + tok_g * 16 + q * 4;
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.f;
+          key_scales<D>(unit + u * TILE + 16 * D + tok_g * (D / 16), q, ks[2 * u]);
+          key_scales<D>(unit + u * TILE + 16 * D + (tok_g + 8) * (D / 16), q, ks[2 * u + 1]);
+        }
+        const uint8_t* kp = unit + tok_g * 16 + q * 4;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-          uint32_t x[4], y[4];
-          e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t*>(kp + w * 256), x[0], x[1], x[2], x[3]);
-          e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t*>(kp + w * 256 + 128), y[0], y[1], y[2], y[3]);
+          uint32_t x[2][4], y[2][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = w & 1 ? scale2_hi(x[j], ks0[w / 2]) : scale2_lo(x[j], ks0[w / 2]);
-            y[j] = w & 1 ? scale2_hi(y[j], ks1[w / 2]) : scale2_lo(y[j], ks1[w / 2]);
+          for (int u = 0; u < 2; ++u) {
+            const uint8_t* p = kp + u * TILE + w * 256;
+            e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t*>(p), x[u][0], x[u][1], x[u][2], x[u][3]);
+            e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t*>(p + 128), y[u][0], y[u][1], y[u][2], y[u][3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[u][j] = w & 1 ? scale2_hi(x[u][j], ks[2 * u][w / 2]) : scale2_lo(x[u][j], ks[2 * u][w / 2]);
+              y[u][j] = w & 1 ? scale2_hi(y[u][j], ks[2 * u + 1][w / 2]) : scale2_lo(y[u][j], ks[2 * u + 1][w / 2]);
+            }
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             uint4 b;
             if constexpr (QS) b = s_q[(n * (D / 32) + w) * 32 + lane];
             else b = make_uint4(qf[n][4 * w], qf[n][4 * w + 1], qf[n][4 * w + 2], qf[n][4 * w + 3]);
-            mk::mma_16816(sc[n], x[0], y[0], x[1], y[1], b.x, b.y);
-            mk::mma_16816(sc[n], x[2], y[2], x[3], y[3], b.z, b.w);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) mk::mma_16816(sc[u][n], x[u][0], y[u][0], x[u][1], y[u][1], b.x, b.y);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) mk::mma_16816(sc[u][n], x[u][2], y[u][2], x[u][3], y[u][3], b.z, b.w);
           }
         }
         // ---- masks, running reference, p ----
-        const bool open = tok0 >= open_lo && tok0 + kTile <= open_hi;
+        const bool open = tok0 >= open_lo && tok0 + kUnit <= open_hi && bad == 0;
         if (!open) {  // products become scores here; their factors are 1 below
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int tok = tok0 + tok_g + 8 * (j >> 1), r = 8 * n + 2 * q + (j & 1);
-              const int row = (r0 + min(r, nrows - 1)) / a.group, x = it.first + row;
-              bool see = tok < it.len;
-              if (a.tree != nullptr) {
-                const int d = tok - it.first;
-                see = see && (d < 0 || (d < 64 && ((a.tree[it.row0 + row] >> d) & 1ull)));
-              } else {
-                see = see && tok <= x && (a.window <= 0 || tok > x - a.window);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int tok = tok0 + kTile * u + tok_g + 8 * (j >> 1), r = 8 * n + 2 * q + (j & 1);
+                const int row = (r0 + min(r, nrows - 1)) / a.group, x = first + row;
+                bool see = tok < len && !((bad >> u) & 1u);
+                if (a.tree != nullptr) {
+                  const int d = tok - first;
+                  see = see && (d < 0 || (d < 64 && ((a.tree[cur.it.row0 + row] >> d) & 1ull)));
+                } else {
+                  see = see && tok <= x && (a.window <= 0 || tok > x - a.window);
+                }
+                sc[u][n][j] = see ? sc[u][n][j] * factor[n][j & 1] : -INFINITY;
               }
-              sc[n][j] = see ? sc[n][j] * factor[n][j & 1] : -INFINITY;
-            }
         }
         float hi[NT][2];
         bool rise = false;
@@ -460,7 +524,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float top = fmaxf(sc[n][j], sc[n][2 + j]);
+            const float top = fmaxf(fmaxf(sc[0][n][j], sc[0][n][2 + j]), fmaxf(sc[1][n][j], sc[1][n][2 + j]));
             hi[n][j] = open ? top * factor[n][j] : top;
             rise |= hi[n][j] > m[n][j] + kSlack;
           }
@@ -479,161 +543,145 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
               for (int k = 0; k < KS; ++k) { acc[n][k][j] *= c; acc[n][k][2 + j] *= c; }
             }
         }
-        uint32_t pf[NT][2];
+        uint32_t pf[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float f0 = open ? factor[n][0] : 1.f, f1 = open ? factor[n][1] : 1.f;
-          const float p0 = exp2_approx(fmaf(sc[n][0], f0, -m[n][0])), p1 = exp2_approx(fmaf(sc[n][1], f1, -m[n][1]));
-          const float p2 = exp2_approx(fmaf(sc[n][2], f0, -m[n][0])), p3 = exp2_approx(fmaf(sc[n][3], f1, -m[n][1]));
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          pf[n][0] = movmatrix(half2_bits(p0, p1));
-          pf[n][1] = movmatrix(half2_bits(p2, p3));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float p0 = exp2_approx(fmaf(sc[u][n][0], f0, -m[n][0])), p1 = exp2_approx(fmaf(sc[u][n][1], f1, -m[n][1]));
+            const float p2 = exp2_approx(fmaf(sc[u][n][2], f0, -m[n][0])), p3 = exp2_approx(fmaf(sc[u][n][3], f1, -m[n][1]));
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            pf[u][n][0] = movmatrix(half2_bits(p0, p1));
+            pf[u][n][1] = movmatrix(half2_bits(p2, p3));
+          }
         }
         // ---- O^T += V^T P^T ----
-        uint32_t vs[4];  // D = 256: two bytes, else one
-        {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* tile = unit + u * TILE;
+          uint32_t vs[4];  // D = 256: two bytes, else one
           const uint8_t* sp = tile + 17 * D + q * (D / 16) + (D == 64 ? g >> 1 : D == 128 ? g : 2 * g);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             vs[j] = D == 256 ? *reinterpret_cast<const uint16_t*>(sp + j * (D / 4)) : sp[j * (D / 4)];
-          if (tok0 + kTile > it.len) {  // scales past the end are not the sequence's: 0, so that 0 * p is 0
+          if (tok0 + kUnit > len || bad != 0) {  // scales that are no token's of the sequence: 0, so that 0 * p is 0
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (tok0 + 4 * j + q >= it.len) vs[j] = 0;
+              if (tok0 + kTile * u + 4 * j + q >= len || ((bad >> u) & 1u)) vs[j] = 0;
           }
-        }
-        Words<D / 64> vc[4];
+          Words<D / 64> vc[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) vc[j] = shared_words<D / 64>(tile + 8 * D + (4 * j + q) * (D / 2) + g * (D / 16));
-        uint32_t vscale[2][D == 256 ? 2 : 1];  // tokens (q, q + 4), (q + 8, q + 12)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t u = vs[2 * j], v = vs[2 * j + 1];
-          if constexpr (D == 256) {
-            const uint32_t four = __byte_perm(u, v, 0x5140);  // u0 v0 u1 v1
-            vscale[j][0] = e4m3x2_to_f16x2(four);
-            vscale[j][1] = e4m3x2_to_f16x2(four >> 16);
-          } else {
-            vscale[j][0] = e4m3x2_to_f16x2(u | (v << 8));
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) {  // words: 8 channels, 4 m-tiles
-          uint32_t e[2][4], o[2][4];        // even and odd channels of each token pair
+          for (int j = 0; j < 4; ++j) vc[j] = shared_words<D / 64>(tile + 8 * D + (4 * j + q) * (D / 2) + g * (D / 16));
+          uint32_t vscale[2][D == 256 ? 2 : 1];  // tokens (q, q + 4), (q + 8, q + 12)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t u = vc[2 * j].w[w], v = vc[2 * j + 1].w[w];
-            const uint32_t we = (u & 0x0f0f0f0fu) | ((v << 4) & 0xf0f0f0f0u);
-            const uint32_t wo = ((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u);
-            e2m1x8_to_f16x2x4(we, e[j][0], e[j][1], e[j][2], e[j][3]);
-            e2m1x8_to_f16x2x4(wo, o[j][0], o[j][1], o[j][2], o[j][3]);
-            const uint32_t s = vscale[j][D == 256 ? w / 2 : 0];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e[j][k] = hmul2_bits(e[j][k], s);
-              o[j][k] = hmul2_bits(o[j][k], s);
+            const uint32_t x = vs[2 * j], y = vs[2 * j + 1];
+            if constexpr (D == 256) {
+              const uint32_t four = __byte_perm(x, y, 0x5140);  // x0 y0 x1 y1
+              vscale[j][0] = e4m3x2_to_f16x2(four);
+              vscale[j][1] = e4m3x2_to_f16x2(four >> 16);
+            } else {
+              vscale[j][0] = e4m3x2_to_f16x2(x | (y << 8));
             }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int w = 0; w < D / 64; ++w) {  // words: 8 channels, 4 m-tiles
+            uint32_t e[2][4], o[2][4];        // even and odd channels of each token pair
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mk::mma_16816(acc[n][4 * w + k], e[0][k], o[0][k], e[1][k], o[1][k], pf[n][0], pf[n][1]);
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t x = vc[2 * j].w[w], y = vc[2 * j + 1].w[w];
+              const uint32_t we = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+              const uint32_t wo = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+              e2m1x8_to_f16x2x4(we, e[j][0], e[j][1], e[j][2], e[j][3]);
+              e2m1x8_to_f16x2x4(wo, o[j][0], o[j][1], o[j][2], o[j][3]);
+              const uint32_t s = vscale[j][D == 256 ? w / 2 : 0];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                e[j][k] = hmul2_bits(e[j][k], s);
+                o[j][k] = hmul2_bits(o[j][k], s);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mk::mma_16816(acc[n][4 * w + k], e[0][k], o[0][k], e[1][k], o[1][k], pf[u][n][0], pf[u][n][1]);
+          }
         }
         __syncwarp();  // every lane has read the stage
       }
-      if (i + S < n_tiles) issue(cur, i + S, stage, h);
+      if (i + S < n_units) issue(cur, i + S, stage, h);
       if (++stage == S) stage = 0;
     }
     if (dead) {  // let what is still in flight land before the memory is given up
       for (int st = 0; st < S; ++st)
-        if (!((invalid >> st) & 1u)) warp_wait(bar0 + 8 * st, parity >> st & 1u, kDrainCycles);
+        if ((invalid >> (2 * st) & 3u) != 3u) warp_wait(bar0 + 8 * st, parity >> st & 1u, kDrainCycles);
     }
-    Walk nxt = cur;
-    const bool more = advance<ROWS>(a, nxt, end);
-    if (more) start(nxt);
-
-    // ---- join the warps: the second half's sums go to the first half's registers through shared
-    // memory, the first half's to all threads ----
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], o);
-        l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], o);
-      }
-      if (g == 0) {
-        const int r = 8 * n + 2 * q;
-        s_m[warp * ROWS + r] = m[n][0];
-        s_m[warp * ROWS + r + 1] = m[n][1];
-        s_l[warp * ROWS + r] = l[n][0];
-        s_l[warp * ROWS + r + 1] = l[n][1];
-      }
-    }
-    __syncthreads();
-    if (tid < ROWS) {
-      float mt = kLowest, lt = 0.f;
-      for (int w = 0; w < W; ++w) mt = fmaxf(mt, s_m[w * ROWS + tid]);
-      for (int w = 0; w < W; ++w) {
-        const float c = exp2_approx(s_m[w * ROWS + tid] - mt);
-        lt += c * s_l[w * ROWS + tid];
-        s_m[w * ROWS + tid] = c;  // the warp's factor
-      }
-      s_mt[tid] = mt;
-      s_lt[tid] = lt;
-    }
-    __syncthreads();
+    // ---- join the warps: the second half's sums go through shared memory to the first half's, and
+    // theirs to all threads ----
     // accumulator i of m-tile k: channel g D/8 + 2k + (i >> 1), row 2q + (i & 1)
     const int slot = warp % JOIN;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float c = s_m[warp * ROWS + 8 * n + 2 * q + i];
-#pragma unroll
-        for (int k = 0; k < KS; ++k) { acc[n][k][i] *= c; acc[n][k][2 + i] *= c; }
-      }
     auto spot = [&](int n, int i, int k) {
       return reinterpret_cast<float2*>(s_sum + (slot * ROWS + 8 * n + 2 * q + i) * PITCH + g * (D / 8) + 2 * k);
     };
-    if (warp >= JOIN) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], o);
+        if (g == 0) {
+          s_m[warp * ROWS + 8 * n + 2 * q + i] = m[n][i];
+          s_l[warp * ROWS + 8 * n + 2 * q + i] = l[n][i];
+        }
+        if (warp >= JOIN) {
 #pragma unroll
           for (int k = 0; k < KS; ++k) *spot(n, i, k) = make_float2(acc[n][k][i], acc[n][k][2 + i]);
+        }
+      }
+    }
+    if (tid == 0) {
+      Walk& nxt = s_walk[turn ^ 1];
+      nxt = cur;
+      nxt.pos += cur.count;
+      nxt.more = nxt.pos < end;
+      if (nxt.more) {  // the chunk goes on past this item
+        nxt.off = 0;
+        if (++nxt.idx == nxt.it.items) {
+          nxt.idx = 0;
+          int s = nxt.it.s;
+          do nxt.it = item_of<ROWS>(steps, ++s); while (nxt.it.items == 0);
+        }
+        nxt.count = static_cast<int>(min(end - nxt.pos, static_cast<long long>(nxt.it.units)));
+      }
     }
     __syncthreads();
+    const bool more = s_walk[turn ^ 1].more;
+    if (more) start(s_walk[turn ^ 1]);
     if (warp < JOIN) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * n + 2 * q + i;
+          float mt = kLowest;
+#pragma unroll
+          for (int w = 0; w < W; ++w) mt = fmaxf(mt, s_m[w * ROWS + r]);
+          const float c = exp2_approx(m[n][i] - mt), d = exp2_approx(s_m[(warp + JOIN) * ROWS + r] - mt);
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             float2* p = spot(n, i, k);
             const float2 x = *p;
-            *p = make_float2(acc[n][k][i] + x.x, acc[n][k][2 + i] + x.y);
+            *p = make_float2(c * acc[n][k][i] + d * x.x, c * acc[n][k][2 + i] + d * x.y);
           }
+        }
     }
     __syncthreads();
-
-    auto finish = [&](int r, int d4, float4 v, float mt, float lt) {  // channels 4 d4 .. of row r
-      const int step_row = it.row0 + (r0 + r) / a.group, hq = h * a.group + (r0 + r) % a.group;
-      const int64_t at = static_cast<int64_t>(step_row) * (a.c.heads * a.group) + hq;
-      const float f = lt > 0.f || lt != lt ? a.v_ts / lt : 0.f;
-      uint2 o;
-      o.x = pack2(v.x * f, v.y * f, a.fp16);
-      o.y = pack2(v.z * f, v.w * f, a.fp16);
-      *reinterpret_cast<uint2*>(static_cast<char*>(a.out) + 2 * (at * D + 4 * d4)) = o;
-      if (d4 == 0 && a.lse != nullptr)
-        a.lse[at] = lt > 0.f || lt != lt ? (mt + log2f(lt)) * kLn2 : -INFINITY;
-    };
-    const bool whole = count == it.tiles;
-    float* part = a.part + (2 * static_cast<size_t>(blockIdx.x) + (off == 0 ? 1 : 0)) * a.part_floats;
-    for (int i = tid; i < ROWS * (D / 4); i += kThreads) {
+    const bool whole = cur.count == cur.it.units;
+    float* part = a.part + (2 * static_cast<size_t>(blockIdx.x) + (cur.off == 0 ? 1 : 0)) * a.part_floats;
+    for (int i = tid; i < nrows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d4 = i - r * (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -641,74 +689,105 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         const float4 x = *reinterpret_cast<const float4*>(s_sum + (w * ROWS + r) * PITCH + 4 * d4);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
+      float mt = kLowest, lt = 0.f;
+      if (whole || d4 == 0) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) mt = fmaxf(mt, s_m[w * ROWS + r]);
+#pragma unroll
+        for (int w = 0; w < W; ++w) lt += exp2_approx(s_m[w * ROWS + r] - mt) * s_l[w * ROWS + r];
+      }
       if (whole) {
-        if (r < nrows) finish(r, d4, v, s_mt[r], s_lt[r]);
+        finish<D>(a, cur.it.row0, h, r0 + r, d4, v, mt, lt);
       } else {
         *reinterpret_cast<float4*>(part + 4 * i) = v;
         if (d4 == 0) {
-          part[kPartSums + r] = s_mt[r];
-          part[kPartSums + kPartRows + r] = s_lt[r];
+          part[kPartSums + r] = mt;
+          part[kPartSums + kPartRows + r] = lt;
         }
       }
     }
-    if (!whole) {
-      // the CTAs that hold parts of this item: those whose ranges its tiles [b, b + tiles) meet
-      const long long b = cur.pos - off;
-      const int c0 = static_cast<int>(b / per), c1 = static_cast<int>((b + it.tiles - 1) / per);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t old = atom_add_acqrel_u32(a.counters + c0, 1u);
-        s_last = old == static_cast<uint32_t>(c1 - c0);
-        if (s_last) a.counters[c0] = 0;  // for the next call
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        auto part_of = [&](int c) {  // the first CTA's part starts at the item's first tile
-          return a.part + (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * a.part_floats;
-        };
-        if (tid < ROWS) {
-          float mt = kLowest, lt = 0.f;
-          for (int c = c0; c <= c1; ++c) mt = fmaxf(mt, ld(part_of(c) + kPartSums + tid));
-          for (int c = c0; c <= c1; ++c)
-            lt += exp2_approx(ld(part_of(c) + kPartSums + tid) - mt) * ld(part_of(c) + kPartSums + kPartRows + tid);
-          s_mt[tid] = mt;
-          s_lt[tid] = lt;
-        }
-        __syncthreads();
-        for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-          const int r = i / (D / 4), d4 = i - r * (D / 4);
-          const float mt = s_mt[r];
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = c0; c <= c1; ++c) {
-            const float* p = part_of(c);
-            const float f = exp2_approx(ld(p + kPartSums + r) - mt);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 4 * i));
-            v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
-          }
-          finish(r, d4, v, mt, s_lt[r]);
-        }
-      }
+    if (tid == 0 && !whole && cur.off == 0) {  // the item goes on in the chunks up to that of its last unit
+      Piece p;
+      p.on = 1;
+      p.last = static_cast<int>((cur.pos + cur.it.units - 1) / per);
+      p.row0 = cur.it.row0; p.r0 = r0; p.nrows = nrows; p.h = h;
+      a.pieces[blockIdx.x] = p;
     }
-    __syncthreads();  // the shared arrays are free for the next item
-
     if (!more) break;
-    cur = nxt;
   }
+}
+
+// Joins the parts of the items that were cut: CTA (c, y) the rows 8 y .. of the item that begins in
+// chunk c and goes on past it, in the order of the chunks.
+template <int D>
+__global__ void __launch_bounds__(2 * D) join_kernel(AttendArgs a) {
+  __shared__ float s_w[kMaxChunks][8];  // m, then weights
+  __shared__ float s_total[8], s_top[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c0 = blockIdx.x, tid = threadIdx.x, row8 = 8 * blockIdx.y;
+  const int4* pp = reinterpret_cast<const int4*>(a.pieces + c0);
+  const int4 x = __ldcg(pp), y = __ldcg(pp + 1);
+  const Piece p{x.x, x.y, x.z, x.w, y.x, y.y};
+  if (!p.on || row8 >= p.nrows) return;
+  const int n = p.last - c0 + 1;
+  // of the chunk c0 + c: the first chunk's part starts at the item's first unit
+  auto part_of = [&](int c) { return a.part + (2 * static_cast<size_t>(c0 + c) + (c == 0 ? 1 : 0)) * a.part_floats; };
+  for (int i = tid; i < 8 * n; i += 2 * D) s_w[i >> 3][i & 7] = __ldcg(part_of(i >> 3) + kPartSums + row8 + (i & 7));
+  const int r = tid / (D / 4), d4 = tid - r * (D / 4), i4 = (row8 + r) * (D / 4) + d4;
+  __syncthreads();
+  if (tid < 256) {  // a warp a row (D = 64: four warps take two rows each)
+    for (int row = tid >> 5; row < 8; row += 2 * D / 32) {
+      const int lane = tid & 31;
+      float top = kLowest, l = 0.f;
+      for (int c = lane; c < n; c += 32) top = fmaxf(top, s_w[c][row]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int c = lane; c < n; c += 32) {
+        const float w = exp2_approx(s_w[c][row] - top);
+        l += w * __ldcg(part_of(c) + kPartSums + kPartRows + row8 + row);
+        s_w[c][row] = w;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        s_total[row] = l;
+        s_top[row] = top;
+      }
+    }
+  }
+  __syncthreads();
+  if (row8 + r >= p.nrows) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < n; c += 8) {
+    float4 z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < n) z[j] = __ldcg(reinterpret_cast<const float4*>(part_of(c + j)) + i4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < n) {
+        const float w = s_w[c + j][r];
+        v.x += w * z[j].x; v.y += w * z[j].y; v.z += w * z[j].z; v.w += w * z[j].w;
+      }
+  }
+  finish<D>(a, p.row0, p.h, p.r0 + row8 + r, d4, v, s_top[r], s_total[r]);
 }
 
 template <int D, int NT, int W, int S, int CTAS, bool QS>
 cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
-  constexpr int smem = Shape<D, NT, W, S, QS>::kSmem;
+  constexpr int smem = Shape<D, NT, W, S>::kTotal;
+  static_assert(smem <= 227 * 1024 / CTAS - 2048, "shared memory");
   static_assert(8 * NT * D <= kPartSums && 8 * NT <= kPartRows, "a partial result holds a block");
   auto kernel = attend_kernel<D, NT, W, S, CTAS, QS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // t / tiles_per_page = umulhi(t, magic): exact for t below 2^26 (2^30 tokens) and up to 64 tiles a page
   a.page_magic = static_cast<uint32_t>(((1ull << 32) + a.c.tiles_per_page - 1) / a.c.tiles_per_page);
-  const int grid = min(CTAS * num_sms, kMaxGrid);
-  return launch_pdl(kernel, dim3(grid), dim3(32 * W), smem, stream, a);
+  const int grid = min(CTAS * num_sms, kMaxChunks);
+  e = launch_pdl(kernel, dim3(grid), dim3(32 * W), smem, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(join_kernel<D>, dim3(grid, NT), dim3(2 * D), 0, stream, a);
 }
 
 }  // namespace
@@ -716,15 +795,15 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream) {
   switch (a.c.dim) {
     case 64:
-      return row_tile <= 8    ? launch<64, 1, 8, 6, 2, false>(a, num_sms, stream)
-             : row_tile <= 16 ? launch<64, 2, 8, 6, 2, false>(a, num_sms, stream)
-                              : launch<64, 4, 12, 6, 1, false>(a, num_sms, stream);
+      return row_tile <= 8    ? launch<64, 1, 8, 4, 2, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<64, 2, 8, 4, 2, false>(a, num_sms, stream)
+                              : launch<64, 4, 12, 3, 1, false>(a, num_sms, stream);
     case 128:
-      return row_tile <= 8    ? launch<128, 1, 8, 4, 2, false>(a, num_sms, stream)
-             : row_tile <= 16 ? launch<128, 2, 12, 4, 1, false>(a, num_sms, stream)
-                              : launch<128, 4, 8, 4, 1, true>(a, num_sms, stream);
+      return row_tile <= 8    ? launch<128, 1, 8, 2, 2, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<128, 2, 12, 3, 1, false>(a, num_sms, stream)
+                              : launch<128, 4, 8, 3, 1, true>(a, num_sms, stream);
     default:
-      return row_tile <= 8 ? launch<256, 1, 12, 3, 1, false>(a, num_sms, stream) : launch<256, 2, 8, 4, 1, true>(a, num_sms, stream);
+      return row_tile <= 8 ? launch<256, 1, 8, 2, 1, false>(a, num_sms, stream) : launch<256, 2, 8, 2, 1, true>(a, num_sms, stream);
   }
 }
 

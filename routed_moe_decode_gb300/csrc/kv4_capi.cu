@@ -83,7 +83,7 @@ int moe_kv4_workspace_init(const moe_kv4_cache* c, moe_stream_t stream) {
   if (rc != MOE_OK) return rc;
   const WsLayout L = moe::kv4::ws_layout(*c);
   if (!c->workspace || !aligned(c->workspace, 256) || c->workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
-  return done("workspace init", cudaMemsetAsync(c->workspace, 0, L.copies, stream));  // status word and counters
+  return done("workspace init", cudaMemsetAsync(c->workspace, 0, L.pieces, stream));  // the status word
 }
 
 int moe_kv4_append(const moe_kv4_cache* c, int layer, const void* k, int64_t k_row_stride, int64_t k_head_stride,
@@ -148,7 +148,7 @@ int moe_kv4_attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_r
   a.out = out; a.lse = lse;
   a.part = at<float>(c, L.part);
   a.part_floats = L.part_floats;
-  a.counters = at<uint32_t>(c, L.counters);
+  a.pieces = at<moe::kv4::Piece>(c, L.pieces);
   const int64_t block = static_cast<int64_t>(max_rows < 1 ? 1 : max_rows) * a.group;
   return done("attend launch", moe::kv4::launch_attend(a, static_cast<int>(block > 1024 ? 1024 : block), sms, stream));
 }

@@ -9,7 +9,7 @@ namespace moe {
 namespace kv4 {
 
 constexpr int kTile = 16;       // tokens of a tile
-constexpr int kMaxGrid = 1024;  // CTAs of an attention launch at most
+constexpr int kMaxChunks = 512;  // CTAs of an attention launch at most, each with one chunk of the work
 constexpr int kStepRows = 64;   // rows of a sequence's step with a tree or in a compaction
 
 // A cache as the kernels see it.
@@ -25,8 +25,15 @@ struct Cache {
   size_t page_bytes;    // heads * tiles_per_page * tile_bytes
 };
 
+// An item of the attention's work that its first chunk does not end (on: there is one).
+struct alignas(16) Piece {
+  int on, last;  // the item's last chunk
+  int row0, r0, nrows, h;
+  int unused[2];
+};
+
 struct WsLayout {
-  size_t status, counters, copies, need, part, total;
+  size_t status, pieces, copies, need, part, total;
   size_t part_floats;  // floats of one partial result of the attention
 };
 
@@ -40,12 +47,12 @@ inline WsLayout ws_layout(const moe_kv4_cache& c) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   L.status = take(64);
-  L.counters = take(size_t(kMaxGrid) * 4);
+  L.pieces = take(size_t(kMaxChunks) * sizeof(Piece));
   // moe_kv4_reserve: copies [1 + 2 * seqs] (their number, then page pairs), need [seqs + 1]
   L.copies = take((1 + 2 * size_t(c.seqs)) * 4);
   L.need = take((1 + size_t(c.seqs)) * 8);
   L.part_floats = kPartSums + 2 * kPartRows;
-  L.part = take(size_t(2) * kMaxGrid * L.part_floats * 4);
+  L.part = take(size_t(2) * kMaxChunks * L.part_floats * 4);
   L.total = o;
   return L;
 }
@@ -136,7 +143,7 @@ struct AttendArgs {
   uint32_t page_magic;  // set by the launcher
   float* part;
   size_t part_floats;
-  uint32_t* counters;
+  Piece* pieces;
 };
 
 struct PageArgs {
