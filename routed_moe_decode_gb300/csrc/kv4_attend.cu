@@ -17,17 +17,16 @@
 // tokens q, q + 4, q + 8, q + 12, channels [g D/8, (g + 1) D/8).
 //
 // Memory.  Every warp streams its own tiles (18 D bytes, contiguous) through its own ring in shared
-// memory, one bulk copy a tile, kStages tiles ahead, so that no warp waits for another and the bytes
-// in flight do not cost registers: with loads to registers one tile ahead the same products ran at
-// 45 % of the copy bandwidth, waiting for memory.  The first tiles of the next item are in flight
-// while the warps' results of this one are joined.
+// memory by bulk copies, so that the bytes in flight do not cost registers: with loads to registers
+// one tile ahead the same products ran at 45 % of the copy bandwidth, waiting for memory.
 //
-// Work split.  The (sequence, K/V head, block of 8 NT rows) items are laid end to end, each as
-// long as the tiles of 16 tokens it has to read, and cut into one equal range per CTA, so that any
-// mix of lengths keeps every SM busy.  A CTA joins its warps' results per item in shared memory; an
-// item cut over several CTAs leaves partial results (FP32 sums, m and l) in the workspace, and the
-// last of its CTAs to arrive joins them in the order of the CTAs, so results do not depend on
-// timing.  The ranges are found on the device from the lengths: no host wait, no plan.
+// Work split.  The (sequence, K/V head, block of 8 NT rows) items are laid end to end, each as long
+// as the units of 32 tokens it has to read, and cut into one equal chunk per warp of the grid, so that
+// any mix of lengths keeps every SM busy and no warp ever waits for another: joining the warps of a CTA
+// at the end of every item cost a quarter of a batch of 32 ragged sequences.  An item that is cut
+// leaves partial results (FP32 sums, m and l) in the workspace, and a second small kernel joins them
+// in the order of the chunks, so results do not depend on timing.  The chunks are found on the device
+// from the lengths: no host wait, no plan.
 #include "kv4_common.cuh"
 #include "mma_parts.cuh"
 
@@ -196,38 +195,34 @@ __device__ __forceinline__ long long block_prefix(long long v, long long* sums, 
   return before + x - v;
 }
 
-// Channels 4 d4 .. of row r (step row r / group, query head r % group of K/V head h) of the step that
-// begins at row0: from the sums v, their reference m and the sum l.
+// Channels c, c + 1 of row r (step row r / group, query head r % group of K/V head h) of the step that
+// begins at row0: from the sums, their reference m and the sum l.
 template <int D>
-__device__ __forceinline__ void finish(const AttendArgs& a, int row0, int h, int r, int d4, float4 v, float m, float l) {
+__device__ __forceinline__ void finish(const AttendArgs& a, int row0, int h, int r, int c, float v0, float v1, float m, float l) {
   const int step_row = r / a.group, hq = h * a.group + r - step_row * a.group;
   const int64_t at = static_cast<int64_t>(row0 + step_row) * (a.c.heads * a.group) + hq;
   const bool seen = l > 0.f || l != l;
   const float f = seen ? a.v_ts / l : 0.f;
-  uint2 o;
-  o.x = pack2(v.x * f, v.y * f, a.fp16);
-  o.y = pack2(v.z * f, v.w * f, a.fp16);
-  *reinterpret_cast<uint2*>(static_cast<char*>(a.out) + 2 * (at * D + 4 * d4)) = o;
-  if (d4 == 0 && a.lse != nullptr) a.lse[at] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
+  *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + 2 * (at * D + c)) = pack2(v0 * f, v1 * f, a.fp16);
+  if (c == 0 && a.lse != nullptr) a.lse[at] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // W warps, blocks of 8 NT rows, rings of S units; QS: the query rows' operands are read from shared
-// memory for every unit instead of being kept in registers.  The offsets in dynamic shared memory:
-template <int D, int NT, int W, int S>
+// memory for every unit instead of being kept in registers.  The offsets in dynamic shared memory,
+// and the floats of a partial result: [NT][D / 16][32 lanes][4] sums as the accumulators lie in the
+// warp's registers, then [2][8 NT] m and l.
+template <int D, int NT, int W, int S, bool QS>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kJoin = W / 2;                          // warps whose sums lie in shared memory
-  static constexpr int kRing = 0;                              // [W][S] units
-  static constexpr int kSums = kRing + W * S * 36 * D;         // [kJoin][rows][D + 4] floats
-  static constexpr int kQuery = kSums + kJoin * kRows * (D + 4) * 4;  // [rows][D] as they lie in memory; QS: then [NT][D / 32][32] uint4
-  static constexpr int kStats = kQuery + kRows * D * 2;        // [2][W][rows] floats: the warps' m and l
-  static constexpr int kFactors = kStats + 2 * W * kRows * 4;  // [rows]
-  static constexpr int kBars = kFactors + kRows * 4;
-  static constexpr int kSeqs = kBars + W * S * 8;              // cu [kSeqCache + 1], lens [kSeqCache]
+  static constexpr int kRing = 0;                               // [W][S] units
+  static constexpr int kQuery = kRing + W * S * 36 * D;         // QS: [W][NT][D / 32][32] uint4
+  static constexpr int kBars = kQuery + (QS ? W * kRows * D * 2 : 0);
+  static constexpr int kSeqs = kBars + W * S * 8;               // cu [kSeqCache + 1], lens [kSeqCache]
   static constexpr int kTotal = kSeqs + (2 * kSeqCache + 1) * 4;
+  static constexpr int kPart = kRows * D + 2 * kRows;
 };
 
-// A CTA's place in the work: an item and the part of it that lies in the CTA's chunk.
+// A warp's place in the work: an item and the part of it that lies in the warp's chunk.
 struct Walk {
   Item it;
   int idx, off, count;  // item of the sequence, first unit of the item, units
@@ -237,33 +232,29 @@ struct Walk {
 
 template <int D, int NT, int W, int S, int CTAS, bool QS>
 __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
-  typedef Shape<D, NT, W, S> L;
+  typedef Shape<D, NT, W, S, QS> L;
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;   // k16 steps of a score, and m16 tiles of the output
-  constexpr int PITCH = D + 4;
   constexpr int TILE = 18 * D;
   constexpr int UNIT = 2 * TILE;
   constexpr int kThreads = 32 * W;
-  constexpr int JOIN = W / 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_sum = reinterpret_cast<float*>(smem + L::kSums);
-  uint4* s_q = reinterpret_cast<uint4*>(smem + L::kQuery);
-  float* s_m = reinterpret_cast<float*>(smem + L::kStats);
-  float* s_l = s_m + W * ROWS;
-  float* s_factor = reinterpret_cast<float*>(smem + L::kFactors);
   int* s_cu = reinterpret_cast<int*>(smem + L::kSeqs);
   int* s_len = s_cu + kSeqCache + 1;
   __shared__ long long s_scan[W];
-  __shared__ Walk s_walk[2];  // this part, the next
+  __shared__ long long s_before[kThreads];
+  __shared__ Walk s_walk[W][2];  // this part, the next
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const uint8_t* ring = smem + L::kRing + warp * S * UNIT;
+  uint4* queries = reinterpret_cast<uint4*>(smem + L::kQuery) + warp * (QS ? NT * (D / 32) * 32 : 0);
   const uint32_t ring_addr = smem_addr(ring), bar0 = smem_addr(smem + L::kBars + warp * S * 8);
   if (lane < S) mbar_init(bar0 + 8 * lane, 1);
   fence_barrier_init();
   pdl_wait();
   pdl_launch_dependents();
 
-  // the work, cut into one chunk of `per` units per CTA: this one's is [pos, end)
+  // the work, cut into one chunk of `per` units per warp of the grid: this one's is [begin, end).
+  // Neighbouring chunks go to different SMs, so that a few units keep as many SMs busy.
   const bool cached = a.c.seqs <= kSeqCache;
   if (cached) {
     for (int s = tid; s <= a.c.seqs; s += kThreads) {
@@ -279,14 +270,22 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS>(steps, s));
   long long total;
   const long long before = block_prefix<W>(mine, s_scan, total);
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(W));
-  const long long begin = per * blockIdx.x, end = min(begin + per, total);
-  if (tid == 0) a.pieces[blockIdx.x].on = 0;
+  const int chunk = warp * gridDim.x + blockIdx.x;
+  const long long per = (total + a.chunks - 1) / a.chunks;
+  const long long begin = per * chunk, end = min(begin + per, total);
+  if (lane == 0) a.pieces[chunk].on = 0;
+  s_before[tid] = before;
+  __syncthreads();
   if (begin >= end) return;
-  if (begin >= before && begin < before + mine) {
+  if (lane == 0) {
+    int lo = 0, hi = kThreads - 1;  // the last thread whose sequences begin at or before `begin`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_before[mid] <= begin) lo = mid; else hi = mid - 1;
+    }
     Walk w;
-    long long at = before;
-    for (int s = sa; s < sb; ++s) {
+    long long at = s_before[lo];
+    for (int s = lo * per_thread;; ++s) {
       w.it = item_of<ROWS>(steps, s);
       const long long n = work_of(w.it);
       if (begin < at + n) break;
@@ -297,23 +296,27 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     w.off = static_cast<int>(begin - at - static_cast<long long>(w.idx) * w.it.units);
     w.count = static_cast<int>(min(end - begin, static_cast<long long>(w.it.units - w.off)));
     w.more = 1;
-    s_walk[0] = w;
+    s_walk[warp][0] = w;
   }
-  __syncthreads();
+  __syncwarp();
 
-  // ---- this warp's ring.  Its i-th unit of an item's part is unit `warp + i W` of the part ----
+  // ---- this warp's ring ----
   int stage = 0;            // next stage to be consumed; all stages are empty between items
   uint32_t parity = 0;      // bit st: of stage st's phase
   uint32_t invalid = 0;     // bits 2 st, 2 st + 1: the unit's tile has no page
   bool dead = false;        // a copy did not arrive
-  int pids = 0, pids_next = 0;  // this lane's page numbers: of the warp's tiles 32 b + lane, and the batch after
+  // the places of the warp's tiles in the cache, 32 at a time (16 units): lane l holds that of tile
+  // 32 b + l, issues its copy, and has the page number of the tile 32 further on
+  long long place = 0;
+  uint32_t there = 0;       // lanes whose tile has a page
+  int page_next = -1;
   auto page_slot = [&](int t) {
     return a.c.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), a.page_magic));
   };
-  auto load_pids = [&](const Walk& w, int i) {  // of the warp's i-th tile of the part
-    const int n = (i >> 1) * W + warp;
-    const int t = 2 * (w.it.lo + w.off + n) + (i & 1);
-    if (n >= w.count || t * kTile >= w.it.len) return -1;
+  auto tile_at = [&](const Walk& w, int i) { return 2 * (w.it.lo + w.off) + i; };
+  auto load_page = [&](const Walk& w, int i) {  // of the warp's i-th tile of the part
+    const int t = tile_at(w, i);
+    if (i >= 2 * w.count || t * kTile >= w.it.len) return -1;
     const int page = ld(a.c.table + static_cast<size_t>(w.it.s) * a.c.max_pages + page_slot(t));
     if (page < 0 || page >= a.c.pages) {
       atomicOr(a.c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
@@ -321,59 +324,44 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     }
     return page;
   };
-  // start the copies of the part's unit i (this warp's count) into stage st
-  auto issue = [&](const Walk& w, int i, int st, int h) {
-    if (i > 0 && (i & 15) == 0) {
-      pids = pids_next;
-      pids_next = load_pids(w, 2 * i + 32 + lane);
+  auto set_places = [&](const Walk& w, int i, int page) {
+    const int t = tile_at(w, i), h = w.idx / w.it.blocks;
+    place = static_cast<long long>(page) * static_cast<long long>(a.c.page_bytes) +
+            static_cast<long long>(h * a.c.tiles_per_page + t - page_slot(t) * a.c.tiles_per_page) * TILE;
+    there = __ballot_sync(0xffffffffu, page >= 0);
+  };
+  // start the copies of the part's unit i into stage st
+  auto issue = [&](const Walk& w, int i, int st) {
+    const int j = i & 15;
+    if (j == 0 && i > 0) {
+      set_places(w, 2 * i + lane, page_next);
+      page_next = load_page(w, 2 * i + 32 + lane);
     }
-    const int p0 = __shfl_sync(0xffffffffu, pids, 2 * (i & 15)), p1 = __shfl_sync(0xffffffffu, pids, 2 * (i & 15) + 1);
-    const uint32_t bad = (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
+    const uint32_t bad = ~(there >> (2 * j)) & 3u;
     invalid = (invalid & ~(3u << (2 * st))) | (bad << (2 * st));
-    if (lane == 0 && bad != 3u) {
-      const uint32_t bar = bar0 + 8 * st, dst = ring_addr + st * UNIT;
-      const int t = 2 * (w.it.lo + w.off + i * W + warp);
-      const int first = h * a.c.tiles_per_page;
-      mbar_arrive_expect_tx(bar, bad == 0 ? UNIT : TILE);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int page = u ? p1 : p0;
-        if (page < 0) continue;
-        const uint8_t* src = a.c.pool + static_cast<size_t>(page) * a.c.page_bytes +
-                             static_cast<size_t>(first + t + u - page_slot(t + u) * a.c.tiles_per_page) * TILE;
-        bulk_copy_g2s(dst + u * TILE, src, TILE, bar);
-      }
+    if ((lane >> 1) == j && ((there >> lane) & 1u)) {
+      const uint32_t bar = bar0 + 8 * st;
+      // one lane announces both copies; the other's may land before, which the barrier allows
+      if ((lane & 1) == 0 || bad == 1u) mbar_arrive_expect_tx(bar, bad == 0 ? UNIT : TILE);
+      bulk_copy_g2s(ring_addr + st * UNIT + (lane & 1) * TILE, a.c.pool + place, TILE, bar);
     }
   };
-  auto units_of = [&](const Walk& w) { return w.count > warp ? (w.count - warp + W - 1) / W : 0; };
-  // the first units of a part, and its query rows
+  // the first units of a part
   auto start = [&](const Walk& w) {
-    const int n = units_of(w), h = w.idx / w.it.blocks, r0 = (w.idx - h * w.it.blocks) * ROWS;
-    if (!dead) pids = load_pids(w, lane);
-    for (int i = tid; i < ROWS * (D / 8); i += kThreads) {
-      const int r = i / (D / 8), piece = i - r * (D / 8), x = r0 + r;
-      if (x < w.it.n * a.group) {
-        const int step_row = x / a.group, hq = h * a.group + x - step_row * a.group;
-        cp_async_16(smem_addr(smem + L::kQuery + 16 * i), static_cast<const char*>(a.q) +
-                    2 * ((w.it.row0 + step_row) * a.q_row + hq * a.q_head + 8 * piece));
-      } else {
-        *reinterpret_cast<uint4*>(smem + L::kQuery + 16 * i) = make_uint4(0, 0, 0, 0);
-      }
-    }
     if (dead) return;
-    pids_next = n > 16 ? load_pids(w, 32 + lane) : -1;
+    const int page = load_page(w, lane);
+    page_next = w.count > 16 ? load_page(w, 32 + lane) : -1;
+    set_places(w, lane, page);
     int st = stage;
-    for (int i = 0; i < S && i < n; ++i) {
-      issue(w, i, st, h);
+    for (int i = 0; i < S && i < w.count; ++i) {
+      issue(w, i, st);
       if (++st == S) st = 0;
     }
   };
-  start(s_walk[0]);
+  start(s_walk[warp][0]);
 
   for (int turn = 0;; turn ^= 1) {
-    const Walk& cur = s_walk[turn];
-    cp_async_wait_all();
-    __syncthreads();  // the query rows are here; the last item's shared sums are done with
+    const Walk& cur = s_walk[warp][turn];
     const int h = cur.idx / cur.it.blocks;
     const int r0 = (cur.idx - h * cur.it.blocks) * ROWS;  // first of the block's rows: row r is (step row r / group, query head r % group)
     const int nrows = min(ROWS, cur.it.n * a.group - r0);
@@ -386,12 +374,15 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
       const float sign = a.scale2 < 0.f ? -1.f : 1.f, size = fabsf(a.scale2);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if (QS && t % W != warp) continue;
-        const uint8_t* src = smem + L::kQuery + (8 * t + g) * (2 * D) + 16 * q;
+        const int x = r0 + 8 * t + g;
+        const bool ok = 8 * t + g < nrows;
+        const int step_row = x / a.group, hq = h * a.group + x - step_row * a.group;
+        const char* src = static_cast<const char*>(a.q) +
+                          2 * ((cur.it.row0 + (ok ? step_row : 0)) * a.q_row + (ok ? hq : 0) * a.q_head + 8 * q);
         uint32_t raw[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {  // channels 32 i + 8 q ..
-          const uint4 v = *reinterpret_cast<const uint4*>(src + 64 * i);
+          const uint4 v = ok ? *reinterpret_cast<const uint4*>(src + 64 * i) : make_uint4(0, 0, 0, 0);
           raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
         }
         float top = 0.f;
@@ -413,24 +404,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
           raw[i] = half2_bits(f.x * up, f.y * up);
           if constexpr (!QS) qf[t][i] = raw[i];
         }
-        if constexpr (QS) {  // in place: the tile's 8 rows are this warp's
-          __syncwarp();
+        if constexpr (QS) {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
-            s_q[(t * (D / 32) + i) * 32 + lane] = make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
-          if (q == 0) s_factor[8 * t + g] = down;
-        } else {
-          factor[t][0] = __shfl_sync(0xffffffffu, down, 8 * q);      // lane of row 2q: g = 2q
-          factor[t][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
+            queries[(t * (D / 32) + i) * 32 + lane] = make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
         }
-      }
-    }
-    if constexpr (QS) {
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        factor[t][0] = s_factor[8 * t + 2 * q];
-        factor[t][1] = s_factor[8 * t + 2 * q + 1];
+        factor[t][0] = __shfl_sync(0xffffffffu, down, 8 * q);      // lane of row 2q: g = 2q
+        factor[t][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
       }
     }
 
@@ -448,9 +428,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     const int open_hi = a.tree != nullptr ? first : min(first + r0 / a.group + 1, len);
     const int open_lo = a.window > 0 ? max(first + (r0 + nrows - 1) / a.group - a.window + 1, 0) : 0;
 
-    const int n_units = dead ? 0 : units_of(cur);
-    int tok0 = (cur.it.lo + cur.off + warp) * kUnit;
-    for (int i = 0; i < n_units; ++i, tok0 += W * kUnit) {
+    const int n_units = dead ? 0 : cur.count;
+    int tok0 = (cur.it.lo + cur.off) * kUnit;
+    for (int i = 0; i < n_units; ++i, tok0 += kUnit) {
       const uint32_t bad = invalid >> (2 * stage) & 3u;
       if (bad != 3u) {
         if (!warp_wait(bar0 + 8 * stage, parity >> stage & 1u, kWaitCycles)) {
@@ -489,7 +469,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             uint4 b;
-            if constexpr (QS) b = s_q[(n * (D / 32) + w) * 32 + lane];
+            if constexpr (QS) b = queries[(n * (D / 32) + w) * 32 + lane];
             else b = make_uint4(qf[n][4 * w], qf[n][4 * w + 1], qf[n][4 * w + 2], qf[n][4 * w + 3]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) mk::mma_16816(sc[u][n], x[u][0], y[u][0], x[u][1], y[u][1], b.x, b.y);
@@ -612,38 +592,16 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         }
         __syncwarp();  // every lane has read the stage
       }
-      if (i + S < n_units) issue(cur, i + S, stage, h);
+      if (i + S < n_units) issue(cur, i + S, stage);
       if (++stage == S) stage = 0;
     }
     if (dead) {  // let what is still in flight land before the memory is given up
       for (int st = 0; st < S; ++st)
         if ((invalid >> (2 * st) & 3u) != 3u) warp_wait(bar0 + 8 * st, parity >> st & 1u, kDrainCycles);
     }
-    // ---- join the warps: the second half's sums go through shared memory to the first half's, and
-    // theirs to all threads ----
-    // accumulator i of m-tile k: channel g D/8 + 2k + (i >> 1), row 2q + (i & 1)
-    const int slot = warp % JOIN;
-    auto spot = [&](int n, int i, int k) {
-      return reinterpret_cast<float2*>(s_sum + (slot * ROWS + 8 * n + 2 * q + i) * PITCH + g * (D / 8) + 2 * k);
-    };
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], o);
-        if (g == 0) {
-          s_m[warp * ROWS + 8 * n + 2 * q + i] = m[n][i];
-          s_l[warp * ROWS + 8 * n + 2 * q + i] = l[n][i];
-        }
-        if (warp >= JOIN) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k) *spot(n, i, k) = make_float2(acc[n][k][i], acc[n][k][2 + i]);
-        }
-      }
-    }
-    if (tid == 0) {
-      Walk& nxt = s_walk[turn ^ 1];
+    // the next part of the chunk: its first units are in flight while this one's results leave
+    if (lane == 0) {
+      Walk& nxt = s_walk[warp][turn ^ 1];
       nxt = cur;
       nxt.pos += cur.count;
       nxt.more = nxt.pos < end;
@@ -657,137 +615,171 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         nxt.count = static_cast<int>(min(end - nxt.pos, static_cast<long long>(nxt.it.units)));
       }
     }
-    __syncthreads();
-    const bool more = s_walk[turn ^ 1].more;
-    if (more) start(s_walk[turn ^ 1]);
-    if (warp < JOIN) {
+    __syncwarp();
+    const bool more = s_walk[warp][turn ^ 1].more;
+    if (more) start(s_walk[warp][turn ^ 1]);
+
+    const bool whole = cur.count == cur.it.units;
+    float* part = a.part + (2 * static_cast<size_t>(chunk) + (cur.off == 0 ? 1 : 0)) * L::kPart;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], o);
+      }
+      // accumulator 2 e + i of m-tile k: channel g D/8 + 2k + e, row 2q + i
+      if (whole) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = 8 * n + 2 * q + i;
-          float mt = kLowest;
+          if (r < nrows) {
 #pragma unroll
-          for (int w = 0; w < W; ++w) mt = fmaxf(mt, s_m[w * ROWS + r]);
-          const float c = exp2_approx(m[n][i] - mt), d = exp2_approx(s_m[(warp + JOIN) * ROWS + r] - mt);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            float2* p = spot(n, i, k);
-            const float2 x = *p;
-            *p = make_float2(c * acc[n][k][i] + d * x.x, c * acc[n][k][2 + i] + d * x.y);
+            for (int k = 0; k < KS; ++k)
+              finish<D>(a, cur.it.row0, h, r0 + r, g * (D / 8) + 2 * k, acc[n][k][i], acc[n][k][2 + i], m[n][i], l[n][i]);
           }
         }
-    }
-    __syncthreads();
-    const bool whole = cur.count == cur.it.units;
-    float* part = a.part + (2 * static_cast<size_t>(blockIdx.x) + (cur.off == 0 ? 1 : 0)) * a.part_floats;
-    for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d4 = i - r * (D / 4);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < JOIN; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(s_sum + (w * ROWS + r) * PITCH + 4 * d4);
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-      }
-      float mt = kLowest, lt = 0.f;
-      if (whole || d4 == 0) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) mt = fmaxf(mt, s_m[w * ROWS + r]);
-#pragma unroll
-        for (int w = 0; w < W; ++w) lt += exp2_approx(s_m[w * ROWS + r] - mt) * s_l[w * ROWS + r];
-      }
-      if (whole) {
-        finish<D>(a, cur.it.row0, h, r0 + r, d4, v, mt, lt);
       } else {
-        *reinterpret_cast<float4*>(part + 4 * i) = v;
-        if (d4 == 0) {
-          part[kPartSums + r] = mt;
-          part[kPartSums + kPartRows + r] = lt;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          reinterpret_cast<float4*>(part)[(n * KS + k) * 32 + lane] =
+              make_float4(acc[n][k][0], acc[n][k][1], acc[n][k][2], acc[n][k][3]);
+        if (g == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            part[ROWS * D + 8 * n + 2 * q + i] = m[n][i];
+            part[ROWS * D + ROWS + 8 * n + 2 * q + i] = l[n][i];
+          }
         }
       }
     }
-    if (tid == 0 && !whole && cur.off == 0) {  // the item goes on in the chunks up to that of its last unit
+    if (lane == 0 && !whole && cur.off == 0) {  // the item goes on in the chunks up to that of its last unit
       Piece p;
       p.on = 1;
       p.last = static_cast<int>((cur.pos + cur.it.units - 1) / per);
       p.row0 = cur.it.row0; p.r0 = r0; p.nrows = nrows; p.h = h;
-      a.pieces[blockIdx.x] = p;
+      a.pieces[chunk] = p;
     }
     if (!more) break;
   }
 }
 
-// Joins the parts of the items that were cut: CTA (c, y) the rows 8 y .. of the item that begins in
-// chunk c and goes on past it, in the order of the chunks.
-template <int D>
-__global__ void __launch_bounds__(2 * D) join_kernel(AttendArgs a) {
-  __shared__ float s_w[kMaxChunks][8];  // m, then weights
-  __shared__ float s_total[8], s_top[8];
+// Joins the parts of the items that were cut.  CTA (b, n): n-tile n of the items that begin in the
+// chunks [b kJoinChunks, + kJoinChunks) and go on past them.  A warp takes one m-tile of the output
+// and every GROUPS-th part of the item.  It is all latency, so the sums of a batch of parts are under
+// way before their m and l are here: two trips to memory for up to 16 GROUPS parts.
+constexpr int kJoinThreads = 512, kJoinChunks = 8;
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
+  constexpr int ROWS = 8 * NT, KS = D / 16, PART = ROWS * D + 2 * ROWS, GROUPS = kJoinThreads / 32 / KS;
+  constexpr int DEEP = 16, BATCH = DEEP * GROUPS;
+  __shared__ float s_w[BATCH][8], s_l[BATCH][8];  // m of a batch of parts, then their weights; their l
+  __shared__ float s_top[8], s_total[8], s_worth[8];  // of the batches so far
+  __shared__ float4 s_sum[kJoinThreads];
   pdl_wait();
   pdl_launch_dependents();
-  const int c0 = blockIdx.x, tid = threadIdx.x, row8 = 8 * blockIdx.y;
-  const int4* pp = reinterpret_cast<const int4*>(a.pieces + c0);
-  const int4 x = __ldcg(pp), y = __ldcg(pp + 1);
-  const Piece p{x.x, x.y, x.z, x.w, y.x, y.y};
-  if (!p.on || row8 >= p.nrows) return;
-  const int n = p.last - c0 + 1;
-  // of the chunk c0 + c: the first chunk's part starts at the item's first unit
-  auto part_of = [&](int c) { return a.part + (2 * static_cast<size_t>(c0 + c) + (c == 0 ? 1 : 0)) * a.part_floats; };
-  for (int i = tid; i < 8 * n; i += 2 * D) s_w[i >> 3][i & 7] = __ldcg(part_of(i >> 3) + kPartSums + row8 + (i & 7));
-  const int r = tid / (D / 4), d4 = tid - r * (D / 4), i4 = (row8 + r) * (D / 4) + d4;
-  __syncthreads();
-  if (tid < 256) {  // a warp a row (D = 64: four warps take two rows each)
-    for (int row = tid >> 5; row < 8; row += 2 * D / 32) {
-      const int lane = tid & 31;
-      float top = kLowest, l = 0.f;
-      for (int c = lane; c < n; c += 32) top = fmaxf(top, s_w[c][row]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      for (int c = lane; c < n; c += 32) {
-        const float w = exp2_approx(s_w[c][row] - top);
-        l += w * __ldcg(part_of(c) + kPartSums + kPartRows + row8 + row);
-        s_w[c][row] = w;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = warp % KS, group = warp / KS, n = blockIdx.y;
+  const int q = lane & 3;
+  // lane l of every warp looks at the CTA's chunk l
+  int4 px = make_int4(0, 0, 0, 0), py = px;
+  if (lane < kJoinChunks && blockIdx.x * kJoinChunks + lane < a.chunks) {
+    const int4* pp = reinterpret_cast<const int4*>(a.pieces + blockIdx.x * kJoinChunks + lane);
+    px = __ldcg(pp);
+    py = __ldcg(pp + 1);
+  }
+  uint32_t on = __ballot_sync(0xffffffffu, px.x != 0 && 8 * n < py.x);
+  for (; on != 0; on &= on - 1) {
+    const int src = __ffs(on) - 1, c0 = blockIdx.x * kJoinChunks + src;
+    const int parts = __shfl_sync(0xffffffffu, px.y, src) - c0 + 1, row0 = __shfl_sync(0xffffffffu, px.z, src);
+    const int r0 = __shfl_sync(0xffffffffu, px.w, src), nrows = __shfl_sync(0xffffffffu, py.x, src);
+    const int h = __shfl_sync(0xffffffffu, py.y, src);
+    // of the chunk c0 + c: the first chunk's part starts at the item's first unit
+    auto part_of = [&](int c) { return a.part + (2 * static_cast<size_t>(c0 + c) + (c == 0 ? 1 : 0)) * PART; };
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < 8) {
+      s_top[tid] = kLowest;
+      s_total[tid] = 0.f;
+    }
+    for (int cb = 0; cb < parts; cb += BATCH) {
+      const int nb = min(BATCH, parts - cb);
+      for (int i = tid; i < 8 * nb; i += kJoinThreads) {
+        const float* p = part_of(cb + (i >> 3)) + ROWS * D + 8 * n + (i & 7);
+        s_w[i >> 3][i & 7] = __ldcg(p);
+        s_l[i >> 3][i & 7] = __ldcg(p + ROWS);
       }
+      float4 z[DEEP];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) {
-        s_total[row] = l;
-        s_top[row] = top;
+      for (int j = 0; j < DEEP; ++j)
+        if (group + j * GROUPS < nb)
+          z[j] = __ldcg(reinterpret_cast<const float4*>(part_of(cb + group + j * GROUPS)) + (n * KS + k) * 32 + lane);
+      __syncthreads();
+      if (warp < 8) {  // a warp a row
+        const float old = s_top[warp];
+        float top = old, l = 0.f;
+        for (int c = lane; c < nb; c += 32) top = fmaxf(top, s_w[c][warp]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int c = lane; c < nb; c += 32) {
+          const float w = exp2_approx(s_w[c][warp] - top);
+          s_w[c][warp] = w;
+          l += w * s_l[c][warp];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) {
+          const float f = exp2_approx(old - top);
+          s_top[warp] = top;
+          s_total[warp] = s_total[warp] * f + l;
+          s_worth[warp] = f;
+        }
+      }
+      __syncthreads();
+      const float f0 = s_worth[2 * q], f1 = s_worth[2 * q + 1];
+      v.x *= f0; v.y *= f1; v.z *= f0; v.w *= f1;
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j)
+        if (group + j * GROUPS < nb) {
+          const float w0 = s_w[group + j * GROUPS][2 * q], w1 = s_w[group + j * GROUPS][2 * q + 1];
+          v.x += w0 * z[j].x; v.y += w1 * z[j].y; v.z += w0 * z[j].z; v.w += w1 * z[j].w;
+        }
+      __syncthreads();  // the weights have been used
+    }
+    if constexpr (GROUPS > 1) {
+      s_sum[tid] = v;
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int j = 1; j < GROUPS; ++j) {
+          const float4 y = s_sum[tid + j * KS * 32];
+          v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
       }
     }
+    if (group == 0) {
+      const int c = (lane >> 2) * (D / 8) + 2 * k, r = 8 * n + 2 * q;
+      if (r < nrows) finish<D>(a, row0, h, r0 + r, c, v.x, v.z, s_top[2 * q], s_total[2 * q]);
+      if (r + 1 < nrows) finish<D>(a, row0, h, r0 + r + 1, c, v.y, v.w, s_top[2 * q + 1], s_total[2 * q + 1]);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (row8 + r >= p.nrows) return;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < n; c += 8) {
-    float4 z[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < n) z[j] = __ldcg(reinterpret_cast<const float4*>(part_of(c + j)) + i4);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < n) {
-        const float w = s_w[c + j][r];
-        v.x += w * z[j].x; v.y += w * z[j].y; v.z += w * z[j].z; v.w += w * z[j].w;
-      }
-  }
-  finish<D>(a, p.row0, p.h, p.r0 + row8 + r, d4, v, s_top[r], s_total[r]);
 }
 
 template <int D, int NT, int W, int S, int CTAS, bool QS>
 cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
-  constexpr int smem = Shape<D, NT, W, S>::kTotal;
+  typedef Shape<D, NT, W, S, QS> L;
+  constexpr int smem = L::kTotal;
   static_assert(smem <= 227 * 1024 / CTAS - 2048, "shared memory");
-  static_assert(8 * NT * D <= kPartSums && 8 * NT <= kPartRows, "a partial result holds a block");
   auto kernel = attend_kernel<D, NT, W, S, CTAS, QS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // t / tiles_per_page = umulhi(t, magic): exact for t below 2^26 (2^30 tokens) and up to 64 tiles a page
   a.page_magic = static_cast<uint32_t>(((1ull << 32) + a.c.tiles_per_page - 1) / a.c.tiles_per_page);
-  const int grid = min(CTAS * num_sms, kMaxChunks);
+  constexpr int stride = L::kPart;  // floats of a partial result
+  const int grid = max(1, min(CTAS * num_sms, min(kMaxChunks / W, static_cast<int>(kPartFloats / 2 / stride / W))));
+  a.chunks = grid * W;
   e = launch_pdl(kernel, dim3(grid), dim3(32 * W), smem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<D>, dim3(grid, NT), dim3(2 * D), 0, stream, a);
+  return launch_pdl(join_kernel<D, NT>, dim3((a.chunks + kJoinChunks - 1) / kJoinChunks, NT), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -797,10 +789,10 @@ cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaSt
     case 64:
       return row_tile <= 8    ? launch<64, 1, 8, 4, 2, false>(a, num_sms, stream)
              : row_tile <= 16 ? launch<64, 2, 8, 4, 2, false>(a, num_sms, stream)
-                              : launch<64, 4, 12, 3, 1, false>(a, num_sms, stream);
+                              : launch<64, 4, 8, 4, 1, false>(a, num_sms, stream);
     case 128:
-      return row_tile <= 8    ? launch<128, 1, 8, 2, 2, false>(a, num_sms, stream)
-             : row_tile <= 16 ? launch<128, 2, 12, 3, 1, false>(a, num_sms, stream)
+      return row_tile <= 8    ? launch<128, 1, 16, 2, 1, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<128, 2, 12, 3, 1, true>(a, num_sms, stream)
                               : launch<128, 4, 8, 3, 1, true>(a, num_sms, stream);
     default:
       return row_tile <= 8 ? launch<256, 1, 8, 2, 1, false>(a, num_sms, stream) : launch<256, 2, 8, 2, 1, true>(a, num_sms, stream);

@@ -147,7 +147,6 @@ int moe_kv4_attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_r
   a.tree = reinterpret_cast<const unsigned long long*>(tree);
   a.out = out; a.lse = lse;
   a.part = at<float>(c, L.part);
-  a.part_floats = L.part_floats;
   a.pieces = at<moe::kv4::Piece>(c, L.pieces);
   const int64_t block = static_cast<int64_t>(max_rows < 1 ? 1 : max_rows) * a.group;
   return done("attend launch", moe::kv4::launch_attend(a, static_cast<int>(block > 1024 ? 1024 : block), sms, stream));

@@ -9,7 +9,8 @@ namespace moe {
 namespace kv4 {
 
 constexpr int kTile = 16;       // tokens of a tile
-constexpr int kMaxChunks = 512;  // CTAs of an attention launch at most, each with one chunk of the work
+constexpr int kMaxChunks = 2560;              // warps of an attention launch at most, each with one chunk of the work
+constexpr size_t kPartFloats = 2 * 1280 * 4224;  // floats of the partial results: two per chunk
 constexpr int kStepRows = 64;   // rows of a sequence's step with a tree or in a compaction
 
 // A cache as the kernels see it.
@@ -34,13 +35,7 @@ struct alignas(16) Piece {
 
 struct WsLayout {
   size_t status, pieces, copies, need, part, total;
-  size_t part_floats;  // floats of one partial result of the attention
 };
-
-// A partial result holds up to 4096 / dim ... rows of dim + 2 floats; the widest row block of
-// every head size is kept at or below 4096 sums, so that one partial is 4096 + 2 * 64 floats.
-constexpr int kPartSums = 4096;
-constexpr int kPartRows = 64;
 
 inline WsLayout ws_layout(const moe_kv4_cache& c) {
   WsLayout L{};
@@ -51,8 +46,7 @@ inline WsLayout ws_layout(const moe_kv4_cache& c) {
   // moe_kv4_reserve: copies [1 + 2 * seqs] (their number, then page pairs), need [seqs + 1]
   L.copies = take((1 + 2 * size_t(c.seqs)) * 4);
   L.need = take((1 + size_t(c.seqs)) * 8);
-  L.part_floats = kPartSums + 2 * kPartRows;
-  L.part = take(size_t(2) * kMaxChunks * L.part_floats * 4);
+  L.part = take(kPartFloats * 4);
   L.total = o;
   return L;
 }
@@ -140,9 +134,9 @@ struct AttendArgs {
   const unsigned long long* tree;
   void* out;
   float* lse;
-  uint32_t page_magic;  // set by the launcher
+  uint32_t page_magic;  // set by the launcher, as is
+  int chunks;           // the number of chunks
   float* part;
-  size_t part_floats;
   Piece* pieces;
 };
 
