@@ -85,7 +85,7 @@ MOE_API size_t moe_kv4_workspace_bytes(const moe_kv4_cache* cache);
 /* MOE_OK, MOE_ERR_INVALID_ARG or MOE_ERR_UNSUPPORTED for the sizes of a cache (host only). */
 MOE_API int moe_kv4_check(const moe_kv4_cache* cache);
 
-/* Zero the status word of a fresh workspace.  Once after allocation. */
+/* Zero the status word and the counters of a fresh workspace.  Once after allocation. */
 MOE_API int moe_kv4_workspace_init(const moe_kv4_cache* cache, moe_stream_t stream);
 
 /* Quantise the step's K and V rows into `layer`.

@@ -769,17 +769,14 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
   typedef Shape<D, NT, W, S, QS> L;
   constexpr int smem = L::kTotal;
   static_assert(smem <= 227 * 1024 / CTAS - 2048, "shared memory");
-  auto kernel = attend_kernel<D, NT, W, S, CTAS, QS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   // t / tiles_per_page = umulhi(t, magic): exact for t below 2^26 (2^30 tokens) and up to 64 tiles a page
   a.page_magic = static_cast<uint32_t>(((1ull << 32) + a.c.tiles_per_page - 1) / a.c.tiles_per_page);
   constexpr int stride = L::kPart;  // floats of a partial result
   const int grid = max(1, min(CTAS * num_sms, min(kMaxChunks / W, static_cast<int>(kPartFloats / 2 / stride / W))));
   a.chunks = grid * W;
-  e = launch_pdl(kernel, dim3(grid), dim3(32 * W), smem, stream, a);
+  const cudaError_t e = launch_ready<attend_kernel<D, NT, W, S, CTAS, QS>>(dim3(grid), dim3(32 * W), smem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<D, NT>, dim3((a.chunks + kJoinChunks - 1) / kJoinChunks, NT), dim3(kJoinThreads), 0, stream, a);
+  return launch_ready<join_kernel<D, NT>>(dim3((a.chunks + kJoinChunks - 1) / kJoinChunks, NT), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace

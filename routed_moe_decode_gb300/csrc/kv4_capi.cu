@@ -83,7 +83,7 @@ int moe_kv4_workspace_init(const moe_kv4_cache* c, moe_stream_t stream) {
   if (rc != MOE_OK) return rc;
   const WsLayout L = moe::kv4::ws_layout(*c);
   if (!c->workspace || !aligned(c->workspace, 256) || c->workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
-  return done("workspace init", cudaMemsetAsync(c->workspace, 0, L.pieces, stream));  // the status word
+  return done("workspace init", cudaMemsetAsync(c->workspace, 0, L.pieces, stream));  // the status word and the arrivals
 }
 
 int moe_kv4_append(const moe_kv4_cache* c, int layer, const void* k, int64_t k_row_stride, int64_t k_head_stride,
@@ -101,7 +101,10 @@ int moe_kv4_append(const moe_kv4_cache* c, int layer, const void* k, int64_t k_r
   if (static_cast<int64_t>(rows) * c->kv_heads * c->head_dim > (1ll << 36)) return MOE_ERR_UNSUPPORTED;
   a.k = k; a.v = v; a.k_row = k_row_stride; a.k_head = k_head_stride; a.v_row = v_row_stride; a.v_head = v_head_stride;
   a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16; a.k_ts = c->k_scale; a.v_ts = c->v_scale;
-  return done("append launch", moe::kv4::launch_append(a, stream));
+  int sms = 0;
+  const int src = moe::device_sms(&sms);
+  if (src != MOE_OK) return src;
+  return done("append launch", moe::kv4::launch_append(a, sms, stream));
 }
 
 int moe_kv4_read(const moe_kv4_cache* c, int layer, void* k, void* v, int dtype, const int32_t* cu_rows, int rows,
@@ -116,7 +119,10 @@ int moe_kv4_read(const moe_kv4_cache* c, int layer, void* k, void* v, int dtype,
   if (static_cast<int64_t>(rows) * c->kv_heads * c->head_dim > (1ll << 36)) return MOE_ERR_UNSUPPORTED;
   a.k_out = k; a.v_out = v;
   a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16; a.k_ts = c->k_scale; a.v_ts = c->v_scale;
-  return done("read launch", moe::kv4::launch_read(a, stream));
+  int sms = 0;
+  const int src = moe::device_sms(&sms);
+  if (src != MOE_OK) return src;
+  return done("read launch", moe::kv4::launch_read(a, sms, stream));
 }
 
 int moe_kv4_attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -200,6 +206,7 @@ int moe_kv4_compact(const moe_kv4_cache* c, const uint8_t* keep, const int32_t* 
   if (rows == 0) return MOE_OK;
   if (!keep || !cu_rows || !aligned(cu_rows, 4)) return MOE_ERR_INVALID_ARG;
   a.keep = keep; a.cu = cu_rows; a.rows = rows;
+  a.arrivals = at<uint32_t>(c, L.arrivals);
   return done("compact launch", moe::kv4::launch_compact(a, stream));
 }
 

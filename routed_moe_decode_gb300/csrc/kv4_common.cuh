@@ -34,7 +34,7 @@ struct alignas(16) Piece {
 };
 
 struct WsLayout {
-  size_t status, pieces, copies, need, part, total;
+  size_t status, arrivals, pieces, copies, need, part, total;
 };
 
 inline WsLayout ws_layout(const moe_kv4_cache& c) {
@@ -42,6 +42,7 @@ inline WsLayout ws_layout(const moe_kv4_cache& c) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   L.status = take(64);
+  L.arrivals = take(size_t(c.seqs) * 4);  // moe_kv4_compact: CTAs of each sequence
   L.pieces = take(size_t(kMaxChunks) * sizeof(Piece));
   // moe_kv4_reserve: copies [1 + 2 * seqs] (their number, then page pairs), need [seqs + 1]
   L.copies = take((1 + 2 * size_t(c.seqs)) * 4);
@@ -66,17 +67,6 @@ MOE_DEVICE StepRows step_rows(const int* __restrict__ cu, int s, int rows) {
   const int a = min(max(ld(cu + s), 0), rows);
   const int b = min(max(ld(cu + s + 1), a), rows);
   return {a, b - a};
-}
-
-// The sequence that row r belongs to: the last s with cu[s] <= r (binary search; empty
-// sequences share a start and are passed over).
-MOE_DEVICE int seq_of_row(const int* __restrict__ cu, int seqs, int r) {
-  int lo = 0, hi = seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (ld(cu + mid) <= r) lo = mid; else hi = mid - 1;
-  }
-  return lo;
 }
 
 // The tile that holds token `pos` of sequence s and head h, or nullptr where it has no page.
@@ -116,6 +106,7 @@ struct RowArgs {
   void* v_out;
   const int* cu;
   int rows;
+  int rows_per_cta;  // set by the launcher
   bool fp16;
   float k_ts, v_ts;
 };
@@ -147,12 +138,13 @@ struct PageArgs {
   const uint8_t* keep;
   const int* cu;
   int n, rows;
+  uint32_t* arrivals;
   int* copies;
   unsigned long long* need;
 };
 
-cudaError_t launch_append(const RowArgs& a, cudaStream_t stream);
-cudaError_t launch_read(const RowArgs& a, cudaStream_t stream);
+cudaError_t launch_append(const RowArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_read(const RowArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream);
 cudaError_t launch_reserve(const PageArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_fork(const PageArgs& a, cudaStream_t stream);

@@ -115,20 +115,32 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
   if (tid == 0) entry[c.seqs] = total;
   __syncthreads();
 
-  unsigned free;
-  int found = 0;
+  unsigned free0 = 0, free;  // of the first round, which mostly is the only one
+  int found = 0, rank0 = 0, first_round = 0;
   for (int base = 0; base < c.pages && found < all; base += 4 * kAllocThreads) {
     unsigned long long round;
-    block_scan(static_cast<unsigned>(first_free(c, base + 4 * tid, free)), warp_sums, round);
+    const int n = first_free(c, base + 4 * tid, free);
+    const int before_me = found + static_cast<int>(block_scan(static_cast<unsigned>(n), warp_sums, round));
+    if (base == 0) {
+      free0 = free;
+      rank0 = before_me;
+      first_round = static_cast<int>(round);
+    }
     found += static_cast<int>(round);
   }
   const int got = min(found, all);
   int seen = 0;
   for (int base = 0; base < c.pages && seen < got; base += 4 * kAllocThreads) {
-    unsigned long long round;
-    const int n = first_free(c, base + 4 * tid, free);
-    int rank = seen + static_cast<int>(block_scan(static_cast<unsigned>(n), warp_sums, round));
-    seen += static_cast<int>(round);
+    int rank = rank0;
+    if (base == 0) {
+      free = free0;
+      seen = first_round;
+    } else {
+      unsigned long long round;
+      const int n = first_free(c, base + 4 * tid, free);
+      rank = seen + static_cast<int>(block_scan(static_cast<unsigned>(n), warp_sums, round));
+      seen += static_cast<int>(round);
+    }
     for (; free != 0 && rank < got; free &= free - 1, ++rank) {
       const int page = base + 4 * tid + __ffs(free) - 1;
       int lo = 0, hi = c.seqs - 1;  // the last sequence that starts at or before `rank`: it needs the page
@@ -255,12 +267,13 @@ __device__ __forceinline__ unsigned long long kept_rows(const PageArgs& a, const
 // layer and head: D / 32 pieces of 16 bytes of K codes, as many of V codes, one of D / 16 bytes of
 // K scales and one of V scales.  Its thread moves that piece of every kept row, in order; a row
 // only ever moves to an earlier place, which by then has been read, so no other thread has to be
-// waited for.  Eight rows are read before the first of them is written.
+// waited for.  Eight rows are read before the first of them is written.  The sequence's last CTA to
+// have looked at its length and table cuts it to what it keeps (the moves need neither again).
 constexpr int kMoveThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(PageArgs a) {
   __shared__ int s_page_from[kStepRows], s_page_to[kStepRows], s_from[kStepRows], s_to[kStepRows];
-  __shared__ int s_moves;
+  __shared__ int s_moves, s_kept;
   pdl_wait();
   pdl_launch_dependents();
   const Cache& c = a.c;
@@ -293,9 +306,21 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(PageArgs a) {
       s_to[m] = max(pt, 0) % c.page_size;
     }
     if (bad) atomicOr(c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
-    if (threadIdx.x == 0) s_moves = moves;
+    if (threadIdx.x == 0) {
+      s_moves = moves;
+      s_kept = __popcll(kept);
+    }
   }
   __syncthreads();
+  if (threadIdx.x < 32) {
+    int last = 0;
+    if (threadIdx.x == 0) last = atom_add_acqrel_u32(a.arrivals + s, 1u) == gridDim.x - 1;
+    if (__shfl_sync(0xffffffffu, last, 0)) {
+      if (threadIdx.x == 0) a.arrivals[s] = 0;  // for the next call
+      const int len = max(ld(c.lens + s), 0);
+      cut(c, s, len, min(max(len - st.n, 0) + s_kept, len));
+    }
+  }
   const int moves = s_moves;
   if (moves == 0) return;
   constexpr int kCodes = D / 32, kPieces = 2 * kCodes + 2;
@@ -334,39 +359,26 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(PageArgs a) {
   else move(uint32_t());
 }
 
-// The sequences cut to what they keep, after the moves.
-__global__ void __launch_bounds__(32 * kTrimWarps) compact_cut_kernel(PageArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int s = blockIdx.x * kTrimWarps + (threadIdx.x >> 5);
-  if (s >= a.c.seqs) return;
-  const StepRows st = step_rows(a.cu, s, a.rows);
-  if (st.n == 0) return;
-  const int len = max(ld(a.c.lens + s), 0), kept = __popcll(kept_rows(a, st));
-  cut(a.c, s, len, min(max(len - st.n, 0) + kept, len));
-}
-
 }  // namespace
 
 cudaError_t launch_reserve(const PageArgs& a, int num_sms, cudaStream_t stream) {
-  const cudaError_t e = launch_pdl(reserve_kernel, dim3(1), dim3(kAllocThreads), 0, stream, a);
+  const cudaError_t e = launch_ready<reserve_kernel>(dim3(1), dim3(kAllocThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(copy_kernel, dim3(num_sms * 8), dim3(kCopyThreads), 0, stream, a);
+  return launch_ready<copy_kernel>(dim3(num_sms * 8), dim3(kCopyThreads), 0, stream, a);
 }
 cudaError_t launch_fork(const PageArgs& a, cudaStream_t stream) {
-  return launch_pdl(fork_kernel, dim3(a.n), dim3(128), 0, stream, a);
+  return launch_ready<fork_kernel>(dim3(a.n), dim3(128), 0, stream, a);
 }
 cudaError_t launch_trim(const PageArgs& a, cudaStream_t stream) {
-  return launch_pdl(trim_kernel, dim3((a.c.seqs + kTrimWarps - 1) / kTrimWarps), dim3(32 * kTrimWarps), 0, stream, a);
+  return launch_ready<trim_kernel>(dim3((a.c.seqs + kTrimWarps - 1) / kTrimWarps), dim3(32 * kTrimWarps), 0, stream, a);
 }
 cudaError_t launch_compact(const PageArgs& a, cudaStream_t stream) {
   const Cache& c = a.c;
   const long long units = static_cast<long long>(c.layers) * c.heads * (c.dim / 16 + 2);
-  const dim3 grid(static_cast<unsigned>((units + kMoveThreads - 1) / kMoveThreads), c.seqs);
-  auto kernel = c.dim == 64 ? compact_kernel<64> : c.dim == 128 ? compact_kernel<128> : compact_kernel<256>;
-  const cudaError_t e = launch_pdl(kernel, grid, dim3(kMoveThreads), 0, stream, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(compact_cut_kernel, dim3((c.seqs + kTrimWarps - 1) / kTrimWarps), dim3(32 * kTrimWarps), 0, stream, a);
+  const dim3 grid(static_cast<unsigned>((units + kMoveThreads - 1) / kMoveThreads), c.seqs), block(kMoveThreads);
+  return c.dim == 64    ? launch_ready<compact_kernel<64>>(grid, block, 0, stream, a)
+         : c.dim == 128 ? launch_ready<compact_kernel<128>>(grid, block, 0, stream, a)
+                        : launch_ready<compact_kernel<256>>(grid, block, 0, stream, a);
 }
 
 }  // namespace kv4
