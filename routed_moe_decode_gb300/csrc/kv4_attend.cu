@@ -124,9 +124,10 @@ __device__ __forceinline__ Words<N> shared_words(const uint8_t* p) {
   return o;
 }
 
-// The work is counted in units of two tiles (32 tokens), each of which a warp takes as one step: two
-// independent chains of products, and one look at the masks and at the reference m for both.
-constexpr int kUnit = 2 * kTile;
+// The work is counted in units of U tiles (16 U tokens), each of which a warp takes as one step.  With
+// one n-tile of rows U is 2: two independent chains of products, and one look at the masks and at the
+// reference m for both; with more rows the n-tiles are the independent chains, and U is 1, which
+// leaves registers for more warps.
 
 // A sequence's items.
 struct Item {
@@ -152,7 +153,7 @@ struct Steps {
   __device__ __forceinline__ int len(int s) const { return max(lens != nullptr ? lens[s] : ld(a.c.lens + s), 0); }
 };
 
-template <int ROWS>
+template <int ROWS, int UNIT_TOKENS>
 __device__ __forceinline__ Item item_of(const Steps& st, int s) {
   const AttendArgs& a = st.a;
   Item it;
@@ -166,8 +167,8 @@ __device__ __forceinline__ Item item_of(const Steps& st, int s) {
   it.len = static_cast<int>(min(static_cast<long long>(st.len(s)), room));
   it.first = it.len - it.n;
   const int from = a.window > 0 ? max(it.first - a.window + 1, 0) : 0;
-  it.lo = min(from, max(it.len - 1, 0)) / kUnit;
-  it.units = max((it.len + kUnit - 1) / kUnit - it.lo, 1);
+  it.lo = min(from, max(it.len - 1, 0)) / UNIT_TOKENS;
+  it.units = max((it.len + UNIT_TOKENS - 1) / UNIT_TOKENS - it.lo, 1);
   it.blocks = static_cast<int>((static_cast<long long>(it.n) * a.group + ROWS - 1) / ROWS);
   it.items = a.c.heads * it.blocks;
   return it;
@@ -211,11 +212,11 @@ __device__ __forceinline__ void finish(const AttendArgs& a, int row0, int h, int
 // memory for every unit instead of being kept in registers.  The offsets in dynamic shared memory,
 // and the floats of a partial result: [NT][D / 16][32 lanes][4] sums as the accumulators lie in the
 // warp's registers, then [2][8 NT] m and l.
-template <int D, int NT, int W, int S, bool QS>
+template <int D, int NT, int U, int W, int S, bool QS>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kRing = 0;                               // [W][S] units
-  static constexpr int kQuery = kRing + W * S * 36 * D;         // QS: [W][NT][D / 32][32] uint4
+  static constexpr int kQuery = kRing + W * S * U * 18 * D;         // QS: [W][NT][D / 32][32] uint4
   static constexpr int kBars = kQuery + (QS ? W * kRows * D * 2 : 0);
   static constexpr int kSeqs = kBars + W * S * 8;               // cu [kSeqCache + 1], lens [kSeqCache]
   static constexpr int kTotal = kSeqs + (2 * kSeqCache + 1) * 4;
@@ -230,13 +231,14 @@ struct Walk {
   long long pos;
 };
 
-template <int D, int NT, int W, int S, int CTAS, bool QS>
+template <int D, int NT, int U, int W, int S, int CTAS, bool QS>
 __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
-  typedef Shape<D, NT, W, S, QS> L;
+  typedef Shape<D, NT, U, W, S, QS> L;
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;   // k16 steps of a score, and m16 tiles of the output
   constexpr int TILE = 18 * D;
-  constexpr int UNIT = 2 * TILE;
+  constexpr int UNIT = U * TILE;
+  constexpr int kUnit = U * kTile;  // tokens
   constexpr int kThreads = 32 * W;
   extern __shared__ __align__(128) uint8_t smem[];
   int* s_cu = reinterpret_cast<int*>(smem + L::kSeqs);
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   const int per_thread = (a.c.seqs + kThreads - 1) / kThreads;
   const int sa = min(tid * per_thread, a.c.seqs), sb = min(sa + per_thread, a.c.seqs);
   long long mine = 0;
-  for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS>(steps, s));
+  for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS, kUnit>(steps, s));
   long long total;
   const long long before = block_prefix<W>(mine, s_scan, total);
   const int chunk = warp * gridDim.x + blockIdx.x;
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     Walk w;
     long long at = s_before[lo];
     for (int s = lo * per_thread;; ++s) {
-      w.it = item_of<ROWS>(steps, s);
+      w.it = item_of<ROWS, kUnit>(steps, s);
       const long long n = work_of(w.it);
       if (begin < at + n) break;
       at += n;
@@ -303,9 +305,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   // ---- this warp's ring ----
   int stage = 0;            // next stage to be consumed; all stages are empty between items
   uint32_t parity = 0;      // bit st: of stage st's phase
-  uint32_t invalid = 0;     // bits 2 st, 2 st + 1: the unit's tile has no page
+  uint32_t invalid = 0;     // bits U st ..: the unit's tile has no page
   bool dead = false;        // a copy did not arrive
-  // the places of the warp's tiles in the cache, 32 at a time (16 units): lane l holds that of tile
+  // the places of the warp's tiles in the cache, 32 at a time (32 / U units): lane l holds that of tile
   // 32 b + l, issues its copy, and has the page number of the tile 32 further on
   long long place = 0;
   uint32_t there = 0;       // lanes whose tile has a page
@@ -313,10 +315,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   auto page_slot = [&](int t) {
     return a.c.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), a.page_magic));
   };
-  auto tile_at = [&](const Walk& w, int i) { return 2 * (w.it.lo + w.off) + i; };
+  auto tile_at = [&](const Walk& w, int i) { return U * (w.it.lo + w.off) + i; };
   auto load_page = [&](const Walk& w, int i) {  // of the warp's i-th tile of the part
     const int t = tile_at(w, i);
-    if (i >= 2 * w.count || t * kTile >= w.it.len) return -1;
+    if (i >= U * w.count || t * kTile >= w.it.len) return -1;
     const int page = ld(a.c.table + static_cast<size_t>(w.it.s) * a.c.max_pages + page_slot(t));
     if (page < 0 || page >= a.c.pages) {
       atomicOr(a.c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
@@ -332,25 +334,26 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   };
   // start the copies of the part's unit i into stage st
   auto issue = [&](const Walk& w, int i, int st) {
-    const int j = i & 15;
+    const int j = i % (32 / U);
     if (j == 0 && i > 0) {
-      set_places(w, 2 * i + lane, page_next);
-      page_next = load_page(w, 2 * i + 32 + lane);
+      set_places(w, U * i + lane, page_next);
+      page_next = load_page(w, U * i + 32 + lane);
     }
-    const uint32_t bad = ~(there >> (2 * j)) & 3u;
-    invalid = (invalid & ~(3u << (2 * st))) | (bad << (2 * st));
-    if ((lane >> 1) == j && ((there >> lane) & 1u)) {
+    constexpr uint32_t kAll = (1u << U) - 1u;
+    const uint32_t bad = ~(there >> (U * j)) & kAll;
+    invalid = (invalid & ~(kAll << (U * st))) | (bad << (U * st));
+    if (lane / U == j && ((there >> lane) & 1u)) {
       const uint32_t bar = bar0 + 8 * st;
-      // one lane announces both copies; the other's may land before, which the barrier allows
-      if ((lane & 1) == 0 || bad == 1u) mbar_arrive_expect_tx(bar, bad == 0 ? UNIT : TILE);
-      bulk_copy_g2s(ring_addr + st * UNIT + (lane & 1) * TILE, a.c.pool + place, TILE, bar);
+      // one lane announces the copies of both; the other's may land before, which the barrier allows
+      if (lane % U == 0 || bad == 1u) mbar_arrive_expect_tx(bar, bad == 0 ? UNIT : TILE);
+      bulk_copy_g2s(ring_addr + st * UNIT + lane % U * TILE, a.c.pool + place, TILE, bar);
     }
   };
   // the first units of a part
   auto start = [&](const Walk& w) {
     if (dead) return;
     const int page = load_page(w, lane);
-    page_next = w.count > 16 ? load_page(w, 32 + lane) : -1;
+    page_next = w.count > 32 / U ? load_page(w, 32 + lane) : -1;
     set_places(w, lane, page);
     int st = stage;
     for (int i = 0; i < S && i < w.count; ++i) {
@@ -431,8 +434,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     const int n_units = dead ? 0 : cur.count;
     int tok0 = (cur.it.lo + cur.off) * kUnit;
     for (int i = 0; i < n_units; ++i, tok0 += kUnit) {
-      const uint32_t bad = invalid >> (2 * stage) & 3u;
-      if (bad != 3u) {
+      const uint32_t bad = invalid >> (U * stage) & ((1u << U) - 1u);
+      if (bad != (1u << U) - 1u) {
         if (!warp_wait(bar0 + 8 * stage, parity >> stage & 1u, kWaitCycles)) {
           if (lane == 0) atomicOr(a.c.status, kStatusTimeout);
           dead = true;
@@ -442,10 +445,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         const uint8_t* unit = ring + stage * UNIT;
         const int tok_g = (g >> 1) + 4 * (g & 1);
         // ---- S^T = K Q^T, one word (8 channels, half a scale block) of each token at a time ----
-        float sc[2][NT][4];
-        uint32_t ks[4][D / 64];
+        float sc[U][NT][4];
+        uint32_t ks[2 * U][D / 64];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.f;
           key_scales<D>(unit + u * TILE + 16 * D + tok_g * (D / 16), q, ks[2 * u]);
@@ -454,9 +457,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         const uint8_t* kp = unit + tok_g * 16 + q * 4;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-          uint32_t x[2][4], y[2][4];
+          uint32_t x[U][4], y[U][4];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < U; ++u) {
             const uint8_t* p = kp + u * TILE + w * 256;
             e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t*>(p), x[u][0], x[u][1], x[u][2], x[u][3]);
             e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t*>(p + 128), y[u][0], y[u][1], y[u][2], y[u][3]);
@@ -472,16 +475,16 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
             if constexpr (QS) b = queries[(n * (D / 32) + w) * 32 + lane];
             else b = make_uint4(qf[n][4 * w], qf[n][4 * w + 1], qf[n][4 * w + 2], qf[n][4 * w + 3]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) mk::mma_16816(sc[u][n], x[u][0], y[u][0], x[u][1], y[u][1], b.x, b.y);
+            for (int u = 0; u < U; ++u) mk::mma_16816(sc[u][n], x[u][0], y[u][0], x[u][1], y[u][1], b.x, b.y);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) mk::mma_16816(sc[u][n], x[u][2], y[u][2], x[u][3], y[u][3], b.z, b.w);
+            for (int u = 0; u < U; ++u) mk::mma_16816(sc[u][n], x[u][2], y[u][2], x[u][3], y[u][3], b.z, b.w);
           }
         }
         // ---- masks, running reference, p ----
         const bool open = tok0 >= open_lo && tok0 + kUnit <= open_hi && bad == 0;
         if (!open) {  // products become scores here; their factors are 1 below
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -504,7 +507,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float top = fmaxf(fmaxf(sc[0][n][j], sc[0][n][2 + j]), fmaxf(sc[1][n][j], sc[1][n][2 + j]));
+            float top = fmaxf(sc[0][n][j], sc[0][n][2 + j]);
+            if constexpr (U == 2) top = fmaxf(top, fmaxf(sc[1][n][j], sc[1][n][2 + j]));
             hi[n][j] = open ? top * factor[n][j] : top;
             rise |= hi[n][j] > m[n][j] + kSlack;
           }
@@ -523,12 +527,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
               for (int k = 0; k < KS; ++k) { acc[n][k][j] *= c; acc[n][k][2 + j] *= c; }
             }
         }
-        uint32_t pf[2][NT][2];
+        uint32_t pf[U][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float f0 = open ? factor[n][0] : 1.f, f1 = open ? factor[n][1] : 1.f;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < U; ++u) {
             const float p0 = exp2_approx(fmaf(sc[u][n][0], f0, -m[n][0])), p1 = exp2_approx(fmaf(sc[u][n][1], f1, -m[n][1]));
             const float p2 = exp2_approx(fmaf(sc[u][n][2], f0, -m[n][0])), p3 = exp2_approx(fmaf(sc[u][n][3], f1, -m[n][1]));
             l[n][0] += p0 + p2;
@@ -539,7 +543,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         }
         // ---- O^T += V^T P^T ----
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
           const uint8_t* tile = unit + u * TILE;
           uint32_t vs[4];  // D = 256: two bytes, else one
           const uint8_t* sp = tile + 17 * D + q * (D / 16) + (D == 64 ? g >> 1 : D == 128 ? g : 2 * g);
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     }
     if (dead) {  // let what is still in flight land before the memory is given up
       for (int st = 0; st < S; ++st)
-        if ((invalid >> (2 * st) & 3u) != 3u) warp_wait(bar0 + 8 * st, parity >> st & 1u, kDrainCycles);
+        if ((invalid >> (U * st) & ((1u << U) - 1u)) != (1u << U) - 1u) warp_wait(bar0 + 8 * st, parity >> st & 1u, kDrainCycles);
     }
     // the next part of the chunk: its first units are in flight while this one's results leave
     if (lane == 0) {
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         if (++nxt.idx == nxt.it.items) {
           nxt.idx = 0;
           int s = nxt.it.s;
-          do nxt.it = item_of<ROWS>(steps, ++s); while (nxt.it.items == 0);
+          do nxt.it = item_of<ROWS, kUnit>(steps, ++s); while (nxt.it.items == 0);
         }
         nxt.count = static_cast<int>(min(end - nxt.pos, static_cast<long long>(nxt.it.units)));
       }
@@ -764,9 +768,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
   }
 }
 
-template <int D, int NT, int W, int S, int CTAS, bool QS>
+template <int D, int NT, int U, int W, int S, int CTAS, bool QS>
 cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
-  typedef Shape<D, NT, W, S, QS> L;
+  typedef Shape<D, NT, U, W, S, QS> L;
   constexpr int smem = L::kTotal;
   static_assert(smem <= 227 * 1024 / CTAS - 2048, "shared memory");
   // t / tiles_per_page = umulhi(t, magic): exact for t below 2^26 (2^30 tokens) and up to 64 tiles a page
@@ -774,7 +778,7 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
   constexpr int stride = L::kPart;  // floats of a partial result
   const int grid = max(1, min(CTAS * num_sms, min(kMaxChunks / W, static_cast<int>(kPartFloats / 2 / stride / W))));
   a.chunks = grid * W;
-  const cudaError_t e = launch_ready<attend_kernel<D, NT, W, S, CTAS, QS>>(dim3(grid), dim3(32 * W), smem, stream, a);
+  const cudaError_t e = launch_ready<attend_kernel<D, NT, U, W, S, CTAS, QS>>(dim3(grid), dim3(32 * W), smem, stream, a);
   if (e != cudaSuccess) return e;
   return launch_ready<join_kernel<D, NT>>(dim3((a.chunks + kJoinChunks - 1) / kJoinChunks, NT), dim3(kJoinThreads), 0, stream, a);
 }
@@ -784,15 +788,15 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream) {
   switch (a.c.dim) {
     case 64:
-      return row_tile <= 8    ? launch<64, 1, 8, 4, 2, false>(a, num_sms, stream)
-             : row_tile <= 16 ? launch<64, 2, 8, 4, 2, false>(a, num_sms, stream)
-                              : launch<64, 4, 8, 4, 1, false>(a, num_sms, stream);
+      return row_tile <= 8    ? launch<64, 1, 2, 8, 4, 2, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<64, 2, 2, 8, 4, 2, false>(a, num_sms, stream)
+                              : launch<64, 4, 2, 8, 4, 1, false>(a, num_sms, stream);
     case 128:
-      return row_tile <= 8    ? launch<128, 1, 16, 2, 1, false>(a, num_sms, stream)
-             : row_tile <= 16 ? launch<128, 2, 12, 3, 1, true>(a, num_sms, stream)
-                              : launch<128, 4, 8, 3, 1, true>(a, num_sms, stream);
+      return row_tile <= 8    ? launch<128, 1, 2, 16, 2, 1, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<128, 2, 2, 12, 3, 1, true>(a, num_sms, stream)
+                              : launch<128, 4, 2, 8, 3, 1, true>(a, num_sms, stream);
     default:
-      return row_tile <= 8 ? launch<256, 1, 8, 2, 1, false>(a, num_sms, stream) : launch<256, 2, 8, 2, 1, true>(a, num_sms, stream);
+      return row_tile <= 8 ? launch<256, 1, 2, 8, 2, 1, false>(a, num_sms, stream) : launch<256, 2, 2, 8, 2, 1, true>(a, num_sms, stream);
   }
 }
 
