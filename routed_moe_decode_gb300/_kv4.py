@@ -49,6 +49,7 @@ class Kv4Cache:
             device = pool.device
         self.pool = self._tensor("pool", pool, (a.layers, a.pages, self.page_bytes), torch.uint8, 0, device)
         self.device = self.pool.device
+        self._index = self.device.index
         self.table = self._tensor("table", table, (a.seqs, a.max_pages), torch.int32, -1, self.device)
         self.lens = self._tensor("lens", lens, (a.seqs,), torch.int32, 0, self.device)
         self.refs = self._tensor("refs", refs, (a.pages,), torch.int32, 0, self.device)
@@ -62,7 +63,6 @@ class Kv4Cache:
         self._default_scale = 1.0 / math.sqrt(a.head_dim)
         self._attend, self._append, self._read = (self._lib.moe_kv4_attend, self._lib.moe_kv4_append,
                                                   self._lib.moe_kv4_read)
-        self._index = self.device.index
 
     @staticmethod
     def _tensor(name, t, shape, dtype, fill, device):
@@ -83,30 +83,30 @@ class Kv4Cache:
             raise _lib.MoeError(fn, rc)
 
     def _ints(self, name, t, n):
-        if t.dtype is not torch.int32 or t.device != self.device or not t.is_contiguous() or t.dim() != 1 or \
+        if t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous() or t.dim() != 1 or \
                 (n is not None and t.shape[0] != n):
             raise ValueError(f"{name}: contiguous int32{'' if n is None else f' [{n}]'} on {self.device}")
         return t.data_ptr()
 
-    def _rows(self, name, t, heads, dtype, rows=None):
-        """A [rows, heads, head_dim] tensor whose channels are consecutive."""
-        s = t.shape
-        if len(s) != 3 or s[2] != self.head_dim or (heads is not None and s[1] != heads) or t.stride(2) != 1 or \
-                t.dtype is not dtype or t.device != self.device or (rows is not None and s[0] != rows):
-            raise ValueError(f"{name}: [rows, {heads if heads else 'heads'}, {self.head_dim}] of {dtype} on "
+    def _rows(self, name, t, heads):
+        """Type code, strides and rows of a [rows, heads, head_dim] tensor whose channels are consecutive."""
+        dtype = _DTYPES.get(t.dtype)
+        shape, stride = t.shape, t.stride()
+        if dtype is None or len(shape) != 3 or shape[2] != self.head_dim or (heads and shape[1] != heads) or \
+                stride[2] != 1 or t.get_device() != self._index:
+            raise ValueError(f"{name}: [rows, {heads or 'heads'}, {self.head_dim}] of bfloat16 or float16 on "
                              f"{self.device} with consecutive channels")
+        return dtype, stride[0], stride[1], shape[0]
 
     def append(self, layer, k, v, cu_rows, stream=None):
         """Quantise the step's K and V rows, [rows, kv_heads, head_dim] of bfloat16 or float16, into
         the pages (row and head strides multiples of 8)."""
-        dtype = _DTYPES.get(k.dtype)
-        if dtype is None:
-            raise ValueError("k, v: bfloat16 or float16")
-        self._rows("k", k, self.kv_heads, k.dtype)
-        self._rows("v", v, self.kv_heads, k.dtype, k.shape[0])
-        rc = self._append(self._ref, layer, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                          v.stride(1), dtype, self._ints("cu_rows", cu_rows, self.seqs + 1), k.shape[0],
-                          self._stream(stream))
+        dtype, k_row, k_head, rows = self._rows("k", k, self.kv_heads)
+        v_dtype, v_row, v_head, v_rows = self._rows("v", v, self.kv_heads)
+        if v_dtype != dtype or v_rows != rows:
+            raise ValueError("k and v: of one type and as many rows")
+        rc = self._append(self._ref, layer, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row, v_head, dtype,
+                          self._ints("cu_rows", cu_rows, self.seqs + 1), rows, self._stream(stream))
         if rc != 0:
             raise _lib.MoeError("moe_kv4_append", rc)
 
@@ -119,13 +119,12 @@ class Kv4Cache:
             out = tuple(torch.zeros((rows, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
                         for _ in range(2))
         k, v = out
-        code = _DTYPES.get(k.dtype)
-        if code is None or not k.is_contiguous() or not v.is_contiguous():
-            raise ValueError("out: contiguous bfloat16 or float16")
-        self._rows("out[0]", k, self.kv_heads, k.dtype)
-        self._rows("out[1]", v, self.kv_heads, k.dtype, k.shape[0])
+        code, _, _, n = self._rows("out[0]", k, self.kv_heads)
+        v_code, _, _, v_n = self._rows("out[1]", v, self.kv_heads)
+        if v_code != code or v_n != n or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("out: two contiguous tensors of one type and as many rows")
         rc = self._read(self._ref, layer, k.data_ptr(), v.data_ptr(), code, self._ints("cu_rows", cu_rows, self.seqs + 1),
-                        k.shape[0], self._stream(stream))
+                        n, self._stream(stream))
         if rc != 0:
             raise _lib.MoeError("moe_kv4_read", rc)
         return out
@@ -136,22 +135,19 @@ class Kv4Cache:
         (default head_dim ** -0.5); window > 0: a row sees that many tokens back, itself included;
         tree [rows] int64: bit j set where the row sees the step's token j.  Returns out (like q,
         contiguous), or (out, lse) if lse [rows, q_heads] float32 is given."""
-        dtype = _DTYPES.get(q.dtype)
-        if dtype is None:
-            raise ValueError("q: bfloat16 or float16")
-        self._rows("q", q, None, q.dtype)
-        rows, heads, _ = q.shape
+        dtype, q_row, q_head, rows = self._rows("q", q, None)
+        heads = q.shape[1]
         if out is None:
             out = torch.empty((rows, heads, self.head_dim), dtype=q.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype is not q.dtype or out.device != self.device or not out.is_contiguous():
+        elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != self._index or not out.is_contiguous():
             raise ValueError("out: contiguous, of q's shape and type")
         if lse is not None and (lse.shape != (rows, heads) or lse.dtype is not torch.float32 or
-                                lse.device != self.device or not lse.is_contiguous()):
+                                lse.get_device() != self._index or not lse.is_contiguous()):
             raise ValueError("lse: contiguous [rows, q_heads] of float32")
         if tree is not None and (tree.dtype is not torch.int64 or tree.shape != (rows,) or
-                                 tree.device != self.device or not tree.is_contiguous()):
+                                 tree.get_device() != self._index or not tree.is_contiguous()):
             raise ValueError("tree: contiguous [rows] of int64")
-        rc = self._attend(self._ref, layer, q.data_ptr(), q.stride(0), q.stride(1), heads, dtype,
+        rc = self._attend(self._ref, layer, q.data_ptr(), q_row, q_head, heads, dtype,
                           self._ints("cu_rows", cu_rows, self.seqs + 1), rows, max_rows,
                           self._default_scale if scale is None else scale, window,
                           None if tree is None else tree.data_ptr(), out.data_ptr(),

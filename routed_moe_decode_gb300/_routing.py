@@ -50,12 +50,13 @@ class Routing:
             raise ValueError(f"ids, weights: contiguous [{T}, {self.k}] of int32 and float32")
         if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (E,) or not bias.is_contiguous()):
             raise ValueError(f"bias: contiguous [{E}] of float32")
-        if not logits.is_cuda or ids.device != logits.device or weights.device != logits.device or \
-                (bias is not None and bias.device != logits.device):
+        index = logits.get_device()
+        if index < 0 or ids.get_device() != index or weights.get_device() != index or \
+                (bias is not None and bias.get_device() != index):
             raise ValueError("logits, bias, ids and weights lie on one CUDA device")
         rc = self._route(self._ref, T, logits.data_ptr(), logits.stride(0) if T > 1 else E, dtype,
                          None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                         _raw_stream(logits.device.index) if stream is None else stream.cuda_stream)
+                         _raw_stream(index) if stream is None else stream.cuda_stream)
         if rc != 0:
             raise _lib.MoeError("moe_route_grouped", rc)
         return ids, weights

@@ -15,7 +15,7 @@ namespace kv4 {
 namespace {
 
 constexpr int kAllocThreads = 1024;
-constexpr int kNeedShared = 4096;  // sequences whose running needs fit in shared memory
+constexpr int kNeedShared = 2048;  // sequences whose needs and lengths are kept in shared memory
 
 __device__ __forceinline__ int pages_of(int tokens, int page_size) {
   return tokens / page_size + (tokens % page_size != 0);
@@ -73,18 +73,26 @@ __device__ __forceinline__ int first_free(const Cache& c, int p0, unsigned& free
 __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
   __shared__ unsigned long long warp_sums[32];
   __shared__ Entry s_entry[kNeedShared + 1];
+  __shared__ int s_len[kNeedShared], s_grow[kNeedShared];
   __shared__ int s_copies;
   pdl_wait();
   pdl_launch_dependents();
   const Cache& c = a.c;
   const int tid = threadIdx.x;
-  Entry* entry = c.seqs <= kNeedShared ? s_entry : a.need;  // [seqs + 1]
+  const bool kept = c.seqs <= kNeedShared;
+  Entry* entry = kept ? s_entry : a.need;  // [seqs + 1]
+  unsigned free0;  // of the first 4096 pages, which mostly are enough: under way with the lengths
+  const int n0 = first_free(c, 4 * tid, free0);
   if (tid == 0) s_copies = 0;
   const int per = (c.seqs + kAllocThreads - 1) / kAllocThreads;
   const int s0 = min(tid * per, c.seqs), s1 = min(s0 + per, c.seqs);
   Entry mine = 0;  // needs << 32 | copies << 2
   for (int s = s0; s < s1; ++s) {
     const int len = max(ld(c.lens + s), 0), grow = max(ld(a.a + s), 0);
+    if (kept) {
+      s_len[s] = len;
+      s_grow[s] = grow;
+    }
     Entry flags = 0;
     int need = 0;
     if (grow > 0) {
@@ -115,14 +123,13 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
   if (tid == 0) entry[c.seqs] = total;
   __syncthreads();
 
-  unsigned free0 = 0, free;  // of the first round, which mostly is the only one
+  unsigned free;
   int found = 0, rank0 = 0, first_round = 0;
   for (int base = 0; base < c.pages && found < all; base += 4 * kAllocThreads) {
     unsigned long long round;
-    const int n = first_free(c, base + 4 * tid, free);
+    const int n = base == 0 ? n0 : first_free(c, base + 4 * tid, free);
     const int before_me = found + static_cast<int>(block_scan(static_cast<unsigned>(n), warp_sums, round));
     if (base == 0) {
-      free0 = free;
       rank0 = before_me;
       first_round = static_cast<int>(round);
     }
@@ -152,7 +159,7 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
       if (entry_start(entry[lo + 1]) > got) continue;  // not all its needs are met
       const int slot = rank - entry_start(e), copy = static_cast<int>(e & kCopy);
       int* row = c.table + static_cast<size_t>(lo) * c.max_pages;
-      const int have = pages_of(max(ld(c.lens + lo), 0), c.page_size);
+      const int have = pages_of(kept ? s_len[lo] : max(ld(c.lens + lo), 0), c.page_size);
       if (copy && slot == 0) {
         a.copies[1 + 2 * entry_rank(e)] = ld(row + have - 1);
         a.copies[2 + 2 * entry_rank(e)] = page;
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
   }
   __syncthreads();
   for (int s = s0; s < s1; ++s) {
-    const int grow = max(ld(a.a + s), 0);
+    const int grow = kept ? s_grow[s] : max(ld(a.a + s), 0);
     if (grow == 0) continue;
     const Entry e = entry[s];
     const int end = entry_start(entry[s + 1]);
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
       atomicOr(c.status, static_cast<int>(MOE_KV4_NO_PAGE));
       continue;
     }
-    c.lens[s] = max(ld(c.lens + s), 0) + grow;
+    c.lens[s] = (kept ? s_len[s] : max(ld(c.lens + s), 0)) + grow;
     if (e & kCopy) {
       atomicSub(c.refs + a.copies[1 + 2 * entry_rank(e)], 1);
       atomicAdd(&s_copies, 1);
