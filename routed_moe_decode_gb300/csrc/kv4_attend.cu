@@ -551,16 +551,14 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream) {
-  if (row_tile > 8 && a.c.dim <= 128) return launch_attend_tc(a, row_tile, num_sms, stream);
+  if (a.c.dim == 128 && row_tile > 16) return launch_attend_tc(a, row_tile, num_sms, stream);
   switch (a.c.dim) {
     case 64:
       return row_tile <= 8    ? launch<64, 1, 8, 4, 2, false>(a, num_sms, stream)
              : row_tile <= 16 ? launch<64, 2, 8, 4, 2, false>(a, num_sms, stream)
                               : launch<64, 4, 8, 4, 1, false>(a, num_sms, stream);
     case 128:
-      return row_tile <= 8    ? launch<128, 1, 16, 2, 1, false>(a, num_sms, stream)
-             : row_tile <= 16 ? launch<128, 2, 12, 3, 1, true>(a, num_sms, stream)
-                              : launch<128, 4, 8, 3, 1, true>(a, num_sms, stream);
+      return row_tile <= 8 ? launch<128, 1, 16, 2, 1, false>(a, num_sms, stream) : launch<128, 2, 12, 3, 1, true>(a, num_sms, stream);
     default:
       return row_tile <= 8 ? launch<256, 1, 8, 2, 1, false>(a, num_sms, stream) : launch<256, 2, 8, 2, 1, true>(a, num_sms, stream);
   }
