@@ -188,29 +188,48 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
   if (tid == 0) a.copies[0] = s_copies;  // the sequences that were refused pages are the last that need some
 }
 
-// The pages that reserve_kernel replaced, on every layer: one CTA a page and layer at a time.
-constexpr int kCopyThreads = 256;
+// The pages that reserve_kernel replaced, on every layer, kCopyBytes at a time: one copy and layer's
+// pieces go to the CTAs that come next, so that the last of them end together whatever a page's size.
+constexpr int kCopyThreads = 256, kCopyLoads = 4;
+constexpr int kCopyBytes = 32 * kCopyThreads * kCopyLoads;
+
+struct alignas(32) Line {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Line load_line(const uint8_t* p) {
+  Line l;
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(l.w[0]), "=r"(l.w[1]), "=r"(l.w[2]), "=r"(l.w[3]), "=r"(l.w[4]), "=r"(l.w[5]), "=r"(l.w[6]), "=r"(l.w[7])
+               : "l"(p));
+  return l;
+}
+__device__ __forceinline__ void store_line(uint8_t* p, const Line& l) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(l.w[0]), "r"(l.w[1]), "r"(l.w[2]),
+               "r"(l.w[3]), "r"(l.w[4]), "r"(l.w[5]), "r"(l.w[6]), "r"(l.w[7])
+               : "memory");
+}
+
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PageArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const Cache& c = a.c;
-  const long long units = static_cast<long long>(ld(a.copies)) * c.layers;
+  const long long pieces = (static_cast<long long>(c.page_bytes) + kCopyBytes - 1) / kCopyBytes;
+  const long long units = static_cast<long long>(ld(a.copies)) * c.layers * pieces;
   const size_t layer_bytes = static_cast<size_t>(c.pages) * c.page_bytes;
-  const int n16 = static_cast<int>(c.page_bytes / 16);
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int i = static_cast<int>(u / c.layers), layer = static_cast<int>(u - static_cast<long long>(i) * c.layers);
-    uint8_t* base = c.pool + layer * layer_bytes;
-    const uint4* src = reinterpret_cast<const uint4*>(base + static_cast<size_t>(ld(a.copies + 1 + 2 * i)) * c.page_bytes);
-    uint4* dst = reinterpret_cast<uint4*>(base + static_cast<size_t>(ld(a.copies + 2 + 2 * i)) * c.page_bytes);
-    int p = threadIdx.x;
-    for (; p + 3 * kCopyThreads < n16; p += 4 * kCopyThreads) {
-      uint4 v[4];
+    const long long il = u / pieces;
+    const int i = static_cast<int>(il / c.layers), layer = static_cast<int>(il - static_cast<long long>(i) * c.layers);
+    const long long first = (u - il * pieces) * kCopyBytes + 32 * threadIdx.x;
+    uint8_t* base = c.pool + layer * layer_bytes + first;
+    const uint8_t* src = base + static_cast<size_t>(ld(a.copies + 1 + 2 * i)) * c.page_bytes;
+    uint8_t* dst = base + static_cast<size_t>(ld(a.copies + 2 + 2 * i)) * c.page_bytes;
+    Line v[kCopyLoads];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __ldcs(src + p + j * kCopyThreads);
+    for (int j = 0; j < kCopyLoads; ++j)
+      if (first + 32 * kCopyThreads * j < static_cast<long long>(c.page_bytes)) v[j] = load_line(src + 32 * kCopyThreads * j);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dst[p + j * kCopyThreads] = v[j];
-    }
-    for (; p < n16; p += kCopyThreads) dst[p] = __ldcs(src + p);
+    for (int j = 0; j < kCopyLoads; ++j)
+      if (first + 32 * kCopyThreads * j < static_cast<long long>(c.page_bytes)) store_line(dst + 32 * kCopyThreads * j, v[j]);
   }
 }
 
@@ -371,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(PageArgs a) {
 cudaError_t launch_reserve(const PageArgs& a, int num_sms, cudaStream_t stream) {
   const cudaError_t e = launch_ready<reserve_kernel>(dim3(1), dim3(kAllocThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_ready<copy_kernel>(dim3(num_sms * 8), dim3(kCopyThreads), 0, stream, a);
+  return launch_ready<copy_kernel>(dim3(num_sms * 6), dim3(kCopyThreads), 0, stream, a);
 }
 cudaError_t launch_fork(const PageArgs& a, cudaStream_t stream) {
   return launch_ready<fork_kernel>(dim3(a.n), dim3(128), 0, stream, a);
