@@ -116,7 +116,10 @@ MOE_API int moe_kv4_read(const moe_kv4_cache* cache, int layer, void* k, void* v
  *   tree     [rows] uint64 or NULL
  *   out      [rows][q_heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   lse      [rows][q_heads] float or NULL
- * Scores, softmax statistics and sums are FP32. */
+ * At most 2^30 tokens a sequence are looked at.  Rows of no sequence are left as they are.  Scores,
+ * softmax statistics and sums are FP32; p is rounded to FP16, 11 bits relative to a row's largest.
+ * Two launches: the attention, and the joining of what it cut over several SMs; the result does
+ * not depend on timing. */
 MOE_API int moe_kv4_attend(const moe_kv4_cache* cache, int layer, const void* q, int64_t q_row_stride,
                            int64_t q_head_stride, int q_heads, int dtype, const int32_t* cu_rows, int rows,
                            int max_rows, float scale, int window, const uint64_t* tree, void* out, float* lse,

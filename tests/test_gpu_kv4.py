@@ -320,6 +320,35 @@ def test_append_outside_the_sequence_is_reported(moe):
     assert (k[:2] == 0).all() and (k[2:4] == held_one()).all() and (k[4:] == 0).all()
 
 
+def test_offsets_past_32_bits(moe):
+    # two layers of 2.4 GB: the last pages of the last layer lie past 2^32 bytes
+    heads, D, page, pages = 8, 256, 64, 16400
+    cache = moe.Kv4Cache(2, pages, heads, D, page, 3, 4)
+    assert cache.page_bytes * pages > 2 ** 31 and cache.page_bytes * pages * 2 > 2 ** 32
+    cache.refs[:pages - 6] = 1
+    cache.reserve(dev([70, 40, 0]))
+    assert cache.table[0, :2].tolist() == [pages - 6, pages - 5] and cache.table[1, 0] == pages - 4
+    cu = dev([0, 70, 110, 110])
+    kv = torch.randn((110, 2, heads, D), device="cuda").to(torch.bfloat16)
+    cache.append(1, kv[:, 0], kv[:, 1], cu)
+    k, v = cache.read(1, cu, rows=110)
+    for got, x in ((k, kv[:, 0]), (v, kv[:, 1])):
+        want = P.values(*P.quantise(x[::29].double().cpu().numpy(), 1.0), 1.0)
+        assert np.array_equal(got[::29].double().cpu().numpy(), want)
+    q = torch.randn((110, heads, D), device="cuda").to(torch.bfloat16)
+    out = cache.attend(1, q, cu, max_rows=70).double()
+    see = torch.ones(70, 70, dtype=torch.bool, device="cuda").tril()
+    z = torch.einsum("rhd,thd->hrt", q[:70].double(), k[:70].double()) * D ** -0.5
+    want = torch.einsum("hrt,thd->rhd", z.masked_fill(~see, -float("inf")).softmax(-1), v[:70].double())
+    assert (out[:70] - want).abs().max() <= 4 * 2.0 ** -8 + 4 * 2.0 ** -10  # values up to 4: BF16's half unit, p's rounding
+    cache.fork(dev([1]), dev([2]))
+    cache.reserve(dev([0, 0, 1]))  # the shared page is copied on both layers
+    assert cache.table[2, 0] == pages - 3
+    for layer in range(2):
+        assert torch.equal(cache.pool[layer, pages - 3], cache.pool[layer, pages - 4])
+    assert cache.status() == 0
+
+
 # ---- pages ----
 
 def same(cache, plain):
