@@ -7,6 +7,11 @@ High-level use (torch tensors on a CUDA device):
     layer = moe.MoeLayer(T, d, ffn, E, k)
     out = layer(logits, hidden, weights, residual)     # weights: dict of NVFP4 tensors
 
+    cache = moe.Kv4Cache(layers, pages, kv_heads, head_dim, page_size, seqs, max_pages)
+    routing = moe.Routing(E, k, score="sigmoid", groups=8, keep_groups=4, group_score="top2")
+    # a step: cache.reserve, per layer cache.append / cache.attend / MoeLayer(..., routing=routing),
+    # then cache.compact (examples/verify_step.py)
+
 The package contains no compute of its own: every step runs in the library's kernels.
 """
 from ._lib import (ALGO_AUTO, ALGO_MMA, ALGO_SIMT, ALGO_TCGEN05, ALGO_WIDE, MOE_DEV_BAD_EXPERT_ID, MOE_DEV_H_SATURATED, MOE_DEV_Y_SATURATED,
