@@ -545,12 +545,13 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
   a.chunks = grid * W;
   const cudaError_t e = launch_ready<attend_kernel<D, NT, W, S, CTAS, QS>>(dim3(grid), dim3(32 * W), smem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_ready<join_kernel<D, NT>>(dim3((a.chunks + kJoinChunks - 1) / kJoinChunks, NT), dim3(kJoinThreads), 0, stream, a);
+  return launch_join<D, NT, 8, 512>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream) {
+  if (row_tile > 64) return launch_attend_wide(a, num_sms, stream);
   if (a.c.dim == 128 && row_tile > 16) return launch_attend_tc(a, row_tile, num_sms, stream);
   switch (a.c.dim) {
     case 64:

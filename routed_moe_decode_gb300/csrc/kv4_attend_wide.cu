@@ -1,0 +1,596 @@
+// Attention over the 4-bit paged cache for blocks of up to 128 query rows (a step's rows times query
+// heads per K/V head): chunks of a prompt, and draft trees of many heads.
+//
+// The mathematics is that of the warp-MMA kernel (one pass, running reference m, FP32 sums, p
+// rounded to FP16); the products of 64 tokens at a time, a step, are
+//   S [128 rows x 64 tokens] = Q [128 x D] K^T       Q, K: shared memory
+//   O [128 rows x D]        += P [128 x 64] V        P: tensor memory, over its scores; V: shared memory
+// with S (two buffers) and O in tensor memory.  A query row is a lane of tensor memory and a thread:
+// its maximum, its sum and its masks need no other thread.  The cache is dequantised once for 128 rows.
+//
+// Every role has warps of its own, and only barriers in shared memory between them:
+//   a loader copies the tiles of up to S steps ahead into a ring and says what they hold;
+//   four warps dequantise keys and values into the operands' swizzled lines;
+//   an issuer starts the next step's first product before this step's second, so that the scores of
+//   a step are there when the last one's p have been written;
+//   four warps turn scores into p.
+// A row's m moves only when a score exceeds it by kSlack; then the output in tensor memory is rescaled.
+//
+// A block reads no step that none of its rows sees; blocks are walked from both ends of the rows inwards,
+// so that neighbouring items of a causal chunk are about equally long together.
+#include "kv4_attend.cuh"
+#include "kv4_tc.cuh"
+
+namespace moe {
+namespace kv4 {
+namespace {
+
+constexpr int kRows = 128, kTokens = 64, kTiles = kTokens / kTile;
+constexpr int kSoft = 4, kDeq = 4;                   // warps [0, kSoft), [kSoft, kSoft + kDeq)
+constexpr int kLoader = kSoft + kDeq, kIssuer = kLoader + 1, kWarps = kIssuer + 1, kThreads = 32 * kWarps;
+constexpr uint32_t kBIsMn = 1u << 16;  // instruction descriptor: B's rows are consecutive in memory
+// what the loader says of a step: tiles without a page, tokens of the sequence, and
+constexpr uint32_t kFirst = 1u << 16, kEnd = 1u << 17;  // the first of an item; no step, the end of the work
+constexpr int kInfos = 16;
+
+// Offsets in dynamic shared memory (from a 1024-byte boundary), tensor-memory columns, and the floats
+// of a partial result, which lies as the warp-MMA kernel's does.  VB: buffers of values, S: steps in the ring.
+template <int D, int VB, int S>
+struct WideShape {
+  static constexpr int kOperand = kTokens * D * 2;
+  static constexpr int kQ = 0;                          // [D / 64][128 rows][64] FP16, swizzled lines
+  static constexpr int kK = kQ + kRows * D * 2;         // [2][D / 64][64 tokens][64]
+  static constexpr int kV = kK + 2 * kOperand;          // [VB][D / 64][64 tokens][64]
+  static constexpr int kRing = kV + VB * kOperand;      // [S][4 tiles]
+  static constexpr int kBars = kRing + S * kTiles * 18 * D;
+  static constexpr int kNumBars = 2 * S + 2 + VB + 2 + 2 + 2 + 2;
+  static constexpr int kSeqs = kBars + 8 * kNumBars;    // cu [kSeqCache + 1], lens [kSeqCache]
+  static constexpr int kTotal = kSeqs + (2 * kSeqCache + 1) * 4 + 1024;
+  static constexpr int kPart = kRows * D + 2 * kRows;
+  static constexpr int kColO = 2 * kTokens;
+  static constexpr int kCols = kColO + D <= 256 ? 256 : 512;
+};
+
+// The block of rows of an item, and the steps of a part that some of its rows see.
+struct Block {
+  int h, r0, nrows;
+  int unit, steps;  // first step of the part that is taken, and their number
+};
+__device__ __forceinline__ Block block_of(const AttendArgs& a, const Walk& w) {
+  const Item& it = w.it;
+  Block b;
+  b.h = w.idx / it.blocks;
+  const int j = w.idx - b.h * it.blocks;
+  b.r0 = (j & 1 ? it.blocks - 1 - (j >> 1) : j >> 1) * kRows;
+  b.nrows = min(kRows, it.n * a.group - b.r0);
+  const int last = it.first + (b.r0 + b.nrows - 1) / a.group;
+  const int hi = a.tree != nullptr ? it.len : min(it.len, last + 1);
+  const int lo = a.window > 0 ? max(it.first + b.r0 / a.group - a.window + 1, 0) : 0;
+  const int from = it.lo + w.off;
+  b.unit = max(from, lo / kTokens);
+  b.steps = max(min(from + w.count, (max(hi, 0) + kTokens - 1) / kTokens) - b.unit, 0);
+  return b;
+}
+
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
+// Eight codes a word, 32 channels of a token, as FP16 into the token's line: chunks c0 .. c0 + 3 of 16 bytes.
+__device__ __forceinline__ void expand(const uint4& codes, uint32_t scales, uint8_t* line, int c0, int tok) {
+  const uint32_t s = e4m3x2_to_f16x2(scales), lo = bcast_lo_half(s), hi = bcast_hi_half(s);
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t x[4];
+    e2m1x8_to_f16x2x4(w[k], x[0], x[1], x[2], x[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = hmul2_bits(x[e], k < 2 ? lo : hi);
+    *reinterpret_cast<uint4*>(line + (((c0 + k) ^ (tok & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+template <int D, int VB, int S, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs a) {
+  typedef WideShape<D, VB, S> L;
+  constexpr int KS = D / 16, TILE = 18 * D, PIECES = D / 32;
+  static_assert(S + VB + 4 <= kInfos, "steps whose description is alive");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long s_scan[kWarps];
+  __shared__ Walk s_walk[kSoft + 1][2];  // of the warps that walk the items: this part, the next
+  __shared__ uint32_t s_info[kInfos], s_tmem;
+  __shared__ int s_abort;
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_addr(smem);
+  int* s_cu = reinterpret_cast<int*>(smem + L::kSeqs);
+  int* s_len = s_cu + kSeqCache + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // barriers: the ring's stages filled and taken; keys and values written; scores there; p written;
+  // second product done; query rows written; the end
+  const uint32_t full = base + L::kBars, taken = full + 8 * S, k_full = taken + 8 * S, v_full = k_full + 16,
+                 s_full = v_full + 8 * VB, p_full = s_full + 16, o_done = p_full + 16, q_full = o_done + 16,
+                 drain = q_full + 8;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(taken + 8 * i, kDeq);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + 8 * i, kDeq);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, kSoft);
+      mbar_init(o_done + 8 * i, 1);
+    }
+    for (int i = 0; i < VB; ++i) mbar_init(v_full + 8 * i, kDeq);
+    mbar_init(q_full, kSoft);
+    mbar_init(drain, 1);
+    s_abort = 0;
+  }
+  fence_barrier_init();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // the work, cut into one chunk of `per` steps per CTA: this one's is [begin, end)
+  const bool cached = a.c.seqs <= kSeqCache;
+  if (cached) {
+    for (int s = tid; s <= a.c.seqs; s += kThreads) {
+      s_cu[s] = ld(a.cu + s);
+      if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
+    }
+    __syncthreads();
+  }
+  const Steps steps{a, cached ? s_cu : nullptr, cached ? s_len : nullptr};
+  const int per_thread = (a.c.seqs + kThreads - 1) / kThreads;
+  const int sa = min(tid * per_thread, a.c.seqs), sb = min(sa + per_thread, a.c.seqs);
+  long long mine = 0;
+  for (int s = sa; s < sb; ++s) mine += work_of(item_of<kRows, kTokens>(steps, s));
+  long long total;
+  const long long before = block_prefix<kWarps>(mine, s_scan, total);
+  const int chunk = blockIdx.x;
+  const long long per = (total + a.chunks - 1) / a.chunks;
+  const long long begin = per * chunk, end = min(begin + per, total);
+  if (tid == 0) a.pieces[chunk].on = 0;
+  if (begin >= end) return;
+  if (begin >= before && begin < before + mine) {
+    Walk w;
+    settle<kRows, kTokens>(steps, sa, before, begin, end, w);
+    for (int i = 0; i <= kSoft; ++i) s_walk[i][0] = w;
+  }
+  __syncwarp();
+  if (warp == 0) {
+    tmem_alloc(smem_addr(&s_tmem), L::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  // A wait of a whole warp, with a limit: false where it gave up or another warp did; the roles then
+  // leave their work and meet at the end of the kernel.
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    bool ok = phase_done(bar, parity & 1u);
+    if (!__all_sync(0xffffffffu, ok)) {
+      const long long t0 = clock64();
+      while (!ok && clock64() - t0 < kWaitCycles && *reinterpret_cast<volatile int*>(&s_abort) == 0)
+        ok = mbar_try_wait(bar, parity & 1u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) {
+        *reinterpret_cast<volatile int*>(&s_abort) = 1;
+        atomicOr(a.c.status, kStatusTimeout);
+      }
+    }
+    return ok;
+  };
+  auto arrive = [&](uint32_t bar) {  // of a whole warp, once
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto info_of = [&](uint32_t n) { return *reinterpret_cast<volatile uint32_t*>(&s_info[n % kInfos]); };
+
+  if (warp == kLoader) {
+    // lane l holds the place of tile 32 b + l of the part (8 steps), issues its copy, and has the page
+    // number of the tile 32 further on
+    auto page_slot = [&](int t) {
+      return a.c.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(static_cast<uint32_t>(t), a.page_magic));
+    };
+    uint32_t n = 0;  // steps of the chunk
+    bool ok = true;
+    for (int turn = 0; ok; turn ^= 1) {
+      const Walk& w = s_walk[kSoft][turn];
+      const Block b = block_of(a, w);
+      const int tile0 = kTiles * b.unit, tiles = kTiles * b.steps, len = w.it.len;
+      const int head = b.h * a.c.tiles_per_page;
+      const int* table = a.c.table + static_cast<size_t>(w.it.s) * a.c.max_pages;
+      auto load_page = [&](int i) {  // of the part's i-th tile
+        if (i >= tiles || (tile0 + i) * kTile >= len) return -1;
+        const int page = ld(table + page_slot(tile0 + i));
+        if (page < 0 || page >= a.c.pages) {
+          atomicOr(a.c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
+          return -1;
+        }
+        return page;
+      };
+      int page = load_page(lane), page_next = load_page(32 + lane);
+      for (int i = 0; i < b.steps; ++i, ++n) {
+        constexpr int kAtOnce = 32 / kTiles;
+        const int j = i % kAtOnce, st = static_cast<int>(n % S);
+        if (j == 0 && i > 0) {
+          page = page_next;
+          page_next = load_page(kTiles * i + 32 + lane);
+        }
+        const uint32_t good = __ballot_sync(0xffffffffu, page >= 0) >> (kTiles * j) & ((1u << kTiles) - 1u);
+        if (n >= S) ok = wait(taken + 8 * st, n / S - 1);
+        if (!ok) break;
+        if (lane == 0) {
+          const int valid = min(max(len - (tile0 + kTiles * i) * kTile, 0), kTokens);
+          *reinterpret_cast<volatile uint32_t*>(&s_info[n % kInfos]) =
+              (~good & ((1u << kTiles) - 1u)) | (static_cast<uint32_t>(valid) << 8) | (i == 0 ? kFirst : 0u);
+          if (good == 0) mbar_arrive(full + 8 * st);
+          else mbar_arrive_expect_tx(full + 8 * st, __popc(good) * TILE);
+        }
+        __syncwarp();
+        if (lane / kTiles == j && page >= 0) {
+          const int t = tile0 + kTiles * (i - j) + lane;
+          const uint8_t* src = a.c.pool + static_cast<size_t>(page) * a.c.page_bytes +
+                               static_cast<size_t>(head + t - page_slot(t) * a.c.tiles_per_page) * TILE;
+          bulk_copy_g2s(base + L::kRing + (st * kTiles + lane % kTiles) * TILE, src, TILE, full + 8 * st);
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) advance<kRows, kTokens>(steps, w, s_walk[kSoft][turn ^ 1], end);
+      __syncwarp();
+      if (!s_walk[kSoft][turn ^ 1].more) break;
+    }
+    if (ok) {
+      const uint32_t st = n % S;
+      if (n < S || wait(taken + 8 * st, n / S - 1)) {
+        if (lane == 0) {
+          *reinterpret_cast<volatile uint32_t*>(&s_info[n % kInfos]) = kEnd;
+          mbar_arrive(full + 8 * st);
+        }
+      }
+    } else {  // let what is still in flight land before the memory is given up
+      const long long t0 = clock64();
+      for (uint32_t r = n > S ? n - S : 0; r < n; ++r)
+        while (!phase_done(full + 8 * (r % S), (r / S) & 1u) && clock64() - t0 < kDrainCycles) {
+        }
+    }
+  } else if (warp == kIssuer) {
+    // the products, by one lane of a converged warp
+    const uint64_t q_desc = smem_desc_sw128(base + L::kQ, 1024);
+    bool first = false;  // of the step before
+    uint32_t items = 0;
+    auto second = [&](uint32_t m) {  // the second product of step m
+      if (!wait(p_full + 8 * (m & 1u), m >> 1) || !wait(v_full + 8 * (m % VB), m / VB)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t v_desc = desc_mn_sw128(base + L::kV + (m % VB) * L::kOperand, kTokens * 128);
+#pragma unroll
+        for (int k = 0; k < kTokens / 16; ++k)
+          tc_mma_f16_ts(tmem + L::kColO, tmem + (m & 1u) * kTokens + 8 * k, v_desc + (k * 2048 >> 4),
+                        idesc_f16_f32(kRows, D) | kBIsMn, !first || k > 0);
+        tc_commit(o_done + 8 * (m & 1u));
+      }
+      __syncwarp();
+      return true;
+    };
+    for (uint32_t n = 0;; ++n) {
+      if (!wait(k_full + 8 * (n & 1u), n >> 1)) break;
+      const uint32_t info = info_of(n);
+      const bool begins = (info & (kFirst | kEnd)) != 0;
+      if (begins && n > 0 && !second(n - 1)) break;  // the item before ends: its rows make room
+      if (info & kEnd) break;
+      if (begins && !wait(q_full, items++)) break;
+      // the scores of two steps ago have become p, and those have been used
+      if (n >= 2 && !wait(o_done + 8 * (n & 1u), (n >> 1) - 1)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t k_desc = smem_desc_sw128(base + L::kK + (n & 1u) * L::kOperand, 1024);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          mma_f16_ss(tmem + (n & 1u) * kTokens, q_desc + (((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4),
+                     k_desc + (((k >> 2) * (kTokens * 128) + (k & 3) * 32) >> 4), idesc_f16_f32(kRows, kTokens), k > 0);
+        tc_commit(s_full + 8 * (n & 1u));
+      }
+      __syncwarp();
+      if (!begins && !second(n - 1)) break;
+      first = begins;
+    }
+  } else if (warp >= kSoft) {
+    // a lane takes 32 channels of one token of the keys, then of the values; the values' pieces are
+    // dealt so that eight lanes read all 32 banks, although a token's line is D / 2 bytes long
+    const int dt = tid - 32 * kSoft;
+    for (uint32_t n = 0;; ++n) {
+      const int st = static_cast<int>(n % S);
+      if (!wait(full + 8 * st, n / S)) break;
+      if (n >= 2 && !wait(s_full + 8 * (n & 1u), (n >> 1) - 1)) break;
+      const uint32_t info = info_of(n);
+      if (info & kEnd) {
+        arrive(k_full + 8 * (n & 1u));
+        break;
+      }
+      const uint8_t* stage = smem + L::kRing + st * kTiles * TILE;
+      uint8_t* keys = smem + L::kK + (n & 1u) * L::kOperand;
+#pragma unroll
+      for (int r = 0; r < D / 64; ++r) {
+        const int x = (dt >> 4) + 8 * r, piece = x % PIECES, slot = dt & 15, tok = (x / PIECES) * kTile + slot;
+        const uint8_t* tile = stage + (x / PIECES) * TILE;
+        expand(*reinterpret_cast<const uint4*>(tile + piece * 256 + slot * 16),
+               *reinterpret_cast<const uint16_t*>(tile + 16 * D + slot * (D / 16) + 2 * piece),
+               keys + (piece >> 1) * (kTokens * 128) + tok * 128, (piece & 1) * 4, tok);
+      }
+      fence_proxy_async_smem();
+      arrive(k_full + 8 * (n & 1u));
+      if (n >= VB && !wait(o_done + 8 * ((n - VB) & 1u), (n - VB) >> 1)) break;
+      uint8_t* values = smem + L::kV + (n % VB) * L::kOperand;
+      const int tok = dt & (kTokens - 1), slot = tok & 15;
+      const uint8_t* tile = stage + (tok >> 4) * TILE;
+      // a token that is none of the sequence's is 0, so that 0 * p is 0
+      const bool real = tok < static_cast<int>(info >> 8 & 0xffu) && !((info >> (tok >> 4)) & 1u);
+#pragma unroll
+      for (int r = 0; r < D / 64; ++r) {
+        const int piece = (tok / (8 / PIECES) + (dt >> 6) * (PIECES / 2) + r) % PIECES;
+        const uint32_t scales = *reinterpret_cast<const uint16_t*>(tile + 17 * D + slot * (D / 16) + 2 * piece);
+        expand(*reinterpret_cast<const uint4*>(tile + 8 * D + slot * (D / 2) + piece * 16), real ? scales : 0u,
+               values + (piece >> 1) * (kTokens * 128) + tok * 128, (piece & 1) * 4, tok);
+      }
+      fence_proxy_async_smem();
+      arrive(v_full + 8 * (n % VB));
+      arrive(taken + 8 * st);
+    }
+  } else {
+    const int r = tid;  // this thread's row of the block, and its lane of tensor memory
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    uint32_t n = 0;
+    bool ok = true;
+    for (int turn = 0; ok; turn ^= 1) {
+      const Walk& cur = s_walk[warp][turn];
+      const Block b = block_of(a, cur);
+      const int len = cur.it.len, first = cur.it.first;
+      const bool mine_ok = r < b.nrows, warp_on = 32 * warp < b.nrows;
+      const int x = b.r0 + min(r, b.nrows - 1), step_row = x / a.group, hq = b.h * a.group + x - step_row * a.group;
+      const int pos = first + step_row;
+      float factor = 1.f;
+      unsigned long long tree = 0;
+      if (b.steps > 0) {
+        // the query row as FP16, brought near 2^10 by a power of two that z's factor takes back; the
+        // sign of the scale goes to the row, so that a larger product is a larger score
+        if (warp_on) {
+          const char* src = static_cast<const char*>(a.q) + 2 * ((cur.it.row0 + step_row) * a.q_row + hq * a.q_head);
+          if (a.tree != nullptr) tree = a.tree[cur.it.row0 + step_row];
+          constexpr int PASS = D / 64, HELD = 8;  // 16-byte words held at a time
+          uint4 v[HELD];
+          float top = 0.f;
+          auto load = [&](int p) {
+#pragma unroll
+            for (int j = 0; j < HELD; ++j)
+              v[j] = mine_ok ? *reinterpret_cast<const uint4*>(src + 16 * (p * HELD + j)) : make_uint4(0, 0, 0, 0);
+          };
+#pragma unroll
+          for (int p = 0; p < PASS; ++p) {
+            load(p);
+#pragma unroll
+            for (int j = 0; j < HELD; ++j) {
+              const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack2(w[e], a.fp16);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+            }
+          }
+          const int e = static_cast<int>(__float_as_uint(top) >> 23);
+          const int shift = e == 0 || e == 255 ? 0 : min(max(137 - e, -100), 100);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23) * (a.scale2 < 0.f ? -1.f : 1.f);
+          // above 0, so that a masked score stays -infinity
+          factor = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - shift) << 23) * fabsf(a.scale2), 1.2e-38f);
+#pragma unroll
+          for (int p = PASS - 1; p >= 0; --p) {
+            if (p < PASS - 1) load(p);
+#pragma unroll
+            for (int j = 0; j < HELD; ++j) {
+              const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+              uint32_t o[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2(w[i], a.fp16);
+                o[i] = half2_bits(f.x * up, f.y * up);
+              }
+              const int c = p * HELD + j;
+              *reinterpret_cast<uint4*>(smem + L::kQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        arrive(q_full);
+      }
+      float m = kLowest, l = 0.f;
+      // tokens that every row of the block sees without a look at the masks: from `open_lo`, before `open_hi`
+      const int open_hi = a.tree != nullptr ? first : min(first + b.r0 / a.group + 1, len);
+      const int open_lo = a.window > 0 ? max(first + (b.r0 + b.nrows - 1) / a.group - a.window + 1, 0) : 0;
+      int tok0 = b.unit * kTokens;
+      for (int i = 0; i < b.steps; ++i, ++n, tok0 += kTokens) {
+        ok = wait(s_full + 8 * (n & 1u), n >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (warp_on) {
+          const uint32_t cols = lanes + (n & 1u) * kTokens;
+          const uint32_t bad = info_of(n) & ((1u << kTiles) - 1u);
+          const bool open = tok0 >= open_lo && tok0 + kTokens <= open_hi && bad == 0;
+          unsigned long long see = ~0ull;  // of the step's tokens
+          if (!open) {
+            see = low_bits(len - tok0);
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u)
+              if ((bad >> u) & 1u) see &= ~(0xffffull << (kTile * u));
+            if (a.tree != nullptr) {
+              const int d = tok0 - first;  // of the step's first token
+              if (d > -64) see &= d <= 0 ? low_bits(-d) | (tree << -d) : d < 64 ? tree >> d : 0ull;
+            } else {
+              see &= low_bits(pos + 1 - tok0);
+              if (a.window > 0 && pos >= a.window) see &= ~low_bits(pos + 1 - a.window - tok0);
+            }
+          }
+          // the scores, 16 tokens at a time, the next 16 under way
+          auto scores = [&](auto use) {
+            uint32_t sv[2][16];
+            tmem_ld_x16(cols, sv[0]);
+            tc_wait_ld();
+#pragma unroll
+            for (int c0 = 0; c0 < kTokens; c0 += 16) {
+              uint32_t(&v)[16] = sv[c0 / 16 & 1];
+              if (c0 + 16 < kTokens) tmem_ld_x16(cols + c0 + 16, sv[c0 / 16 + 1 & 1]);
+              if (!open) {
+                const uint32_t bits = static_cast<uint32_t>(see >> c0);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = (bits >> c) & 1u ? v[c] : 0xff800000u;
+              }
+              use(c0, v);
+              if (c0 + 16 < kTokens) tc_wait_ld();
+            }
+          };
+          float higher = -INFINITY;
+          scores([&](int, const uint32_t (&v)[16]) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) higher = fmaxf(higher, __uint_as_float(v[c]));
+          });
+          higher *= factor;
+          if (__any_sync(0xffffffffu, higher > m + kSlack)) {
+            higher = fmaxf(m, higher);
+            const float worth = exp2_approx(m - higher);
+            m = higher;
+            l *= worth;
+            if (i > 0) {
+              ok = wait(o_done + 8 * ((n - 1) & 1u), (n - 1) >> 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(lanes + L::kColO + c0, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * worth);
+                tmem_store(lanes + L::kColO + c0, o);
+              }
+            }
+          }
+          float s0 = 0.f, s1 = 0.f;
+          scores([&](int c0, const uint32_t (&v)[16]) {
+            uint32_t p[8];
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const float p0 = exp2_approx(fmaf(__uint_as_float(v[c]), factor, -m));
+              const float p1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), factor, -m));
+              s0 += p0;
+              s1 += p1;
+              p[c / 2] = half2_bits(p0, p1);
+            }
+            tmem_store(cols + c0 / 2, p);  // over scores that have been read
+          });
+          l += s0 + s1;
+          tc_wait_st();
+        }
+        tc_fence_before();
+        arrive(p_full + 8 * (n & 1u));
+      }
+      if (!ok) break;
+      if (lane == 0) advance<kRows, kTokens>(steps, cur, s_walk[warp][turn ^ 1], end);
+      __syncwarp();
+      if (b.steps > 0) {
+        ok = wait(o_done + 8 * ((n - 1) & 1u), (n - 1) >> 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool whole = cur.count == cur.it.units;
+      if (warp_on) {
+        float* part = a.part + (2 * static_cast<size_t>(chunk) + (cur.off == 0 ? 1 : 0)) * L::kPart;
+        const int64_t at = static_cast<int64_t>(cur.it.row0 + step_row) * (a.c.heads * a.group) + hq;
+        const bool seen = l > 0.f || l != l;
+        const float f = seen ? a.v_ts / l : 0.f;
+        float* mine = part + ((r >> 3) * KS * 32 + ((r & 7) >> 1)) * 4 + (r & 1);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          if (b.steps > 0) {
+            tmem_ld_x32(lanes + L::kColO + c0, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = 0u;
+          }
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(a.out) + 2 * (at * D + c0));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = seen ? pack2(__uint_as_float(o[8 * j + 2 * e]) * f, __uint_as_float(o[8 * j + 2 * e + 1]) * f, a.fp16) : 0u;
+              if (mine_ok) dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int ch = c0 + c, g = ch / (D / 8), k = ch % (D / 8) / 2;
+              mine[(k * 32 + g * 4) * 4 + 2 * (c & 1)] = __uint_as_float(o[c]);
+            }
+          }
+        }
+        if (!whole) {
+          part[kRows * D + r] = m;
+          part[kRows * D + kRows + r] = l;
+        } else if (mine_ok && a.lse != nullptr) {
+          a.lse[at] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+      }
+      if (tid == 0 && !whole && cur.off == 0) {  // the item goes on in the chunks up to that of its last unit
+        Piece p;
+        p.on = 1;
+        p.last = static_cast<int>((cur.pos + cur.it.units - 1) / per);
+        p.row0 = cur.it.row0; p.r0 = b.r0; p.nrows = b.nrows; p.h = b.h;
+        a.pieces[chunk] = p;
+      }
+      if (!s_walk[warp][turn ^ 1].more) break;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (s_abort != 0 && warp == kIssuer) {  // let the products in flight end before the memory is given up
+    if (elect_one()) tc_commit(drain);
+    __syncwarp();
+    const long long t0 = clock64();
+    while (!phase_done(drain, 0) && clock64() - t0 < kDrainCycles) {
+    }
+  }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, L::kCols);
+}
+
+template <int D, int VB, int S, int CTAS>
+cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
+  typedef WideShape<D, VB, S> L;
+  constexpr int smem = L::kTotal;
+  static_assert(smem <= 227 * 1024 / CTAS - 3072 && CTAS * L::kCols <= 512, "shared memory and tensor memory of an SM");
+  a.page_magic = page_magic(a.c);
+  const int grid = max(1, min(CTAS * num_sms, min(kMaxChunks, static_cast<int>(kPartFloats / 2 / L::kPart))));
+  a.chunks = grid;
+  const cudaError_t e = launch_ready<attend_wide_kernel<D, VB, S, CTAS>>(dim3(grid), dim3(kThreads), smem, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_join<D, kRows / 8, 1, 2 * D>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_wide(const AttendArgs& a, int num_sms, cudaStream_t stream) {
+  return a.c.dim == 64    ? launch<64, 2, 4, 2>(a, num_sms, stream)
+         : a.c.dim == 128 ? launch<128, 1, 3, 2>(a, num_sms, stream)
+                          : launch<256, 1, 3, 1>(a, num_sms, stream);
+}
+
+}  // namespace kv4
+}  // namespace moe

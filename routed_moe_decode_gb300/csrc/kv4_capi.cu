@@ -149,7 +149,7 @@ int moe_kv4_attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_r
   a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16;
   a.scale2 = scale * c->k_scale * 1.44269504088896340736f;
   a.v_ts = c->v_scale;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // as many tokens as there can be; first - window stays an int
   a.tree = reinterpret_cast<const unsigned long long*>(tree);
   a.out = out; a.lse = lse;
   a.part = at<float>(c, L.part);
