@@ -301,31 +301,35 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
     // a lane takes 32 channels of one token of the keys, then of the values; the values' pieces are
     // dealt so that eight lanes read all 32 banks, although a token's line is D / 2 bytes long
     const int dt = tid - 32 * kSoft;
-    for (uint32_t n = 0;; ++n) {
-      const int st = static_cast<int>(n % S);
-      if (!wait(full + 8 * st, n / S)) break;
-      if (n >= 2 && !wait(s_full + 8 * (n & 1u), (n >> 1) - 1)) break;
-      const uint32_t info = info_of(n);
-      if (info & kEnd) {
-        arrive(k_full + 8 * (n & 1u));
-        break;
-      }
-      const uint8_t* stage = smem + L::kRing + st * kTiles * TILE;
-      uint8_t* keys = smem + L::kK + (n & 1u) * L::kOperand;
+    auto stage_of = [&](uint32_t n) { return smem + L::kRing + static_cast<int>(n % S) * kTiles * TILE; };
+    bool ok = true, more = true;
+    auto keys = [&](uint32_t n) {  // of step n; or the end of the work is passed on
+      ok = wait(full + 8 * (n % S), n / S) && (n < 2 || wait(s_full + 8 * (n & 1u), (n >> 1) - 1));
+      if (!ok) return;
+      more = (info_of(n) & kEnd) == 0;
+      if (more) {
+        uint8_t* dst = smem + L::kK + (n & 1u) * L::kOperand;
 #pragma unroll
-      for (int r = 0; r < D / 64; ++r) {
-        const int x = (dt >> 4) + 8 * r, piece = x % PIECES, slot = dt & 15, tok = (x / PIECES) * kTile + slot;
-        const uint8_t* tile = stage + (x / PIECES) * TILE;
-        expand(*reinterpret_cast<const uint4*>(tile + piece * 256 + slot * 16),
-               *reinterpret_cast<const uint16_t*>(tile + 16 * D + slot * (D / 16) + 2 * piece),
-               keys + (piece >> 1) * (kTokens * 128) + tok * 128, (piece & 1) * 4, tok);
+        for (int r = 0; r < D / 64; ++r) {
+          const int x = (dt >> 4) + 8 * r, piece = x % PIECES, slot = dt & 15, tok = (x / PIECES) * kTile + slot;
+          const uint8_t* tile = stage_of(n) + (x / PIECES) * TILE;
+          expand(*reinterpret_cast<const uint4*>(tile + piece * 256 + slot * 16),
+                 *reinterpret_cast<const uint16_t*>(tile + 16 * D + slot * (D / 16) + 2 * piece),
+                 dst + (piece >> 1) * (kTokens * 128) + tok * 128, (piece & 1) * 4, tok);
+        }
+        fence_proxy_async_smem();
       }
-      fence_proxy_async_smem();
       arrive(k_full + 8 * (n & 1u));
+    };
+    keys(0);
+    for (uint32_t n = 0; ok && more; ++n) {  // the keys are a step ahead
+      keys(n + 1);
+      if (!ok) break;
       if (n >= VB && !wait(o_done + 8 * ((n - VB) & 1u), (n - VB) >> 1)) break;
+      const uint32_t info = info_of(n);
       uint8_t* values = smem + L::kV + (n % VB) * L::kOperand;
       const int tok = dt & (kTokens - 1), slot = tok & 15;
-      const uint8_t* tile = stage + (tok >> 4) * TILE;
+      const uint8_t* tile = stage_of(n) + (tok >> 4) * TILE;
       // a token that is none of the sequence's is 0, so that 0 * p is 0
       const bool real = tok < static_cast<int>(info >> 8 & 0xffu) && !((info >> (tok >> 4)) & 1u);
 #pragma unroll
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
       }
       fence_proxy_async_smem();
       arrive(v_full + 8 * (n % VB));
-      arrive(taken + 8 * st);
+      arrive(taken + 8 * (n % S));
     }
   } else {
     const int r = tid;  // this thread's row of the block, and its lane of tensor memory
