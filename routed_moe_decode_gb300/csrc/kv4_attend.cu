@@ -545,7 +545,7 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
   a.chunks = grid * W;
   const cudaError_t e = launch_ready<attend_kernel<D, NT, W, S, CTAS, QS>>(dim3(grid), dim3(32 * W), smem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_join<D, NT, 8, 512>(a, stream);
+  return launch_ready<join_kernel<D, NT>>(dim3((a.chunks + kJoinChunks - 1) / kJoinChunks, NT), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace

@@ -154,30 +154,31 @@ __device__ __forceinline__ void finish(const AttendArgs& a, int row0, int h, int
 }
 
 // Joins the parts of the items that were cut.  CTA (b, n): n-tile n of the items that begin in the
-// chunks [b CHUNKS, + CHUNKS) and go on past them.  A warp takes one m-tile of the output
+// chunks [b kJoinChunks, + kJoinChunks) and go on past them.  A warp takes one m-tile of the output
 // and every GROUPS-th part of the item.  It is all latency, so the sums of a batch of parts are under
 // way before their m and l are here: two trips to memory for up to 16 GROUPS parts.
-template <int D, int NT, int CHUNKS, int THREADS>
-__global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a) {
-  constexpr int ROWS = 8 * NT, KS = D / 16, PART = ROWS * D + 2 * ROWS, GROUPS = THREADS / 32 / KS;
+constexpr int kJoinThreads = 512, kJoinChunks = 8;
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
+  constexpr int ROWS = 8 * NT, KS = D / 16, PART = ROWS * D + 2 * ROWS, GROUPS = kJoinThreads / 32 / KS;
   constexpr int DEEP = 16, BATCH = DEEP * GROUPS;
   __shared__ float s_w[BATCH][8], s_l[BATCH][8];  // m of a batch of parts, then their weights; their l
   __shared__ float s_top[8], s_total[8], s_worth[8];  // of the batches so far
-  __shared__ float4 s_sum[GROUPS > 1 ? THREADS : 1];
+  __shared__ float4 s_sum[kJoinThreads];
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = warp % KS, group = warp / KS, n = blockIdx.y;
   const int q = lane & 3;
   // lane l of every warp looks at the CTA's chunk l
   int4 px = make_int4(0, 0, 0, 0), py = px;
-  if (lane < CHUNKS && blockIdx.x * CHUNKS + lane < a.chunks) {
-    const int4* pp = reinterpret_cast<const int4*>(a.pieces + blockIdx.x * CHUNKS + lane);
+  if (lane < kJoinChunks && blockIdx.x * kJoinChunks + lane < a.chunks) {
+    const int4* pp = reinterpret_cast<const int4*>(a.pieces + blockIdx.x * kJoinChunks + lane);
     px = __ldcg(pp);
     py = __ldcg(pp + 1);
   }
   uint32_t on = __ballot_sync(0xffffffffu, px.x != 0 && 8 * n < py.x);
   for (; on != 0; on &= on - 1) {
-    const int src = __ffs(on) - 1, c0 = blockIdx.x * CHUNKS + src;
+    const int src = __ffs(on) - 1, c0 = blockIdx.x * kJoinChunks + src;
     const int parts = __shfl_sync(0xffffffffu, px.y, src) - c0 + 1, row0 = __shfl_sync(0xffffffffu, px.z, src);
     const int r0 = __shfl_sync(0xffffffffu, px.w, src), nrows = __shfl_sync(0xffffffffu, py.x, src);
     const int h = __shfl_sync(0xffffffffu, py.y, src);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a) {
     }
     for (int cb = 0; cb < parts; cb += BATCH) {
       const int nb = min(BATCH, parts - cb);
-      for (int i = tid; i < 8 * nb; i += THREADS) {
+      for (int i = tid; i < 8 * nb; i += kJoinThreads) {
         const float* p = part_of(cb + (i >> 3)) + ROWS * D + 8 * n + (i & 7);
         s_w[i >> 3][i & 7] = __ldcg(p);
         s_l[i >> 3][i & 7] = __ldcg(p + ROWS);
@@ -201,24 +202,24 @@ __global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a) {
         if (group + j * GROUPS < nb)
           z[j] = __ldcg(reinterpret_cast<const float4*>(part_of(cb + group + j * GROUPS)) + (n * KS + k) * 32 + lane);
       __syncthreads();
-      for (int r = warp; r < 8; r += THREADS / 32) {  // a warp a row
-        const float old = s_top[r];
+      if (warp < 8) {  // a warp a row
+        const float old = s_top[warp];
         float top = old, l = 0.f;
-        for (int c = lane; c < nb; c += 32) top = fmaxf(top, s_w[c][r]);
+        for (int c = lane; c < nb; c += 32) top = fmaxf(top, s_w[c][warp]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         for (int c = lane; c < nb; c += 32) {
-          const float w = exp2_approx(s_w[c][r] - top);
-          s_w[c][r] = w;
-          l += w * s_l[c][r];
+          const float w = exp2_approx(s_w[c][warp] - top);
+          s_w[c][warp] = w;
+          l += w * s_l[c][warp];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         if (lane == 0) {
           const float f = exp2_approx(old - top);
-          s_top[r] = top;
-          s_total[r] = s_total[r] * f + l;
-          s_worth[r] = f;
+          s_top[warp] = top;
+          s_total[warp] = s_total[warp] * f + l;
+          s_worth[warp] = f;
         }
       }
       __syncthreads();
@@ -250,12 +251,6 @@ __global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a) {
     }
     __syncthreads();
   }
-}
-
-template <int D, int NT, int CHUNKS, int THREADS>
-cudaError_t launch_join(const AttendArgs& a, cudaStream_t stream) {
-  static_assert(THREADS % (2 * D) == 0, "a warp takes one m-tile");
-  return launch_ready<join_kernel<D, NT, CHUNKS, THREADS>>(dim3((a.chunks + CHUNKS - 1) / CHUNKS, NT), dim3(THREADS), 0, stream, a);
 }
 
 }  // namespace

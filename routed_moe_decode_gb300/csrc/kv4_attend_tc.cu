@@ -574,7 +574,7 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
   a.chunks = grid;
   const cudaError_t e = launch_ready<attend_tc_kernel<N, G, S, CTAS>>(dim3(grid), dim3(128 * G + 32), smem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_join<D, N / 8, 8, 512>(a, stream);
+  return launch_ready<join_kernel<D, N / 8>>(dim3((a.chunks + kJoinChunks - 1) / kJoinChunks, N / 8), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace

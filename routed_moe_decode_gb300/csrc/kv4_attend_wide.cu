@@ -34,7 +34,8 @@ constexpr uint32_t kFirst = 1u << 16, kEnd = 1u << 17;  // the first of an item;
 constexpr int kInfos = 16;
 
 // Offsets in dynamic shared memory (from a 1024-byte boundary), tensor-memory columns, and the floats
-// of a partial result, which lies as the warp-MMA kernel's does.  VB: buffers of values, S: steps in the ring.
+// of a partial result: [D / 4][128 rows][4] sums, so that a warp's 32 rows are consecutive, then m and l.
+// VB: buffers of values, S: steps in the ring.
 template <int D, int VB, int S>
 struct WideShape {
   static constexpr int kOperand = kTokens * D * 2;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
         if (warp_on) {
           const char* src = static_cast<const char*>(a.q) + 2 * ((cur.it.row0 + step_row) * a.q_row + hq * a.q_head);
           if (a.tree != nullptr) tree = a.tree[cur.it.row0 + step_row];
-          constexpr int PASS = D / 64, HELD = 8;  // 16-byte words held at a time
+          constexpr int PASS = D > 128 ? 2 : 1, HELD = D / 8 / PASS;  // 16-byte words held at a time
           uint4 v[HELD];
           float top = 0.f;
           auto load = [&](int p) {
@@ -437,29 +438,17 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
               if (a.window > 0 && pos >= a.window) see &= ~low_bits(pos + 1 - a.window - tok0);
             }
           }
-          // the scores, 16 tokens at a time, the next 16 under way
-          auto scores = [&](auto use) {
-            uint32_t sv[2][16];
-            tmem_ld_x16(cols, sv[0]);
-            tc_wait_ld();
+          uint32_t v[2][32];
+          tmem_ld_x32(cols, v[0]);
+          tmem_ld_x32(cols + 32, v[1]);
+          tc_wait_ld();
+          if (!open) {
 #pragma unroll
-            for (int c0 = 0; c0 < kTokens; c0 += 16) {
-              uint32_t(&v)[16] = sv[c0 / 16 & 1];
-              if (c0 + 16 < kTokens) tmem_ld_x16(cols + c0 + 16, sv[c0 / 16 + 1 & 1]);
-              if (!open) {
-                const uint32_t bits = static_cast<uint32_t>(see >> c0);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) v[c] = (bits >> c) & 1u ? v[c] : 0xff800000u;
-              }
-              use(c0, v);
-              if (c0 + 16 < kTokens) tc_wait_ld();
-            }
-          };
+            for (int c = 0; c < kTokens; ++c) v[c >> 5][c & 31] = (see >> c) & 1u ? v[c >> 5][c & 31] : 0xff800000u;
+          }
           float higher = -INFINITY;
-          scores([&](int, const uint32_t (&v)[16]) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) higher = fmaxf(higher, __uint_as_float(v[c]));
-          });
+          for (int c = 0; c < kTokens; ++c) higher = fmaxf(higher, __uint_as_float(v[c >> 5][c & 31]));
           higher *= factor;
           if (__any_sync(0xffffffffu, higher > m + kSlack)) {
             higher = fmaxf(m, higher);
@@ -482,18 +471,19 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
             }
           }
           float s0 = 0.f, s1 = 0.f;
-          scores([&](int c0, const uint32_t (&v)[16]) {
-            uint32_t p[8];
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              const float p0 = exp2_approx(fmaf(__uint_as_float(v[c]), factor, -m));
-              const float p1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), factor, -m));
+          for (int c0 = 0; c0 < kTokens; c0 += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float p0 = exp2_approx(fmaf(__uint_as_float(v[c0 >> 5][c]), factor, -m));
+              const float p1 = exp2_approx(fmaf(__uint_as_float(v[c0 >> 5][c + 1]), factor, -m));
               s0 += p0;
               s1 += p1;
               p[c / 2] = half2_bits(p0, p1);
             }
             tmem_store(cols + c0 / 2, p);  // over scores that have been read
-          });
+          }
           l += s0 + s1;
           tc_wait_st();
         }
@@ -514,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
         const int64_t at = static_cast<int64_t>(cur.it.row0 + step_row) * (a.c.heads * a.group) + hq;
         const bool seen = l > 0.f || l != l;
         const float f = seen ? a.v_ts / l : 0.f;
-        float* mine = part + ((r >> 3) * KS * 32 + ((r & 7) >> 1)) * 4 + (r & 1);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
@@ -537,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int ch = c0 + c, g = ch / (D / 8), k = ch % (D / 8) / 2;
-              mine[(k * 32 + g * 4) * 4 + 2 * (c & 1)] = __uint_as_float(o[c]);
-            }
+            for (int j = 0; j < 8; ++j)
+              reinterpret_cast<float4*>(part)[(c0 / 4 + j) * kRows + r] =
+                  make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+                              __uint_as_float(o[4 * j + 3]));
           }
         }
         if (!whole) {
@@ -575,6 +564,73 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
   if (warp == 0) tmem_dealloc(tmem, L::kCols);
 }
 
+// Joins the parts of the items that were cut.  CTA (c, g, y): the item that begins in chunk c and goes on
+// past it, 32 of its rows, a lane a row, and 64 channels, 8 a warp; kBatch parts' trips to memory at a time.
+constexpr int kBatch = 4;
+template <int D>
+__global__ void __launch_bounds__(256) join_wide_kernel(AttendArgs a) {
+  constexpr int PART = kRows * D + 2 * kRows;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = 32 * blockIdx.y + lane;
+  const int4* pp = reinterpret_cast<const int4*>(a.pieces + blockIdx.x);
+  const int4 px = __ldcg(pp), py = __ldcg(pp + 1);
+  if (px.x == 0 || 32 * static_cast<int>(blockIdx.y) >= py.x) return;
+  const int c0 = blockIdx.x, parts = px.y - c0 + 1, quad = blockIdx.z * 16 + 2 * warp;
+  // of the chunk c0 + c: the first chunk's part starts at the item's first unit
+  auto part_of = [&](int c) { return a.part + (2 * static_cast<size_t>(c0 + c) + (c == 0 ? 1 : 0)) * PART; };
+  float m = kLowest, l = 0.f, v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  for (int cb = 0; cb < parts; cb += kBatch) {
+    float pm[kBatch], pl[kBatch];
+    float4 z[kBatch][2];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      pm[j] = kLowest;
+      pl[j] = 0.f;
+      z[j][0] = z[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (cb + j < parts) {
+        const float* part = part_of(cb + j);
+        pm[j] = __ldcg(part + kRows * D + r);
+        pl[j] = __ldcg(part + kRows * D + kRows + r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) z[j][i] = __ldcg(reinterpret_cast<const float4*>(part) + (quad + i) * kRows + r);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) top = fmaxf(top, pm[j]);
+    const float f = exp2_approx(m - top);
+    m = top;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float w = exp2_approx(pm[j] - top);
+      l += w * pl[j];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[4 * i] += w * z[j][i].x;
+        v[4 * i + 1] += w * z[j][i].y;
+        v[4 * i + 2] += w * z[j][i].z;
+        v[4 * i + 3] += w * z[j][i].w;
+      }
+    }
+  }
+  if (r >= py.x) return;
+  const int x = px.w + r, step_row = x / a.group, hq = py.y * a.group + x - step_row * a.group;
+  const int64_t at = static_cast<int64_t>(px.z + step_row) * (a.c.heads * a.group) + hq;
+  const bool seen = l > 0.f || l != l;
+  const float f = seen ? a.v_ts / l : 0.f;
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = seen ? pack2(v[2 * e] * f, v[2 * e + 1] * f, a.fp16) : 0u;
+  *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + 2 * (at * D + 4 * quad)) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (quad == 0 && a.lse != nullptr) a.lse[at] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
 template <int D, int VB, int S, int CTAS>
 cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
   typedef WideShape<D, VB, S> L;
@@ -585,7 +641,7 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
   a.chunks = grid;
   const cudaError_t e = launch_ready<attend_wide_kernel<D, VB, S, CTAS>>(dim3(grid), dim3(kThreads), smem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_join<D, kRows / 8, 1, 2 * D>(a, stream);
+  return launch_ready<join_wide_kernel<D>>(dim3(grid, kRows / 32, D / 64), dim3(256), 0, stream, a);
 }
 
 }  // namespace
