@@ -438,17 +438,27 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
               if (a.window > 0 && pos >= a.window) see &= ~low_bits(pos + 1 - a.window - tok0);
             }
           }
-          uint32_t v[2][32];
-          tmem_ld_x32(cols, v[0]);
-          tmem_ld_x32(cols + 32, v[1]);
-          tc_wait_ld();
-          if (!open) {
+          // the scores are read twice, 16 at a time, in short loops: the warps of an SM sub-partition run the
+          // code of four roles and fetch it through one small cache (64 at a time in registers, unrolled:
+          // 5 to 7 % slower)
+          constexpr int CH = 16;
+          auto scores = [&](int c0, uint32_t (&v)[CH]) {
+            tmem_ld_x16(cols + c0, v);
+            tc_wait_ld();
+            if (!open) {
+              const uint32_t bits = static_cast<uint32_t>(see >> c0);
 #pragma unroll
-            for (int c = 0; c < kTokens; ++c) v[c >> 5][c & 31] = (see >> c) & 1u ? v[c >> 5][c & 31] : 0xff800000u;
-          }
+              for (int c = 0; c < CH; ++c) v[c] = (bits >> c) & 1u ? v[c] : 0xff800000u;
+            }
+          };
           float higher = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kTokens; c0 += CH) {
+            uint32_t v[CH];
+            scores(c0, v);
 #pragma unroll
-          for (int c = 0; c < kTokens; ++c) higher = fmaxf(higher, __uint_as_float(v[c >> 5][c & 31]));
+            for (int c = 0; c < CH; ++c) higher = fmaxf(higher, __uint_as_float(v[c]));
+          }
           higher *= factor;
           if (__any_sync(0xffffffffu, higher > m + kSlack)) {
             higher = fmaxf(m, higher);
@@ -471,13 +481,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
             }
           }
           float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kTokens; c0 += CH) {
+            uint32_t v[CH], p[CH / 2];
+            scores(c0, v);
 #pragma unroll
-          for (int c0 = 0; c0 < kTokens; c0 += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float p0 = exp2_approx(fmaf(__uint_as_float(v[c0 >> 5][c]), factor, -m));
-              const float p1 = exp2_approx(fmaf(__uint_as_float(v[c0 >> 5][c + 1]), factor, -m));
+            for (int c = 0; c < CH; c += 2) {
+              const float p0 = exp2_approx(fmaf(__uint_as_float(v[c]), factor, -m));
+              const float p1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), factor, -m));
               s0 += p0;
               s1 += p1;
               p[c / 2] = half2_bits(p0, p1);
