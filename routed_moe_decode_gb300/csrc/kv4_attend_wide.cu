@@ -18,8 +18,15 @@
 //
 // A block reads no step that none of its rows sees; blocks are walked from both ends of the rows inwards,
 // so that neighbouring items of a causal chunk are about equally long together.
+//
+// A step takes a CTA ~2000 (head size 64) to ~2600 cycles (128), two CTAs an SM.  Most of it is the chain
+// scores -> maximum -> p of one warp; at 128 the operands' traffic through shared memory (105 KB a step, of
+// which the query rows are 32) comes to two thirds of it.  Measured: 24 sequences of up to 6001 tokens, 112 rows, 4 K/V heads
+// of 64: 42 us (79 with the warp-MMA kernel); a chunk of 2048 rows with 4 query heads a K/V head over 4096
+// tokens, 8 heads of 128: 151 us (692); 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 68 us (110).
+// Two threads a row (eight warps for p) and eight warps that dequantise were both slower (51 and 42 against 42, 175 and
+// 160 against 151 us): what the warps of an SM share is the fetching of their code.
 #include "kv4_attend.cuh"
-#include "kv4_tc.cuh"
 
 namespace moe {
 namespace kv4 {
@@ -32,6 +39,50 @@ constexpr uint32_t kBIsMn = 1u << 16;  // instruction descriptor: B's rows are c
 // what the loader says of a step: tiles without a page, tokens of the sequence, and
 constexpr uint32_t kFirst = 1u << 16, kEnd = 1u << 17;  // the first of an item; no step, the end of the work
 constexpr int kInfos = 16;
+
+// D[tmem] (+)= A[smem] B[smem]^T, FP16 inputs, FP32 sums.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of an operand whose rows (the M or N index) are consecutive in memory: 128-byte lines of 64
+// rows for one k, swizzled like smem_desc_sw128, 1024 bytes from 8 k to the next 8, `next` bytes
+// from 64 rows to the next 64.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t next) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t((next >> 4) & 0x3FFFu) << 16 | uint64_t(1024u >> 4) << 32 |
+         uint64_t(1u) << 46 | uint64_t(2u) << 61;
+}
+
+// Whether a barrier's phase is complete.
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// 32 lanes x 32 bits, 8 or 16 consecutive columns, written.
+__device__ __forceinline__ void tmem_store(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t t, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 
 // Offsets in dynamic shared memory (from a 1024-byte boundary), tensor-memory columns, and the floats
 // of a partial result: [D / 4][128 rows][4] sums, so that a warp's 32 rows are consecutive, then m and l.
@@ -94,7 +145,7 @@ __device__ __forceinline__ void expand(const uint4& codes, uint32_t scales, uint
 template <int D, int VB, int S, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs a) {
   typedef WideShape<D, VB, S> L;
-  constexpr int KS = D / 16, TILE = 18 * D, PIECES = D / 32;
+  constexpr int TILE = 18 * D, PIECES = D / 32;
   static_assert(S + VB + 4 <= kInfos, "steps whose description is alive");
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long s_scan[kWarps];
@@ -289,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
       if (elect_one()) {
         const uint64_t k_desc = smem_desc_sw128(base + L::kK + (n & 1u) * L::kOperand, 1024);
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < D / 16; ++k)
           mma_f16_ss(tmem + (n & 1u) * kTokens, q_desc + (((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4),
                      k_desc + (((k >> 2) * (kTokens * 128) + (k & 3) * 32) >> 4), idesc_f16_f32(kRows, kTokens), k > 0);
         tc_commit(s_full + 8 * (n & 1u));

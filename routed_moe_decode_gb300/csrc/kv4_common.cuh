@@ -146,7 +146,6 @@ struct PageArgs {
 cudaError_t launch_append(const RowArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_read(const RowArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream);
-cudaError_t launch_attend_tc(const AttendArgs& a, int block_rows, int num_sms, cudaStream_t stream);
 cudaError_t launch_attend_wide(const AttendArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_reserve(const PageArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_fork(const PageArgs& a, cudaStream_t stream);

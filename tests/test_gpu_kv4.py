@@ -229,6 +229,86 @@ def test_attend_on_another_stream_and_in_a_graph(moe):
     assert torch.equal(out, want)
 
 
+# Blocks of many rows (a step's rows times query heads per K/V head).
+
+@pytest.mark.parametrize("D,group,dtype", [(64, 4, "bf16"), (64, 7, "fp16"), (128, 4, "fp16"), (128, 1, "bf16"), (256, 3, "bf16")])
+@pytest.mark.parametrize("window", [0, 1, 70, 2 ** 31 - 1])
+def test_attend_chunks_of_a_prompt(moe, D, group, dtype, window):
+    # several blocks a head, blocks that end inside 64 tokens, steps that a block does not see, a short step beside them
+    check_attend(moe, [700, 150, 0, 1203, 64], [150, 150, 0, 40, 1], heads=2, group=group, D=D, page=48, dtype=dtype,
+                 window=window, seed=window % 97 + D)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_many_rows_that_see_nothing(moe, D):
+    # more rows than tokens, an empty sequence, tree rows without a bit
+    check_attend(moe, [30, 0, 5], [90, 41, 44], heads=1, group=3, D=D, page=16)
+    check_attend(moe, [30, 0, 5], [90, 41, 44], heads=1, group=3, D=D, page=16, window=4)
+    trees = np.zeros(100, dtype=np.int64)
+    trees[[3, 63, 70]] = 5
+    check_attend(moe, [64, 36], [64, 36], heads=2, group=2, D=D, page=32, trees=trees)
+
+
+@pytest.mark.parametrize("D,group", [(64, 7), (128, 5), (256, 9)])
+def test_attend_trees_of_many_heads(moe, D, group):
+    rng = np.random.default_rng(D)
+    rows, lens = [16, 64, 5], [3000, 64, 191]
+    trees = [(int(rng.integers(0, 2 ** 62)) & ((1 << (i + 1)) - 1)) | (1 << i) for n in rows for i in range(n)]
+    trees = [t - 2 ** 64 if t >> 63 else t for t in trees]
+    check_attend(moe, lens, rows, heads=2, group=group, D=D, page=16, dtype="fp16", trees=np.array(trees, dtype=np.int64))
+
+
+def test_attend_many_rows_scores_and_strides(moe):
+    for D in (64, 128, 256):
+        check_attend(moe, [900], [12], heads=1, group=6, D=D, page=64, q_std=60.0)  # references that rise on the way
+        check_attend(moe, [300], [12], heads=1, group=6, D=D, page=64, q_std=1e-20)
+        check_attend(moe, [150, 190], [30, 24], heads=2, group=4, D=D, page=32, strided=True, layers=3, layer=2, k_scale=0.37,
+                     v_scale=12.5, scale=-0.21, seed=9)
+
+
+def test_attend_many_rows_of_many_sequences(moe):
+    rng = np.random.default_rng(0)
+    rows = rng.integers(0, 4, 300)
+    check_attend(moe, rows + rng.integers(0, 90, 300), rows, heads=1, group=16, D=128, page=16, max_rows=3)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_many_rows_same_bits_and_rows_apart(moe, D):
+    cache, *_ = make_cache(moe, [5000, 30, 2000], 2, D, 64, seed=4)
+    q = torch.randn((50, 16, D), device="cuda").to(torch.bfloat16)
+    cu = dev([0, 20, 40, 50])
+    first = cache.attend(0, q, cu, max_rows=20)
+    for _ in range(20):
+        assert torch.equal(first, cache.attend(0, q, cu, max_rows=20))
+    # a row of NaN and one of infinities spoil no other
+    q[3, 5] = float("nan")
+    q[45, 0] = float("inf")
+    other = cache.attend(0, q, cu, max_rows=20)
+    spoiled = torch.zeros((50, 16), dtype=torch.bool, device="cuda")
+    spoiled[3, 5] = spoiled[45, 0] = True
+    assert torch.equal(first[~spoiled], other[~spoiled]) and not torch.isfinite(other[3, 5].float()).any()
+    assert cache.status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_many_rows_bad_page_and_stale_tokens(moe, D):
+    lens, page = [300, 100], 32
+    cache, pool, table, _, _ = make_cache(moe, lens, 2, D, page, seed=6)
+    q = torch.randn((60, 16, D), device="cuda").to(torch.bfloat16)
+    cu = dev([0, 30, 60])
+    want = cache.attend(0, q, cu, max_rows=30)
+    # the unused end of a sequence's last page holds NaN scales: no difference
+    tile = 18 * D
+    last = int(table[1, 3])
+    cache.pool.view(1, -1, 2, page // 16, tile)[0, last, :, 1, 16 * D:] = 0xff
+    cache.pool.view(1, -1, 2, page // 16, tile)[0, last, :, 0, 16 * D:].view(2, 2, 16, D // 16)[:, :, 4:] = 0xff
+    assert torch.equal(want, cache.attend(0, q, cu, max_rows=30))
+    cache.table[0, 2] = 10 ** 6
+    out = cache.attend(0, q, cu, max_rows=30)
+    assert torch.isfinite(out.float()).all() and torch.equal(out[30:], want[30:])
+    assert cache.status() == moe.KV4_BAD_PAGE and cache.status() == 0
+
+
 # ---- append and read ----
 
 @pytest.mark.parametrize("D", [64, 128, 256])
