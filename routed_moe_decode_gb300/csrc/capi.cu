@@ -307,6 +307,7 @@ int moe_route_grouped(const moe_routing* r, int T, const void* logits, int64_t r
   a.T = T; a.E = r->E; a.k = r->k; a.groups = r->groups; a.keep_groups = r->keep_groups; a.dtype = dtype;
   a.softmax = r->softmax != 0; a.top2 = r->top2 != 0; a.renormalise = r->renormalise != 0;
   a.vec = aligned(logits, 16) && (row_stride * size) % 16 == 0;
+  a.vec_bias = aligned(bias, 16);
   a.scale = r->scale;
   const cudaError_t e = moe::launch_route_grouped(a, stream);
   if (e != cudaSuccess) { set_error("grouped router launch", e); return MOE_ERR_CUDA; }

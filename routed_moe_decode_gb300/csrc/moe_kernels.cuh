@@ -349,7 +349,8 @@ struct RouteGroupedArgs {
   int32_t* ids;
   float* weights;
   int T, E, k, groups, keep_groups, dtype;
-  bool softmax, top2, renormalise, vec;
+  bool softmax, top2, renormalise;
+  bool vec, vec_bias;  // 16-byte loads of the logits, of the bias
   float scale;
 };
 cudaError_t launch_route_grouped(const RouteGroupedArgs& a, cudaStream_t stream);

@@ -118,8 +118,19 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(RouteGrouped
   }
   float bias[NPL];
   if (a.bias != nullptr) {
+    if (NPL % 4 == 0 && a.vec_bias && nvalid == NPL) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) bias[i] = i < nvalid ? a.bias[base + i] : 0.f;
+      for (int j = 0; j < NPL / 4; ++j) {
+        const float4 w = reinterpret_cast<const float4*>(a.bias + base)[j];
+        bias[4 * j] = w.x;
+        bias[4 * j + 1] = w.y;
+        bias[4 * j + 2] = w.z;
+        bias[4 * j + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) bias[i] = i < nvalid ? a.bias[base + i] : 0.f;
+    }
   }
   float mx = 0.f, sum = 1.f;  // of the softmax
   if (a.softmax) {
