@@ -101,6 +101,7 @@ int moe_kv4_append(const moe_kv4_cache* c, int layer, const void* k, int64_t k_r
   if (static_cast<int64_t>(rows) * c->kv_heads * c->head_dim > (1ll << 36)) return MOE_ERR_UNSUPPORTED;
   a.k = k; a.v = v; a.k_row = k_row_stride; a.k_head = k_head_stride; a.v_row = v_row_stride; a.v_head = v_head_stride;
   a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16; a.k_ts = c->k_scale; a.v_ts = c->v_scale;
+  a.wide = aligned(k, 32) && aligned(v, 32) && (k_row_stride | k_head_stride | v_row_stride | v_head_stride) % 16 == 0;
   int sms = 0;
   const int src = moe::device_sms(&sms);
   if (src != MOE_OK) return src;
@@ -119,6 +120,7 @@ int moe_kv4_read(const moe_kv4_cache* c, int layer, void* k, void* v, int dtype,
   if (static_cast<int64_t>(rows) * c->kv_heads * c->head_dim > (1ll << 36)) return MOE_ERR_UNSUPPORTED;
   a.k_out = k; a.v_out = v;
   a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16; a.k_ts = c->k_scale; a.v_ts = c->v_scale;
+  a.wide = aligned(k, 32) && aligned(v, 32);
   int sms = 0;
   const int src = moe::device_sms(&sms);
   if (src != MOE_OK) return src;

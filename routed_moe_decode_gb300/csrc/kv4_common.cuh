@@ -97,6 +97,23 @@ MOE_DEVICE uint32_t pack2(float a, float b, bool fp16) {
   return o;
 }
 
+// 32 bytes in one access (a whole sector).
+struct alignas(32) Line {
+  uint32_t w[8];
+};
+MOE_DEVICE Line load_line(const uint8_t* p) {
+  Line l;
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(l.w[0]), "=r"(l.w[1]), "=r"(l.w[2]), "=r"(l.w[3]), "=r"(l.w[4]), "=r"(l.w[5]), "=r"(l.w[6]), "=r"(l.w[7])
+               : "l"(p));
+  return l;
+}
+MOE_DEVICE void store_line(uint8_t* p, const Line& l) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(l.w[0]), "r"(l.w[1]), "r"(l.w[2]),
+               "r"(l.w[3]), "r"(l.w[4]), "r"(l.w[5]), "r"(l.w[6]), "r"(l.w[7])
+               : "memory");
+}
+
 struct RowArgs {
   Cache c;
   const void* k;
@@ -108,6 +125,7 @@ struct RowArgs {
   int rows;
   int rows_per_cta;  // set by the launcher
   bool fp16;
+  bool wide;  // the rows' 32-byte pieces are aligned to 32 bytes
   float k_ts, v_ts;
 };
 

@@ -193,22 +193,6 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
 constexpr int kCopyThreads = 256, kCopyLoads = 4;
 constexpr int kCopyBytes = 32 * kCopyThreads * kCopyLoads;
 
-struct alignas(32) Line {
-  uint32_t w[8];
-};
-__device__ __forceinline__ Line load_line(const uint8_t* p) {
-  Line l;
-  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(l.w[0]), "=r"(l.w[1]), "=r"(l.w[2]), "=r"(l.w[3]), "=r"(l.w[4]), "=r"(l.w[5]), "=r"(l.w[6]), "=r"(l.w[7])
-               : "l"(p));
-  return l;
-}
-__device__ __forceinline__ void store_line(uint8_t* p, const Line& l) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(l.w[0]), "r"(l.w[1]), "r"(l.w[2]),
-               "r"(l.w[3]), "r"(l.w[4]), "r"(l.w[5]), "r"(l.w[6]), "r"(l.w[7])
-               : "memory");
-}
-
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PageArgs a) {
   pdl_wait();
   pdl_launch_dependents();

@@ -167,7 +167,7 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], bool fp16, flo
 }
 
 struct Piece32 {
-  uint4 v[4];
+  Line v[2];  // two blocks
 };
 
 template <int D>
@@ -182,8 +182,13 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(RowArgs a
     const int64_t row = row0 + u.row;
     const int64_t off = u.is_v ? row * a.v_row + u.head * a.v_head : row * a.k_row + u.head * a.k_head;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(u.is_v ? a.v : a.k) + 2 * (off + u.piece * 32));
+    if (a.wide) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x.v[k] = src[k];
+      for (int k = 0; k < 2; ++k) x.v[k] = load_line(reinterpret_cast<const uint8_t*>(src) + 32 * k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(x.v)[k] = src[k];
+    }
   };
   Piece32 x, next;
   unsigned j = threadIdx.x;
@@ -195,10 +200,8 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(RowArgs a
     const RowPlace p = s_place[u.row];
     if (p.tile != nullptr) {
       const float ts = u.is_v ? a.v_ts : a.k_ts;
-      const uint32_t w0[8] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w, x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w};
-      const uint32_t w1[8] = {x.v[2].x, x.v[2].y, x.v[2].z, x.v[2].w, x.v[3].x, x.v[3].y, x.v[3].z, x.v[3].w};
       uint32_t s0, s1;
-      const uint2 c0 = quantise(w0, a.fp16, ts, s0, a.c.status), c1 = quantise(w1, a.fp16, ts, s1, a.c.status);
+      const uint2 c0 = quantise(x.v[0].w, a.fp16, ts, s0, a.c.status), c1 = quantise(x.v[1].w, a.fp16, ts, s1, a.c.status);
       uint8_t* tile = u.tile(a.c, p);
       *u.codes(tile, p.slot) = make_uint4(c0.x, c0.y, c1.x, c1.y);
       *u.scales(tile, p.slot) = static_cast<uint16_t>(s0 | (s1 << 8));
@@ -231,18 +234,27 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) read_kernel(RowArgs a) {
     const float ts = u.is_v ? a.v_ts : a.k_ts;
     const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
     const int64_t row = row0 + u.row;
-    uint4* q = reinterpret_cast<uint4*>(dst + 2 * ((row * a.c.heads + u.head) * D + u.piece * 32));
+    uint8_t* q = reinterpret_cast<uint8_t*>(dst) + 2 * ((row * a.c.heads + u.head) * D + u.piece * 32);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float f = e4m3_float(k < 2 ? sb & 0xffu : sb >> 8) * ts;
-      uint32_t h[4], o[4];
-      e2m1x8_to_f16x2x4(c[k], h[0], h[1], h[2], h[3]);
+    for (int block = 0; block < 2; ++block) {
+      const float f = e4m3_float(block == 0 ? sb & 0xffu : sb >> 8) * ts;
+      Line o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack2(h[i], true);
-        o[i] = pack2(v.x * f, v.y * f, a.fp16);
+      for (int k = 0; k < 2; ++k) {
+        uint32_t h[4];
+        e2m1x8_to_f16x2x4(c[2 * block + k], h[0], h[1], h[2], h[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = unpack2(h[i], true);
+          o.w[4 * k + i] = pack2(v.x * f, v.y * f, a.fp16);
+        }
       }
-      q[k] = make_uint4(o[0], o[1], o[2], o[3]);
+      if (a.wide) {
+        store_line(q + 32 * block, o);
+      } else {
+        reinterpret_cast<uint4*>(q)[2 * block] = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+        reinterpret_cast<uint4*>(q)[2 * block + 1] = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
+      }
     }
   }
 }
