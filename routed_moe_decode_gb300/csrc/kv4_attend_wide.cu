@@ -84,6 +84,23 @@ __device__ __forceinline__ void tmem_store(uint32_t t, const uint32_t (&v)[16]) 
       : "memory");
 }
 
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return d;
+}
+
 // Offsets in dynamic shared memory (from a 1024-byte boundary), tensor-memory columns, and the floats
 // of a partial result: [D / 4][128 rows][4] sums, so that a warp's 32 rows are consecutive, then m and l.
 // VB: buffers of values, S: steps in the ring.
@@ -531,22 +548,22 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
               }
             }
           }
-          float s0 = 0.f, s1 = 0.f;
+          float2 sum = make_float2(0.f, 0.f);
+          const float2 factor2 = make_float2(factor, factor), minus_m = make_float2(-m, -m);
 #pragma unroll 1
           for (int c0 = 0; c0 < kTokens; c0 += CH) {
             uint32_t v[CH], p[CH / 2];
             scores(c0, v);
 #pragma unroll
             for (int c = 0; c < CH; c += 2) {
-              const float p0 = exp2_approx(fmaf(__uint_as_float(v[c]), factor, -m));
-              const float p1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), factor, -m));
-              s0 += p0;
-              s1 += p1;
-              p[c / 2] = half2_bits(p0, p1);
+              const float2 z = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), factor2, minus_m);
+              const float2 e = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+              sum = add2(sum, e);
+              p[c / 2] = half2_bits(e.x, e.y);
             }
             tmem_store(cols + c0 / 2, p);  // over scores that have been read
           }
-          l += s0 + s1;
+          l += sum.x + sum.y;
           tc_wait_st();
         }
         tc_fence_before();
