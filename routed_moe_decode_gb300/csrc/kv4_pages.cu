@@ -7,6 +7,10 @@
 // sequence that needs one), and reads the counts 4096 pages a round until it has enough.  The
 // data moves (copy on write, compaction) are separate grids over every layer and are bound by
 // the bytes they read and write.
+//
+// Measured: forking 16 prompts into 128 branches and reserving for them on 48 layers (906 MB copied, the 16 sources
+// from L2) 125 us; one prompt into 4 on 12 layers 11 us, bound by three launches; compaction of 64 steps on 48 layers with the calls
+// around it (23 MB in 16-byte pieces) 28 us.
 #include "kv4_common.cuh"
 
 namespace moe {
