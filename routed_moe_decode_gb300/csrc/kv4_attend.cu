@@ -556,9 +556,9 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 // Blocks of up to 128 rows from 17 rows on at head size 128, and from 33 on at 64 and 256; measured on 32 sequences
-// of 4096 to 8192 tokens and 8 (at 256: 2) K/V heads, wide against warp-MMA: 32 rows of 128 116 against 123 us, 16 rows
-// 116 against 73; 32 rows of 64 95 against 82; 32 rows of 256 72 against 60; on 16 such sequences 64 rows of
-// 128 68 against 110.
+// of 4096 to 8192 tokens and 8 (at 256: 2) K/V heads, wide against warp-MMA: 32 rows of 128 115 against 118 us, 16 rows
+// 115 against 73; 32 rows of 64 95 against 82, 16 rows 94 against 58; 32 rows of 256 72 against 60; on 16 such
+// sequences 64 rows of 128 68 against 105.
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream) {
   if (row_tile > (a.c.dim == 128 ? 16 : 32)) return launch_attend_wide(a, num_sms, stream);
   switch (a.c.dim) {

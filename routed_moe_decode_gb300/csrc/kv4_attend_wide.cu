@@ -22,9 +22,9 @@
 // A step takes a CTA ~2000 (head size 64) to ~2500 cycles (128), two CTAs an SM.  At 128 the operands' traffic through
 // shared memory (105 KB a step, of which the query rows are 32) comes to two thirds of that; otherwise what
 // the warps share is the issue and fetching of four roles' code (18.7 M instructions for the trees below, issue
-// slots 41 to 50 % busy).  Measured: 24 sequences of up to 6001 tokens, 112 rows, 4 K/V heads of 64: 41 us (79 with the
-// warp-MMA kernel); a chunk of 2048 rows with 4 query heads a K/V head over 4096 tokens, 8 heads of 128: 148 us (692),
-// 0.7 PFLOP/s of unmasked products; 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 68 us (110).  More warps
+// slots 41 to 50 % busy).  Measured: 24 sequences of up to 6001 tokens, 112 rows, 4 K/V heads of 64: 41 us (78 with the
+// warp-MMA kernel); a chunk of 2048 rows with 4 query heads a K/V head over 4096 tokens, 8 heads of 128: 148 us (657),
+// 0.7 PFLOP/s of unmasked products; 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 68 us (105).  More warps
 // were slower: two threads a row 51 and 175, two groups of them on alternate steps 47 and 167, eight warps that
 // dequantise 42 and 160 (against 42 and 151 at the time).
 #include "kv4_attend.cuh"
