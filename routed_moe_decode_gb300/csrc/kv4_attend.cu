@@ -28,7 +28,7 @@
 // in the order of the chunks, so results do not depend on timing.  The chunks are found on the device
 // from the lengths: no host wait, no plan.
 //
-// Measured: four sequences of 131072 tokens, 8 K/V heads of 128 with 8 query heads each (604 MB) 116 us, 0.77 of the
+// Measured: four sequences of 131072 tokens, 8 K/V heads of 128 with 8 query heads each (604 MB) 114 us, 0.78 of the
 // copy bandwidth; 32 sequences of 4096 to 8192 tokens, 16 rows (228 MB) 73 us, of which joining is ~8.  Bound by
 // the conversions, multiplies and MMAs of an SM sub-partition, which add up instead of overlapping (at 8
 // rows the ALU pipe is 51 % busy, at 16 rows 42 % and the MMA pipe 36 %; 8 warps run as fast as 12).
@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   __shared__ long long s_scan[W];
   __shared__ long long s_before[kThreads];
   __shared__ Walk s_walk[W][2];  // this part, the next
+  __shared__ Chunk s_chunk[W];   // of the warp: lane 0's, out of the registers
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const uint8_t* ring = smem + L::kRing + warp * S * UNIT;
   uint4* queries = reinterpret_cast<uint4*>(smem + L::kQuery) + warp * (QS ? NT * (D / 32) * 32 : 0);
@@ -156,36 +157,42 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   // the work, cut into one chunk of `per` units per warp of the grid: this one's is [begin, end).
   // Neighbouring chunks go to different SMs, so that a few units keep as many SMs busy.
   const bool cached = a.c.seqs <= kSeqCache;
-  if (cached) {
-    for (int s = tid; s <= a.c.seqs; s += kThreads) {
-      s_cu[s] = ld(a.cu + s);
-      if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
-    }
-    __syncthreads();
-  }
   const Steps steps{a, cached ? s_cu : nullptr, cached ? s_len : nullptr};
-  const int per_thread = (a.c.seqs + kThreads - 1) / kThreads;
-  const int sa = min(tid * per_thread, a.c.seqs), sb = min(sa + per_thread, a.c.seqs);
-  long long mine = 0;
-  for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS, kUnit>(steps, s));
-  long long total;
-  const long long before = block_prefix<W>(mine, s_scan, total);
   const int chunk = warp * gridDim.x + blockIdx.x;
-  const long long per = (total + a.chunks - 1) / a.chunks;
-  const long long begin = per * chunk, end = min(begin + per, total);
   if (lane == 0) a.pieces[chunk].on = 0;
-  s_before[tid] = before;
-  __syncthreads();
-  if (begin >= end) return;
-  if (lane == 0) {
-    int lo = 0, hi = kThreads - 1;  // the last thread whose sequences begin at or before `begin`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_before[mid] <= begin) lo = mid; else hi = mid - 1;
+  Chunk c;
+  if (a.c.seqs <= 32) {
+    if (!settle_warp<ROWS, kUnit>(a, s_cu, s_len, chunk, c, &s_walk[warp][0])) return;
+  } else {
+    if (cached) {
+      for (int s = tid; s <= a.c.seqs; s += kThreads) {
+        s_cu[s] = ld(a.cu + s);
+        if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
+      }
+      __syncthreads();
     }
-    settle<ROWS, kUnit>(steps, lo * per_thread, s_before[lo], begin, end, s_walk[warp][0]);
+    const int per_thread = (a.c.seqs + kThreads - 1) / kThreads;
+    const int sa = min(tid * per_thread, a.c.seqs), sb = min(sa + per_thread, a.c.seqs);
+    long long mine = 0;
+    for (int s = sa; s < sb; ++s) mine += work_of(item_of<ROWS, kUnit>(steps, s));
+    long long total;
+    s_before[tid] = block_prefix<W>(mine, s_scan, total);
+    c.per = quotient(total + a.chunks - 1, a.chunks);
+    c.begin = c.per * chunk;
+    c.end = min(c.begin + c.per, total);
+    __syncthreads();
+    if (c.begin >= c.end) return;
+    if (lane == 0) {
+      int lo = 0, hi = kThreads - 1;  // the last thread whose sequences begin at or before the chunk
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_before[mid] <= c.begin) lo = mid; else hi = mid - 1;
+      }
+      settle<ROWS, kUnit>(steps, lo * per_thread, s_before[lo], c.begin, c.end, s_walk[warp][0]);
+    }
+    __syncwarp();
   }
-  __syncwarp();
+  if (lane == 0) s_chunk[warp] = c;
 
   // ---- this warp's ring ----
   int stage = 0;            // next stage to be consumed; all stages are empty between items
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         if ((invalid >> (U * st) & ((1u << U) - 1u)) != (1u << U) - 1u) warp_wait(bar0 + 8 * st, parity >> st & 1u, kDrainCycles);
     }
     // the next part of the chunk: its first units are in flight while this one's results leave
-    if (lane == 0) advance<ROWS, kUnit>(steps, cur, s_walk[warp][turn ^ 1], end);
+    if (lane == 0) advance<ROWS, kUnit>(steps, cur, s_walk[warp][turn ^ 1], s_chunk[warp].end);
     __syncwarp();
     const bool more = s_walk[warp][turn ^ 1].more;
     if (more) start(s_walk[warp][turn ^ 1]);
@@ -531,7 +538,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     if (lane == 0 && !whole && cur.off == 0) {  // the item goes on in the chunks up to that of its last unit
       Piece p;
       p.on = 1;
-      p.last = static_cast<int>((cur.pos + cur.it.units - 1) / per);
+      p.last = static_cast<int>((cur.pos + cur.it.units - 1) / s_chunk[warp].per);
       p.row0 = cur.it.row0; p.r0 = r0; p.nrows = nrows; p.h = h;
       a.pieces[chunk] = p;
     }

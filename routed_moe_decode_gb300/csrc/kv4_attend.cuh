@@ -52,6 +52,11 @@ struct Steps {
   __device__ __forceinline__ int len(int s) const { return max(lens != nullptr ? lens[s] : ld(a.c.lens + s), 0); }
 };
 
+// a / b, a >= 0: nearly always of 32 bits, whose division is far shorter.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a <= 0x7fffffffll ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+}
+
 template <int ROWS, int UNIT_TOKENS>
 __device__ __forceinline__ Item item_of(const Steps& st, int s) {
   const AttendArgs& a = st.a;
@@ -103,8 +108,17 @@ __device__ __forceinline__ void advance(const Steps& steps, const Walk& cur, Wal
   nxt.count = static_cast<int>(min(end - nxt.pos, static_cast<long long>(nxt.it.units)));
 }
 
-// The place of position `begin` of the work, from the sequences s, s + 1, ... of which the first
-// begins at `at`, in a chunk that ends at `end`.
+// The place of position `begin` of the work in a chunk that ends at `end`: in w.it, a sequence's items,
+// which begin at `at`.
+__device__ __forceinline__ void settle_in(long long at, long long begin, long long end, Walk& w) {
+  w.pos = begin;
+  w.idx = static_cast<int>(quotient(begin - at, w.it.units));
+  w.off = static_cast<int>(begin - at - static_cast<long long>(w.idx) * w.it.units);
+  w.count = static_cast<int>(min(end - begin, static_cast<long long>(w.it.units - w.off)));
+  w.more = 1;
+}
+
+// The same from the sequences s, s + 1, ..., of which the first begins at `at`.
 template <int ROWS, int UNIT_TOKENS>
 __device__ __forceinline__ void settle(const Steps& steps, int s, long long at, long long begin, long long end, Walk& w) {
   for (;; ++s) {
@@ -113,11 +127,46 @@ __device__ __forceinline__ void settle(const Steps& steps, int s, long long at, 
     if (begin < at + n) break;
     at += n;
   }
-  w.pos = begin;
-  w.idx = static_cast<int>((begin - at) / w.it.units);
-  w.off = static_cast<int>(begin - at - static_cast<long long>(w.idx) * w.it.units);
-  w.count = static_cast<int>(min(end - begin, static_cast<long long>(w.it.units - w.off)));
-  w.more = 1;
+  settle_in(at, begin, end, w);
+}
+
+// A chunk of the work and its first part, found by a warp alone, for up to 32 sequences (a lane a sequence):
+// the sums over a block take longer (one short sequence 12.1 against 11.3 us, long documents 116 against 114).  Fills cu and
+// lens (every warp of a CTA with the same values).  False: there is nothing in the chunk.
+struct Chunk {
+  long long per, begin, end;
+};
+template <int ROWS, int UNIT_TOKENS>
+__device__ __forceinline__ bool settle_warp(const AttendArgs& a, int* cu, int* lens, int chunk, Chunk& c, Walk* w) {
+  const int lane = threadIdx.x & 31, n = a.c.seqs;
+  if (lane < n) {
+    cu[lane] = ld(a.cu + lane);
+    lens[lane] = ld(a.c.lens + lane);
+    if (lane == n - 1) cu[n] = ld(a.cu + n);
+  }
+  __syncwarp();
+  Item it;
+  it.items = 0;
+  it.units = 1;
+  if (lane < n) it = item_of<ROWS, UNIT_TOKENS>(Steps{a, cu, lens}, lane);
+  const long long mine = work_of(it);
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const long long total = __shfl_sync(0xffffffffu, upto, 31);
+  c.per = quotient(total + a.chunks - 1, a.chunks);
+  c.begin = c.per * chunk;
+  c.end = min(c.begin + c.per, total);
+  if (c.begin >= c.end) return false;
+  if (w != nullptr && c.begin >= upto - mine && c.begin < upto) {
+    w->it = it;
+    settle_in(upto - mine, c.begin, c.end, *w);
+  }
+  __syncwarp();
+  return true;
 }
 
 // Exclusive prefix sum of one value per thread over the block, and the block's sum.

@@ -202,31 +202,39 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
 
   // the work, cut into one chunk of `per` steps per CTA: this one's is [begin, end)
   const bool cached = a.c.seqs <= kSeqCache;
-  if (cached) {
-    for (int s = tid; s <= a.c.seqs; s += kThreads) {
-      s_cu[s] = ld(a.cu + s);
-      if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
-    }
-    __syncthreads();
-  }
   const Steps steps{a, cached ? s_cu : nullptr, cached ? s_len : nullptr};
-  const int per_thread = (a.c.seqs + kThreads - 1) / kThreads;
-  const int sa = min(tid * per_thread, a.c.seqs), sb = min(sa + per_thread, a.c.seqs);
-  long long mine = 0;
-  for (int s = sa; s < sb; ++s) mine += work_of(item_of<kRows, kTokens>(steps, s));
-  long long total;
-  const long long before = block_prefix<kWarps>(mine, s_scan, total);
   const int chunk = blockIdx.x;
-  const long long per = (total + a.chunks - 1) / a.chunks;
-  const long long begin = per * chunk, end = min(begin + per, total);
   if (tid == 0) a.pieces[chunk].on = 0;
-  if (begin >= end) return;
-  if (begin >= before && begin < before + mine) {
-    Walk w;
-    settle<kRows, kTokens>(steps, sa, before, begin, end, w);
-    for (int i = 0; i <= kSoft; ++i) s_walk[i][0] = w;
+  Chunk c;
+  if (a.c.seqs <= 32) {
+    Walk* own = warp < kSoft ? &s_walk[warp][0] : warp == kLoader ? &s_walk[kSoft][0] : nullptr;
+    if (!settle_warp<kRows, kTokens>(a, s_cu, s_len, chunk, c, own)) return;
+  } else {
+    if (cached) {
+      for (int s = tid; s <= a.c.seqs; s += kThreads) {
+        s_cu[s] = ld(a.cu + s);
+        if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
+      }
+      __syncthreads();
+    }
+    const int per_thread = (a.c.seqs + kThreads - 1) / kThreads;
+    const int sa = min(tid * per_thread, a.c.seqs), sb = min(sa + per_thread, a.c.seqs);
+    long long mine = 0;
+    for (int s = sa; s < sb; ++s) mine += work_of(item_of<kRows, kTokens>(steps, s));
+    long long total;
+    const long long before = block_prefix<kWarps>(mine, s_scan, total);
+    c.per = quotient(total + a.chunks - 1, a.chunks);
+    c.begin = c.per * chunk;
+    c.end = min(c.begin + c.per, total);
+    if (c.begin >= c.end) return;
+    if (c.begin >= before && c.begin < before + mine) {
+      Walk w;
+      settle<kRows, kTokens>(steps, sa, before, c.begin, c.end, w);
+      for (int i = 0; i <= kSoft; ++i) s_walk[i][0] = w;
+    }
+    __syncwarp();
   }
-  __syncwarp();
+  const long long end = c.end;
   if (warp == 0) {
     tmem_alloc(smem_addr(&s_tmem), L::kCols);
     tmem_relinquish();
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
       if (tid == 0 && !whole && cur.off == 0) {  // the item goes on in the chunks up to that of its last unit
         Piece p;
         p.on = 1;
-        p.last = static_cast<int>((cur.pos + cur.it.units - 1) / per);
+        p.last = static_cast<int>((cur.pos + cur.it.units - 1) / c.per);
         p.row0 = cur.it.row0; p.r0 = b.r0; p.nrows = b.nrows; p.h = b.h;
         a.pieces[chunk] = p;
       }
