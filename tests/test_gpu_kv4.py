@@ -272,6 +272,15 @@ def test_attend_many_rows_of_many_sequences(moe):
     check_attend(moe, rows + rng.integers(0, 90, 300), rows, heads=1, group=16, D=128, page=16, max_rows=3)
 
 
+@pytest.mark.parametrize("group", [1, 16])  # few and many rows
+@pytest.mark.parametrize("seqs", [31, 32, 33, 256, 257])
+def test_attend_numbers_of_sequences(moe, seqs, group):
+    rng = np.random.default_rng(seqs)
+    rows = rng.integers(0, 4, seqs)
+    rows[-1] = 2
+    check_attend(moe, rows + rng.integers(0, 70, seqs), rows, heads=1, group=group, D=128, page=16, max_rows=3, seed=seqs)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attend_many_rows_same_bits_and_rows_apart(moe, D):
     cache, *_ = make_cache(moe, [5000, 30, 2000], 2, D, 64, seed=4)
@@ -349,6 +358,28 @@ def test_append_and_read(moe, D, dtype, heads, page, ts):
     gk, gv = cache.read(1, dev(cu), rows=total, dtype=dt)
     for got, want in ((gk, want_k), (gv, want_v)):
         assert torch.equal(got.cpu(), torch.tensor(want).float().to(dt))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_and_read_rows_aligned_to_16_bytes_only(moe, D):
+    heads, n = 3, 40
+    cu = dev([0, n])
+    caches = [make_cache(moe, [n + 7], heads, D, 48, fill=False)[0] for _ in range(2)]
+    g = torch.Generator().manual_seed(D)
+    wide = torch.randn((2, n, heads, D + 8), generator=g).to(torch.bfloat16).cuda()
+    k, v = wide[0, :, :, 8:], wide[1, :, :, 8:]  # 16 bytes past a row's start, heads 16 bytes further apart
+    assert k.data_ptr() % 32 == 16
+    caches[0].append(0, k, v, cu)
+    caches[1].append(0, k.contiguous(), v.contiguous(), cu)
+    assert torch.equal(caches[0].pool, caches[1].pool)
+    want = caches[0].read(0, cu, rows=n)
+    room = torch.full((2, n * heads * D + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = tuple(r[8:8 + n * heads * D].view(n, heads, D) for r in room)
+    assert out[0].data_ptr() % 32 == 16
+    caches[0].read(0, cu, out=out)
+    for a, b, r in zip(out, want, room):
+        assert torch.equal(a, b) and (r[:8] == 7).all() and (r[8 + n * heads * D:] == 7).all()
+    assert caches[0].status() == 0
 
 
 def test_append_ties_go_to_even(moe):

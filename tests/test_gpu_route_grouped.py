@@ -93,6 +93,14 @@ def test_shapes(moe, E, groups, keep, score, group_score):
     check(moe, logits, bias, k, score, groups, keep, group_score, scale=2.5)
 
 
+@pytest.mark.parametrize("E,offset", [(512, 1), (512, 4), (100, 3), (500, 4)])
+def test_bias_alignment(moe, E, offset):
+    g = torch.Generator().manual_seed(E + offset)
+    logits = torch.randn((37, E), generator=g).cuda()
+    bias = (0.1 * torch.randn(E + offset, generator=g)).cuda()[offset:]
+    check(moe, logits, bias, 8, "sigmoid", 4, 2, "top2")
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("stride", [0, 1, 8])
 def test_types_and_strides(moe, dtype, stride):
