@@ -10,7 +10,7 @@
 //
 // Measured: forking 16 prompts into 128 branches and reserving for them on 48 layers (906 MB copied, the 16 sources
 // from L2) 125 us; one prompt into 4 on 12 layers 11 us, bound by three launches; compaction of 64 steps on 48 layers with the calls
-// around it (23 MB in 16-byte pieces) 28 us.
+// around it (23 MB in 16-byte pieces) 25 us.
 #include "kv4_common.cuh"
 
 namespace moe {
@@ -277,13 +277,13 @@ __device__ __forceinline__ unsigned long long kept_rows(const PageArgs& a, const
   return (static_cast<unsigned long long>(hi) << 32) | lo;
 }
 
-// grid (units of one sequence / 256, sequences).  A unit is one piece of a token's bytes on one
+// grid (units of one sequence / kMoveThreads, sequences).  A unit is one piece of a token's bytes on one
 // layer and head: D / 32 pieces of 16 bytes of K codes, as many of V codes, one of D / 16 bytes of
 // K scales and one of V scales.  Its thread moves that piece of every kept row, in order; a row
 // only ever moves to an earlier place, which by then has been read, so no other thread has to be
 // waited for.  Eight rows are read before the first of them is written.  The sequence's last CTA to
 // have looked at its length and table cuts it to what it keeps (the moves need neither again).
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;  // 64 steps on 48 layers: 25.3 us with the calls around it, 256 threads 28.8, 64 26.0
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(PageArgs a) {
   __shared__ int s_page_from[kStepRows], s_page_to[kStepRows], s_from[kStepRows], s_to[kStepRows];
