@@ -26,7 +26,7 @@
 // warp-MMA kernel); a chunk of 2048 rows with 4 query heads a K/V head over 4096 tokens, 8 heads of 128: 148 us (657),
 // 0.7 PFLOP/s of unmasked products; 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 68 us (105).  More warps
 // were slower: two threads a row 51 and 175, two groups of them on alternate steps 47 and 167, eight warps that
-// dequantise 42 and 160 (against 42 and 151 at the time).
+// dequantise the chunk 160 (against 42 and 151 at the time).
 #include "kv4_attend.cuh"
 
 namespace moe {
