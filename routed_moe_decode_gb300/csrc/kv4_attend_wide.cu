@@ -119,6 +119,9 @@ struct WideShape {
   static constexpr int kPart = kRows * D + 2 * kRows;
   static constexpr int kColO = 2 * kTokens;
   static constexpr int kCols = kColO + D <= 256 ? 256 : 512;
+  // p in columns of its own, where there are some left: its scores can then be read again
+  static constexpr bool kApart = kColO + D + kTokens <= kCols;
+  static constexpr int kColP = kApart ? kColO + D : 0, kStepP = kApart ? kTokens / 2 : kTokens;
 };
 
 // The block of rows of an item, and the steps of a part that some of its rows see.
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
         const uint64_t v_desc = desc_mn_sw128(base + L::kV + (m % VB) * L::kOperand, kTokens * 128);
 #pragma unroll
         for (int k = 0; k < kTokens / 16; ++k)
-          tc_mma_f16_ts(tmem + L::kColO, tmem + (m & 1u) * kTokens + 8 * k, v_desc + (k * 2048 >> 4),
+          tc_mma_f16_ts(tmem + L::kColO, tmem + L::kColP + (m & 1u) * L::kStepP + 8 * k, v_desc + (k * 2048 >> 4),
                         idesc_f16_f32(kRows, D) | kBIsMn, !first || k > 0);
         tc_commit(o_done + 8 * (m & 1u));
       }
@@ -515,9 +518,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
               if (a.window > 0 && pos >= a.window) see &= ~low_bits(pos + 1 - a.window - tok0);
             }
           }
-          // the scores are read twice, 16 at a time, in short loops: the warps of an SM sub-partition run the
-          // code of four roles and fetch it through one small cache (64 at a time in registers, unrolled:
-          // 5 to 7 % slower)
+          // 16 scores at a time, in short loops: the warps of an SM sub-partition run the code of four roles and
+          // fetch it through one small cache (64 at a time in registers, unrolled: 5 to 7 % slower)
           constexpr int CH = 16;
           auto scores = [&](int c0, uint32_t (&v)[CH]) {
             tmem_ld_x16(cols + c0, v);
@@ -528,50 +530,71 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
               for (int c = 0; c < CH; ++c) v[c] = (bits >> c) & 1u ? v[c] : 0xff800000u;
             }
           };
-          float higher = -INFINITY;
+          auto largest = [&]() {
+            float top = -INFINITY;
 #pragma unroll 1
-          for (int c0 = 0; c0 < kTokens; c0 += CH) {
-            uint32_t v[CH];
-            scores(c0, v);
+            for (int c0 = 0; c0 < kTokens; c0 += CH) {
+              uint32_t v[CH];
+              scores(c0, v);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) higher = fmaxf(higher, __uint_as_float(v[c]));
-          }
-          higher *= factor;
-          if (__any_sync(0xffffffffu, higher > m + kSlack)) {
+              for (int c = 0; c < CH; ++c) top = fmaxf(top, __uint_as_float(v[c]));
+            }
+            return top * factor;
+          };
+          auto raise = [&](float higher) {  // the reference; false: a wait gave up
             higher = fmaxf(m, higher);
             const float worth = exp2_approx(m - higher);
             m = higher;
             l *= worth;
-            if (i > 0) {
-              ok = wait(o_done + 8 * ((n - 1) & 1u), (n - 1) >> 1);
-              if (!ok) break;
-              tc_fence_after();
+            if (i == 0) return true;
+            if (!wait(o_done + 8 * ((n - 1) & 1u), (n - 1) >> 1)) return false;
+            tc_fence_after();
 #pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld_x16(lanes + L::kColO + c0, o);
-                tc_wait_ld();
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t o[16];
+              tmem_ld_x16(lanes + L::kColO + c0, o);
+              tc_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * worth);
-                tmem_store(lanes + L::kColO + c0, o);
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * worth);
+              tmem_store(lanes + L::kColO + c0, o);
+            }
+            return true;
+          };
+          const uint32_t cols_p = lanes + L::kColP + (n & 1u) * L::kStepP;
+          float2 sum;
+          auto powers = [&]() {  // p and their sum; returns the largest exponent
+            sum = make_float2(0.f, 0.f);
+            float most = -INFINITY;
+            const float2 factor2 = make_float2(factor, factor), minus_m = make_float2(-m, -m);
+#pragma unroll 1
+            for (int c0 = 0; c0 < kTokens; c0 += CH) {
+              uint32_t v[CH], p[CH / 2];
+              scores(c0, v);
+#pragma unroll
+              for (int c = 0; c < CH; c += 2) {
+                const float2 z = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), factor2, minus_m);
+                const float2 e = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                if (L::kApart) most = fmaxf(most, fmaxf(z.x, z.y));
+                sum = add2(sum, e);
+                p[c / 2] = half2_bits(e.x, e.y);
               }
+              tmem_store(cols_p + c0 / 2, p);  // kApart false: over scores that have been read
             }
-          }
-          float2 sum = make_float2(0.f, 0.f);
-          const float2 factor2 = make_float2(factor, factor), minus_m = make_float2(-m, -m);
-#pragma unroll 1
-          for (int c0 = 0; c0 < kTokens; c0 += CH) {
-            uint32_t v[CH], p[CH / 2];
-            scores(c0, v);
-#pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-              const float2 z = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), factor2, minus_m);
-              const float2 e = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-              sum = add2(sum, e);
-              p[c / 2] = half2_bits(e.x, e.y);
+            return most;
+          };
+          if constexpr (L::kApart) {
+            // against the reference as it is, and once more where that was too low
+            for (int again = 0; ok; ++again) {
+              const float most = powers();
+              if (again > 0 || !__any_sync(0xffffffffu, most > kSlack)) break;
+              ok = raise(largest());
             }
-            tmem_store(cols + c0 / 2, p);  // over scores that have been read
+          } else {
+            const float higher = largest();
+            if (__any_sync(0xffffffffu, higher > m + kSlack)) ok = raise(higher);
+            if (ok) powers();
           }
+          if (!ok) break;
           l += sum.x + sum.y;
           tc_wait_st();
         }
