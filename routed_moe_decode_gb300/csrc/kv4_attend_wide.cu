@@ -4,9 +4,10 @@
 // The mathematics is that of the warp-MMA kernel (one pass, running reference m, FP32 sums, p
 // rounded to FP16); the products of 64 tokens at a time, a step, are
 //   S [128 rows x 64 tokens] = Q [128 x D] K^T       Q, K: shared memory
-//   O [128 rows x D]        += P [128 x 64] V        P: tensor memory, over its scores; V: shared memory
-// with S (two buffers) and O in tensor memory.  A query row is a lane of tensor memory and a thread:
-// its maximum, its sum and its masks need no other thread.  The cache is dequantised once for 128 rows.
+//   O [128 rows x D]        += P [128 x 64] V        P: tensor memory; V: shared memory
+// with S (two buffers) and O in tensor memory, at head size 128 p over its scores.  A query row is a lane
+// of tensor memory and a thread: its maximum, its sum and its masks need no other thread.  The cache is
+// dequantised once for 128 rows.
 //
 // Every role has warps of its own, and only barriers in shared memory between them:
 //   a loader copies the tiles of up to S steps ahead into a ring and says what they hold;
@@ -19,14 +20,16 @@
 // A block reads no step that none of its rows sees; blocks are walked from both ends of the rows inwards,
 // so that neighbouring items of a causal chunk are about equally long together.
 //
-// A step takes a CTA ~2000 (head size 64) to ~2500 cycles (128), two CTAs an SM.  At 128 the operands' traffic through
-// shared memory (105 KB a step, of which the query rows are 32) comes to two thirds of that; otherwise what
-// the warps share is the issue and fetching of four roles' code (18.7 M instructions for the trees below, issue
-// slots 41 to 50 % busy).  Measured: 24 sequences of up to 6001 tokens, 112 rows, 4 K/V heads of 64: 41 us (78 with the
-// warp-MMA kernel); a chunk of 2048 rows with 4 query heads a K/V head over 4096 tokens, 8 heads of 128: 148 us (657),
-// 0.7 PFLOP/s of unmasked products; 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 68 us (105).  More warps
-// were slower: two threads a row 51 and 175, two groups of them on alternate steps 47 and 167, eight warps that
-// dequantise the chunk 160 (against 42 and 151 at the time).
+// A step takes a CTA 0.99 us at head size 64 and 1.23 at 128, two CTAs an SM (from the slope between 12001 and 24001
+// tokens of 24 sequences).  At 128 the operands' traffic through shared memory (105 KB a step, of which the query
+// rows are 32) comes to two thirds of that; otherwise what the warps share is the issue and fetching of four roles' code
+// (17.9 M instructions for the trees below, issue slots ~40 % busy).  17 to 20 us of a call do not depend on
+// the tokens: ~4 until the first products, the end of an item and the start of the next, joining, CTAs that have more to do.
+// Measured: 24 sequences of up to 6001 tokens, 112 rows, 4 K/V heads of 64: 40 us (78 with the warp-MMA kernel); a chunk of
+// 2048 rows with 4 query heads a K/V head over 4096 tokens, 8 heads of 128: 147 us (657), 0.7 PFLOP/s of unmasked
+// products; 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 68 us (105).  More warps were slower:
+// two threads a row 51 and 175, two groups of them on alternate steps 47 and 167, eight warps that dequantise the
+// chunk 160 (against 42 and 151 at the time).
 #include "kv4_attend.cuh"
 
 namespace moe {
