@@ -109,6 +109,18 @@ __device__ __forceinline__ Words<N> shared_words(const uint8_t* p) {
   return o;
 }
 
+// Channels c, c + 1 of row r (step row r / group, query head r % group of K/V head h) of the step that
+// begins at row0: from the sums, their reference m and the sum l.
+template <int D>
+__device__ __forceinline__ void finish(const AttendArgs& a, int row0, int h, int r, int c, float v0, float v1, float m, float l) {
+  const int step_row = r / a.group, hq = h * a.group + r - step_row * a.group;
+  const int64_t at = static_cast<int64_t>(row0 + step_row) * (a.c.heads * a.group) + hq;
+  const bool seen = l > 0.f || l != l;
+  const float f = seen ? a.v_ts / l : 0.f;
+  *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + 2 * (at * D + c)) = pack2(v0 * f, v1 * f, a.fp16);
+  if (c == 0 && a.lse != nullptr) a.lse[at] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
 // The work is counted in units of two tiles (32 tokens), each of which a warp takes as one step: two
 // independent chains of products, and one look at the masks and at the reference m for both.  (One
 // tile a step leaves registers for more warps, and measured 0 to 30 % slower at every size.)
@@ -543,6 +555,106 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
       a.pieces[chunk] = p;
     }
     if (!more) break;
+  }
+}
+
+// Joins the parts of the items that were cut.  CTA (b, n): n-tile n of the items that begin in the
+// chunks [b kJoinChunks, + kJoinChunks) and go on past them.  A warp takes one m-tile of the output
+// and every GROUPS-th part of the item.  It is all latency, so the sums of a batch of parts are under
+// way before their m and l are here: two trips to memory for up to 16 GROUPS parts.
+constexpr int kJoinThreads = 512, kJoinChunks = 8;
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
+  constexpr int ROWS = 8 * NT, KS = D / 16, PART = ROWS * D + 2 * ROWS, GROUPS = kJoinThreads / 32 / KS;
+  constexpr int DEEP = 16, BATCH = DEEP * GROUPS;
+  __shared__ float s_w[BATCH][8], s_l[BATCH][8];  // m of a batch of parts, then their weights; their l
+  __shared__ float s_top[8], s_total[8], s_worth[8];  // of the batches so far
+  __shared__ float4 s_sum[kJoinThreads];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = warp % KS, group = warp / KS, n = blockIdx.y;
+  const int q = lane & 3;
+  // lane l of every warp looks at the CTA's chunk l
+  int4 px = make_int4(0, 0, 0, 0), py = px;
+  if (lane < kJoinChunks && blockIdx.x * kJoinChunks + lane < a.chunks) {
+    const int4* pp = reinterpret_cast<const int4*>(a.pieces + blockIdx.x * kJoinChunks + lane);
+    px = __ldcg(pp);
+    py = __ldcg(pp + 1);
+  }
+  uint32_t on = __ballot_sync(0xffffffffu, px.x != 0 && 8 * n < py.x);
+  for (; on != 0; on &= on - 1) {
+    const int src = __ffs(on) - 1, c0 = blockIdx.x * kJoinChunks + src;
+    const int parts = __shfl_sync(0xffffffffu, px.y, src) - c0 + 1, row0 = __shfl_sync(0xffffffffu, px.z, src);
+    const int r0 = __shfl_sync(0xffffffffu, px.w, src), nrows = __shfl_sync(0xffffffffu, py.x, src);
+    const int h = __shfl_sync(0xffffffffu, py.y, src);
+    // of the chunk c0 + c: the first chunk's part starts at the item's first unit
+    auto part_of = [&](int c) { return a.part + (2 * static_cast<size_t>(c0 + c) + (c == 0 ? 1 : 0)) * PART; };
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < 8) {
+      s_top[tid] = kLowest;
+      s_total[tid] = 0.f;
+    }
+    for (int cb = 0; cb < parts; cb += BATCH) {
+      const int nb = min(BATCH, parts - cb);
+      for (int i = tid; i < 8 * nb; i += kJoinThreads) {
+        const float* p = part_of(cb + (i >> 3)) + ROWS * D + 8 * n + (i & 7);
+        s_w[i >> 3][i & 7] = __ldcg(p);
+        s_l[i >> 3][i & 7] = __ldcg(p + ROWS);
+      }
+      float4 z[DEEP];
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j)
+        if (group + j * GROUPS < nb)
+          z[j] = __ldcg(reinterpret_cast<const float4*>(part_of(cb + group + j * GROUPS)) + (n * KS + k) * 32 + lane);
+      __syncthreads();
+      if (warp < 8) {  // a warp a row
+        const float old = s_top[warp];
+        float top = old, l = 0.f;
+        for (int c = lane; c < nb; c += 32) top = fmaxf(top, s_w[c][warp]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int c = lane; c < nb; c += 32) {
+          const float w = exp2_approx(s_w[c][warp] - top);
+          s_w[c][warp] = w;
+          l += w * s_l[c][warp];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) {
+          const float f = exp2_approx(old - top);
+          s_top[warp] = top;
+          s_total[warp] = s_total[warp] * f + l;
+          s_worth[warp] = f;
+        }
+      }
+      __syncthreads();
+      const float f0 = s_worth[2 * q], f1 = s_worth[2 * q + 1];
+      v.x *= f0; v.y *= f1; v.z *= f0; v.w *= f1;
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j)
+        if (group + j * GROUPS < nb) {
+          const float w0 = s_w[group + j * GROUPS][2 * q], w1 = s_w[group + j * GROUPS][2 * q + 1];
+          v.x += w0 * z[j].x; v.y += w1 * z[j].y; v.z += w0 * z[j].z; v.w += w1 * z[j].w;
+        }
+      __syncthreads();  // the weights have been used
+    }
+    if constexpr (GROUPS > 1) {
+      s_sum[tid] = v;
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int j = 1; j < GROUPS; ++j) {
+          const float4 y = s_sum[tid + j * KS * 32];
+          v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
+      }
+    }
+    if (group == 0) {
+      const int c = (lane >> 2) * (D / 8) + 2 * k, r = 8 * n + 2 * q;
+      if (r < nrows) finish<D>(a, row0, h, r0 + r, c, v.x, v.z, s_top[2 * q], s_total[2 * q]);
+      if (r + 1 < nrows) finish<D>(a, row0, h, r0 + r + 1, c, v.y, v.w, s_top[2 * q + 1], s_total[2 * q + 1]);
+    }
+    __syncthreads();
   }
 }
 
