@@ -49,8 +49,9 @@ extern "C" {
 
 /* Status bits of a cache's workspace. */
 #define MOE_KV4_NO_PAGE 0x1u   /* moe_kv4_reserve ran out of free pages or table entries: this
-                                  sequence and (for pages) those after it that needed some keep
-                                  their length and pages */
+                                  sequence and (for pages) those after it that needed some are
+                                  refused: they keep their length, pages and tokens, and the
+                                  step's later calls leave them out (moe_kv4_reserve) */
 #define MOE_KV4_BAD_PAGE 0x2u  /* a token in use lies on a page number outside [0, pages), or
                                   before its sequence's start: it was skipped */
 #define MOE_KV4_NONFINITE 0x4u /* moe_kv4_append met an infinity or a NaN */
@@ -85,7 +86,7 @@ MOE_API size_t moe_kv4_workspace_bytes(const moe_kv4_cache* cache);
 /* MOE_OK, MOE_ERR_INVALID_ARG or MOE_ERR_UNSUPPORTED for the sizes of a cache (host only). */
 MOE_API int moe_kv4_check(const moe_kv4_cache* cache);
 
-/* Zero the status word and the counters of a fresh workspace.  Once after allocation. */
+/* Zero the status word, the counters and the refusals of a fresh workspace.  Once after allocation. */
 MOE_API int moe_kv4_workspace_init(const moe_kv4_cache* cache, moe_stream_t stream);
 
 /* Quantise the step's K and V rows into `layer`.
@@ -99,7 +100,8 @@ MOE_API int moe_kv4_append(const moe_kv4_cache* cache, int layer, const void* k,
 
 /* The values held for the step's rows (the last cu_rows[s+1] - cu_rows[s] tokens of every
  * sequence) of `layer`: k, v [rows][kv_heads][head_dim] of `dtype`, contiguous, 16-byte aligned
- * (either may be NULL).  Rows that lie before their sequence's start are zeroed. */
+ * (either may be NULL).  Rows that lie before their sequence's start are zeroed, as are those of a
+ * refused sequence. */
 MOE_API int moe_kv4_read(const moe_kv4_cache* cache, int layer, void* k, void* v, int dtype, const int32_t* cu_rows,
                          int rows, moe_stream_t stream);
 
@@ -109,7 +111,8 @@ MOE_API int moe_kv4_read(const moe_kv4_cache* cache, int layer, void* k, void* v
  * with k_t, v_t of the head h / (q_heads / kv_heads).  The row at position x sees the tokens
  * t <= x, with window > 0 only t > x - window.  With `tree` the row sees every token before the
  * step, and token j of the step where bit j of tree[row] is set (a step has at most 64 tokens
- * then; window must be 0).  A row that sees nothing gets out 0 and lse -infinity.
+ * then; window must be 0).  A row that sees nothing, or whose sequence
+ * was refused, gets out 0 and lse -infinity.
  *   q        [rows][q_heads][head_dim] of `dtype`; strides in elements, multiples of 8
  *   max_rows the largest number of rows of a sequence, as far as the host knows: it chooses the
  *            kernel's tile; more rows are computed all the same
@@ -128,7 +131,12 @@ MOE_API int moe_kv4_attend(const moe_kv4_cache* cache, int layer, const void* q,
 /* Room for new_tokens[s] >= 0 more tokens of every sequence (device, [seqs]; negative counts as
  * 0): lens grows by it, and free pages, lowest numbers first in the order of the sequences, are
  * added to the tables.  Where a sequence's last page is partly filled and shared (refs above 1
- * before the call), it is first replaced by a free page holding a copy of it on every layer. */
+ * before the call), it is first replaced by a free page holding a copy of it on every layer.
+ * A sequence that gets no room (MOE_KV4_NO_PAGE) is refused: its lens stays as it was, and until a
+ * later reservation for it succeeds, moe_kv4_trim cuts it or moe_kv4_fork replaces it, the calls of
+ * a step treat its rows as rows without a place: append and compact skip them (no token or page of
+ * it, or of a sequence it shares pages with, changes), read gives zeros, and attend out 0 and lse
+ * -infinity.  So a step can go on without asking for the status first. */
 MOE_API int moe_kv4_reserve(const moe_kv4_cache* cache, const int32_t* new_tokens, moe_stream_t stream);
 
 /* Sequence dst[i] becomes a copy of sequence src[i], sharing its pages, for i < n (device

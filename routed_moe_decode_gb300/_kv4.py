@@ -158,7 +158,8 @@ class Kv4Cache:
 
     def reserve(self, new_tokens, stream=None):
         """Room for new_tokens[s] more tokens of every sequence ([seqs] int32 on the device): lens grows,
-        pages are added, and a shared page that the step will write is replaced by a copy."""
+        pages are added, and a shared page that the step will write is replaced by a copy.  A sequence that
+        gets no room (KV4_NO_PAGE) keeps its lens, and the step's calls leave its rows out."""
         self._call("moe_kv4_reserve", stream, self._ints("new_tokens", new_tokens, self.seqs))
 
     def fork(self, src, dst, stream=None):

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     if (cached) {
       for (int s = tid; s <= a.c.seqs; s += kThreads) {
         s_cu[s] = ld(a.cu + s);
-        if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
+        if (s < a.c.seqs) s_len[s] = step_len(a.c, s);
       }
       __syncthreads();
     }

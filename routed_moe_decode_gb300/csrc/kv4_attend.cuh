@@ -48,7 +48,7 @@ struct Steps {
   const int* cu;    // shared: [seqs + 1], [seqs]; nullptr past kSeqCache
   const int* lens;
   __device__ __forceinline__ int row(int s) const { return min(max(cu != nullptr ? cu[s] : ld(a.cu + s), 0), a.rows); }
-  __device__ __forceinline__ int len(int s) const { return max(lens != nullptr ? lens[s] : ld(a.c.lens + s), 0); }
+  __device__ __forceinline__ int len(int s) const { return max(lens != nullptr ? lens[s] : step_len(a.c, s), 0); }
 };
 
 // a / b, a >= 0: nearly always of 32 bits, whose division is far shorter.
@@ -140,7 +140,7 @@ __device__ __forceinline__ bool settle_warp(const AttendArgs& a, int* cu, int* l
   const int lane = threadIdx.x & 31, n = a.c.seqs;
   if (lane < n) {
     cu[lane] = ld(a.cu + lane);
-    lens[lane] = ld(a.c.lens + lane);
+    lens[lane] = step_len(a.c, lane);
     if (lane == n - 1) cu[n] = ld(a.cu + n);
   }
   __syncwarp();

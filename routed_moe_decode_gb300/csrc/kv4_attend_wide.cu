@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
     if (cached) {
       for (int s = tid; s <= a.c.seqs; s += kThreads) {
         s_cu[s] = ld(a.cu + s);
-        if (s < a.c.seqs) s_len[s] = ld(a.c.lens + s);
+        if (s < a.c.seqs) s_len[s] = step_len(a.c, s);
       }
       __syncthreads();
     }

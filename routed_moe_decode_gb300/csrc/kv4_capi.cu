@@ -45,6 +45,7 @@ int view(const moe_kv4_cache* c, int layer, Cache* v, WsLayout* L) {
   v->page_bytes = page_bytes(*c);
   v->pool = static_cast<uint8_t*>(c->pool) + static_cast<size_t>(layer) * c->pages * v->page_bytes;
   v->table = c->table; v->lens = c->lens; v->refs = c->refs;
+  v->refused = reinterpret_cast<int*>(static_cast<char*>(c->workspace) + L->refused);
   v->status = reinterpret_cast<int*>(static_cast<char*>(c->workspace) + L->status);
   return MOE_OK;
 }
@@ -83,7 +84,7 @@ int moe_kv4_workspace_init(const moe_kv4_cache* c, moe_stream_t stream) {
   if (rc != MOE_OK) return rc;
   const WsLayout L = moe::kv4::ws_layout(*c);
   if (!c->workspace || !aligned(c->workspace, 256) || c->workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
-  return done("workspace init", cudaMemsetAsync(c->workspace, 0, L.pieces, stream));  // the status word and the arrivals
+  return done("workspace init", cudaMemsetAsync(c->workspace, 0, L.pieces, stream));  // the status word, the arrivals, the refusals
 }
 
 int moe_kv4_append(const moe_kv4_cache* c, int layer, const void* k, int64_t k_row_stride, int64_t k_head_stride,

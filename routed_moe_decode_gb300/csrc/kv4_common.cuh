@@ -19,6 +19,7 @@ struct Cache {
   int* table;
   int* lens;
   int* refs;
+  int* refused;  // [seqs] 1: the sequence's last reservation was refused
   int* status;
   int layers, pages, heads, dim, page_size, seqs, max_pages;
   int tile_bytes;       // 18 * dim
@@ -34,7 +35,7 @@ struct alignas(16) Piece {
 };
 
 struct WsLayout {
-  size_t status, arrivals, pieces, copies, need, part, total;
+  size_t status, arrivals, refused, pieces, copies, need, part, total;
 };
 
 inline WsLayout ws_layout(const moe_kv4_cache& c) {
@@ -43,6 +44,7 @@ inline WsLayout ws_layout(const moe_kv4_cache& c) {
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   L.status = take(64);
   L.arrivals = take(size_t(c.seqs) * 4);  // moe_kv4_compact: CTAs of each sequence
+  L.refused = take(size_t(c.seqs) * 4);
   L.pieces = take(size_t(kMaxChunks) * sizeof(Piece));
   // moe_kv4_reserve: copies [1 + 2 * seqs] (their number, then page pairs), need [seqs + 1]
   L.copies = take((1 + 2 * size_t(c.seqs)) * 4);
@@ -67,6 +69,13 @@ MOE_DEVICE StepRows step_rows(const int* __restrict__ cu, int s, int rows) {
   const int a = min(max(ld(cu + s), 0), rows);
   const int b = min(max(ld(cu + s + 1), a), rows);
   return {a, b - a};
+}
+
+// The tokens of sequence s for the calls of a step: none where its reservation was refused, since the step's rows
+// then have no place and its last tokens are older ones.
+MOE_DEVICE int step_len(const Cache& c, int s) {
+  const int len = ld(c.lens + s), refused = ld(c.refused + s);
+  return refused != 0 ? 0 : len;
 }
 
 // The tile that holds token `pos` of sequence s and head h, or nullptr where it has no page.

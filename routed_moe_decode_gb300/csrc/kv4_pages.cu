@@ -71,7 +71,7 @@ __device__ __forceinline__ int first_free(const Cache& c, int p0, unsigned& free
 
 // One CTA.  1: what every sequence needs and the running sums; 2: the free pages are counted, as
 // far as they are needed; 3: the i-th free page goes to the sequence whose needs cover i, if all
-// its needs are met; 4: lengths, and the counts of the pages that were replaced by a copy.  Pages
+// its needs are met; 4: lengths, refusals, and the counts of the pages that were replaced by a copy.  Pages
 // given up by a copy are counted down only in 4, so that none is handed out here while the copy
 // still has to read it.
 __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
@@ -180,8 +180,10 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PageArgs a) {
     const int end = entry_start(entry[s + 1]);
     if ((e & kRefused) || (end > got && end > entry_start(e))) {
       atomicOr(c.status, static_cast<int>(MOE_KV4_NO_PAGE));
+      c.refused[s] = 1;
       continue;
     }
+    c.refused[s] = 0;
     c.lens[s] = (kept ? s_len[s] : max(ld(c.lens + s), 0)) + grow;
     if (e & kCopy) {
       atomicSub(c.refs + a.copies[1 + 2 * entry_rank(e)], 1);
@@ -247,7 +249,10 @@ __global__ void __launch_bounds__(128) fork_kernel(PageArgs a) {
     if (page >= 0 && page < c.pages) atomicAdd(c.refs + page, 1);
     if (old != page) to[j] = page;
   }
-  if (threadIdx.x == 0) c.lens[d] = len;
+  if (threadIdx.x == 0) {
+    c.lens[d] = len;
+    c.refused[d] = 0;
+  }
 }
 
 // Sequence s keeps `to` tokens: a warp takes its further pages out of the table.
@@ -266,7 +271,9 @@ __global__ void __launch_bounds__(32 * kTrimWarps) trim_kernel(PageArgs a) {
   const int s = blockIdx.x * kTrimWarps + (threadIdx.x >> 5);
   if (s >= a.c.seqs) return;
   const int len = max(ld(a.c.lens + s), 0);
-  cut(a.c, s, len, min(max(ld(a.a + s), 0), len));
+  const int to = min(max(ld(a.a + s), 0), len);
+  cut(a.c, s, len, to);
+  if (to != len && (threadIdx.x & 31) == 0) a.c.refused[s] = 0;
 }
 
 // The kept rows of sequence s's step, as bits: row i of the first 64.
@@ -292,8 +299,9 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(PageArgs a) {
   pdl_launch_dependents();
   const Cache& c = a.c;
   const int s = blockIdx.y;
+  const int refused = ld(c.refused + s);
   const StepRows st = step_rows(a.cu, s, a.rows);
-  if (st.n == 0) return;
+  if (st.n == 0 || refused != 0) return;
   if (threadIdx.x < 32) {
     const unsigned long long kept = kept_rows(a, st);
     const int first = ld(c.lens + s) - st.n;

@@ -50,23 +50,25 @@ __device__ __forceinline__ RowPlace find_row(const RowArgs& a, int row) {
     span = min(step, lo + span - nlo);
     lo = nlo;
   }
-  int begin = 0x7fffffff, end = 0, len = 0;
+  int begin = 0x7fffffff, end = 0, len = 0, refused = 0;
   if (lane < span) {
     begin = ld(a.cu + lo + lane);
     end = ld(a.cu + lo + lane + 1);
     len = ld(a.c.lens + lo + lane);
+    refused = ld(a.c.refused + lo + lane);
   }
   const unsigned m = __ballot_sync(0xffffffffu, lane < span && begin <= row);
   const int l = m ? 31 - __clz(m) : 0;
   begin = min(max(__shfl_sync(0xffffffffu, begin, l), 0), a.rows);
   end = min(max(__shfl_sync(0xffffffffu, end, l), begin), a.rows);
   len = __shfl_sync(0xffffffffu, len, l);
+  refused = __shfl_sync(0xffffffffu, refused, l);
   RowPlace p{nullptr, -1};
   if (row >= begin && row < end) {
     const int pos = len - (end - row);
-    p.tile = tile_of(a.c, lo + l, pos, 0);
+    if (refused == 0) p.tile = tile_of(a.c, lo + l, pos, 0);
     p.slot = pos & (kTile - 1);
-    if (p.tile == nullptr && lane == 0) atomicOr(a.c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
+    if (refused == 0 && p.tile == nullptr && lane == 0) atomicOr(a.c.status, static_cast<int>(MOE_KV4_BAD_PAGE));
   }
   return p;
 }

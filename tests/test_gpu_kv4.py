@@ -523,6 +523,81 @@ def test_reserve_out_of_pages(moe):
     assert list(plain.lens) == [48, 32, 23, 16, 90]
 
 
+def test_step_after_a_refused_reservation(moe):
+    # 0 and 1 share a partly filled page and get no free one to copy it to, 2 grows inside its page, 3 has no room in
+    # its table: a whole step leaves every byte of 0, 1 and 3 as it was, and does for 2 what it does without them
+    lens, heads, D, page, layers = [21, 0, 18, 64], 2, 64, 16, 2
+    cache, pool, table, lens, refs = make_cache(moe, lens, heads, D, page, layers=layers, extra_pages=0, max_pages=4, seed=3)
+    cache.fork(dev([0]), dev([1]))
+    before = [t.clone() for t in (cache.pool, cache.table, cache.lens, cache.refs)]
+    rows, group = [3, 3, 3, 3], 4
+    cu, keep = dev(cu_of(rows)), dev([0, 0, 1] * 4, torch.uint8)
+    g = torch.Generator().manual_seed(7)
+    k, v = (torch.randn((12, heads, D), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn((12, heads * group, D), generator=g).to(torch.bfloat16).cuda()
+
+    def step(cache, only=None):
+        new = dev([3 if only is None or s in only else 0 for s in range(4)])
+        c, i = (cu, slice(0, 12)) if only is None else (dev([0, 0, 0, 3, 3]), slice(6, 9))
+        cache.reserve(new)
+        got = []
+        for layer in range(layers):
+            cache.append(layer, k[i], v[i], c)
+            got += cache.read(layer, c, rows=q[i].shape[0])
+            for hint in (3, 64):  # few rows a block, many rows a block
+                lse = torch.full(q[i].shape[:2], 7.0, dtype=torch.float32, device="cuda")
+                out = torch.full(q[i].shape, 7.0, dtype=torch.bfloat16, device="cuda")
+                got += cache.attend(layer, q[i], c, max_rows=hint, out=out, lse=lse)
+        cache.compact(keep[i], c, max_rows=3)
+        return got
+
+    got = step(cache)
+    assert cache.status() == moe.KV4_NO_PAGE
+    alone, *_ = make_cache(moe, lens, heads, D, page, layers=layers, extra_pages=0, max_pages=4, seed=3)
+    want = step(alone, only=[2])
+    assert alone.status() == 0
+    out = torch.ones(12, dtype=torch.bool, device="cuda")
+    out[6:9] = False
+    for a, b in zip(got, want):
+        assert torch.equal(a[6:9], b)
+        assert (a[out] == (0 if a.dim() == 3 else -float("inf"))).all()
+    assert cache.lens.tolist() == [21, 21, 19, 64] and torch.equal(cache.table, before[1]) and torch.equal(cache.refs, before[3])
+    assert torch.equal(cache.pool, alone.pool)
+    mine = table[2, :2]
+    others = [p for p in range(cache.pool.shape[1]) if p not in mine]
+    assert torch.equal(cache.pool[:, others], before[0][:, others])
+
+
+def test_refused_sequences_take_part_again(moe):
+    lens = [21, 0, 40]
+    cache, _ = random_cache(moe, lens, 2, 64, 16, 2, 0, 4, 5)
+    cache.fork(dev([0]), dev([1]))
+    x = torch.ones((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+
+    def held(rows, seq):  # whether the sequence's rows are written and read
+        cu = dev([0 if s <= seq else rows for s in range(4)])
+        cache.append(1, x[:rows], x[:rows], cu)
+        return bool((cache.read(1, cu, rows=rows)[0] == held_one()).all())
+
+    cache.reserve(dev([2, 0, 0]))
+    assert cache.status() == moe.KV4_NO_PAGE and not held(2, 0) and held(1, 2)
+    cache.reserve(dev([0, 0, 3]))      # another sequence's reservation changes nothing for it
+    assert not held(2, 0) and held(3, 2)
+    cache.trim(dev([21, 21, 16]))      # two pages are free: its next reservation succeeds
+    cache.reserve(dev([2, 0, 0]))
+    assert held(2, 0) and cache.status() == 0
+    cache.reserve(dev([0, 30, 0]))     # refused, then cut
+    assert cache.status() == moe.KV4_NO_PAGE and not held(1, 1)
+    cache.trim(dev([100, 16, 100]))
+    bits = [cache.read(1, cu, rows=n)[0].view(torch.int16) for cu, n in ((dev([0, 0, 16, 16]), 16), (dev([0, 23, 23, 23]), 23))]
+    assert torch.equal(bits[0], bits[1][:16]) and bits[0].any()  # the page that 0 and 1 share
+    assert held(1, 2)
+    cache.reserve(dev([0, 60, 0]))     # refused, then replaced by a fork
+    assert cache.status() == moe.KV4_NO_PAGE
+    cache.fork(dev([2]), dev([1]))
+    assert (cache.read(1, dev([0, 0, 1, 2]), rows=2)[0] == held_one()).all() and cache.status() == 0
+
+
 def test_reserve_shared_page_of_several_writers(moe):
     # the last page of a sequence shared by three, two of which write: both copy; then all three
     for writers in ([1, 2], [0, 1, 2]):
