@@ -176,7 +176,8 @@ typedef struct moe_routing {
 /* Step 1 in its grouped form.  Every expert has a score s_e (sigmoid or softmax of the logits) and
  * a key s_e + bias_e that only selects; the keep_groups groups with the largest group scores stay,
  * and the k largest keys among their experts are selected (larger first; equal values go to the
- * lower index, of groups and of experts).  With softmax and no bias the key is the logit itself.
+ * lower index, of groups and of experts).  With softmax and no bias the key is the logit itself,
+ * whose order is the score's, except where groups are ranked by the sum of two keys.
  * The weights are the selected experts' scores, without the bias.
  *   logits     [T, E] of `dtype` (moe_dtype), rows row_stride elements apart, aligned to an element;
  *              NaN counts as -infinity

@@ -1,7 +1,8 @@
 // Grouped routing of one token by one warp.
 //
 //   s_e   = sigmoid(l_e), or the softmax of the row
-//   key_e = s_e + bias_e  (softmax without a bias: l_e itself, whose order is that of s_e)
+//   key_e = s_e + bias_e  (softmax without a bias: l_e itself, whose order is that of s_e; not where
+//           groups are ranked by sums of two keys, since sums of logits have another order)
 //   a group's score is its largest key, or the sum of its two largest; the keep_groups groups of
 //   the largest scores stay; the k largest keys among their experts are selected, larger first;
 //   equal scores and equal keys go to the lower index
@@ -101,7 +102,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(RouteGrouped
   const int E = a.E, k = a.k, base = NPL * lane;
   const int nvalid = max(0, min(NPL, E - base));
   const T* row = static_cast<const T*>(a.logits) + static_cast<int64_t>(t) * a.row_stride;
-  const bool by_logit = a.softmax && a.bias == nullptr;
+  const bool sums = a.top2 && a.keep_groups < a.groups && a.groups < E;  // groups are ranked by sums of two keys
+  const bool by_logit = a.softmax && a.bias == nullptr && !sums;
 
   float v[NPL];
   constexpr int kVec = 16 / sizeof(T);

@@ -93,6 +93,24 @@ def test_shapes(moe, E, groups, keep, score, group_score):
     check(moe, logits, bias, k, score, groups, keep, group_score, scale=2.5)
 
 
+@pytest.mark.parametrize("E,groups,keep", [(512, 8, 4), (64, 16, 3), (40, 5, 2), (96, 3, 1), (1024, 32, 8), (24, 24, 9)])
+def test_softmax_groups_ranked_by_two_scores(moe, E, groups, keep):
+    # the sum is of scores, whether there is a bias of zeros or none: a sum of logits would rank groups by the product
+    g = torch.Generator().manual_seed(E)
+    logits = (2 * torch.randn((64, E), generator=g)).cuda()
+    k = min(6, keep * E // groups)
+    with_zeros = check(moe, logits, torch.zeros(E, device="cuda"), k, "softmax", groups, keep, "top2")
+    r = moe.Routing(E, k, score="softmax", groups=groups, keep_groups=keep, group_score="top2")
+    ids, w = torch.empty((64, k), dtype=torch.int32, device="cuda"), torch.empty((64, k), device="cuda")
+    r.route(logits, None, ids, w)
+    assert np.array_equal(ids.cpu().numpy(), with_zeros[0]) and np.array_equal(w.double().cpu().numpy(), with_zeros[1])
+    # by hand: scores e^5 + e^-5 against e + e
+    two = torch.tensor([[1.0, 1.0, 5.0, -5.0]], device="cuda")
+    ids, w = torch.empty((1, 2), dtype=torch.int32, device="cuda"), torch.empty((1, 2), device="cuda")
+    moe.Routing(4, 2, score="softmax", groups=2, keep_groups=1, group_score="top2").route(two, None, ids, w)
+    assert ids.tolist() == [[2, 3]]
+
+
 @pytest.mark.parametrize("E,offset", [(512, 1), (512, 4), (100, 3), (500, 4)])
 def test_bias_alignment(moe, E, offset):
     g = torch.Generator().manual_seed(E + offset)
