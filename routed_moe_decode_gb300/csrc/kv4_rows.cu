@@ -157,8 +157,10 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], bool fp16, flo
   scale = e4m3_byte(fminf(__fdiv_rn(top, 6.0f * ts), 448.0f));
   const float d = e4m3_float(scale) * ts;
   float y[16];
-  if (d >= 0x1p-60f && d <= 0x1p60f && finite) {
-    const float r = __frcp_rn(d);
+  const float r = __frcp_rn(d);
+  // where no quotient and no product with d leaves FP32's range (a block far above 448 * 6 * ts has quotients
+  // that do, and their remainders are no numbers)
+  if (d >= 0x1p-60f && d <= 0x1p60f && top * r <= 0x1p60f && finite) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const float y0 = x[k] * r;

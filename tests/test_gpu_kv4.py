@@ -421,6 +421,27 @@ def test_append_nonfinite(moe):
     assert k[0, 0, 20] == 0 and k[0, 0, 21] == one and (k[1] == one).all() and (v.float() == one).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("ts", [2.0 ** -13, 0.001, 2.0 ** -60, 2.0 ** -100, 1e-30, 2.0 ** 60, 2.0 ** 100])
+def test_append_far_from_the_tensor_scale(moe, dtype, ts):
+    # finite values whose quotient by the scale leaves FP32, or all but does: the code keeps their sign
+    ts = float(np.float32(ts))
+    top = torch.finfo(DT[dtype]).max
+    x = np.zeros((4, 1, 64))
+    x[0, 0, :6] = top, -top, top / 2, -top / 3, 1.0, -1.0
+    x[1, 0, :3] = -top, 0.5 * top, -1e-4
+    x[2, 0, 16:20] = -1.0, 0.25, 1e-4, -1e-3
+    x[3, 0, :2] = -448 * 6 * ts * np.array([1.0, 0.5])
+    x = np.clip(x, -top, top)
+    cache, *_ = make_cache(moe, [4], 1, 64, 16, k_scale=ts, v_scale=ts, fill=False)
+    t = dev(x, torch.float64).to(DT[dtype])
+    cache.append(0, t, -t, dev([0, 4]))
+    assert cache.status() == 0
+    for got, sign in zip(cache.read(0, dev([0, 4]), rows=4, dtype=DT[dtype]), (1.0, -1.0)):
+        want = P.values(*P.quantise(sign * t.double().cpu().numpy(), ts), ts)
+        assert np.array_equal(got.double().cpu().numpy(), torch.tensor(want).float().to(DT[dtype]).double().numpy())
+
+
 def test_append_outside_the_sequence_is_reported(moe):
     cache, pool, *_ = make_cache(moe, [2, 5], 1, 64, 16, fill=False)
     x = torch.ones((8, 1, 64), dtype=torch.bfloat16, device="cuda")
