@@ -120,7 +120,8 @@ MOE_API int moe_kv4_read(const moe_kv4_cache* cache, int layer, void* k, void* v
  *   out      [rows][q_heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   lse      [rows][q_heads] float or NULL
  * At most 2^30 tokens a sequence are looked at.  Rows of no sequence are left as they are.  Scores,
- * softmax statistics and sums are FP32; p is rounded to FP16, 11 bits relative to a row's largest.
+ * softmax statistics and sums are FP32; p is rounded to FP16: 11 bits, fewer where it is
+ * below 2^-21 of its row's largest, none below 2^-32.
  * Two launches: the attention, and the joining of what it cut over several SMs; the result does
  * not depend on timing. */
 MOE_API int moe_kv4_attend(const moe_kv4_cache* cache, int layer, const void* q, int64_t q_row_stride,

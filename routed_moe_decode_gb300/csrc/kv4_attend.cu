@@ -5,7 +5,7 @@
 // MMAs (m16n8k16, FP16 operands, FP32 accumulators).  E2M1 x E4M3 has at most 6 significant bits
 // and is exact in FP16, and a query row is brought by a power of two into FP16's range, so the
 // scores are exact products summed in FP32; the one rounding inside is that of p to FP16 (11
-// bits, relative to a row's largest about 1).
+// bits; p below 2^-21 of a row's largest have fewer, and those below 2^-32 none).
 //
 // Both products take the cache as the 16-row operand and the query rows as the 8-column one:
 //   S^T [16 tokens x 8 rows]   = K [16 x D]  Q^T         O^T [D x 8 rows] += V^T [D x 16] P^T
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
                 sc[u][n][j] = see ? sc[u][n][j] * factor[n][j & 1] : -INFINITY;
               }
         }
-        float hi[NT][2];
+        float hi[NT][2];  // the largest product; compared as its p's exponent is formed, so that no p is above 2^kSlack
         bool rise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -413,15 +413,15 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
           for (int j = 0; j < 2; ++j) {
             float top = fmaxf(sc[0][n][j], sc[0][n][2 + j]);
             if constexpr (U == 2) top = fmaxf(top, fmaxf(sc[1][n][j], sc[1][n][2 + j]));
-            hi[n][j] = open ? top * factor[n][j] : top;
-            rise |= hi[n][j] > m[n][j] + kSlack;
+            hi[n][j] = top;
+            rise |= fmaf(top, open ? factor[n][j] : 1.f, -m[n][j]) > kSlack;
           }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float v = fmaxf(hi[n][j], m[n][j]);
+              float v = fmaxf((open ? hi[n][j] * factor[n][j] : hi[n][j]) - kBelow, m[n][j]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
               const float c = exp2_approx(m[n][j] - v);

@@ -8,9 +8,12 @@ namespace kv4 {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
-// A row's reference m moves only when a score exceeds it by more than this (in powers of two): p
-// stays below 2^8, far inside FP16, and the sums are rescaled a few times instead of at every tile.
-constexpr float kSlack = 8.0f;
+// A row's reference m is set kBelow under its largest score (all in powers of two) and moves only when a score
+// exceeds it by more than kSlack: p stays below 2^15, inside FP16, and the sums are rescaled a few times instead
+// of at every tile.  The row's largest p is then at least 2^7, and what FP16 cannot hold of a small p (2^-25)
+// is below 2^-32 of the largest: with m at the largest score itself it was 2^-25, and the many small p of a long
+// row beside one large score were in l but not in the output.
+constexpr float kSlack = 15.0f, kBelow = 7.0f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;

@@ -15,7 +15,7 @@
 //   an issuer starts the next step's first product before this step's second, so that the scores of
 //   a step are there when the last one's p have been written;
 //   four warps turn scores into p.
-// A row's m moves only when a score exceeds it by kSlack; then the output in tensor memory is rescaled.
+// A row's m moves only when a score exceeds it by more than kSlack; then the output in tensor memory is rescaled.
 //
 // A block reads no step that none of its rows sees; blocks are walked from both ends of the rows inwards,
 // so that neighbouring items of a causal chunk are about equally long together.
@@ -543,10 +543,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
 #pragma unroll
               for (int c = 0; c < CH; ++c) top = fmaxf(top, __uint_as_float(v[c]));
             }
-            return top * factor;
+            return top;
           };
-          auto raise = [&](float higher) {  // the reference; false: a wait gave up
-            higher = fmaxf(m, higher);
+          auto raise = [&](float top) {  // the reference, for that product; false: a wait gave up
+            const float higher = fmaxf(m, top * factor - kBelow);
             const float worth = exp2_approx(m - higher);
             m = higher;
             l *= worth;
@@ -594,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
               ok = raise(largest());
             }
           } else {
-            const float higher = largest();
-            if (__any_sync(0xffffffffu, higher > m + kSlack)) ok = raise(higher);
+            const float top = largest();
+            if (__any_sync(0xffffffffu, fmaf(top, factor, -m) > kSlack)) ok = raise(top);
             if (ok) powers();
           }
           if (!ok) break;

@@ -281,6 +281,57 @@ def test_attend_numbers_of_sequences(moe, seqs, group):
     check_attend(moe, rows + rng.integers(0, 70, seqs), rows, heads=1, group=group, D=128, page=16, max_rows=3, seed=seqs)
 
 
+@pytest.mark.parametrize("D,group,dtype", [(64, 1, "fp16"), (64, 12, "bf16"), (64, 24, "fp16"), (64, 40, "fp16"), (128, 1, "bf16"),
+                                           (128, 12, "fp16"), (128, 40, "fp16"), (256, 1, "fp16"), (256, 12, "fp16"),
+                                           (256, 40, "bf16")])
+def test_attend_small_p_beside_a_large_one(moe, D, group, dtype):
+    # every row's first token has a score 25.5 (in powers of two) above the others', and a value of 0: the output is what
+    # the many small p give.  As many items as there are parts of the work, so that they are cut in few places
+    seqs, heads, N, page = 40, 64, 320, 64
+    cache = moe.Kv4Cache(1, seqs * N // page, heads, D, page, seqs, N // page, v_scale=1000.0)
+    cache.reserve(dev([N] * seqs))
+    k = torch.zeros((seqs, N, heads, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.full((seqs, N, heads, D), 6000.0, dtype=torch.bfloat16, device="cuda")
+    k[:, 0], v[:, 0] = 6.0, 0.0
+    cache.append(0, k.view(-1, heads, D), v.view(-1, heads, D), dev(N * np.arange(seqs + 1)))
+    q = torch.ones((seqs, heads * group, D), dtype=DT[dtype], device="cuda")
+    lse = torch.empty((seqs, heads * group), dtype=torch.float32, device="cuda")
+    scale = 25.5 * np.log(2.0) / (6 * D)
+    out, lse = cache.attend(0, q, dev(np.arange(seqs + 1)), max_rows=1, scale=scale, lse=lse)
+    assert cache.status() == 0
+    scale = float(np.float32(scale))
+    small = (N - 1) * np.exp(-scale * 6 * D)
+    want, want_lse = 6000.0 * small / (1 + small), scale * 6 * D + np.log1p(small)
+    # p in FP16: 2^-11, and 2^-25 against a largest p of at least 2^7; the score in FP32 (18 natural units, as are its
+    # factor's roundings), exp2 to 2^-21, sums of 320 tokens; the output's own rounding
+    half = BF16_HALF_ULP_REL if dtype == "bf16" else 2.0 ** -11
+    rel = 2.0 ** -11 + 4 * 18 * 2.0 ** -23 + 2.0 ** -20 + (N / 16 + 64) * 2.0 ** -22
+    bound = want * rel + (N - 1) * 2.0 ** -25 * 2.0 ** -7 * 6000.0 + want * half * 1.01
+    assert (out.double() - want).abs().max() <= bound, (float((out.double() - want).abs().max()), bound)
+    assert (lse.double() - want_lse).abs().max() <= 4 * 18 * 2.0 ** -23 + 2.0 ** -20 + (N / 16 + 64) * 2.0 ** -22
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_scores_of_any_size(moe, D):
+    # references far from 0, where their own spacing is above 1: finite, and the tokens of the largest score
+    cache = moe.Kv4Cache(1, 8, 1, D, 64, 1, 8)
+    n = 500
+    cache.reserve(dev([n]))
+    k = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    k[:, 0, 0] = torch.arange(n, device="cuda") % 7 - 3.0          # held as 0, +-1.03, +-2.06, +-3
+    v = (torch.arange(n, device="cuda") % 7 - 3.0)[:, None, None].expand(n, 1, D).to(torch.bfloat16).contiguous()
+    cache.append(0, k, v, dev([0, n]))
+    for group in (1, 40):
+        for size in (1e3, 1e5, 1e6, 3e7):
+            q = torch.zeros((1, group, D), dtype=torch.bfloat16, device="cuda")
+            q[..., 0] = size
+            q[:, ::2, 0] = -size
+            out = cache.attend(0, q, dev([0, 1]), max_rows=1, scale=1.0).float()
+            # scores are at least 900 apart: only the tokens of the largest count
+            assert (out[:, 1::2] == 3).all() and (out[:, ::2] == -3).all(), (group, size)
+    assert cache.status() == 0
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attend_many_rows_same_bits_and_rows_apart(moe, D):
     cache, *_ = make_cache(moe, [5000, 30, 2000], 2, D, 64, seed=4)
