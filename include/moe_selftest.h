@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "moe.h"
+#include "moe_kv4.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -103,6 +104,17 @@ MOE_API int moe_selftest_expert_part(const moe_shape* shape, const uint8_t* w13_
                                      const uint8_t* w2_codes, const uint8_t* w2_scales, float w2_scale,
                                      void* workspace, size_t workspace_bytes, int algo, int part,
                                      moe_stream_t stream);
+
+/* moe_kv4_attend (no window, tree or log-sum-exp) with every wait of its kernels limited to
+ * wait_limit_cycles SM cycles.  With stuck 1 the waits for copies expect an arrival that nothing
+ * makes, so that they run out; with 0 a wait gives up where what it waits for is not there within
+ * the limit (0: at once).  A wait that gives up sets MOE_KV4_TIMEOUT; what is in flight lands,
+ * tensor memory is released, the launches complete and the outputs are undefined.  Nothing of it
+ * is left for the next call on the cache. */
+MOE_API int moe_selftest_kv4_attend(const moe_kv4_cache* cache, int layer, const void* q, int64_t q_row_stride,
+                                    int64_t q_head_stride, int q_heads, int dtype, const int32_t* cu_rows, int rows,
+                                    int max_rows, float scale, void* out, int stuck, long long wait_limit_cycles,
+                                    moe_stream_t stream);
 
 #ifdef __cplusplus
 }

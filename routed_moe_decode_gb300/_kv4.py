@@ -186,3 +186,13 @@ class Kv4Cache:
         if rc not in (_lib.MOE_OK, _lib.MOE_ERR_DEVICE):
             raise _lib.MoeError("moe_kv4_read_status", rc)
         return int(bits.value)
+
+
+def selftest_kv4_attend(cache, layer, q, cu_rows, max_rows, out, stuck, wait_limit_cycles, stream=None):
+    """cache.attend(layer, q, cu_rows, max_rows, out=out) with every wait of the kernels limited to
+    `wait_limit_cycles`, and with `stuck` the waits for copies never met (include/moe_selftest.h)."""
+    dtype, q_row, q_head, rows = cache._rows("q", q, None)
+    _lib._check("moe_selftest_kv4_attend", cache._lib.moe_selftest_kv4_attend(
+        cache._ref, layer, q.data_ptr(), q_row, q_head, q.shape[1], dtype, cache._ints("cu_rows", cu_rows, cache.seqs + 1),
+        rows, max_rows, cache._default_scale, out.data_ptr(), int(stuck), int(wait_limit_cycles), cache._stream(stream)))
+    return out

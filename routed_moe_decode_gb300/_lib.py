@@ -113,6 +113,7 @@ SIGNATURES = {
     "moe_kv4_compact": (_I, [_KP, _P, _P, _I, _I, _P]),
     "moe_kv4_read_status": (_I, [_KP, _I, ctypes.POINTER(ctypes.c_uint32), _P]),
     # include/moe_selftest.h
+    "moe_selftest_kv4_attend": (_I, [_KP, _I, _P, _L, _L, _I, _I, _P, _I, _I, _F, _P, _I, ctypes.c_longlong, _P]),
     "moe_selftest_expert_timeout": (_I, [_SP, _P, _P, _F, _P, _P, _F, _P, _P, _P, ctypes.c_size_t, _I, _I,
                                          ctypes.c_longlong, _P]),
     "moe_selftest_expert_part": (_I, [_SP, _P, _P, _F, _P, _P, _F, _P, ctypes.c_size_t, _I, _I, _P]),

@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 }
 // Wait for a phase of a barrier by the whole warp, with a limit.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long limit) {
-  bool ok = mbar_try_wait(bar, parity);
+  bool ok = phase_done(bar, parity);
   if (!__all_sync(0xffffffffu, ok)) {
     const long long t0 = clock64();
     while (!ok && clock64() - t0 < limit) ok = mbar_try_wait(bar, parity);
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   const uint8_t* ring = smem + L::kRing + warp * S * UNIT;
   uint4* queries = reinterpret_cast<uint4*>(smem + L::kQuery) + warp * (QS ? NT * (D / 32) * 32 : 0);
   const uint32_t ring_addr = smem_addr(ring), bar0 = smem_addr(smem + L::kBars + warp * S * 8);
-  if (lane < S) mbar_init(bar0 + 8 * lane, 1);
+  if (lane < S) mbar_init(bar0 + 8 * lane, a.copy_arrivals);
   fence_barrier_init();
   pdl_wait();
   pdl_launch_dependents();
@@ -210,7 +210,6 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   int stage = 0;            // next stage to be consumed; all stages are empty between items
   uint32_t parity = 0;      // bit st: of stage st's phase
   uint32_t invalid = 0;     // bits U st ..: the unit's tile has no page
-  bool dead = false;        // a copy did not arrive
   // the places of the warp's tiles in the cache, 32 at a time (32 / U units): lane l holds that of tile
   // 32 b + l, issues its copy, and has the page number of the tile 32 further on
   long long place = 0;
@@ -255,7 +254,6 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
   };
   // the first units of a part
   auto start = [&](const Walk& w) {
-    if (dead) return;
     const int page = load_page(w, lane);
     page_next = w.count > 32 / U ? load_page(w, 32 + lane) : -1;
     set_places(w, lane, page);
@@ -335,15 +333,19 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
     const int open_hi = a.tree != nullptr ? first : min(first + r0 / a.group + 1, len);
     const int open_lo = a.window > 0 ? max(first + (r0 + nrows - 1) / a.group - a.window + 1, 0) : 0;
 
-    const int n_units = dead ? 0 : cur.count;
+    const int n_units = cur.count;
     int tok0 = (cur.it.lo + cur.off) * kUnit;
     for (int i = 0; i < n_units; ++i, tok0 += kUnit) {
       const uint32_t bad = invalid >> (U * stage) & ((1u << U) - 1u);
       if (bad != (1u << U) - 1u) {
-        if (!warp_wait(bar0 + 8 * stage, parity >> stage & 1u, kWaitCycles)) {
+        if (!warp_wait(bar0 + 8 * stage, parity >> stage & 1u, a.wait_cycles)) {
           if (lane == 0) atomicOr(a.c.status, kStatusTimeout);
-          dead = true;
-          break;
+          for (int j = i; j < min(i + S, n_units); ++j) {  // what is in flight lands before the memory is given up
+            if ((invalid >> (U * stage) & ((1u << U) - 1u)) != (1u << U) - 1u)
+              warp_wait(bar0 + 8 * stage, parity >> stage & 1u, kDrainCycles);
+            if (++stage == S) stage = 0;
+          }
+          return;
         }
         parity ^= 1u << stage;
         const uint8_t* unit = ring + stage * UNIT;
@@ -502,10 +504,6 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
       }
       if (i + S < n_units) issue(cur, i + S, stage);
       if (++stage == S) stage = 0;
-    }
-    if (dead) {  // let what is still in flight land before the memory is given up
-      for (int st = 0; st < S; ++st)
-        if ((invalid >> (U * st) & ((1u << U) - 1u)) != (1u << U) - 1u) warp_wait(bar0 + 8 * st, parity >> st & 1u, kDrainCycles);
     }
     // the next part of the chunk: its first units are in flight while this one's results leave
     if (lane == 0) advance<ROWS, kUnit>(steps, cur, s_walk[warp][turn ^ 1], s_chunk[warp].end);

@@ -27,8 +27,20 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 
 constexpr float kLowest = -3.0e38f;  // a row's reference before it has seen a token
 constexpr int kStatusTimeout = static_cast<int>(MOE_KV4_TIMEOUT);
-constexpr long long kWaitCycles = 1ll << 32;   // ~2 s: a copy takes microseconds
-constexpr long long kDrainCycles = 1ll << 24;
+constexpr long long kDrainCycles = 1ll << 24;  // ~8 ms, for what is in flight after a wait gave up
+
+// Whether a barrier's phase is complete.
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // A sequence's items.
 struct Item {

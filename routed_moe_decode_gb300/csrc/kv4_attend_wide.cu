@@ -61,19 +61,6 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t next)
          uint64_t(1u) << 46 | uint64_t(2u) << 61;
 }
 
-// Whether a barrier's phase is complete.
-__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // 32 lanes x 32 bits, 8 or 16 consecutive columns, written.
 __device__ __forceinline__ void tmem_store(uint32_t t, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]), "r"(v[1]),
@@ -189,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
                  drain = q_full + 8;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, a.copy_arrivals);
       mbar_init(taken + 8 * i, kDeq);
     }
     for (int i = 0; i < 2; ++i) {
@@ -257,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
     bool ok = phase_done(bar, parity & 1u);
     if (!__all_sync(0xffffffffu, ok)) {
       const long long t0 = clock64();
-      while (!ok && clock64() - t0 < kWaitCycles && *reinterpret_cast<volatile int*>(&s_abort) == 0)
+      while (!ok && clock64() - t0 < a.wait_cycles && *reinterpret_cast<volatile int*>(&s_abort) == 0)
         ok = mbar_try_wait(bar, parity & 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) {
@@ -327,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
       __syncwarp();
       if (!s_walk[kSoft][turn ^ 1].more) break;
     }
+    uint32_t r = n > S ? n - S : 0;  // first of the steps that may not have landed
     if (ok) {
       const uint32_t st = n % S;
       if (n < S || wait(taken + 8 * st, n / S - 1)) {
@@ -334,13 +322,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
           *reinterpret_cast<volatile uint32_t*>(&s_info[n % kInfos]) = kEnd;
           mbar_arrive(full + 8 * st);
         }
+        if (n >= S) r = n - S + 1;  // step n - S has been taken, and its stage's barrier says the end
       }
-    } else {  // let what is still in flight land before the memory is given up
-      const long long t0 = clock64();
-      for (uint32_t r = n > S ? n - S : 0; r < n; ++r)
-        while (!phase_done(full + 8 * (r % S), (r / S) & 1u) && clock64() - t0 < kDrainCycles) {
-        }
     }
+    // whichever role gives up, now or later: the copies land before the memory is given up
+    const long long t0 = clock64();
+    for (; r < n; ++r)
+      while (!mbar_try_wait(full + 8 * (r % S), (r / S) & 1u) && clock64() - t0 < kDrainCycles) {
+      }
   } else if (warp == kIssuer) {
     // the products, by one lane of a converged warp
     const uint64_t q_desc = smem_desc_sw128(base + L::kQ, 1024);
@@ -663,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
       }
       if (!s_walk[warp][turn ^ 1].more) break;
     }
+    tc_wait_st();  // of a step that was left
   }
   __syncwarp();
   tc_fence_before();

@@ -1,6 +1,7 @@
 // Host entry points of the 4-bit K/V cache (include/moe_kv4.h).
 #include <cmath>
 
+#include "../../include/moe_selftest.h"
 #include "kv4_common.cuh"
 
 namespace {
@@ -67,6 +68,40 @@ bool rows_ok(const void* p, int64_t row_stride, int64_t head_stride) {
   return p && aligned(p, 16) && row_stride % 8 == 0 && head_stride % 8 == 0;
 }
 
+int attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+           int dtype, const int32_t* cu_rows, int rows, int max_rows, float scale, int window, const uint64_t* tree,
+           void* out, float* lse, long long wait_cycles, int copy_arrivals, moe_stream_t stream) {
+  moe::kv4::AttendArgs a{};
+  WsLayout L;
+  int rc = view(c, layer, &a.c, &L);
+  if (rc != MOE_OK) return rc;
+  if (rows < 0 || max_rows < 0 || window < 0 || q_heads <= 0 || q_heads % c->kv_heads || !dtype_ok(dtype) ||
+      !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (tree && (window > 0 || max_rows > moe::kv4::kStepRows)) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(rows) * q_heads > 0x7fffffffll / 2) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!rows_ok(q, q_row_stride, q_head_stride) || !cu_rows || !aligned(cu_rows, 4) || !out || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(tree, 8))
+    return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = moe::device_sms(&sms);
+  if (rc != MOE_OK) return rc;
+  a.q = q; a.q_row = q_row_stride; a.q_head = q_head_stride;
+  a.group = q_heads / c->kv_heads;
+  a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16;
+  a.scale2 = scale * c->k_scale * 1.44269504088896340736f;
+  a.v_ts = c->v_scale;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // as many tokens as there can be; first - window stays an int
+  a.tree = reinterpret_cast<const unsigned long long*>(tree);
+  a.out = out; a.lse = lse;
+  a.part = at<float>(c, L.part);
+  a.pieces = at<moe::kv4::Piece>(c, L.pieces);
+  a.wait_cycles = wait_cycles; a.copy_arrivals = copy_arrivals;
+  const int64_t block = static_cast<int64_t>(max_rows < 1 ? 1 : max_rows) * a.group;
+  return done("attend launch", moe::kv4::launch_attend(a, static_cast<int>(block > 1024 ? 1024 : block), sms, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -131,34 +166,17 @@ int moe_kv4_read(const moe_kv4_cache* c, int layer, void* k, void* v, int dtype,
 int moe_kv4_attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride,
                    int q_heads, int dtype, const int32_t* cu_rows, int rows, int max_rows, float scale, int window,
                    const uint64_t* tree, void* out, float* lse, moe_stream_t stream) {
-  moe::kv4::AttendArgs a{};
-  WsLayout L;
-  int rc = view(c, layer, &a.c, &L);
-  if (rc != MOE_OK) return rc;
-  if (rows < 0 || max_rows < 0 || window < 0 || q_heads <= 0 || q_heads % c->kv_heads || !dtype_ok(dtype) ||
-      !std::isfinite(scale))
-    return MOE_ERR_INVALID_ARG;
-  if (tree && (window > 0 || max_rows > moe::kv4::kStepRows)) return MOE_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(rows) * q_heads > 0x7fffffffll / 2) return MOE_ERR_UNSUPPORTED;
-  if (rows == 0) return MOE_OK;
-  if (!rows_ok(q, q_row_stride, q_head_stride) || !cu_rows || !aligned(cu_rows, 4) || !out || !aligned(out, 16) ||
-      !aligned(lse, 4) || !aligned(tree, 8))
-    return MOE_ERR_INVALID_ARG;
-  int sms = 0;
-  rc = moe::device_sms(&sms);
-  if (rc != MOE_OK) return rc;
-  a.q = q; a.q_row = q_row_stride; a.q_head = q_head_stride;
-  a.group = q_heads / c->kv_heads;
-  a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16;
-  a.scale2 = scale * c->k_scale * 1.44269504088896340736f;
-  a.v_ts = c->v_scale;
-  a.window = window < (1 << 30) ? window : 1 << 30;  // as many tokens as there can be; first - window stays an int
-  a.tree = reinterpret_cast<const unsigned long long*>(tree);
-  a.out = out; a.lse = lse;
-  a.part = at<float>(c, L.part);
-  a.pieces = at<moe::kv4::Piece>(c, L.pieces);
-  const int64_t block = static_cast<int64_t>(max_rows < 1 ? 1 : max_rows) * a.group;
-  return done("attend launch", moe::kv4::launch_attend(a, static_cast<int>(block > 1024 ? 1024 : block), sms, stream));
+  return attend(c, layer, q, q_row_stride, q_head_stride, q_heads, dtype, cu_rows, rows, max_rows, scale, window, tree, out,
+                lse, moe::kv4::kWaitCycles, 1, stream);
+}
+
+int moe_selftest_kv4_attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_row_stride,
+                            int64_t q_head_stride, int q_heads, int dtype, const int32_t* cu_rows, int rows,
+                            int max_rows, float scale, void* out, int stuck, long long wait_limit_cycles,
+                            moe_stream_t stream) {
+  if (stuck < 0 || stuck > 1 || wait_limit_cycles < 0) return MOE_ERR_INVALID_ARG;
+  return attend(c, layer, q, q_row_stride, q_head_stride, q_heads, dtype, cu_rows, rows, max_rows, scale, 0, nullptr, out,
+                nullptr, wait_limit_cycles, 1 + stuck, stream);
 }
 
 int moe_kv4_reserve(const moe_kv4_cache* c, const int32_t* new_tokens, moe_stream_t stream) {
