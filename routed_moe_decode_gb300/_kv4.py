@@ -28,7 +28,8 @@ class Kv4Cache:
         table [seqs, max_pages] int32   page numbers of each sequence's tokens, -1 past them
         lens  [seqs] int32              tokens of each sequence
         refs  [pages] int32             table entries that point at each page (0: free)
-    k_scale, v_scale: FP32 tensor scales of the values.  One cache's calls are ordered on one stream.
+    k_scale, v_scale: FP32 tensor scales of the values.  One cache's calls are ordered on one stream,
+    and its device is the current one when they are made.
 
     A step: reserve(new_tokens); for every layer append(...) and attend(...); compact(keep, ...).
     Rows of a step are those of sequence 0, then of sequence 1, ...; cu_rows [seqs + 1] int32 on the
@@ -73,12 +74,8 @@ class Kv4Cache:
             raise ValueError(f"{name}: contiguous {list(shape)} of {dtype} on {device}")
         return t
 
-    def _stream(self, stream):
-        return _raw_stream(self._index) if stream is None else stream.cuda_stream
-
     def _call(self, fn, stream, *args):
-        index = self.device.index
-        rc = getattr(self._lib, fn)(self._ref, *args, _raw_stream(index) if stream is None else stream.cuda_stream)
+        rc = getattr(self._lib, fn)(self._ref, *args, _raw_stream(self._index, stream))
         if rc != 0:
             raise _lib.MoeError(fn, rc)
 
@@ -106,7 +103,7 @@ class Kv4Cache:
         if v_dtype != dtype or v_rows != rows:
             raise ValueError("k and v: of one type and as many rows")
         rc = self._append(self._ref, layer, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row, v_head, dtype,
-                          self._ints("cu_rows", cu_rows, self.seqs + 1), rows, self._stream(stream))
+                          self._ints("cu_rows", cu_rows, self.seqs + 1), rows, _raw_stream(self._index, stream))
         if rc != 0:
             raise _lib.MoeError("moe_kv4_append", rc)
 
@@ -124,7 +121,7 @@ class Kv4Cache:
         if v_code != code or v_n != n or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("out: two contiguous tensors of one type and as many rows")
         rc = self._read(self._ref, layer, k.data_ptr(), v.data_ptr(), code, self._ints("cu_rows", cu_rows, self.seqs + 1),
-                        n, self._stream(stream))
+                        n, _raw_stream(self._index, stream))
         if rc != 0:
             raise _lib.MoeError("moe_kv4_read", rc)
         return out
@@ -151,7 +148,7 @@ class Kv4Cache:
                           self._ints("cu_rows", cu_rows, self.seqs + 1), rows, max_rows,
                           self._default_scale if scale is None else scale, window,
                           None if tree is None else tree.data_ptr(), out.data_ptr(),
-                          None if lse is None else lse.data_ptr(), self._stream(stream))
+                          None if lse is None else lse.data_ptr(), _raw_stream(self._index, stream))
         if rc != 0:
             raise _lib.MoeError("moe_kv4_attend", rc)
         return out if lse is None else (out, lse)
@@ -182,7 +179,7 @@ class Kv4Cache:
     def status(self, clear=True, stream=None):
         """The cache's status bits (KV4_*), waiting for the stream."""
         bits = ctypes.c_uint32(0)
-        rc = self._lib.moe_kv4_read_status(self._ref, 1 if clear else 0, ctypes.byref(bits), self._stream(stream))
+        rc = self._lib.moe_kv4_read_status(self._ref, 1 if clear else 0, ctypes.byref(bits), _raw_stream(self._index, stream))
         if rc not in (_lib.MOE_OK, _lib.MOE_ERR_DEVICE):
             raise _lib.MoeError("moe_kv4_read_status", rc)
         return int(bits.value)
@@ -194,5 +191,5 @@ def selftest_kv4_attend(cache, layer, q, cu_rows, max_rows, out, stuck, wait_lim
     dtype, q_row, q_head, rows = cache._rows("q", q, None)
     _lib._check("moe_selftest_kv4_attend", cache._lib.moe_selftest_kv4_attend(
         cache._ref, layer, q.data_ptr(), q_row, q_head, q.shape[1], dtype, cache._ints("cu_rows", cu_rows, cache.seqs + 1),
-        rows, max_rows, cache._default_scale, out.data_ptr(), int(stuck), int(wait_limit_cycles), cache._stream(stream)))
+        rows, max_rows, cache._default_scale, out.data_ptr(), int(stuck), int(wait_limit_cycles), _raw_stream(cache._index, stream)))
     return out

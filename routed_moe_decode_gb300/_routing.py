@@ -10,8 +10,25 @@ from . import _lib
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-def _raw_stream(device_index):
-    return torch._C._cuda_getCurrentRawStream(device_index)
+_devices = 0  # CUDA devices that there are, counted at the first call
+
+
+def _raw_stream(index, stream=None):
+    """The handle of `stream`, or of the current stream, for a call on tensors of CUDA device `index`.  A launch goes to
+    the current device (handle 0 is that device's default stream), so another device than the tensors' is refused;
+    where there is one device it is not asked for, which takes 0.2 us."""
+    global _devices
+    if _devices != 1:
+        _devices = _devices or torch.cuda.device_count()
+        current = torch.cuda.current_device()
+        if current != index:
+            raise ValueError(f"the tensors lie on cuda:{index} and the current device is cuda:{current}: call it under "
+                             f"torch.cuda.device({index})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the tensors lie on cuda:{index} and the stream is one of {stream.device}")
+    return stream.cuda_stream
 
 
 class Routing:
@@ -56,7 +73,7 @@ class Routing:
             raise ValueError("logits, bias, ids and weights lie on one CUDA device")
         rc = self._route(self._ref, T, logits.data_ptr(), logits.stride(0) if T > 1 else E, dtype,
                          None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                         _raw_stream(index) if stream is None else stream.cuda_stream)
+                         _raw_stream(index, stream))
         if rc != 0:
             raise _lib.MoeError("moe_route_grouped", rc)
         return ids, weights

@@ -715,6 +715,30 @@ def test_fork_bad_sequences_are_reported(moe):
     assert cache.status() == moe.KV4_BAD_SEQ
 
 
+def test_another_current_device_is_refused(moe, monkeypatch):
+    from routed_moe_decode_gb300 import _routing
+    cache, *_ = make_cache(moe, [20, 30], 2, 64, 16)
+    cu, q = dev([0, 1, 2]), torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    r = moe.Routing(16, 2)
+    route = (torch.zeros((3, 16), device="cuda"), None, torch.zeros((3, 2), dtype=torch.int32, device="cuda"),
+             torch.zeros((3, 2), device="cuda"))
+    calls = [lambda: cache.append(0, q, q, cu), lambda: cache.read(0, cu, rows=2), lambda: cache.attend(0, q, cu, max_rows=1),
+             lambda: cache.reserve(dev([0, 0])), lambda: cache.trim(dev([20, 30])), lambda: cache.fork(dev([0]), dev([1])),
+             lambda: cache.compact(dev([1, 1], torch.uint8), cu, max_rows=1), cache.status, lambda: r.route(*route),
+             lambda: moe.Kv4Cache(1, 4, 2, 64, 16, 2, 4, device="cuda:0")]
+    before = [t.clone() for t in (cache.pool, cache.table, cache.lens, cache.refs)]
+    monkeypatch.setattr(_routing, "_devices", 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)  # the tensors lie on device 0
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    monkeypatch.undo()
+    for a, b in zip(before, (cache.pool, cache.table, cache.lens, cache.refs)):
+        assert torch.equal(a, b)
+    for call in calls:
+        call()
+
+
 def test_refusals(moe):
     with pytest.raises(moe.MoeError):
         moe.Kv4Cache(1, 4, 2, 96, 16, 2, 4)  # head size
