@@ -423,9 +423,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float v = fmaxf((open ? hi[n][j] * factor[n][j] : hi[n][j]) - kBelow, m[n][j]);
+              float top = hi[n][j];
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              // of the rows that need it alone: a row's result does not depend on the block's others
+              const float f = open ? factor[n][j] : 1.f;
+              const float v = fmaf(top, f, -m[n][j]) > kSlack ? top * f - kBelow : m[n][j];
               const float c = exp2_approx(m[n][j] - v);
               m[n][j] = v;
               l[n][j] *= c;

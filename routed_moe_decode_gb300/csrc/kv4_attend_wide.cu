@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
             return top;
           };
           auto raise = [&](float top) {  // the reference, for that product; false: a wait gave up
-            const float higher = fmaxf(m, top * factor - kBelow);
+            // of the rows that need it alone: a row's result does not depend on the block's others
+            const float higher = fmaf(top, factor, -m) > kSlack ? top * factor - kBelow : m;
             const float worth = exp2_approx(m - higher);
             m = higher;
             l *= worth;

@@ -350,6 +350,31 @@ def test_attend_many_rows_same_bits_and_rows_apart(moe, D):
     assert cache.status() == 0
 
 
+@pytest.mark.parametrize("D,group", [(64, 8), (64, 16), (64, 32), (64, 40), (128, 8), (128, 16), (128, 40), (256, 8), (256, 16),
+                                     (256, 40)])
+def test_attend_rows_do_not_depend_on_their_neighbours(moe, D, group):
+    # one row of a head has scores that rise by far more than the others' in the middle of the sequence: the others'
+    # bits stay.  So many heads that a part of the work is several steps long
+    n, heads, page = 6400, 64, 128
+    cache = moe.Kv4Cache(1, n // page, heads, D, page, 1, n // page)
+    cache.reserve(dev([n]))
+    g = torch.Generator(device="cuda").manual_seed(D + group)
+    k, v = (torch.randn((n, heads, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    cache.append(0, k, v, dev([0, n]))
+    q = torch.randn((1, heads, group, D), generator=g, device="cuda").to(torch.bfloat16)
+    cu, at = dev([0, 1]), torch.arange(heads, device="cuda")
+    first = cache.attend(0, q.view(1, -1, D), cu, max_rows=1).view(heads, group, D)
+    for row in (0, 5):
+        token = (97 * at + 150) % n
+        other = q.clone()
+        other[0, :, row] = 4 * k[token, at]
+        got = cache.attend(0, other.view(1, -1, D), cu, max_rows=1).view(heads, group, D)
+        apart = torch.arange(group, device="cuda") != row
+        assert torch.equal(first[:, apart], got[:, apart]), row
+        assert (got[:, row].float() - v[token, at].float()).abs().max() < 1
+    assert cache.status() == 0
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attend_many_rows_bad_page_and_stale_tokens(moe, D):
     lens, page = [300, 100], 32
