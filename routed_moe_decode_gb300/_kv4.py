@@ -79,6 +79,13 @@ class Kv4Cache:
         if rc != 0:
             raise _lib.MoeError(fn, rc)
 
+    def _new(self, make, shape, dtype, stream):
+        """A result that the call makes: of the stream that it runs on, as whose its memory is filled and given back."""
+        if stream is None:
+            return make(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return make(shape, dtype=dtype, device=self.device)
+
     def _ints(self, name, t, n):
         if t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous() or t.dim() != 1 or \
                 (n is not None and t.shape[0] != n):
@@ -113,8 +120,7 @@ class Kv4Cache:
         if out is None:
             if rows is None:
                 raise ValueError("rows or out is needed")
-            out = tuple(torch.zeros((rows, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
-                        for _ in range(2))
+            out = tuple(self._new(torch.zeros, (rows, self.kv_heads, self.head_dim), dtype, stream) for _ in range(2))
         k, v = out
         code, _, _, n = self._rows("out[0]", k, self.kv_heads)
         v_code, _, _, v_n = self._rows("out[1]", v, self.kv_heads)
@@ -135,7 +141,7 @@ class Kv4Cache:
         dtype, q_row, q_head, rows = self._rows("q", q, None)
         heads = q.shape[1]
         if out is None:
-            out = torch.empty((rows, heads, self.head_dim), dtype=q.dtype, device=self.device)
+            out = self._new(torch.empty, (rows, heads, self.head_dim), q.dtype, stream)
         elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != self._index or not out.is_contiguous():
             raise ValueError("out: contiguous, of q's shape and type")
         if lse is not None and (lse.shape != (rows, heads) or lse.dtype is not torch.float32 or

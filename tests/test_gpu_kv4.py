@@ -229,6 +229,31 @@ def test_attend_on_another_stream_and_in_a_graph(moe):
     assert torch.equal(out, want)
 
 
+def test_results_made_on_another_stream(moe):
+    # the current stream is busy and then writes into memory it has freed: a call on another stream, which makes its own
+    # results, is not disturbed by either
+    cache, *_ = make_cache(moe, [500, 77], 2, 128, 64, seed=8)
+    q = torch.randn((4, 8, 128), device="cuda").to(torch.bfloat16)
+    cu = dev([0, 2, 4])
+    want, held = cache.attend(0, q, cu, max_rows=2).clone(), [t.clone() for t in cache.read(0, cu, rows=4)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    junk = [torch.empty_like(t) for t in (want, *held)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # about 50 ms
+    for t in junk:
+        t.fill_(7.0)
+    del junk, t
+    out = cache.attend(0, q, cu, max_rows=2, stream=side)
+    got = cache.read(0, cu, rows=4, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    for a, b in zip(got, held):
+        assert torch.equal(a, b)
+    assert cache.status() == 0
+
+
 # Blocks of many rows (a step's rows times query heads per K/V head).
 
 @pytest.mark.parametrize("D,group,dtype", [(64, 4, "bf16"), (64, 7, "fp16"), (128, 4, "fp16"), (128, 1, "bf16"), (256, 3, "bf16")])
