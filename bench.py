@@ -21,6 +21,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -180,13 +181,28 @@ def load_tensor_peak():
     return 1900.0, "fallback bf16 (burst)"
 
 
-def kernel_source_digest(kernel: str) -> str:
-    """First 16 hex digits of the SHA-256 of the kernel's .cu file followed by every shared
-    header of the CUDA sources (sorted by name): the source a DRAM capture was taken of."""
+def kernel_headers(kernel: str):
+    """The shared headers of the CUDA sources that the kernel's .cu file includes, directly or
+    through one another, sorted by name."""
     csrc = os.path.join(ROOT, "routed_moe_decode_gb300", "csrc")
-    h = hashlib.sha256(open(os.path.join(csrc, f"{kernel}.cu"), "rb").read())
-    for name in sorted(f for f in os.listdir(csrc) if f.endswith(".cuh")):
-        h.update(open(os.path.join(csrc, name), "rb").read())
+    found, todo = set(), [f"{kernel}.cu"]
+    while todo:
+        with open(os.path.join(csrc, todo.pop()), encoding="utf-8") as f:
+            for name in re.findall(r'^#include "(\w+\.cuh)"', f.read(), flags=re.M):
+                if name not in found:
+                    found.add(name)
+                    todo.append(name)
+    return sorted(found)
+
+
+def kernel_source_digest(kernel: str) -> str:
+    """First 16 hex digits of the SHA-256 of the kernel's .cu file followed by the shared headers
+    that it includes: the source a DRAM capture was taken of."""
+    csrc = os.path.join(ROOT, "routed_moe_decode_gb300", "csrc")
+    h = hashlib.sha256()
+    for name in [f"{kernel}.cu", *kernel_headers(kernel)]:
+        with open(os.path.join(csrc, name), "rb") as f:
+            h.update(f.read())
     return h.hexdigest()[:16]
 
 

@@ -8,7 +8,7 @@
 #include <mutex>
 
 #include "../../include/moe_selftest.h"
-#include "moe_kernels.cuh"
+#include "launch.cuh"
 
 namespace {
 

@@ -3,7 +3,7 @@
 #pragma once
 
 #include "../../include/moe_kv4.h"
-#include "moe_kernels.cuh"
+#include "launch.cuh"
 
 namespace moe {
 namespace kv4 {
