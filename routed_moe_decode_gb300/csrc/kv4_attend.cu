@@ -46,11 +46,11 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   return d;
 }
 // Wait for a phase of a barrier by the whole warp, with a limit.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long limit) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t limit) {
   bool ok = phase_done(bar, parity);
   if (!__all_sync(0xffffffffu, ok)) {
-    const long long t0 = clock64();
-    while (!ok && clock64() - t0 < limit) ok = mbar_try_wait(bar, parity);
+    const uint32_t t0 = cycles();
+    while (!ok && cycles() - t0 < limit) ok = mbar_try_wait(bar, parity);
     ok = __all_sync(0xffffffffu, ok);
   }
   return ok;
@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         const int e = static_cast<int>(__float_as_uint(top) >> 23);
         const int shift = e == 0 || e == 255 ? 0 : min(max(137 - e, -100), 100);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23) * sign;
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) * size;
+        // above 0, so that a masked score stays -infinity
+        const float down = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - shift) << 23) * size, 1.2e-38f);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           const float2 f = unpack2(raw[i], a.fp16);
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         }
         // ---- masks, running reference, p ----
         const bool open = tok0 >= open_lo && tok0 + kUnit <= open_hi && bad == 0;
-        if (!open) {  // products become scores here; their factors are 1 below
+        if (!open) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
                 } else {
                   see = see && tok <= x && (a.window <= 0 || tok > x - a.window);
                 }
-                sc[u][n][j] = see ? sc[u][n][j] * factor[n][j & 1] : -INFINITY;
+                if (!see) sc[u][n][j] = -INFINITY;
               }
         }
         float hi[NT][2];  // the largest product; compared as its p's exponent is formed, so that no p is above 2^kSlack
@@ -414,9 +415,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float top = fmaxf(sc[0][n][j], sc[0][n][2 + j]);
-            if constexpr (U == 2) top = fmaxf(top, fmaxf(sc[1][n][j], sc[1][n][2 + j]));
+            top = fmaxf(top, fmaxf(sc[1][n][j], sc[1][n][2 + j]));
             hi[n][j] = top;
-            rise |= fmaf(top, open ? factor[n][j] : 1.f, -m[n][j]) > kSlack;
+            rise |= fmaf(top, factor[n][j], -m[n][j]) > kSlack;
           }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -427,8 +428,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
               // of the rows that need it alone: a row's result does not depend on the block's others
-              const float f = open ? factor[n][j] : 1.f;
-              const float v = fmaf(top, f, -m[n][j]) > kSlack ? top * f - kBelow : m[n][j];
+              const float v = fmaf(top, factor[n][j], -m[n][j]) > kSlack ? top * factor[n][j] - kBelow : m[n][j];
               const float c = exp2_approx(m[n][j] - v);
               m[n][j] = v;
               l[n][j] *= c;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) attend_kernel(AttendArgs a) {
         uint32_t pf[U][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float f0 = open ? factor[n][0] : 1.f, f1 = open ? factor[n][1] : 1.f;
+          const float f0 = factor[n][0], f1 = factor[n][1];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const float p0 = exp2_approx(fmaf(sc[u][n][0], f0, -m[n][0])), p1 = exp2_approx(fmaf(sc[u][n][1], f1, -m[n][1]));

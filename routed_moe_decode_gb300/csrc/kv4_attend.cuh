@@ -27,7 +27,10 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 
 constexpr float kLowest = -3.0e38f;  // a row's reference before it has seen a token
 constexpr int kStatusTimeout = static_cast<int>(MOE_KV4_TIMEOUT);
-constexpr long long kDrainCycles = 1ll << 24;  // ~8 ms, for what is in flight after a wait gave up
+constexpr uint32_t kDrainCycles = 1u << 24;  // ~8 ms, for what is in flight after a wait gave up
+
+// Cycles, of which differences below 2^32 count: every wait has its own copy of the comparison.
+__device__ __forceinline__ uint32_t cycles() { return static_cast<uint32_t>(clock()); }
 
 // Whether a barrier's phase is complete.
 __device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {

@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
   __shared__ long long s_scan[kWarps];
   __shared__ Walk s_walk[kSoft + 1][2];  // of the warps that walk the items: this part, the next
   __shared__ uint32_t s_info[kInfos], s_tmem;
-  __shared__ int s_abort;
+  __shared__ uint32_t s_limit;  // of a wait, in cycles; 0 once one gave up
+  __shared__ uint32_t s_landed, s_issued;  // steps whose copies the loader knows to have landed, has started
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_addr(smem);
   int* s_cu = reinterpret_cast<int*>(smem + L::kSeqs);
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
     for (int i = 0; i < VB; ++i) mbar_init(v_full + 8 * i, kDeq);
     mbar_init(q_full, kSoft);
     mbar_init(drain, 1);
-    s_abort = 0;
+    s_limit = a.wait_cycles;
   }
   fence_barrier_init();
   pdl_wait();
@@ -243,12 +244,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
   auto wait = [&](uint32_t bar, uint32_t parity) {
     bool ok = phase_done(bar, parity & 1u);
     if (!__all_sync(0xffffffffu, ok)) {
-      const long long t0 = clock64();
-      while (!ok && clock64() - t0 < a.wait_cycles && *reinterpret_cast<volatile int*>(&s_abort) == 0)
-        ok = mbar_try_wait(bar, parity & 1u);
+      const uint32_t t0 = cycles();
+      while (!ok && cycles() - t0 < *reinterpret_cast<volatile uint32_t*>(&s_limit)) ok = mbar_try_wait(bar, parity & 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) {
-        *reinterpret_cast<volatile int*>(&s_abort) = 1;
+        *reinterpret_cast<volatile uint32_t*>(&s_limit) = 0;
         atomicOr(a.c.status, kStatusTimeout);
       }
     }
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
       __syncwarp();
       if (!s_walk[kSoft][turn ^ 1].more) break;
     }
-    uint32_t r = n > S ? n - S : 0;  // first of the steps that may not have landed
+    uint32_t landed = n > S ? n - S : 0;
     if (ok) {
       const uint32_t st = n % S;
       if (n < S || wait(taken + 8 * st, n / S - 1)) {
@@ -322,14 +322,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
           *reinterpret_cast<volatile uint32_t*>(&s_info[n % kInfos]) = kEnd;
           mbar_arrive(full + 8 * st);
         }
-        if (n >= S) r = n - S + 1;  // step n - S has been taken, and its stage's barrier says the end
+        if (n >= S) landed = n - S + 1;  // step n - S has been taken, and its stage's barrier says the end
       }
     }
-    // whichever role gives up, now or later: the copies land before the memory is given up
-    const long long t0 = clock64();
-    for (; r < n; ++r)
-      while (!mbar_try_wait(full + 8 * (r % S), (r / S) & 1u) && clock64() - t0 < kDrainCycles) {
-      }
+    if (lane == 0) {
+      s_landed = landed;
+      s_issued = n;
+    }
   } else if (warp == kIssuer) {
     // the products, by one lane of a converged warp
     const uint64_t q_desc = smem_desc_sw128(base + L::kQ, 1024);
@@ -659,11 +658,17 @@ __global__ void __launch_bounds__(kThreads, CTAS) attend_wide_kernel(AttendArgs 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s_abort != 0 && warp == kIssuer) {  // let the products in flight end before the memory is given up
-    if (elect_one()) tc_commit(drain);
-    __syncwarp();
-    const long long t0 = clock64();
-    while (!phase_done(drain, 0) && clock64() - t0 < kDrainCycles) {
+  if (s_limit == 0) {  // whichever role gave up: what is in flight ends before the memory is given up
+    const uint32_t t0 = cycles();
+    if (warp == kIssuer) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      while (!phase_done(drain, 0) && cycles() - t0 < kDrainCycles) {
+      }
+    } else if (warp == kLoader) {
+      for (uint32_t r = s_landed; r < s_issued; ++r)
+        while (!phase_done(full + 8 * (r % S), (r / S) & 1u) && cycles() - t0 < kDrainCycles) {
+        }
     }
   }
   __syncthreads();

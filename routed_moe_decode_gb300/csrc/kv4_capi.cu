@@ -70,7 +70,7 @@ bool rows_ok(const void* p, int64_t row_stride, int64_t head_stride) {
 
 int attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride, int q_heads,
            int dtype, const int32_t* cu_rows, int rows, int max_rows, float scale, int window, const uint64_t* tree,
-           void* out, float* lse, long long wait_cycles, int copy_arrivals, moe_stream_t stream) {
+           void* out, float* lse, uint32_t wait_cycles, int copy_arrivals, moe_stream_t stream) {
   moe::kv4::AttendArgs a{};
   WsLayout L;
   int rc = view(c, layer, &a.c, &L);
@@ -175,8 +175,9 @@ int moe_selftest_kv4_attend(const moe_kv4_cache* c, int layer, const void* q, in
                             int max_rows, float scale, void* out, int stuck, long long wait_limit_cycles,
                             moe_stream_t stream) {
   if (stuck < 0 || stuck > 1 || wait_limit_cycles < 0) return MOE_ERR_INVALID_ARG;
+  const uint32_t limit = static_cast<uint32_t>(wait_limit_cycles < 0xffffffffll ? wait_limit_cycles : 0xffffffffll);
   return attend(c, layer, q, q_row_stride, q_head_stride, q_heads, dtype, cu_rows, rows, max_rows, scale, 0, nullptr, out,
-                nullptr, wait_limit_cycles, 1 + stuck, stream);
+                nullptr, limit, 1 + stuck, stream);
 }
 
 int moe_kv4_reserve(const moe_kv4_cache* c, const int32_t* new_tokens, moe_stream_t stream) {

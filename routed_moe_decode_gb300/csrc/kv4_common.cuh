@@ -27,7 +27,7 @@ struct Cache {
   size_t page_bytes;    // heads * tiles_per_page * tile_bytes
 };
 
-constexpr long long kWaitCycles = 1ll << 32;  // ~2 s: a copy takes microseconds
+constexpr uint32_t kWaitCycles = 1u << 31;  // ~1 s: a copy takes microseconds
 
 // An item of the attention's work that its first chunk does not end (on: there is one).
 struct alignas(16) Piece {
@@ -158,7 +158,7 @@ struct AttendArgs {
   int chunks;           // the number of chunks
   float* part;
   Piece* pieces;
-  long long wait_cycles;  // limit of every wait
+  uint32_t wait_cycles;  // limit of every wait
   int copy_arrivals;      // arrivals that complete a stage's barrier: 1; 2, which none has, in the self-test
 };
 
