@@ -62,7 +62,7 @@ extern "C" {
 typedef enum moe_kv4_dtype { MOE_KV4_BF16 = 0, MOE_KV4_FP16 = 1 } moe_kv4_dtype;
 
 /* One cache.  head_dim 64, 128 or 256; page_size a multiple of 16 up to 1024; kv_heads 1 to
- * 1024; seqs and pages up to 65536 and 2^30; pool and workspace 256-byte aligned.
+ * 1024; seqs and pages up to 65535 and 2^30; pool and workspace 256-byte aligned.
  *   lens  [seqs] int32             tokens of each sequence (0: empty)
  *   table [seqs][max_pages] int32  page numbers of its tokens, -1 past them
  *   refs  [pages] int32            table entries that point at a page; 0: the page is free
@@ -79,7 +79,7 @@ typedef struct moe_kv4_cache {
 } moe_kv4_cache;
 
 /* Bytes of one page of one layer, and of the workspace of a cache (0 if the sizes are
- * unsupported).  Host functions: need no GPU and no pointer of the cache. */
+ * unsupported): 43 MB for partial results of the attention, whatever the sizes, and 28 a sequence.  Host functions: need no GPU and no pointer of the cache. */
 MOE_API size_t moe_kv4_page_bytes(const moe_kv4_cache* cache);
 MOE_API size_t moe_kv4_workspace_bytes(const moe_kv4_cache* cache);
 
@@ -115,7 +115,9 @@ MOE_API int moe_kv4_read(const moe_kv4_cache* cache, int layer, void* k, void* v
  * was refused, gets out 0 and lse -infinity.
  *   q        [rows][q_heads][head_dim] of `dtype`; strides in elements, multiples of 8
  *   max_rows the largest number of rows of a sequence, as far as the host knows: it chooses the
- *            kernel's tile; more rows are computed all the same
+ *            kernel's tile, for the whole call; more rows are computed all the same.  A prompt's
+ *            chunk among single rows is faster in a call of its own, with cu_rows that leave the
+ *            others out
  *   tree     [rows] uint64 or NULL
  *   out      [rows][q_heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   lse      [rows][q_heads] float or NULL

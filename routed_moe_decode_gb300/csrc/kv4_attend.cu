@@ -28,10 +28,10 @@
 // in the order of the chunks, so results do not depend on timing.  The chunks are found on the device
 // from the lengths: no host wait, no plan.
 //
-// Measured: four sequences of 131072 tokens, 8 K/V heads of 128 with 8 query heads each (604 MB) 114 us, 0.78 of the
-// copy bandwidth; 32 sequences of 4096 to 8192 tokens, 16 rows (228 MB) 73 us, of which joining is ~8.  Bound by
+// Measured: four sequences of 131072 tokens, 8 K/V heads of 128 with 8 query heads each (604 MB) 112 us, 0.79 of the
+// copy bandwidth; 32 sequences of 4096 to 8192 tokens, 16 rows (228 MB) 71 us, of which joining is ~8.  Bound by
 // the conversions, multiplies and MMAs of an SM sub-partition, which add up instead of overlapping (at 8
-// rows the ALU pipe is 51 % busy, at 16 rows 42 % and the MMA pipe 36 %; 8 warps run as fast as 12).
+// rows the ALU pipe is 51 % busy, at 16 rows 42 % and the MMA pipe 37 %; 8 warps run as fast as 12).
 #include "kv4_attend.cuh"
 #include "mma_parts.cuh"
 
@@ -676,15 +676,19 @@ cudaError_t launch(AttendArgs a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 // Blocks of up to 128 rows from 17 rows on at head size 128, and from 33 on at 64 and 256; measured on 32 sequences
-// of 4096 to 8192 tokens and 8 (at 256: 2) K/V heads, wide against warp-MMA: 32 rows of 128 115 against 118 us, 16 rows
-// 115 against 73; 32 rows of 64 95 against 82, 16 rows 94 against 58; 32 rows of 256 72 against 60; on 16 such
-// sequences 64 rows of 128 68 against 105.
+// of 4096 to 8192 tokens and 8 (at 256: 2) K/V heads, wide against warp-MMA, in us:
+//   128: 16 rows 110 and 71, 32 rows 110 and 124, 64 rows 115 and 230
+//    64: 16 rows 84 and 55, 32 rows 84 and 83, 64 rows 88 and 147
+//   256: 16 rows 70 and 45, 32 rows 71 and 67, 64 rows 73 and 114
+// The wide kernel's time goes by tokens and hardly by rows.  The warp-MMA kernel's goes by blocks: of 32 rows at 64, of 16 at
+// 128 and 256, so that 17 to 32 rows read the cache twice there and take what 32 take.  One kernel takes a whole call: a long
+// step among short ones takes them all to the wide one.
 cudaError_t launch_attend(const AttendArgs& a, int row_tile, int num_sms, cudaStream_t stream) {
   if (row_tile > (a.c.dim == 128 ? 16 : 32)) return launch_attend_wide(a, num_sms, stream);
   switch (a.c.dim) {
     case 64:
       return row_tile <= 8    ? launch<64, 1, 8, 4, 2, false>(a, num_sms, stream)
-             : row_tile <= 16 ? launch<64, 2, 8, 4, 2, false>(a, num_sms, stream)
+             : row_tile <= 16 ? launch<64, 2, 8, 4, 2, false>(a, num_sms, stream)  // 28 bytes spilled for two CTAs an SM
                               : launch<64, 4, 8, 4, 1, false>(a, num_sms, stream);
     case 128:
       return row_tile <= 8 ? launch<128, 1, 16, 2, 1, false>(a, num_sms, stream) : launch<128, 2, 12, 3, 1, true>(a, num_sms, stream);

@@ -20,16 +20,16 @@
 // A block reads no step that none of its rows sees; blocks are walked from both ends of the rows inwards,
 // so that neighbouring items of a causal chunk are about equally long together.
 //
-// A step takes a CTA 0.99 us at head size 64 and 1.23 at 128, two CTAs an SM (from the slope between 12001 and 24001
+// A step takes a CTA 0.95 us at head size 64 and 1.20 at 128, two CTAs an SM (from the slope between 12001 and 24001
 // tokens of 24 sequences).  At 128 the operands' traffic through shared memory (105 KB a step, of which the query
 // rows are 32) comes to two thirds of that; otherwise what the warps share is the issue and fetching of four roles' code
-// (17.9 M instructions for the trees below, issue slots ~40 % busy).  17 to 20 us of a call do not depend on
+// (17.8 M instructions for the trees below, issue slots ~40 % busy).  17 to 20 us of a call do not depend on
 // the tokens: ~4 until the first products, the end of an item and the start of the next, joining, CTAs that have more to do.
 // Measured: 24 sequences of up to 6001 tokens, 112 rows, 4 K/V heads of 64: 40 us (78 with the warp-MMA kernel); a chunk of
-// 2048 rows with 4 query heads a K/V head over 4096 tokens, 8 heads of 128: 147 us (657), 0.7 PFLOP/s of unmasked
-// products; 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 68 us (105).  More warps were slower:
+// 2048 rows with 4 query heads a K/V head over 4096 tokens, 8 heads of 128: 143 us (657), 0.7 PFLOP/s of unmasked
+// products; 64 rows of 16 sequences of 4096 to 8192 tokens, 8 heads of 128: 64 us (105).  More warps were slower:
 // two threads a row 51 and 175, two groups of them on alternate steps 47 and 167, eight warps that dequantise the
-// chunk 160 (against 42 and 151 at the time).
+// chunk 160 (against 42 and 151 at the time).  One word for the waits' limit and the flag that ends them: 143 against 147.
 #include "kv4_attend.cuh"
 
 namespace moe {
@@ -110,7 +110,7 @@ struct WideShape {
   static constexpr int kColO = 2 * kTokens;
   static constexpr int kCols = kColO + D <= 256 ? 256 : 512;
   // p in columns of its own, where there are some left: scores are then read once, and again only where the
-  // reference rises (16 sequences, 64 rows of 64: 51.2 us, and 53.0 with a pass for the maximum first)
+  // reference rises (16 sequences, 64 rows of 64: 51.2 us, and 53.0 with a pass for the maximum first, at the time; now 50.4)
   static constexpr bool kApart = kColO + D + kTokens <= kCols;
   static constexpr int kColP = kApart ? kColO + D : 0, kStepP = kApart ? kTokens / 2 : kTokens;
 };

@@ -10,7 +10,8 @@ namespace kv4 {
 
 constexpr int kTile = 16;       // tokens of a tile
 constexpr int kMaxChunks = 2560;              // warps of an attention launch at most, each with one chunk of the work
-constexpr size_t kPartFloats = 2 * 1280 * 4224;  // floats of the partial results: two per chunk
+// floats of the partial results, two per chunk (43 MB): 163 CTAs of the wide kernel at head size 256, more of any other
+constexpr size_t kPartFloats = 2 * 1280 * 4224;
 constexpr int kStepRows = 64;   // rows of a sequence's step with a tree or in a compaction
 
 // A cache as the kernels see it.
@@ -33,8 +34,7 @@ constexpr uint32_t kWaitCycles = 1u << 31;  // ~1 s: a copy takes microseconds
 struct alignas(16) Piece {
   int on, last;  // the item's last chunk
   int row0, r0, nrows, h;
-  int unused[2];
-};
+};  // 32 bytes, read as two of 16
 
 struct WsLayout {
   size_t status, arrivals, refused, pieces, copies, need, part, total;

@@ -9,7 +9,7 @@
 // the bytes they read and write.
 //
 // Measured: forking 16 prompts into 128 branches and reserving for them on 48 layers (906 MB copied, the 16 sources
-// from L2) 125 us; one prompt into 4 on 12 layers 11 us, bound by three launches; compaction of 64 steps on 48 layers with the calls
+// from L2) 127 us; one prompt into 4 on 12 layers 11 us, bound by three launches; compaction of 64 steps on 48 layers with the calls
 // around it (23 MB in 16-byte pieces) 25 us.
 #include "kv4_common.cuh"
 
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(PageArgs a) {
 cudaError_t launch_reserve(const PageArgs& a, int num_sms, cudaStream_t stream) {
   const cudaError_t e = launch_ready<reserve_kernel>(dim3(1), dim3(kAllocThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  // as many CTAs as an SM holds: 129 us for 128 branches (906 MB), with 4 an SM 136, 10 an SM 125
+  // as many CTAs as an SM holds: 127 us for 128 branches (906 MB); 4 an SM 136 (at the time).  With 10 an SM 124, but
+  // 12.3 us instead of 11.0 for the forks of one prompt, whose few copies wait for CTAs that find none
   return launch_ready<copy_kernel>(dim3(num_sms * 5), dim3(kCopyThreads), 0, stream, a);
 }
 cudaError_t launch_fork(const PageArgs& a, cudaStream_t stream) {

@@ -16,8 +16,8 @@
 // elementary functions on the IBM RISC System/6000 processor", 1990): 3 instructions instead of the
 // ~10 of a division, of which there were 16 a thread.
 //
-// Measured: append and read of 6144 rows of 8 heads of 128 (65 MB in all) 25 us together, 0.38 of the copy
-// bandwidth; with 16 bytes an access instead of a sector's 32, 29 us; a step of 128 rows is bound by its two calls.
+// Measured: append and read of 6144 rows of 8 heads of 128 (65 MB in all) 25.7 us together, 0.37 of the copy
+// bandwidth; with 16 bytes an access instead of a sector's 32, 29 us at the time; a step of 128 rows is bound by its two calls.
 #include "kv4_common.cuh"
 
 namespace moe {
