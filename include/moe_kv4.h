@@ -75,7 +75,7 @@ typedef struct moe_kv4_cache {
   void* workspace;
   size_t workspace_bytes;
   int32_t layers, pages, kv_heads, head_dim, page_size, seqs, max_pages;
-  float k_scale, v_scale; /* tensor scales, finite and above 0 */
+  float k_scale, v_scale; /* tensor scales, above 0, at most 2^119 */
 } moe_kv4_cache;
 
 /* Bytes of one page of one layer, and of the workspace of a cache (0 if the sizes are
@@ -118,6 +118,7 @@ MOE_API int moe_kv4_read(const moe_kv4_cache* cache, int layer, void* k, void* v
  *            kernel's tile, for the whole call; more rows are computed all the same.  A prompt's
  *            chunk among single rows is faster in a call of its own, with cu_rows that leave the
  *            others out
+ *   scale    finite, and times k_scale too
  *   tree     [rows] uint64 or NULL
  *   out      [rows][q_heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   lse      [rows][q_heads] float or NULL

@@ -22,6 +22,7 @@ int check_sizes(const moe_kv4_cache* c) {
     return MOE_ERR_INVALID_ARG;
   if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
     return MOE_ERR_INVALID_ARG;
+  if (c->k_scale > 0x1p119f || c->v_scale > 0x1p119f) return MOE_ERR_UNSUPPORTED;  // 448 * scale is a float
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_ERR_UNSUPPORTED;
   if (c->page_size % moe::kv4::kTile || c->page_size > 1024 || c->kv_heads > 1024 || c->seqs > 65535 ||
       c->pages > (1 << 30) || c->layers > 65536 || c->max_pages > (1 << 27))
@@ -84,13 +85,14 @@ int attend(const moe_kv4_cache* c, int layer, const void* q, int64_t q_row_strid
   if (!rows_ok(q, q_row_stride, q_head_stride) || !cu_rows || !aligned(cu_rows, 4) || !out || !aligned(out, 16) ||
       !aligned(lse, 4) || !aligned(tree, 8))
     return MOE_ERR_INVALID_ARG;
+  a.scale2 = scale * c->k_scale * 1.44269504088896340736f;
+  if (!std::isfinite(a.scale2)) return MOE_ERR_UNSUPPORTED;
   int sms = 0;
   rc = moe::device_sms(&sms);
   if (rc != MOE_OK) return rc;
   a.q = q; a.q_row = q_row_stride; a.q_head = q_head_stride;
   a.group = q_heads / c->kv_heads;
   a.cu = cu_rows; a.rows = rows; a.fp16 = dtype == MOE_KV4_FP16;
-  a.scale2 = scale * c->k_scale * 1.44269504088896340736f;
   a.v_ts = c->v_scale;
   a.window = window < (1 << 30) ? window : 1 << 30;  // as many tokens as there can be; first - window stays an int
   a.tree = reinterpret_cast<const unsigned long long*>(tree);

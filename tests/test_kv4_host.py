@@ -140,3 +140,15 @@ def test_plain_quantise_is_the_nearest():
     grid = np.concatenate([P.E2M1, -P.E2M1])
     best = np.abs(x[..., None] - grid * d[..., None]).min(-1)
     assert np.allclose(np.abs(x - v), best, rtol=0, atol=1e-12)
+
+
+def test_scales_out_of_range_are_refused(L):
+    # above 2^119 a block's factor (448 times the tensor scale) and then 6 times it are no floats, and values would be held as 0
+    lib, p = L.lib(), 0x600000
+    for kw in (dict(k_scale=2.0 ** 120), dict(v_scale=3e38)):
+        assert lib.moe_kv4_check(cache_args(L, **kw)) == L.MOE_ERR_UNSUPPORTED, kw
+        assert lib.moe_kv4_workspace_bytes(cache_args(L, **kw)) == 0
+    assert lib.moe_kv4_check(cache_args(L, k_scale=2.0 ** 119, v_scale=2.0 ** -100)) == 0
+    # the factor of the scores
+    attend = [0, p, 512, 128, 4, 0, p, 4, 1, 1e30, 0, None, p, None, None]
+    assert lib.moe_kv4_attend(cache_args(L, k_scale=1e20), *attend) == L.MOE_ERR_UNSUPPORTED
