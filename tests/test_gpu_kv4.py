@@ -419,6 +419,39 @@ def test_attend_many_rows_bad_page_and_stale_tokens(moe, D):
     assert cache.status() == moe.KV4_BAD_PAGE and cache.status() == 0
 
 
+@pytest.mark.parametrize("D,group", [(64, 3), (64, 24), (128, 8), (128, 24), (256, 2), (256, 20)])
+def test_attend_long_sequences(moe, D, group):
+    # two steps of 2 rows over 140001 and 70003 tokens, against the values that the cache gives back, in 64 bits
+    lens, page, rows = [140001, 70003], 128, 2
+    pages = [-(-n // page) for n in lens]
+    cache = moe.Kv4Cache(1, sum(pages), 1, D, page, 2, max(pages))
+    cache.reserve(dev(lens))
+    g = torch.Generator(device="cuda").manual_seed(D)
+    total, cu_all = sum(lens), dev([0, lens[0], sum(lens)])
+    k, v = (torch.randn((total, 1, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    cache.append(0, k, v, cu_all)
+    k, v = (t[:, 0].double() for t in cache.read(0, cu_all, rows=total))  # at most 6 bits a value: exact in BF16
+    q = (2 * torch.randn((2 * rows, group, D), generator=g, device="cuda")).to(torch.bfloat16)
+    lse = torch.empty((2 * rows, group), dtype=torch.float32, device="cuda")
+    out, lse = cache.attend(0, q, dev([0, rows, 2 * rows]), max_rows=rows, lse=lse)
+    assert cache.status() == 0
+    for s, first in enumerate((0, lens[0])):
+        for r in range(rows):
+            N = lens[s] - rows + r + 1
+            ks, vs, qs = k[first:first + N], v[first:first + N], q[s * rows + r].double()
+            z = qs @ ks.T * D ** -0.5
+            p = z.softmax(-1)
+            want, spread = p @ vs, p @ vs.abs()
+            # the terms of check_attend, with the largest p at least 2^7 where p is rounded to FP16
+            qk = (qs.abs() @ ks.abs().T).max() * D ** -0.5
+            score, sums = D * 2.0 ** -23 * qk, (N / 16 + 64) * 2.0 ** -22
+            bound = spread * (2.0 ** -11 + 2 * score + 2.0 ** -20 + sums) + N * 2.0 ** -32 * vs.abs().max()
+            bound = bound + want.abs() * BF16_HALF_ULP_REL * 1.01 + bound * BF16_HALF_ULP_REL
+            assert ((out[s * rows + r].double() - want).abs() <= bound).all()
+            exact = z.logsumexp(-1)
+            assert ((lse[s * rows + r].double() - exact).abs() <= score + sums + 2.0 ** -20 + exact.abs() * 2.0 ** -22).all()
+
+
 # ---- append and read ----
 
 @pytest.mark.parametrize("D", [64, 128, 256])
