@@ -1,0 +1,203 @@
+// Kernels of the dense path around the layer (include/moe_dense.h): norm and quantised rows, block-scaled
+// products in 8 bits, log probabilities.
+#pragma once
+
+#include <cuda.h>
+
+#include "../../include/moe_dense.h"
+#include "launch.cuh"
+
+namespace moe {
+namespace dense {
+
+constexpr int kBlock = 128;  // channels of a scale, rows and channels of a weight's scale
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery's round-up method).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {d, static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
+__device__ __forceinline__ uint32_t div(const FastDiv& f, uint32_t n) { return (__umulhi(f.mul, n) + n) >> f.shift; }
+
+// Rows of norm_rows.cu; dtype and weight_dtype: MOE_DENSE_*; row r of x and of normed lies at
+// (r / inner) * outer stride + (r % inner) * inner stride.
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* residual_out;
+  void* normed;
+  uint8_t* codes;
+  float* scales;
+  int64_t x_outer, x_inner, n_outer, n_inner, r_stride, ro_stride, code_stride, scale_row, scale_block;
+  FastDiv inner;
+  uint32_t rows;
+  int d, dtype, weight_dtype;
+  float eps, add;  // add: 1 where the norm multiplies by 1 + weight
+  bool vec;        // every row can be read and written 16 bytes (weights: 8 elements) at a time
+  bool vec_codes;  // codes can be written 8 bytes at a time
+};
+cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t stream);
+
+struct QuantArgs {
+  const void* x;
+  uint8_t* codes;
+  float* scales;
+  int64_t x_stride, code_stride, scale_row, scale_block;
+  FastDiv nblocks;  // blocks of a row
+  uint32_t blocks;  // of all rows
+  int d, dtype;
+  bool gated, vec, vec_codes;
+};
+cudaError_t launch_quantize(const QuantArgs& a, int sms, cudaStream_t stream);
+
+// Block-scaled products.
+constexpr uint32_t kWaitCycles = 1u << 31;  // ~1 s: a copy takes microseconds
+constexpr int kMaxGroups = 1024;
+struct MatmulArgs {
+  const uint8_t* x;
+  const uint8_t* w;
+  const float* xs;
+  const float* ws;
+  const int* offsets;  // null: one group of all rows
+  void* out;
+  uint32_t* status;
+  int64_t x_stride, scale_row, scale_block, out_stride;
+  int rows, n, k, groups, out_dtype;
+  uint32_t wait_cycles;
+  int copy_arrivals;  // arrivals that a stage's barrier waits for beside its bytes
+};
+cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, cudaStream_t stream);
+// Map of a matrix of bytes, loaded in boxes of 128 bytes x box_rows rows with the 128-byte swizzle.
+int encode_fp8_map(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, uint64_t stride, uint32_t box_rows);
+
+// Log probabilities.
+struct LogprobArgs {
+  const void* logits;
+  const int* tokens;
+  float* logprobs;
+  float* lse;
+  float* entropy;
+  int* top_ids;
+  float* top_logprobs;
+  int64_t row_stride, token_stride;
+  float scale;
+  int rows, vocab, n_tokens, top, dtype;
+};
+cudaError_t launch_logprobs(const LogprobArgs& a, int sms, cudaStream_t stream);
+
+// Bounded wait of a whole warp for a phase of a barrier.  *limit: cycles that a wait may take, 0 once one of the CTA
+// gave up.  False: give up too.
+__device__ __forceinline__ uint32_t cycles() {
+  uint32_t c;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
+  return c;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* limit, uint32_t* status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint32_t t0 = cycles();
+    while (!(ok = mbar_try_wait(bar, parity))) {
+      const uint32_t most = *limit;
+      if (cycles() - t0 >= most) {
+        if (most) {
+          *limit = 0;
+          atomicOr(status, MOE_DENSE_TIMEOUT);
+        }
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T of E4M3 codes, FP32 sums.
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of it: FP32 sums (bits 4-5 = 1), E4M3 (bits 7-9, 10-12 = 0), both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return d;
+}
+
+// Clusters.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address that `local`, an address of this CTA's shared memory, has in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t mapa(uint32_t local, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// launch_ready for clusters of `cluster` CTAs along x.
+template <auto Kernel, typename... Args>
+cudaError_t launch_cluster(int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
+  static std::atomic<unsigned long long> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((ready.load(std::memory_order_acquire) >> dev) & 1ull)) {
+    if (smem > 48 * 1024)
+      e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, Kernel, static_cast<Args&&>(args)...);
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,383 @@
+// Block-scaled products with the weights as the 128-row operand (include/moe_dense.h): few rows, and groups of rows.
+//
+//   out[t][c] = sum_b xs[t][b] ws[c / 128][b] * (sum over block b of x[t][k] w[c][k])
+//
+// A tile is 128 channels of a weight, which is one row of its scales, times up to NT rows of x.  Each block of 128 k
+// is one product of its own in tensor memory (four tcgen05 MMAs of 32 k, weights 128 x rows n); it is multiplied by its
+// scales on the way into FP32 registers, so nothing is rounded between the blocks.  Weights are read once for all rows of a tile: with
+// few rows the weights' bytes bound the product, with many rows the tensor cores and the sums.
+//
+// Roles: warps 0-7 add up (a lane of tensor memory is a channel; two groups of four warps take half of the rows
+// each), a warp copies tiles into a ring, a warp issues the MMAs, two warps bring xs * ws of a block's rows into shared memory.
+// CTAs take tiles statically, one after the other; the ring runs on across tiles.  Where one row of x tiles would leave
+// SMs idle, a cluster's CTAs take a part of k each and add up through distributed shared memory, in order.
+#include "dense.cuh"
+
+namespace moe {
+namespace dense {
+namespace {
+
+constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarps = 2, kScaleWarp = 10, kThreads = 32 * 12;
+constexpr uint32_t kDrainCycles = 1u << 24;
+constexpr int kPrefetch = 4;  // blocks of scales that are under way in a scale warp's registers
+
+template <int NT>
+struct Shape {
+  static constexpr int kStage = (128 + NT) * 128;
+  static constexpr int kStages = NT == 256 ? 4 : NT == 128 ? 6 : 10;
+  static constexpr int kBufs = NT == 256 ? 2 : NT == 128 ? 4 : 8;  // products in tensor memory
+  static constexpr int kCols = NT * kBufs;
+  static constexpr int kScales = kStage * kStages;                 // [kBufs][NT] floats
+  static constexpr int kBars = kScales + 4 * NT * kBufs;
+  static constexpr int kNumBars = 2 * kStages + 3 * kBufs + 1;
+  static constexpr int kFirst = kBars + 8 * kNumBars;              // groups' first row [kMaxGroups], rows [kMaxGroups]
+  static constexpr int kTiles = kFirst + 8 * kMaxGroups;           // row tiles before a group [kMaxGroups + 1]
+  static constexpr int kTotal = kTiles + 4 * (kMaxGroups + 1) + 1024;
+  static_assert(kTotal <= 227 * 1024);
+};
+
+struct Tile {
+  int64_t w_row;    // row of the weights' matrix at which it begins
+  const float* ws;  // scales of its 128 channels [blocks of k]
+  int c0, row0, rows;
+};
+
+struct Maps {
+  CUtensorMap w, x16, x64;
+};
+
+template <int NT>
+__device__ __forceinline__ Tile tile_of(const MatmulArgs& a, int id, int ctiles, int kblocks, const int* first,
+                                        const int* rows, const int* before) {
+  // the last group with before[g] <= id / ctiles: that one's tiles end behind it, so it has rows
+  int g = 0;
+  if (a.groups > 1) {
+    const int at = id / ctiles;
+    for (int lo = a.groups; lo > 0;) {  // lo: groups from g on that are left
+      const int step = lo >> 1;
+      if (step == 0) break;
+      if (before[g + step] <= at) { g += step; lo -= step; }
+      else lo = step;
+    }
+  }
+  const int local = id - before[g] * ctiles, tts = before[g + 1] - before[g];
+  const int ct = local / tts, tt = local - ct * tts;
+  const int per = ((rows[g] + tts - 1) / tts + 15) & ~15;
+  Tile t;
+  t.c0 = ct * 128;
+  t.w_row = static_cast<int64_t>(g) * a.n + t.c0;
+  t.ws = a.ws + (static_cast<int64_t>(g) * ctiles + ct) * kblocks;
+  t.row0 = first[g] + tt * per;
+  t.rows = max(0, min(per, rows[g] - tt * per));
+  return t;
+}
+
+__device__ __forceinline__ void store_one(const MatmulArgs& a, int64_t row, int c, float v) {
+  if (a.out_dtype == MOE_DENSE_FP32) static_cast<float*>(a.out)[row * a.out_stride + c] = v;
+  else if (a.out_dtype == MOE_DENSE_BF16) static_cast<__nv_bfloat16*>(a.out)[row * a.out_stride + c] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(a.out)[row * a.out_stride + c] = __float2half_rn(v);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MatmulArgs a) {
+  typedef Shape<NT> L;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem, s_limit;
+  __shared__ int s_scan[12];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_addr(smem);
+  int* s_first = reinterpret_cast<int*>(smem + L::kFirst);
+  int* s_rows = s_first + kMaxGroups;
+  int* s_before = reinterpret_cast<int*>(smem + L::kTiles);
+  const uint32_t full = base + L::kBars, empty = full + 8 * L::kStages, done = empty + 8 * L::kStages,
+                 freed = done + 8 * L::kBufs, scaled = freed + 8 * L::kBufs, end = scaled + 8 * L::kBufs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(full + 8 * i, a.copy_arrivals);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < L::kBufs; ++i) {
+      mbar_init(done + 8 * i, 1);
+      mbar_init(freed + 8 * i, kSumWarps);
+      mbar_init(scaled + 8 * i, kScaleWarps);
+    }
+    mbar_init(end, 1);
+    s_limit = a.wait_cycles;
+  }
+  fence_barrier_init();
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&s_tmem), L::kCols);
+    tmem_relinquish();
+  }
+  if (warp == kCopyWarp && lane == 0) {
+    prefetch_tmap(&maps.w);
+    prefetch_tmap(&maps.x16);
+    prefetch_tmap(&maps.x64);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // groups: first rows, rows, row tiles before each
+  {
+    const int per = (a.groups + kThreads - 1) / kThreads;
+    const int g0 = min(tid * per, a.groups), g1 = min(g0 + per, a.groups);
+    int mine = 0;
+    for (int g = g0; g < g1; ++g) {
+      int b = 0, e = a.rows;
+      if (a.offsets) {
+        const int rb = __ldcg(a.offsets + g), re = __ldcg(a.offsets + g + 1);
+        b = min(max(rb, 0), a.rows);
+        e = min(max(re, 0), a.rows);
+        if (blockIdx.x == 0 && (b != rb || e != re || re < rb)) atomicOr(a.status, MOE_DENSE_BAD_OFFSETS);
+      }
+      const int n = max(e - b, 0);
+      s_first[g] = b;
+      s_rows[g] = n;
+      mine += (n + NT - 1) / NT;
+    }
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) s_scan[warp] = sum;
+    __syncthreads();
+    int at = sum - mine;
+    for (int i = 0; i < warp; ++i) at += s_scan[i];
+    for (int g = g0; g < g1; ++g) {
+      s_before[g] = at;
+      at += (s_rows[g] + NT - 1) / NT;
+    }
+    if (tid == kThreads - 1) s_before[a.groups] = at;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile uint32_t* limit = &s_limit;
+
+  const int split = static_cast<int>(cluster_size()), part = static_cast<int>(cluster_rank());
+  const int ctiles = (a.n + 127) / 128, kblocks = (a.k + 127) / 128;
+  const int k0 = kblocks * part / split, k1 = kblocks * (part + 1) / split;
+  const int tiles = s_before[a.groups] * ctiles, stride = gridDim.x / split;
+
+  if (warp == kCopyWarp) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
+      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const int n16 = (t.rows + 15) >> 4;
+      const uint32_t bytes = 128 * 128 + n16 * 16 * 128;
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const uint32_t s = it % L::kStages;
+        if (!(ok = warp_wait(empty + 8 * s, ((it / L::kStages) & 1) ^ 1, limit, a.status))) break;
+        if (elect_one()) {
+          const uint32_t at = base + s * L::kStage, bar = full + 8 * s;
+          mbar_arrive_expect_tx(bar, bytes);
+          tma_load_2d_plain(at, &maps.w, kb * 128, static_cast<int>(t.w_row), bar);
+          int i = 0;
+          if constexpr (NT > 32)
+            for (; i + 4 <= n16; i += 4) tma_load_2d_plain(at + 16384 + i * 2048, &maps.x64, kb * 128, t.row0 + i * 16, bar);
+          for (; i < n16; ++i) tma_load_2d_plain(at + 16384 + i * 2048, &maps.x16, kb * 128, t.row0 + i * 16, bar);
+        }
+        __syncwarp();
+      }
+    }
+    // copies in flight land before the CTA leaves
+    __shared__ uint32_t s_drain;
+    if (lane == 0) s_drain = kDrainCycles;
+    __syncwarp();
+    for (uint32_t i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
+      warp_wait(full + 8 * (i % L::kStages), (i / L::kStages) & 1, &s_drain, a.status);
+  } else if (warp == kMmaWarp) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
+      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const uint32_t idesc = idesc_e4m3(128, max(16, (t.rows + 15) & ~15));
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const uint32_t s = it % L::kStages, b = it % L::kBufs;
+        ok = warp_wait(freed + 8 * b, ((it / L::kBufs) & 1) ^ 1, limit, a.status) &&
+             warp_wait(full + 8 * s, (it / L::kStages) & 1, limit, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t da = smem_desc_sw128(base + s * L::kStage, 1024);
+        const uint64_t db = smem_desc_sw128(base + s * L::kStage + 16384, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_e4m3(tmem + b * NT, da + 2 * k, db + 2 * k, idesc, k > 0);
+          tc_commit(empty + 8 * s);
+          tc_commit(done + 8 * b);
+        }
+        __syncwarp();
+      }
+    }
+    // products in flight end before their memory is given back
+    if (elect_one()) tc_commit(end);
+    __syncwarp();
+    __shared__ uint32_t s_drain_mma;
+    if (lane == 0) s_drain_mma = kDrainCycles;
+    __syncwarp();
+    warp_wait(end, 0, &s_drain_mma, a.status);
+  } else if (warp >= kScaleWarp) {
+    // rows r0, r0 + 64, ...: their scales of the next kPrefetch blocks in registers
+    constexpr int PER = (NT + 63) / 64;
+    const int r0 = (warp - kScaleWarp) * 32 + lane;
+    float* out = reinterpret_cast<float*>(smem + L::kScales);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
+      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      float x[kPrefetch][PER], w[kPrefetch];
+      auto load = [&](int j, int kb) {
+        w[j] = kb < k1 ? __ldcg(t.ws + kb) : 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int r = r0 + 64 * i;
+          x[j][i] = kb < k1 && r < t.rows ? __ldcg(a.xs + (t.row0 + r) * a.scale_row + kb * a.scale_block) : 0.f;
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < kPrefetch; ++j) load(j, k0 + j);
+      for (int kb0 = k0; ok && kb0 < k1; kb0 += kPrefetch) {
+#pragma unroll
+        for (int j = 0; j < kPrefetch; ++j) {
+          const int kb = kb0 + j;
+          if (!ok || kb >= k1) continue;
+          const uint32_t b = it % L::kBufs;
+          ok = warp_wait(freed + 8 * b, ((it / L::kBufs) & 1) ^ 1, limit, a.status);
+          if (!ok) continue;
+          ++it;
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            if (r0 + 64 * i < NT) out[b * NT + r0 + 64 * i] = x[j][i] * w[j];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(scaled + 8 * b);
+          load(j, kb + kPrefetch);
+        }
+      }
+    }
+  } else {
+    constexpr int H = NT / 2;
+    const int half = warp >> 2, quarter = warp & 3;
+    const float* scales = reinterpret_cast<const float*>(smem + L::kScales);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
+      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const int n = (t.rows + 15) & ~15, cut = ((n / 2) + 15) & ~15;  // rows [0, cut) and [cut, n)
+      const int first = half ? cut : 0, mine = half ? n - cut : cut;
+      float2 acc[H / 2];
+#pragma unroll
+      for (int i = 0; i < H / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const uint32_t b = it % L::kBufs, phase = (it / L::kBufs) & 1;
+        ok = warp_wait(scaled + 8 * b, phase, limit, a.status) && warp_wait(done + 8 * b, phase, limit, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = tmem + b * NT + first + (static_cast<uint32_t>(quarter * 32) << 16);
+        const float* s = scales + b * NT + first;
+#pragma unroll
+        for (int c = 0; c < H; c += 16) {
+          if (c >= mine) break;
+          uint32_t v[16];
+          tmem_ld_x16(from + c, v);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(s + c + i);
+            float2& p = acc[(c + i) / 2];
+            float2& q = acc[(c + i) / 2 + 1];
+            p = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(f.x, f.y), p);
+            q = fma2(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), make_float2(f.z, f.w), q);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(freed + 8 * b);
+      }
+      if (!ok) break;
+      const int ch = quarter * 32 + lane;
+      if (split == 1) {
+        if (t.c0 + ch < a.n) {
+#pragma unroll
+          for (int i = 0; i < H / 2; ++i) {
+            const int r = first + 2 * i;
+            if (2 * i < mine && r < t.rows) store_one(a, t.row0 + r, t.c0 + ch, acc[i].x);
+            if (2 * i < mine && r + 1 < t.rows) store_one(a, t.row0 + r + 1, t.c0 + ch, acc[i].y);
+          }
+        }
+      } else {
+        // the only tile of this cluster: its copies have landed and its products have read them, so the ring is free
+        float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < H / 2; ++i) {
+          if (2 * i < mine) {
+            sums[(first + 2 * i) * 128 + ch] = acc[i].x;
+            sums[(first + 2 * i + 1) * 128 + ch] = acc[i].y;
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    cluster_sync();
+    const int id = blockIdx.x / split;
+    if (id < tiles && s_limit) {
+      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const int ch = tid & 127;
+      // three groups of 128 threads, every CTA a row of its own
+      for (int r = part + split * (tid >> 7); r < t.rows; r += 3 * split) {
+        float v = 0.f;
+        for (int p = 0; p < split; ++p) v += ld_cluster(mapa(base + (r * 128 + ch) * 4, p));
+        if (t.c0 + ch < a.n) store_one(a, t.row0 + r, t.c0 + ch, v);
+      }
+    }
+    cluster_sync();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+template <int NT>
+cudaError_t run(const Maps& maps, const MatmulArgs& a, int split, int grid, cudaStream_t stream) {
+  return launch_cluster<fp8_stream_kernel<NT>>(split, dim3(grid), dim3(kThreads), Shape<NT>::kTotal, stream, maps, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, cudaStream_t stream) {
+  Maps maps;
+  const int64_t groups = a.offsets ? a.groups : 1;
+  if (encode_fp8_map(&maps.w, a.w, a.k, groups * a.n, a.k, 128) != MOE_OK ||
+      encode_fp8_map(&maps.x16, a.x, a.k, a.rows, a.x_stride, 16) != MOE_OK ||
+      encode_fp8_map(&maps.x64, a.x, a.k, a.rows, a.x_stride, 64) != MOE_OK)
+    return cudaErrorInvalidValue;
+  const int64_t average = (a.rows + groups - 1) / groups;
+  const int nt = average <= (a.offsets ? 16 : 32) ? 32 : average <= (a.offsets ? 64 : 128) ? 128 : 256;
+  int split = 1;
+  const int ctiles = (a.n + 127) / 128, kblocks = (a.k + 127) / 128;
+  int grid = sms;
+  if (!a.offsets) {
+    const int64_t tiles = static_cast<int64_t>(ctiles) * ((a.rows + nt - 1) / nt);
+    if (tiles < sms) {
+      if (nt < 256)
+        while (split < 8 && tiles * (split + 1) <= sms && split + 1 <= kblocks) ++split;
+      grid = static_cast<int>(tiles) * split;
+    }
+  }
+  if (nt == 32) return run<32>(maps, a, split, grid, stream);
+  if (nt == 128) return run<128>(maps, a, split, grid, stream);
+  return run<256>(maps, a, split, grid, stream);
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,395 @@
+// Root-mean-square norm with the residual's addition, and rows in 8 bits with a scale for each 128 channels.
+//
+//   h = round(x + r);  n = h / sqrt(mean(h^2) + eps) * (w or 1 + w)
+//   s = max|v| / 448 over a block of 128 values v (n, x, or silu(gate) * up);  code = E4M3(v / s)
+//
+// Both kernels read every input and write every output once; memory bounds them from some hundred rows on, and below that
+// the launch and one trip to memory.  A thread has 8 consecutive values (16 bytes of a 16-bit type), so 16 neighbouring
+// lanes have a block, whose maximum takes four shuffles.
+#include "dense.cuh"
+
+namespace moe {
+namespace dense {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v);
+template <>
+__device__ __forceinline__ float to_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float2 pair(uint32_t bits, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&bits)); }
+__device__ __forceinline__ float2 pair(uint32_t bits, __nv_bfloat16) {
+  return make_float2(__uint_as_float(bits << 16), __uint_as_float(bits & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t packed(float lo, float hi, __half) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t packed(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Eight consecutive values from channel c on (zeros past the row's end), 16-byte accesses where VEC.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* row, int c, int d, float (&v)[8]) {
+  if constexpr (VEC && sizeof(T) == 4) {
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(row + c)), b = __ldcg(reinterpret_cast<const float4*>(row + c) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else if constexpr (VEC) {
+    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(row + c));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = pair(w[i], T());
+      v[2 * i] = p.x; v[2 * i + 1] = p.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < d ? to_float<T>(row[c + i]) : 0.f;
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* row, int c, int d, const float (&v)[8]) {
+  if constexpr (VEC && sizeof(T) == 4) {
+    reinterpret_cast<float4*>(row + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(row + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else if constexpr (VEC) {
+    *reinterpret_cast<uint4*>(row + c) =
+        make_uint4(packed(v[0], v[1], T()), packed(v[2], v[3], T()), packed(v[4], v[5], T()), packed(v[6], v[7], T()));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < d) row[c + i] = from_float<T>(v[i]);
+  }
+}
+
+// (lo, hi) as two E4M3 codes, to nearest even, at most 448.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const uint32_t two = e4m3x2_to_f16x2(code & 0x7fu);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(two & 0xffffu)));
+}
+
+// The quotients' errors are below 2^-23 (a rounded reciprocal and a rounded product), so codes of quotients 2^-22
+// smaller and larger are the same unless a border between two codes lies next to the quotient.  There the exact
+// quotient decides: |v| against border * scale, by the sign of one fused multiply-add; on the border the even code.
+// (Rows of 16-bit types meet borders often: v / s is then a fraction of small numbers.  Dividing each value by the
+// scale instead cost a gated chunk of 8192 rows of 4096 as much as its memory.)
+__device__ __noinline__ uint32_t settle(uint32_t less, uint32_t more, float v0, float v1, float v2, float v3, float s) {
+  const float v[4] = {v0, v1, v2, v3};
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = (less >> (8 * i)) & 0xffu, b = (more >> (8 * i)) & 0xffu;
+    uint32_t c = a;
+    if (a != b) {
+      const float border = 0.5f * (e4m3_value(a) + e4m3_value(b));
+      const float over = fmaf(-border, s, fabsf(v[i]));
+      c = over > 0.f ? b : over < 0.f ? a : (a & 1u) ? b : a;
+    }
+    codes |= c << (8 * i);
+  }
+  return codes;
+}
+
+// Codes of a thread's 8 values; 16 neighbouring lanes have a block.  All lanes of the warp take part.
+__device__ __forceinline__ uint2 quantize8(float (&v)[8], float* scale) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
+    most = m > most ? m : most;
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const uint32_t m = __shfl_xor_sync(kAll, most, o);
+    most = m > most ? m : most;
+  }
+  if (most >= 0x7f800000u) {  // an infinity or a NaN
+    *scale = __uint_as_float(0x7fc00000u);
+    return make_uint2(0, 0);
+  }
+  float s = __fdiv_rn(__uint_as_float(most), 448.f);
+  *scale = s;
+  if (s < 0x1p-90f) {  // the same quotients, with a reciprocal and border products inside FP32's range
+    s *= 0x1p64f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= 0x1p64f;
+  }
+  if (s == 0.f) return make_uint2(0, 0);
+  const float inv = __fdiv_rn(1.f, s);
+  const float down = inv * (1.f - 0x1p-22f), up = inv * (1.f + 0x1p-22f);
+  uint32_t less[2], more[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    less[h] = e4m3x2(v[4 * h] * down, v[4 * h + 1] * down) | (e4m3x2(v[4 * h + 2] * down, v[4 * h + 3] * down) << 16);
+    more[h] = e4m3x2(v[4 * h] * up, v[4 * h + 1] * up) | (e4m3x2(v[4 * h + 2] * up, v[4 * h + 3] * up) << 16);
+    if (less[h] != more[h]) less[h] = settle(less[h], more[h], v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3], s);
+  }
+  return make_uint2(less[0], less[1]);
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* row, int c, int d, uint2 codes, bool vec) {
+  if (vec && c + 8 <= d) {
+    *reinterpret_cast<uint2*>(row + c) = codes;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < d) row[c + i] = static_cast<uint8_t>((i < 4 ? codes.x >> (8 * i) : codes.y >> (8 * (i - 4))) & 0xffu);
+}
+
+// Sum over the TPR threads of a row; CTA-wide through red[] where TPR is over a warp.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = lane < TPR / 32 ? red[lane] : 0.f;
+#pragma unroll
+    for (int o = TPR / 64; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    v = __shfl_sync(kAll, v, 0);
+  }
+  return v;
+}
+
+template <typename T>
+struct RowPtrs {
+  const T* x;
+  const T* r;
+  T* ro;
+  T* n;
+  uint8_t* codes;
+  float* scales;
+};
+template <typename T>
+__device__ __forceinline__ RowPtrs<T> row_of(const NormArgs& a, uint32_t row) {
+  const uint32_t o = div(a.inner, row), i = row - o * a.inner.d;
+  RowPtrs<T> p;
+  p.x = static_cast<const T*>(a.x) + o * a.x_outer + i * a.x_inner;
+  p.n = a.normed ? static_cast<T*>(a.normed) + o * a.n_outer + i * a.n_inner : nullptr;
+  p.r = a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr;
+  p.ro = a.residual_out ? static_cast<T*>(a.residual_out) + row * a.ro_stride : nullptr;
+  p.codes = a.codes ? a.codes + row * a.code_stride : nullptr;
+  p.scales = a.codes ? a.scales + row * a.scale_row : nullptr;
+  return p;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[8]) {
+  if (a.weight_dtype == MOE_DENSE_FP32) load8<float, VEC>(static_cast<const float*>(a.weight), c, a.d, w);
+  else if (a.weight_dtype == MOE_DENSE_BF16) load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(a.weight), c, a.d, w);
+  else load8<__half, VEC>(static_cast<const __half*>(a.weight), c, a.d, w);
+}
+
+// h of eight channels: x + r rounded to T.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_h(const NormArgs& a, const RowPtrs<T>& p, int c, float (&h)[8]) {
+  load8<T, VEC>(p.x, c, a.d, h);
+  if (p.r) {
+    float r[8];
+    load8<T, VEC>(p.r, c, a.d, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = to_float<T>(from_float<T>(h[i] + r[i]));
+  }
+}
+
+// The normed values of eight channels and what is written of them.  The weight comes first: h * w of 16-bit values is
+// exact, so that n has one rounding after the factor's.
+template <typename T, bool VEC>
+__device__ __forceinline__ void finish(const NormArgs& a, const RowPtrs<T>& p, int c, bool in, float (&h)[8], float factor) {
+  float w[8];
+  if (in) {
+    load_weight<VEC>(a, c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = h[i] * (a.add + w[i]) * factor;
+    if (p.n) store8<T, VEC>(p.n, c, a.d, h);
+  }
+  if (p.codes) {  // the same for the whole warp
+    float scale;
+    const uint2 codes = quantize8(h, &scale);
+    if (in) {
+      store_codes(p.codes, c, a.d, codes, a.vec_codes);
+      if ((threadIdx.x & 15) == 0) p.scales[(c / kBlock) * a.scale_block] = scale;
+    }
+  }
+}
+
+__device__ __forceinline__ float norm_factor(float squares, const NormArgs& a) {
+  return __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(squares, static_cast<float>(a.d)) + a.eps));
+}
+
+// A row's channels in the registers of TPR threads, VPT times 8 each.
+template <typename T, int TPR, int VPT>
+__global__ void __launch_bounds__(256) norm_kernel(const NormArgs a) {
+  __shared__ float red[8];
+  pdl_wait();
+  const uint32_t row0 = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  const bool live = row0 < a.rows;
+  const RowPtrs<T> p = row_of<T>(a, live ? row0 : a.rows - 1);
+  const int t = threadIdx.x % TPR;
+  float h[VPT][8];
+  float squares = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = 8 * (t + j * TPR);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[j][i] = 0.f;
+    if (live && c < a.d) load_h<T, true>(a, p, c, h[j]);
+  }
+  pdl_launch_dependents();
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(h[j][i], h[j][i], s);
+    squares += s;
+    const int c = 8 * (t + j * TPR);
+    if (p.ro && live && c < a.d) store8<T, true>(p.ro, c, a.d, h[j]);
+  }
+  const float factor = norm_factor(row_sum<TPR>(squares, red), a);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = 8 * (t + j * TPR);
+    finish<T, true>(a, p, c, live && c < a.d, h[j], factor);
+  }
+}
+
+// Any length and alignment: the row is read twice (h again from residual_out, where it is written: x or the residual may
+// be the same memory; each thread reads back what it wrote itself).
+template <typename T, int TPR, bool VEC>
+__global__ void __launch_bounds__(256) norm_long_kernel(const NormArgs a) {
+  __shared__ float red[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t row0 = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  const bool live = row0 < a.rows;
+  const RowPtrs<T> p = row_of<T>(a, live ? row0 : a.rows - 1);
+  const int t = threadIdx.x % TPR;
+  const int steps = (a.d + 8 * TPR - 1) / (8 * TPR);
+  float squares = 0.f;
+  for (int j = 0; j < steps; ++j) {
+    const int c = 8 * (t + j * TPR);
+    if (!live || c >= a.d) continue;
+    float h[8], s = 0.f;
+    load_h<T, VEC>(a, p, c, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
+    squares += s;
+    if (p.ro) store8<T, VEC>(p.ro, c, a.d, h);
+  }
+  const float factor = norm_factor(row_sum<TPR>(squares, red), a);
+  for (int j = 0; j < steps; ++j) {
+    const int c = 8 * (t + j * TPR);
+    const bool in = live && c < a.d;
+    float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in) {
+      if (p.ro) load8<T, VEC>(p.ro, c, a.d, h);
+      else load_h<T, VEC>(a, p, c, h);
+    }
+    finish<T, VEC>(a, p, c, in, h, factor);
+  }
+}
+
+template <typename T, int TPR, int VPT>
+cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
+  const uint32_t per = 256 / TPR;
+  return launch_ready<norm_kernel<T, TPR, VPT>>(dim3((a.rows + per - 1) / per), dim3(256), 0, stream, a);
+}
+template <typename T, int TPR, bool VEC>
+cudaError_t run_norm_long(const NormArgs& a, cudaStream_t stream) {
+  const uint32_t per = 256 / TPR;
+  return launch_ready<norm_long_kernel<T, TPR, VEC>>(dim3((a.rows + per - 1) / per), dim3(256), 0, stream, a);
+}
+
+template <typename T>
+cudaError_t norm_of(const NormArgs& a, int sms, cudaStream_t stream) {
+  if (!a.vec) return a.d <= 1024 ? run_norm_long<T, 32, false>(a, stream) : run_norm_long<T, 256, false>(a, stream);
+  if (a.d <= 128) return run_norm<T, 16, 1>(a, stream);
+  if (a.d <= 256) return run_norm<T, 32, 1>(a, stream);
+  if (a.d <= 512) return run_norm<T, 32, 2>(a, stream);
+  if (a.d <= 1024) return run_norm<T, 32, 4>(a, stream);
+  if (a.d <= 2048) return run_norm<T, 256, 1>(a, stream);
+  if (a.d <= 4096) return run_norm<T, 256, 2>(a, stream);
+  if (a.d <= 8192) return run_norm<T, 256, 4>(a, stream);
+  return run_norm_long<T, 256, true>(a, stream);
+}
+
+// g / (1 + exp(-g)) * u
+__device__ __forceinline__ float gated_value(float g, float u) { return __fdiv_rn(g, 1.f + expf(-g)) * u; }
+
+template <typename T, bool GATED, bool VEC>
+__global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t block = blockIdx.x * 16 + threadIdx.x / 16;
+  const bool live = block < a.blocks;
+  const uint32_t row = div(a.nblocks, live ? block : a.blocks - 1);
+  const uint32_t b = (live ? block : a.blocks - 1) - row * a.nblocks.d;
+  const int c = static_cast<int>(b) * kBlock + 8 * (threadIdx.x & 15);
+  const bool in = live && c < a.d;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (in) {
+    load8<T, VEC>(x, c, a.d, v);
+    if constexpr (GATED) {
+      float u[8];
+      load8<T, VEC>(x + a.d, c, a.d, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = gated_value(v[i], u[i]);
+    }
+  }
+  float scale;
+  const uint2 codes = quantize8(v, &scale);
+  if (in) store_codes(a.codes + row * a.code_stride, c, a.d, codes, a.vec_codes);
+  if (live && (threadIdx.x & 15) == 0) a.scales[row * a.scale_row + b * a.scale_block] = scale;
+}
+
+template <typename T>
+cudaError_t quantize_of(const QuantArgs& a, cudaStream_t stream) {
+  const dim3 grid((a.blocks + 15) / 16), block(256);
+  if (a.gated)
+    return a.vec ? launch_ready<quantize_kernel<T, true, true>>(grid, block, 0, stream, a)
+                 : launch_ready<quantize_kernel<T, true, false>>(grid, block, 0, stream, a);
+  return a.vec ? launch_ready<quantize_kernel<T, false, true>>(grid, block, 0, stream, a)
+               : launch_ready<quantize_kernel<T, false, false>>(grid, block, 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t stream) {
+  if (a.dtype == MOE_DENSE_FP32) return norm_of<float>(a, sms, stream);
+  if (a.dtype == MOE_DENSE_BF16) return norm_of<__nv_bfloat16>(a, sms, stream);
+  return norm_of<__half>(a, sms, stream);
+}
+
+cudaError_t launch_quantize(const QuantArgs& a, int sms, cudaStream_t stream) {
+  if (a.dtype == MOE_DENSE_FP32) return quantize_of<float>(a, stream);
+  if (a.dtype == MOE_DENSE_BF16) return quantize_of<__nv_bfloat16>(a, stream);
+  return quantize_of<__half>(a, stream);
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,516 @@
+"""The dense path in 8 bits against plain 64-bit implementations (tests/dense_plain.py)."""
+import math
+
+import pytest
+import torch
+
+import dense_plain as P
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24  # half a step of FP32, relative
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import __graft_entry__
+    __graft_entry__.build()
+    import routed_moe_decode_gb300 as m
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rand(g, *shape, dtype=FP32, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def half_step(ref, dtype):
+    """Half a step of `dtype` at `ref`, subnormal values included."""
+    tiny = {BF16: 2.0 ** -134, FP16: 2.0 ** -25, FP32: 2.0 ** -150}[dtype]
+    return ref.abs() * (torch.finfo(dtype).eps / 2) + tiny
+
+
+def codes_of(rows):
+    return rows.codes.contiguous().view(torch.uint8).long()
+
+
+def equal_codes(got, want):
+    """Equal codes, +0 and -0 being the same."""
+    fold = lambda c: torch.where(c == 128, torch.zeros_like(c), c)  # noqa: E731
+    return torch.equal(fold(got), fold(want))
+
+
+def check_quantized(rows, n, rel):
+    """Rows in 8 bits against the 64-bit values n that they hold, computed with the relative error `rel`."""
+    _, scales = P.quantize(n)
+    s = rows.scales.double()
+    assert ((s - scales.double()).abs() <= scales.double() * (rel + 2 * U) + 2.0 ** -149).all()
+    v = P.values(rows.codes, rows.scales)
+    se = s.repeat_interleave(128, -1)[:, :n.shape[1]]
+    # a code is off by half a step, 2^-4 of the value or 2^-10 of the scale; the quotient by rel and the scale's error
+    bound = torch.maximum(n.abs() * 2.0 ** -4, se * 2.0 ** -10) * (1 + 1e-5) + n.abs() * (2 * rel + 4 * U)
+    assert ((v - n).abs() <= bound).all(), float(((v - n).abs() - bound).max())
+
+
+# ---- norm ----
+
+# factor: sums of squares (a chain of 8, one of a row's steps, shuffles) below 60 roundings of positive sums, halved by the
+# root, and four more; h * w, 1 + w, the last product
+NORM_REL = 40 * U
+
+NORMS = [(1, 1), (3, 7), (5, 64), (17, 128), (33, 120), (4, 256), (9, 500), (6, 512), (3, 1000), (8, 1024), (5, 1030), (2, 2048),
+         (3, 2047), (700, 2048), (2, 4096), (3, 5000), (2, 8192), (3, 8193), (2, 20000), (1, 65536)]
+
+
+@pytest.mark.parametrize("rows,d", NORMS)
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_norm(moe, rows, d, dtype):
+    g = gen(rows * 100003 + d)
+    x, r = rand(g, rows, d, dtype=dtype), rand(g, rows, d, dtype=dtype, scale=3.0)
+    wtype = {BF16: FP32, FP16: FP16, FP32: BF16}[dtype]
+    w = (1 + rand(g, d, scale=0.2)).to(wtype)
+    for residual, one_plus, quantize in ((True, False, True), (False, True, False), (True, True, False), (False, False, True)):
+        if quantize and d % 16 and d > 1030:
+            continue
+        norm = moe.RmsNorm(w, eps=1e-5, one_plus=one_plus)
+        n, h, q = norm(x, residual=r if residual else None, quantize=quantize)
+        want_h = (x.float() + r.float()).to(dtype) if residual else x
+        if residual:
+            assert torch.equal(h, want_h)
+        else:
+            assert h is None
+        want = P.rms_norm(want_h, w, 1e-5, one_plus)
+        assert ((n.double() - want).abs() <= half_step(want, dtype) * (1 + 2.0 ** -8) + want.abs() * NORM_REL).all()
+        if quantize:
+            check_quantized(q, want, NORM_REL)
+        else:
+            assert q is None
+
+
+def test_norm_strides_heads_and_places(moe):
+    g = gen(1)
+    qkv = rand(g, 37, 12, 96, dtype=BF16)
+    w = rand(g, 96, dtype=BF16)
+    before = qkv.clone()
+    # query heads of a fused projection, in place; then the same with rows in 8 bits
+    q = qkv[:, 2:10]
+    want = P.rms_norm(q, w, 1e-6, True)
+    norm = moe.RmsNorm(w, one_plus=True)
+    n, _, fp8 = norm(q, normed=q, quantize=True)
+    assert n.data_ptr() == q.data_ptr()
+    assert ((q.double() - want).abs() <= half_step(want, BF16) * (1 + 2.0 ** -8) + want.abs() * NORM_REL).all()
+    assert torch.equal(qkv[:, :2], before[:, :2]) and torch.equal(qkv[:, 10:], before[:, 10:])
+    check_quantized(fp8, want.reshape(37 * 8, 96), NORM_REL)
+    # unaligned rows and odd strides
+    buf = rand(g, 19, 203, dtype=FP16)
+    x = buf[:, 1:201]
+    w2 = rand(g, 200)
+    n, _, _ = moe.RmsNorm(w2)(x)
+    want = P.rms_norm(x, w2, 1e-6, False)
+    assert ((n.double() - want).abs() <= half_step(want, FP16) * (1 + 2.0 ** -8) + want.abs() * NORM_REL).all()
+    # the sum in the residual's place, the norm in x's; long rows are read twice
+    for d in (2048, 12000, 333):
+        x, r, w3 = rand(g, 5, d, dtype=BF16), rand(g, 5, d, dtype=BF16), rand(g, d)
+        h = (x.float() + r.float()).to(BF16)
+        want = P.rms_norm(h, w3, 1e-6, False)
+        n, ro, _ = moe.RmsNorm(w3)(x, residual=r, residual_out=r, normed=x)
+        assert ro.data_ptr() == r.data_ptr() and torch.equal(r, h)
+        assert ((x.double() - want).abs() <= half_step(want, BF16) * (1 + 2.0 ** -8) + want.abs() * NORM_REL).all()
+        # without its sum written
+        x, r = rand(g, 5, d, dtype=BF16), rand(g, 5, d, dtype=BF16)
+        want = P.rms_norm((x.float() + r.float()).to(BF16), w3, 1e-6, False)
+        n, ro, _ = moe.RmsNorm(w3)(x, residual=r, residual_out=False, normed=r)
+        assert ro is None and ((r.double() - want).abs() <= half_step(want, BF16) * (1 + 2.0 ** -8) + want.abs() * NORM_REL).all()
+
+
+def test_norm_zeros_infinities_and_refusals(moe):
+    w = torch.ones(256, device="cuda")
+    norm = moe.RmsNorm(w, eps=0.0)
+    x = torch.zeros(4, 256, device="cuda")
+    x[1], x[2, 7], x[3, 200] = 1.0, math.inf, math.nan
+    n, _, q = moe.RmsNorm(w)(x, quantize=True)
+    assert (n[0] == 0).all() and (q.scales[0] == 0).all() and (q.codes[0].float() == 0).all()
+    assert torch.isnan(n[2, 7]) and torch.isnan(n[3]).all()
+    assert torch.isnan(q.scales[3]).all() and torch.isfinite(q.scales[:2]).all()
+    assert torch.isnan(norm(x)[0][0]).all()  # 0 / 0 without an eps
+    y = rand(gen(1), 4, 256)
+    with pytest.raises(ValueError):
+        norm(y[:, ::2])
+    with pytest.raises(ValueError):
+        norm(y.double())
+    with pytest.raises(ValueError):
+        norm(y, residual_out=y)
+    with pytest.raises(ValueError):
+        norm(y, residual=y.half())
+    with pytest.raises(ValueError):
+        norm(y.view(2, 2, 256), residual=y.view(2, 2, 256))
+    with pytest.raises(ValueError):
+        norm(y, quantize=moe.Fp8Rows.empty(3, 256))
+    with pytest.raises(ValueError):  # in x's place with other strides
+        big = rand(gen(2), 8, 256)
+        norm(big[:4], normed=big[::2])
+    with pytest.raises(moe.MoeError):
+        norm(y, normed=False)
+    with pytest.raises(moe.MoeError):
+        h = torch.empty_like(y)
+        norm(y, residual=y, residual_out=h, normed=h)
+    e = torch.empty(0, 256, device="cuda")
+    assert norm(e)[0].shape == (0, 256)
+
+
+# ---- quantised rows ----
+
+@pytest.mark.parametrize("rows,d", [(1, 1), (1, 16), (3, 100), (5, 128), (2, 136), (33, 4096), (7, 1000), (4, 131), (300, 640)])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_quantize(moe, rows, d, dtype):
+    g = gen(d + rows)
+    x = rand(g, rows, d, dtype=dtype)
+    x[rows // 2] *= 1000.0
+    q = moe.quantize_rows(x)
+    codes, scales = P.quantize(x.double())
+    # quotients are exact: the same codes bit by bit
+    assert torch.equal(q.scales, scales)
+    assert equal_codes(codes_of(q), codes)
+
+
+def test_quantize_every_ratio_of_16_bit_values(moe):
+    """Quotients on and next to the borders between codes: every pair of 8-bit significands and a few exponents."""
+    sig = torch.arange(128, 256, device="cuda", dtype=FP32)
+    rows = []
+    for exp in (0, -1, -3, -6, -8, -9, -10):
+        block = torch.empty(128, 128, device="cuda")
+        block[:, :] = sig[None, :] * 2.0 ** exp
+        rows.append(block)
+    x = torch.cat(rows)
+    top = sig.repeat(len(rows)) * 2.0
+    x = torch.cat([top[:, None], x[:, :127]], dim=1)
+    x2 = torch.cat([top[:, None], torch.cat(rows)[:, 1:]], dim=1)
+    for y in (x, x2, -x, x * 2.0 ** -60, x * 2.0 ** -100, x * 2.0 ** -125, x * 2.0 ** 100):
+        q = moe.quantize_rows(y.to(BF16))
+        codes, scales = P.quantize(y.to(BF16).double())
+        assert torch.equal(q.scales, scales)
+        assert equal_codes(codes_of(q), codes)
+
+
+def test_quantize_small_and_large(moe):
+    x = torch.zeros(7, 256, device="cuda")
+    x[0, 3] = 2.0 ** -149
+    x[1] = rand(gen(1), 256) * 1e-40
+    x[2] = 3.4e38
+    x[3, :128] = rand(gen(2), 128)
+    x[3, 5], x[4, 130], x[5, 0] = math.inf, math.nan, -math.inf
+    x[4, :128], x[6, 255] = 1.0, -7.0
+    q = moe.quantize_rows(x)
+    for row in (0, 1, 2, 6):
+        codes, scales = P.quantize(x[row:row + 1].double())
+        assert torch.equal(q.scales[row:row + 1], scales)
+        assert equal_codes(codes_of(q)[row:row + 1], codes)
+    assert torch.isnan(q.scales[3, 0]) and torch.isnan(q.scales[4, 1]) and torch.isnan(q.scales[5, 0])
+    assert q.scales[3, 1] == 0 and q.scales[4, 0] == torch.tensor(1 / 448.0) and (codes_of(q)[3, :128] == 0).all()
+
+
+@pytest.mark.parametrize("rows,d", [(1, 16), (3, 100), (65, 512), (4, 131)])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_quantize_gated(moe, rows, d, dtype):
+    g = gen(d * 3 + rows)
+    x = rand(g, rows, 2 * d, dtype=dtype, scale=4.0)
+    x[0, 0], x[0, 1 % d] = 95.0, -95.0
+    q = moe.quantize_rows(x, gated=True)
+    a, b = x[:, :d].double(), x[:, d:].double()
+    want = a / (1 + torch.exp(-a)) * b
+    # the exponential to 2 units (4 halves), the sum, the quotient, the product
+    check_quantized(q, want, 8 * U)
+    with pytest.raises(ValueError):
+        moe.quantize_rows(x[:, :-1], gated=True)
+
+
+def test_quantize_strides_and_places(moe):
+    g = gen(5)
+    x = rand(g, 20, 300, dtype=BF16)
+    a = moe.quantize_rows(x[::2, 4:204])
+    codes, scales = P.quantize(x[::2, 4:204].double())
+    assert torch.equal(a.scales, scales) and equal_codes(codes_of(a), codes)
+    store = torch.zeros(10, 208, dtype=torch.uint8, device="cuda")
+    out = moe.Fp8Rows(store.view(torch.float8_e4m3fn)[:, :200], torch.zeros(10, 5, device="cuda")[:, ::3])
+    b = moe.quantize_rows(x[::2, 4:204], out=out)
+    assert b is out and torch.equal(out.scales, scales) and equal_codes(codes_of(out), codes)
+    assert (store[:, 200:] == 0).all()
+
+
+# ---- products ----
+
+def make_rows(moe, g, rows, k):
+    return moe.quantize_rows(rand(g, rows, k) * torch.exp(rand(g, k)))
+
+
+def make_weight(g, *shape):
+    n, k = shape[-2:]
+    codes = (rand(g, *shape) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    scales = (0.5 + torch.rand(*shape[:-2], -(-n // 128), -(-k // 128), generator=g, device="cuda")) / 100
+    return codes, scales
+
+
+def check_product(out, x, codes, scales):
+    """A block's sum of 128 products is formed 32 at a time in wider registers, each sum off by at most one step (2^-23) of
+    its largest term for every term: 2^-18 of the sum of magnitudes; a scale, a product and an addition a block more."""
+    xv, wv = P.values(x.codes, x.scales), P.weight_values(codes, scales)
+    want, size = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    blocks = -(-codes.shape[-1] // 128)
+    bound = size * (2.0 ** -18 + (blocks + 3) * U) + half_step(want, out.dtype)
+    assert ((out.double() - want).abs() <= bound).all(), float(((out.double() - want).abs() / bound).max())
+
+
+PRODUCTS = [(1, 1, 16), (1, 128, 128), (4, 100, 144), (4, 5120, 2048), (16, 257, 1040), (17, 128, 512), (31, 300, 80), (32, 640, 4096), (33, 129, 256),
+            (64, 1000, 512), (100, 384, 2064), (128, 2048, 256), (129, 128, 128), (200, 513, 400), (256, 256, 512), (257, 300, 1024),
+            (500, 100, 208), (1000, 513, 272), (1024, 1024, 1024), (2049, 2304, 512), (4000, 4100, 304)]
+
+
+@pytest.mark.parametrize("rows,n,k", PRODUCTS)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_product(moe, rows, n, k, dtype):
+    g = gen(rows + 7 * n + 11 * k)
+    x = make_rows(moe, g, rows, k)
+    codes, scales = make_weight(g, n, k)
+    linear = moe.Fp8Linear(codes, scales)
+    out = linear(x, dtype=dtype)
+    assert out.dtype is dtype and linear.status() == 0
+    check_product(out, x, codes, scales)
+    assert torch.equal(out, linear(x, dtype=dtype))
+
+
+def test_product_of_one_hot_rows_is_the_weight(moe):
+    """Each value of a weight comes back exactly, so rows, channels and scales meet where they should."""
+    g = gen(3)
+    n, k = 300, 272
+    codes, scales = make_weight(g, n, k)
+    one = torch.eye(k, device="cuda")
+    x = moe.quantize_rows(one)  # 1 = 448 * fl(1 / 448)
+    want = P.weight_values(codes, scales).t() * (448.0 * float(x.scales.max()))
+    for rows in (k, 20, 100):
+        part = moe.Fp8Rows(x.codes[:rows], x.scales[:rows])
+        out = moe.Fp8Linear(codes, scales)(part, dtype=FP32)
+        assert ((out.double() - want[:rows]).abs() <= want[:rows].abs() * 4 * U).all()
+
+
+def test_product_strides_types_and_places(moe):
+    g = gen(4)
+    rows, n, k = 50, 200, 160
+    wide = (rand(g, rows, 320) * 50).to(torch.float8_e4m3fn)
+    x = moe.Fp8Rows(wide[:, 128:288], torch.rand(rows, 6, generator=g, device="cuda")[:, 1:5:3])
+    codes, scales = make_weight(g, n, k)
+    linear = moe.Fp8Linear(codes, scales)
+    base = linear(x, dtype=FP32)
+    check_product(base, x, codes, scales)
+    for dtype in (BF16, FP16):
+        check_product(linear(x, dtype=dtype), x, codes, scales)
+    for off, width in ((0, 208), (1, 203), (4, 260)):
+        for dtype in (BF16, FP32):
+            store = torch.full((rows, width + off), 7.0, device="cuda", dtype=dtype)
+            out = linear(x, out=store[:, off:off + n])
+            check_product(out, x, codes, scales)
+            assert (store[:, :off] == 7).all() and (store[:, off + n:] == 7).all()
+    # every other row of a larger array
+    x2 = moe.Fp8Rows(wide[::2, 128:288], x.scales[::2])
+    assert torch.equal(linear(x2, dtype=FP32), base[::2])
+
+
+def test_product_nan_rows_stay_alone(moe):
+    g = gen(6)
+    v = rand(g, 40, 512)
+    v[3, 100] = math.nan
+    v[17, 511] = math.inf
+    x = moe.quantize_rows(v)
+    codes, scales = make_weight(g, 256, 512)
+    out = moe.Fp8Linear(codes, scales)(x)
+    bad = torch.isnan(out).all(-1)
+    assert bad.nonzero().flatten().tolist() == [3, 17] and torch.isfinite(out[~bad]).all()
+
+
+def test_product_refusals(moe):
+    g = gen(8)
+    codes, scales = make_weight(g, 64, 256)
+    linear = moe.Fp8Linear(codes, scales)
+    x = make_rows(moe, g, 4, 256)
+    with pytest.raises(ValueError):
+        linear(make_rows(moe, g, 4, 128))
+    with pytest.raises(ValueError):
+        linear(x, dtype=torch.float64)
+    with pytest.raises(ValueError):
+        linear(x, out=torch.empty(4, 65, device="cuda"))
+    with pytest.raises(ValueError):
+        linear(x, offsets=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        moe.Fp8Linear(codes, scales[:, :1].contiguous())
+    with pytest.raises(ValueError):
+        moe.Fp8Linear(codes.t(), scales)
+    with pytest.raises(moe.MoeError):
+        moe.Fp8Linear(codes[:, :250].contiguous(), scales)
+    with pytest.raises(moe.MoeError):  # rows 250 bytes apart
+        linear(moe.Fp8Rows(torch.zeros(4 * 264, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).view(4, 264)[:, :256],
+                           x.scales))
+    assert linear(make_rows(moe, g, 4, 256)).shape == (4, 64)
+    empty = moe.Fp8Rows(x.codes[:0], x.scales[:0])
+    assert linear(empty).shape == (0, 64)
+
+
+# ---- products of groups ----
+
+GROUPS = [([5], 128, 128), ([0, 3, 0, 0, 7, 1], 200, 272), ([1] * 40, 130, 512), ([0, 0, 0], 128, 128), ([300, 2, 0, 257, 90], 300, 144),
+          ([16, 17, 31, 32, 33, 64, 128, 129], 256, 256), ([1000, 0, 600], 140, 384), ([40] * 100, 128, 128),
+          ([0] * 500 + [9] + [0] * 522 + [1], 64, 64)]
+
+
+@pytest.mark.parametrize("counts,n,k", GROUPS)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_grouped_product(moe, counts, n, k, dtype):
+    g = gen(sum(counts) + n + k)
+    rows = sum(counts)
+    extra = 5  # rows behind the last group, and 2 before the first: left as they were
+    x = make_rows(moe, g, rows + 2 + extra, k)
+    codes, scales = make_weight(g, len(counts), n, k)
+    linear = moe.Fp8Linear(codes, scales)
+    edges = [2]
+    for c in counts:
+        edges.append(edges[-1] + c)
+    offsets = torch.tensor(edges, dtype=torch.int32, device="cuda")
+    out = torch.full((rows + 2 + extra, n), 7.0, dtype=dtype, device="cuda")
+    assert linear(x, offsets=offsets, out=out) is out
+    assert linear.status() == 0
+    assert (out[:2] == 7).all() and (out[rows + 2:] == 7).all()
+    for i, (a, b) in enumerate(zip(edges, edges[1:])):
+        if b > a:
+            check_product(out[a:b], moe.Fp8Rows(x.codes[a:b], x.scales[a:b]), codes[i], scales[i])
+
+
+def test_grouped_product_bad_offsets(moe):
+    """Offsets out of range or decreasing are cut, set a status bit and touch nothing outside."""
+    g = gen(12)
+    x = make_rows(moe, g, 20, 128)
+    codes, scales = make_weight(g, 4, 128, 128)
+    linear = moe.Fp8Linear(codes, scales)
+    for edges, spans in (([0, 5, 5, 25, 30], [(0, 0, 5), (2, 5, 20)]), ([-4, 6, 8, 8, 20], [(0, 0, 6), (1, 6, 8), (3, 8, 20)]),
+                         ([0, 5, 3, 3, 2], [(0, 0, 5)])):
+        store = torch.full((24, 128), 7.0, device="cuda")
+        linear(x, offsets=torch.tensor(edges, dtype=torch.int32, device="cuda"), out=store[2:22])
+        assert linear.status() == moe.DENSE_BAD_OFFSETS and linear.status() == 0
+        rest = torch.ones(24, dtype=torch.bool, device="cuda")
+        for i, a, b in spans:
+            check_product(store[2 + a:2 + b], moe.Fp8Rows(x.codes[a:b], x.scales[a:b]), codes[i], scales[i])
+            rest[2 + a:2 + b] = False
+        assert (store[rest] == 7).all()
+    with pytest.raises(ValueError):
+        linear(x)
+    with pytest.raises(ValueError):
+        linear(x, offsets=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        linear(x, offsets=torch.zeros(5, dtype=torch.int64, device="cuda"))
+
+
+def test_grouped_rows_do_not_depend_on_the_others(moe):
+    """A group's rows have the bits of the same rows alone under the same kernel (order of sums fixed by k alone)."""
+    g = gen(13)
+    x = make_rows(moe, g, 48, 512)
+    codes, scales = make_weight(g, 3, 256, 512)
+    linear = moe.Fp8Linear(codes, scales)
+    a = linear(x, offsets=torch.tensor([0, 20, 20, 48], dtype=torch.int32, device="cuda"))
+    b = linear(x, offsets=torch.tensor([3, 20, 41, 48], dtype=torch.int32, device="cuda"), out=torch.zeros_like(a))
+    assert torch.equal(a[3:20], b[3:20]) and torch.equal(a[41:], b[41:])
+
+
+# ---- log probabilities ----
+
+def check_logprobs(got, logits, tokens, top, scale):
+    want = P.logprobs(logits, tokens.view(tokens.shape[0], -1), top, scale)
+    for i, (given, lse, ent, ids, tops, spread) in enumerate(want):
+        def near(a, b, tol):
+            if math.isnan(b) or math.isinf(b):
+                assert (math.isnan(a) and math.isnan(b)) or a == b, (i, a, b)
+            else:
+                assert abs(a - b) <= tol, (i, a, b, tol)
+        # 61 additions in a row of sums of positive terms, exponentials to 2^-22 and their arguments to 2^-23 of at
+        # most 40: below 1e-5 of the sum; FP32 results
+        near(float(got.lse[i]), lse, 1e-5 + 4 * U * abs(lse))
+        near(float(got.entropy[i]), ent, 2e-5 * (1 + spread))
+        for a, b in zip(got.logprobs[i].view(-1).tolist(), given):
+            near(a, b, 1e-5 + 4 * U * (abs(b) + abs(lse)))
+        if top:
+            assert got.top_ids[i].tolist() == ids
+            for a, b in zip(got.top_logprobs[i].tolist(), tops):
+                near(a, b, 1e-5 + 4 * U * (abs(b) + abs(lse)))
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 1), (2, 3), (3, 17), (5, 100), (4, 1000), (3, 4099), (2, 20000), (1, 131072), (130, 997), (700, 64)])
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+def test_logprobs(moe, rows, vocab, dtype):
+    g = gen(vocab + rows)
+    logits = rand(g, rows, vocab, dtype=dtype, scale=3.0)
+    for n, top, scale in ((1, min(vocab, 8), 1.0), (3, 0, 0.7), (40, min(vocab, 32), 2.5), (2, 1, 1.0)):
+        tokens = torch.randint(0, vocab, (rows, n), generator=g, device="cuda").to(torch.int32)
+        got = moe.token_logprobs(logits, tokens, top=top, scale=scale)
+        assert (got.top_ids is None) == (top == 0)
+        check_logprobs(got, logits, tokens, top, scale)
+
+
+def test_logprobs_masks_ties_and_bad_tokens(moe):
+    g = gen(77)
+    inf = math.inf
+    v = 9000
+    logits = rand(g, 10, v, scale=2.0)
+    logits[0] = -inf                       # nothing left
+    logits[1] = -inf
+    logits[1, 4321] = -3.0                 # one left
+    logits[2] = 1.5                        # all equal
+    logits[3, ::2] = -inf
+    logits[4] = torch.arange(v, device="cuda") * 1e-3   # every value a new best
+    logits[5] = -torch.arange(v, device="cuda") * 1e-3
+    logits[6, 77] = math.nan
+    logits[7, 5] = inf
+    logits[8] = torch.finfo(FP32).min
+    logits[9, 100:140] = 9.0               # more ties than places
+    tokens = torch.tensor([[0, 1, -1, v]] * 10, dtype=torch.int32, device="cuda")
+    tokens[1, 0] = 4321
+    for dtype in (FP32, BF16, FP16):
+        x = logits.to(dtype)
+        for top in (0, 5, 32):
+            check_logprobs(moe.token_logprobs(x, tokens, top=top), x, tokens, top, 1.0)
+    zero = torch.zeros(2, 50, device="cuda")
+    zero[:, 1::2] = -0.0
+    got = moe.token_logprobs(zero, tokens[:2], top=32)
+    assert got.top_ids.tolist() == [list(range(32))] * 2
+    few = torch.full((1, 5000), -inf, device="cuda")
+    few[0, [4000, 17, 2500]] = torch.tensor([1.0, 1.0, 2.0], device="cuda")
+    got = moe.token_logprobs(few, tokens[:1], top=6)
+    assert got.top_ids.tolist() == [[2500, 17, 4000, 0, 1, 2]]
+
+
+def test_logprobs_strides(moe):
+    g = gen(78)
+    for dtype in (FP32, BF16):
+        buf = rand(g, 12, 5013, dtype=dtype)
+        tokens = torch.randint(0, 5000, (6, 8), generator=g, device="cuda").to(torch.int32)
+        for off in range(5):
+            x = buf[::2, off:off + 5001 - off]
+            check_logprobs(moe.token_logprobs(x, tokens[:, 2:5], top=3), x, tokens[:, 2:5], 3, 1.0)
+        flat = moe.token_logprobs(buf[:6], tokens[:, 0].contiguous(), top=3)
+        assert flat.logprobs.shape == (6,)
+        strided = moe.token_logprobs(buf[:6], tokens[:, 0], top=3)
+        assert torch.equal(flat.logprobs, strided.logprobs)
+
+
+def test_logprobs_refusals(moe):
+    x = torch.zeros(4, 100, device="cuda")
+    t = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in (lambda: moe.token_logprobs(x.t(), t), lambda: moe.token_logprobs(x, t.long()), lambda: moe.token_logprobs(x, t[:3]),
+                lambda: moe.token_logprobs(x.double(), t), lambda: moe.token_logprobs(x, t.cpu())):
+        with pytest.raises(ValueError):
+            bad()
+    for kw in (dict(top=33), dict(top=-1), dict(scale=0.0), dict(scale=math.inf)):
+        with pytest.raises(moe.MoeError):
+            moe.token_logprobs(x, t, **kw)
+    with pytest.raises(moe.MoeError):
+        moe.token_logprobs(x[:, :8], t, top=9)
+    assert moe.token_logprobs(x[:0], t[:0], top=2).top_ids.shape == (0, 2)
