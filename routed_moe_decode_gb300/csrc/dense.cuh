@@ -72,8 +72,13 @@ struct MatmulArgs {
   int copy_arrivals;  // arrivals that a stage's barrier waits for beside its bytes
 };
 cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, cudaStream_t stream);
-// Map of a matrix of bytes, loaded in boxes of 128 bytes x box_rows rows with the 128-byte swizzle.
-int encode_fp8_map(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, uint64_t stride, uint32_t box_rows);
+cudaError_t launch_fp8_wide(const MatmulArgs& a, int sms, cudaStream_t stream);
+// Map of a matrix of size-byte elements, copied in boxes of 128 bytes x box_rows rows with the 128-byte swizzle; stride in bytes.
+int encode_rows_map(CUtensorMap* map, const void* base, int size, uint64_t cols, uint64_t rows, uint64_t stride,
+                    uint32_t box_cols, uint32_t box_rows);
+inline int encode_fp8_map(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, uint64_t stride, uint32_t box_rows) {
+  return encode_rows_map(map, base, 1, k, rows, stride, 128, box_rows);
+}
 
 // Log probabilities.
 struct LogprobArgs {
@@ -135,6 +140,16 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=l"(reinterpret_cast<unsigned long long&>(d))
       : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
         "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return d;
+}
+
+// The same, where what is multiplied comes from tensor memory: not moved before the wait for it.
+__device__ __forceinline__ float2 fma2_in_order(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %3;"
+               : "=l"(reinterpret_cast<unsigned long long&>(d))
+               : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+                 "l"(reinterpret_cast<const unsigned long long&>(c)));
   return d;
 }
 

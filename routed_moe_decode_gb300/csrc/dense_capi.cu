@@ -9,7 +9,8 @@
 namespace moe {
 namespace dense {
 
-int encode_fp8_map(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, uint64_t stride, uint32_t box_rows) {
+int encode_rows_map(CUtensorMap* map, const void* base, int size, uint64_t cols, uint64_t rows, uint64_t stride,
+                    uint32_t box_cols, uint32_t box_rows) {
   typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -26,9 +27,9 @@ int encode_fp8_map(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows
     set_last_error_message("no cuTensorMapEncodeTiled");
     return MOE_ERR_CUDA;
   }
-  const cuuint64_t dims[2] = {k, rows}, strides[1] = {stride};
-  const cuuint32_t box[2] = {128, box_rows}, steps[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, steps,
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride};
+  const cuuint32_t box[2] = {box_cols, box_rows}, steps[2] = {1, 1};
+  const CUresult r = encode(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, steps,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -89,7 +90,9 @@ int matmul(int rows, int n, int k, int groups, const uint8_t* codes, int64_t cod
   a.x_stride = rows > 1 ? code_stride : (k + 15) / 16 * 16; a.scale_row = scale_row; a.scale_block = scale_block; a.out_stride = out_stride;
   a.rows = rows; a.n = n; a.k = k; a.groups = groups ? groups : 1; a.out_dtype = out_dtype;
   a.wait_cycles = wait_cycles; a.copy_arrivals = copy_arrivals;
-  return done("product launch", moe::dense::launch_fp8_stream(a, sms, stream));
+  const int64_t average = (rows + a.groups - 1) / a.groups;
+  const bool wide = average > (groups ? 64 : 128);
+  return done("product launch", wide ? moe::dense::launch_fp8_wide(a, sms, stream) : moe::dense::launch_fp8_stream(a, sms, stream));
 }
 
 }  // namespace

@@ -11,7 +11,7 @@
 // each), a warp copies tiles into a ring, a warp issues the MMAs, two warps bring xs * ws of a block's rows into shared memory.
 // CTAs take tiles statically, one after the other; the ring runs on across tiles.  Where one row of x tiles would leave
 // SMs idle, a cluster's CTAs take a part of k each and add up through distributed shared memory, in order.
-#include "dense.cuh"
+#include "fp8_tiles.cuh"
 
 namespace moe {
 namespace dense {
@@ -19,63 +19,48 @@ namespace {
 
 constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarps = 2, kScaleWarp = 10, kThreads = 32 * 12;
 constexpr uint32_t kDrainCycles = 1u << 24;
+constexpr int kSlab = 16;      // rows of x whose sums are staged for writing at a time
 constexpr int kPrefetch = 4;  // blocks of scales that are under way in a scale warp's registers
 
 template <int NT>
 struct Shape {
   static constexpr int kStage = (128 + NT) * 128;
-  static constexpr int kStages = NT == 256 ? 4 : NT == 128 ? 6 : 10;
-  static constexpr int kBufs = NT == 256 ? 2 : NT == 128 ? 4 : 8;  // products in tensor memory
+  static constexpr int kStages = NT == 128 ? 6 : 9;
+  static constexpr int kBufs = NT == 128 ? 4 : 8;  // products in tensor memory
   static constexpr int kCols = NT * kBufs;
   static constexpr int kScales = kStage * kStages;                 // [kBufs][NT] floats
-  static constexpr int kBars = kScales + 4 * NT * kBufs;
+  static constexpr int kStaged = kScales + 4 * NT * kBufs;         // [2][kSlab][128] floats
+  static constexpr int kBars = kStaged + 4 * 2 * kSlab * 128;
   static constexpr int kNumBars = 2 * kStages + 3 * kBufs + 1;
-  static constexpr int kFirst = kBars + 8 * kNumBars;              // groups' first row [kMaxGroups], rows [kMaxGroups]
-  static constexpr int kTiles = kFirst + 8 * kMaxGroups;           // row tiles before a group [kMaxGroups + 1]
-  static constexpr int kTotal = kTiles + 4 * (kMaxGroups + 1) + 1024;
+  static constexpr int kGroups = kBars + 8 * kNumBars;
+  static constexpr int kTotal = kGroups + static_cast<int>(sizeof(Groups)) + 1024;
   static_assert(kTotal <= 227 * 1024);
-};
-
-struct Tile {
-  int64_t w_row;    // row of the weights' matrix at which it begins
-  const float* ws;  // scales of its 128 channels [blocks of k]
-  int c0, row0, rows;
 };
 
 struct Maps {
   CUtensorMap w, x16, x64;
 };
 
-template <int NT>
-__device__ __forceinline__ Tile tile_of(const MatmulArgs& a, int id, int ctiles, int kblocks, const int* first,
-                                        const int* rows, const int* before) {
-  // the last group with before[g] <= id / ctiles: that one's tiles end behind it, so it has rows
-  int g = 0;
-  if (a.groups > 1) {
-    const int at = id / ctiles;
-    for (int lo = a.groups; lo > 0;) {  // lo: groups from g on that are left
-      const int step = lo >> 1;
-      if (step == 0) break;
-      if (before[g + step] <= at) { g += step; lo -= step; }
-      else lo = step;
-    }
-  }
-  const int local = id - before[g] * ctiles, tts = before[g + 1] - before[g];
-  const int ct = local / tts, tt = local - ct * tts;
-  const int per = ((rows[g] + tts - 1) / tts + 15) & ~15;
-  Tile t;
-  t.c0 = ct * 128;
-  t.w_row = static_cast<int64_t>(g) * a.n + t.c0;
-  t.ws = a.ws + (static_cast<int64_t>(g) * ctiles + ct) * kblocks;
-  t.row0 = first[g] + tt * per;
-  t.rows = max(0, min(per, rows[g] - tt * per));
-  return t;
-}
-
 __device__ __forceinline__ void store_one(const MatmulArgs& a, int64_t row, int c, float v) {
   if (a.out_dtype == MOE_DENSE_FP32) static_cast<float*>(a.out)[row * a.out_stride + c] = v;
   else if (a.out_dtype == MOE_DENSE_BF16) static_cast<__nv_bfloat16*>(a.out)[row * a.out_stride + c] = __float2bfloat16_rn(v);
   else static_cast<__half*>(a.out)[row * a.out_stride + c] = __float2half_rn(v);
+}
+
+// Four channels from c on; vec: rows can be written four at a time.
+__device__ __forceinline__ void store4(const MatmulArgs& a, int64_t row, int c, float4 v, bool vec) {
+  if (vec && c + 4 <= a.n) {
+    const int64_t at = row * a.out_stride + c;
+    if (a.out_dtype == MOE_DENSE_FP32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+    else if (a.out_dtype == MOE_DENSE_BF16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = make_uint2(two<__nv_bfloat16>(v.x, v.y), two<__nv_bfloat16>(v.z, v.w));
+    else *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + at) = make_uint2(two<__half>(v.x, v.y), two<__half>(v.z, v.w));
+    return;
+  }
+  const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + i < a.n) store_one(a, row, c + i, f[i]);
 }
 
 template <int NT>
@@ -87,9 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_scan[12];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_addr(smem);
-  int* s_first = reinterpret_cast<int*>(smem + L::kFirst);
-  int* s_rows = s_first + kMaxGroups;
-  int* s_before = reinterpret_cast<int*>(smem + L::kTiles);
+  Groups& gs = *reinterpret_cast<Groups*>(smem + L::kGroups);
   const uint32_t full = base + L::kBars, empty = full + 8 * L::kStages, done = empty + 8 * L::kStages,
                  freed = done + 8 * L::kBufs, scaled = freed + 8 * L::kBufs, end = scaled + 8 * L::kBufs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -119,40 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // groups: first rows, rows, row tiles before each
-  {
-    const int per = (a.groups + kThreads - 1) / kThreads;
-    const int g0 = min(tid * per, a.groups), g1 = min(g0 + per, a.groups);
-    int mine = 0;
-    for (int g = g0; g < g1; ++g) {
-      int b = 0, e = a.rows;
-      if (a.offsets) {
-        const int rb = __ldcg(a.offsets + g), re = __ldcg(a.offsets + g + 1);
-        b = min(max(rb, 0), a.rows);
-        e = min(max(re, 0), a.rows);
-        if (blockIdx.x == 0 && (b != rb || e != re || re < rb)) atomicOr(a.status, MOE_DENSE_BAD_OFFSETS);
-      }
-      const int n = max(e - b, 0);
-      s_first[g] = b;
-      s_rows[g] = n;
-      mine += (n + NT - 1) / NT;
-    }
-    int sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) s_scan[warp] = sum;
-    __syncthreads();
-    int at = sum - mine;
-    for (int i = 0; i < warp; ++i) at += s_scan[i];
-    for (int g = g0; g < g1; ++g) {
-      s_before[g] = at;
-      at += (s_rows[g] + NT - 1) / NT;
-    }
-    if (tid == kThreads - 1) s_before[a.groups] = at;
-  }
+  make_groups<kThreads / 32, NT>(a, gs, s_scan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -162,13 +112,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = static_cast<int>(cluster_size()), part = static_cast<int>(cluster_rank());
   const int ctiles = (a.n + 127) / 128, kblocks = (a.k + 127) / 128;
   const int k0 = kblocks * part / split, k1 = kblocks * (part + 1) / split;
-  const int tiles = s_before[a.groups] * ctiles, stride = gridDim.x / split;
+  const int tiles = gs.before[a.groups] * ctiles, stride = gridDim.x / split;
 
   if (warp == kCopyWarp) {
     uint32_t it = 0;
     bool ok = true;
     for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
-      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const Tile t = tile_of<NT, 128, true>(a, id, ctiles, kblocks, gs);
       const int n16 = (t.rows + 15) >> 4;
       const uint32_t bytes = 128 * 128 + n16 * 16 * 128;
       for (int kb = k0; kb < k1; ++kb, ++it) {
@@ -196,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
-      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const Tile t = tile_of<NT, 128, true>(a, id, ctiles, kblocks, gs);
       const uint32_t idesc = idesc_e4m3(128, max(16, (t.rows + 15) & ~15));
       for (int kb = k0; kb < k1; ++kb, ++it) {
         const uint32_t s = it % L::kStages, b = it % L::kBufs;
@@ -230,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
-      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const Tile t = tile_of<NT, 128, true>(a, id, ctiles, kblocks, gs);
       float x[kPrefetch][PER], w[kPrefetch];
       auto load = [&](int j, int kb) {
         w[j] = kb < k1 ? __ldcg(t.ws + kb) : 0.f;
@@ -264,10 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int H = NT / 2;
     const int half = warp >> 2, quarter = warp & 3;
     const float* scales = reinterpret_cast<const float*>(smem + L::kScales);
+    const int size = a.out_dtype == MOE_DENSE_FP32 ? 4 : 2;
+    const bool vec = reinterpret_cast<uintptr_t>(a.out) % (4 * size) == 0 && a.out_stride % 4 == 0;
     uint32_t it = 0;
     bool ok = true;
     for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
-      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const Tile t = tile_of<NT, 128, true>(a, id, ctiles, kblocks, gs);
       const int n = (t.rows + 15) & ~15, cut = ((n / 2) + 15) & ~15;  // rows [0, cut) and [cut, n)
       const int first = half ? cut : 0, mine = half ? n - cut : cut;
       float2 acc[H / 2];
@@ -299,16 +251,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(freed + 8 * b);
       }
+      // the four warps of a half write together, so they go on or give up together
+      ok = named_bar_and(1 + half, 128, ok);
       if (!ok) break;
       const int ch = quarter * 32 + lane;
       if (split == 1) {
-        if (t.c0 + ch < a.n) {
+        float* staged = reinterpret_cast<float*>(smem + L::kStaged) + half * kSlab * 128;
 #pragma unroll
-          for (int i = 0; i < H / 2; ++i) {
-            const int r = first + 2 * i;
-            if (2 * i < mine && r < t.rows) store_one(a, t.row0 + r, t.c0 + ch, acc[i].x);
-            if (2 * i < mine && r + 1 < t.rows) store_one(a, t.row0 + r + 1, t.c0 + ch, acc[i].y);
+        for (int c = 0; c < H; c += kSlab) {
+          if (c >= mine) break;
+#pragma unroll
+          for (int i = 0; i < kSlab; i += 2) {
+            staged[i * 128 + ch] = acc[(c + i) / 2].x;
+            staged[(i + 1) * 128 + ch] = acc[(c + i) / 2].y;
           }
+          named_bar_sync(1 + half, 128);
+          for (int i = ch; i < kSlab * 32; i += 128) {
+            const int r = first + c + (i >> 5), at = (i & 31) * 4;
+            if (r < t.rows) store4(a, t.row0 + r, t.c0 + at, *reinterpret_cast<const float4*>(staged + 4 * i), vec);
+          }
+          named_bar_sync(1 + half, 128);
         }
       } else {
         // the only tile of this cluster: its copies have landed and its products have read them, so the ring is free
@@ -328,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     const int id = blockIdx.x / split;
     if (id < tiles && s_limit) {
-      const Tile t = tile_of<NT>(a, id, ctiles, kblocks, s_first, s_rows, s_before);
+      const Tile t = tile_of<NT, 128, true>(a, id, ctiles, kblocks, gs);
       const int ch = tid & 127;
       // three groups of 128 threads, every CTA a row of its own
       for (int r = part + split * (tid >> 7); r < t.rows; r += 3 * split) {
@@ -362,21 +324,18 @@ cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, cudaStream_t stream)
       encode_fp8_map(&maps.x64, a.x, a.k, a.rows, a.x_stride, 64) != MOE_OK)
     return cudaErrorInvalidValue;
   const int64_t average = (a.rows + groups - 1) / groups;
-  const int nt = average <= (a.offsets ? 16 : 32) ? 32 : average <= (a.offsets ? 64 : 128) ? 128 : 256;
-  int split = 1;
+  const bool few = average <= (a.offsets ? 16 : 32);
+  const int nt = few ? 32 : 128;
+  int split = 1, grid = sms;
   const int ctiles = (a.n + 127) / 128, kblocks = (a.k + 127) / 128;
-  int grid = sms;
   if (!a.offsets) {
     const int64_t tiles = static_cast<int64_t>(ctiles) * ((a.rows + nt - 1) / nt);
     if (tiles < sms) {
-      if (nt < 256)
-        while (split < 8 && tiles * (split + 1) <= sms && split + 1 <= kblocks) ++split;
+      while (split < 8 && tiles * (split + 1) <= sms && split + 1 <= kblocks) ++split;
       grid = static_cast<int>(tiles) * split;
     }
   }
-  if (nt == 32) return run<32>(maps, a, split, grid, stream);
-  if (nt == 128) return run<128>(maps, a, split, grid, stream);
-  return run<256>(maps, a, split, grid, stream);
+  return few ? run<32>(maps, a, split, grid, stream) : run<128>(maps, a, split, grid, stream);
 }
 
 }  // namespace dense
