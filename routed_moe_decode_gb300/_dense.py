@@ -41,14 +41,27 @@ class Fp8Rows:
     def empty(cls, rows, k, device="cuda", stream=None):
         """Rows to be written: code rows a multiple of 16 bytes apart, a block's scales together (as the products
         read them best)."""
-        codes = _empty((rows, -(-k // 16) * 16), _E4M3, device, stream)
-        return cls(codes[:, :k] if k % 16 else codes, _empty((-(-k // 128), rows), torch.float32, device, stream).t())
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return cls.empty(rows, k, device)
+        self = object.__new__(cls)
+        codes = torch.empty((rows, -(-k // 16) * 16), dtype=_E4M3, device=device)
+        self.codes = codes[:, :k] if k % 16 else codes
+        self.scales = torch.empty_strided((rows, -(-k // 128)), (1, rows), dtype=torch.float32, device=device)
+        self.device, self._index = codes.device, codes.get_device()
+        return self
 
 
 def _rows_to_write(out, rows, k, index):
     if out.codes.shape != (rows, k) or out._index != index:
         raise ValueError(f"8-bit rows: [{rows}, {k}] on cuda:{index}")
     return out
+
+
+def _same_place(out, out_strides, of, of_strides):
+    """An output in an input's place has its strides."""
+    if of is not None and out.data_ptr() == of.data_ptr() and out_strides != of_strides:
+        raise ValueError("an output in an input's place has its strides")
 
 
 class RmsNorm:
@@ -62,6 +75,7 @@ class RmsNorm:
             raise ValueError("weight: contiguous [d] of float32, bfloat16 or float16 on a CUDA device")
         self.weight, self.eps, self.one_plus = weight, float(eps), bool(one_plus)
         self.d, self._index = weight.shape[0], weight.get_device()
+        self._weight_dtype = _DTYPES[weight.dtype]
         self._norm = _lib.lib().moe_rms_norm
 
     def __call__(self, x, residual=None, normed=True, residual_out=None, quantize=False, stream=None):
@@ -73,61 +87,58 @@ class RmsNorm:
             given, which may be x or the residual) receives it; residual_out=False: it is not written;
           quantize: True for new Fp8Rows of [rows, d] (outer * inner rows), Fp8Rows to write, False for none.
         """
-        d, index, shape = self.d, self._index, x.shape
-        dtype = _DTYPES.get(x.dtype)
-        if dtype is None or len(shape) not in (2, 3) or shape[-1] != d or (d > 1 and x.stride(-1) != 1) or x.get_device() != index:
+        d, index, shape, strides = self.d, self._index, x.shape, x.stride()
+        dtype, dims = _DTYPES.get(x.dtype), len(shape)
+        if dtype is None or not 2 <= dims <= 3 or shape[-1] != d or (strides[-1] != 1 and d > 1) or x.get_device() != index:
             raise ValueError(f"x: [rows, {d}] or [outer, inner, {d}] of float32, bfloat16 or float16 on cuda:{index} with "
                              "consecutive channels")
-        if len(shape) == 2:
-            outer, inner, x_outer, x_inner = shape[0], 1, x.stride(0), 0
-        else:
-            outer, inner, x_outer, x_inner = shape[0], shape[1], x.stride(0), x.stride(1)
+        outer, inner = shape[0], shape[1] if dims == 3 else 1
+        x_inner = strides[1] if dims == 3 else 0
+        residual_ptr = sum_ptr = normed_ptr = codes_ptr = scales_ptr = None
         r_stride = ro_stride = n_outer = n_inner = code_stride = scale_row = scale_block = 0
         if residual is not None:
-            if residual.dtype is not x.dtype or residual.shape != shape or len(shape) != 2 or \
-                    (d > 1 and residual.stride(1) != 1) or residual.get_device() != index:
+            if residual.dtype is not x.dtype or residual.shape != shape or dims != 2 or \
+                    (residual.stride(1) != 1 and d > 1) or residual.get_device() != index:
                 raise ValueError(f"residual: of x's type and shape, which is [rows, {d}], with consecutive channels")
-            r_stride = residual.stride(0)
+            residual_ptr, r_stride = residual.data_ptr(), residual.stride(0)
             if residual_out is None:
-                residual_out = _empty(shape, x.dtype, x.device, stream)
+                residual_out, ro_stride = _empty(shape, x.dtype, x.device, stream), d
+                sum_ptr = residual_out.data_ptr()
             elif residual_out is False:
                 residual_out = None
-            if residual_out is not None:
+            else:
                 if residual_out.dtype is not x.dtype or residual_out.shape != shape or \
-                        (d > 1 and residual_out.stride(1) != 1) or residual_out.get_device() != index:
+                        (residual_out.stride(1) != 1 and d > 1) or residual_out.get_device() != index:
                     raise ValueError(f"residual_out: of x's type and shape with consecutive channels on cuda:{index}")
-                ro_stride = residual_out.stride(0)
+                _same_place(residual_out, residual_out.stride(), x, strides)
+                _same_place(residual_out, residual_out.stride(), residual, residual.stride())
+                sum_ptr, ro_stride = residual_out.data_ptr(), residual_out.stride(0)
         elif residual_out is not None and residual_out is not False:
             raise ValueError("residual_out needs a residual")
         else:
             residual_out = None
         if normed is True:
-            normed = _empty(shape, x.dtype, x.device, stream)
-        elif normed is False:
+            normed, n_outer, n_inner = _empty(shape, x.dtype, x.device, stream), inner * d, d
+            normed_ptr = normed.data_ptr()
+        elif normed is False or normed is None:
             normed = None
-        if normed is not None:
-            if normed.dtype is not x.dtype or normed.shape != shape or (d > 1 and normed.stride(-1) != 1) or \
-                    normed.get_device() != index:
+        else:
+            to = normed.stride()
+            if normed.dtype is not x.dtype or normed.shape != shape or (to[-1] != 1 and d > 1) or normed.get_device() != index:
                 raise ValueError(f"normed: of x's type and shape with consecutive channels on cuda:{index}")
-            n_outer, n_inner = normed.stride(0), normed.stride(1) if len(shape) == 3 else 0
+            _same_place(normed, to, x, strides)
+            if residual is not None:
+                _same_place(normed, to, residual, residual.stride())
+            normed_ptr, n_outer, n_inner = normed.data_ptr(), to[0], to[1] if dims == 3 else 0
         fp8 = None
-        if quantize is not False:
+        if quantize is not False and quantize is not None:
             rows = outer * inner
             fp8 = Fp8Rows.empty(rows, d, x.device, stream) if quantize is True else _rows_to_write(quantize, rows, d, index)
-            code_stride = fp8.codes.stride(0)
+            codes_ptr, scales_ptr, code_stride = fp8.codes.data_ptr(), fp8.scales.data_ptr(), fp8.codes.stride(0)
             scale_row, scale_block = fp8.scales.stride()
-        for a, b, sa, sb in ((residual_out, x, ro_stride, x_outer), (residual_out, residual, ro_stride, r_stride),
-                             (normed, x, n_outer, x_outer), (normed, residual, n_outer, r_stride)):
-            if a is not None and b is not None and outer > 1 and a.data_ptr() == b.data_ptr() and sa != sb:
-                raise ValueError("an output in an input's place has its strides")
-        rc = self._norm(outer, inner, d, dtype, x.data_ptr(), x_outer, x_inner,
-                        None if residual is None else residual.data_ptr(), r_stride, self.weight.data_ptr(),
-                        _DTYPES[self.weight.dtype], self.one_plus, self.eps,
-                        None if residual_out is None else residual_out.data_ptr(), ro_stride,
-                        None if normed is None else normed.data_ptr(), n_outer, n_inner,
-                        None if fp8 is None else fp8.codes.data_ptr(), code_stride,
-                        None if fp8 is None else fp8.scales.data_ptr(), scale_row, scale_block,
-                        _raw_stream(index, stream))
+        rc = self._norm(outer, inner, d, dtype, x.data_ptr(), strides[0], x_inner, residual_ptr, r_stride,
+                        self.weight.data_ptr(), self._weight_dtype, self.one_plus, self.eps, sum_ptr, ro_stride, normed_ptr, n_outer, n_inner,
+                        codes_ptr, code_stride, scales_ptr, scale_row, scale_block, _raw_stream(index, stream))
         if rc != 0:
             raise _lib.MoeError("moe_rms_norm", rc)
         return normed, residual_out, fp8
@@ -136,15 +147,16 @@ class RmsNorm:
 def quantize_rows(x, gated=False, out=None, stream=None):
     """x [rows, d] of float32, bfloat16 or float16 (consecutive channels) as Fp8Rows (in `out`, if given); gated: x is
     [rows, 2 d], gate then up, and silu(gate) * up is quantised."""
-    dtype = _DTYPES.get(x.dtype)
-    index = x.get_device()
-    if dtype is None or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or index < 0 or (gated and x.shape[1] % 2):
+    dtype, index, (row, channel) = _DTYPES.get(x.dtype), x.get_device(), x.stride() if x.dim() == 2 else (0, 0)
+    rows, d = x.shape if x.dim() == 2 else (0, 0)
+    if dtype is None or x.dim() != 2 or (channel != 1 and d > 1) or index < 0 or (gated and d % 2):
         raise ValueError("x: [rows, d] (gated: [rows, 2 d]) of float32, bfloat16 or float16 on a CUDA device with "
                          "consecutive channels")
-    rows, d = x.shape[0], x.shape[1] // (2 if gated else 1)
+    if gated:
+        d //= 2
     out = Fp8Rows.empty(rows, d, x.device, stream) if out is None else _rows_to_write(out, rows, d, index)
     scale_row, scale_block = out.scales.stride()
-    rc = _lib.lib().moe_quantize_rows(rows, d, bool(gated), dtype, x.data_ptr(), x.stride(0), out.codes.data_ptr(),
+    rc = _lib.lib().moe_quantize_rows(rows, d, 1 if gated else 0, dtype, x.data_ptr(), row, out.codes.data_ptr(),
                                       out.codes.stride(0), out.scales.data_ptr(), scale_row, scale_block,
                                       _raw_stream(index, stream))
     if rc != 0:
@@ -180,13 +192,16 @@ class Fp8Linear:
         """x: Fp8Rows [rows, k]; the product [rows, n] in `out` (consecutive channels) if given, else a new tensor of
         `dtype`.  With groups, offsets [groups + 1] int32 on the device: rows offsets[g] .. offsets[g + 1] - 1 meet weight
         g; rows of no group are left as they were."""
-        index, rows, n = self._index, x.codes.shape[0], self.n
-        if x.codes.shape[1] != self.k or x._index != index:
+        index, n = self._index, self.n
+        rows, k = x.codes.shape
+        if k != self.k or x._index != index:
             raise ValueError(f"x: [rows, {self.k}] on cuda:{index}")
         if out is None:
-            out = _empty((rows, n), dtype, self.device, stream)
-        elif out.shape != (rows, n) or (n > 1 and out.stride(1) != 1) or out.get_device() != index:
-            raise ValueError(f"out: [{rows}, {n}] with consecutive channels on cuda:{index}")
+            out, out_stride = _empty((rows, n), dtype, self.device, stream), n
+        else:
+            out_stride, channel = out.stride() if out.dim() == 2 else (0, 0)
+            if out.shape != (rows, n) or (channel != 1 and n > 1) or out.get_device() != index:
+                raise ValueError(f"out: [{rows}, {n}] with consecutive channels on cuda:{index}")
         out_dtype = _DTYPES.get(out.dtype)
         if out_dtype is None:
             raise ValueError("out is of float32, bfloat16 or float16")
@@ -198,9 +213,9 @@ class Fp8Linear:
         elif offsets is not None:
             raise ValueError("offsets need a weight with groups")
         scale_row, scale_block = x.scales.stride()
-        rc = self._matmul(rows, n, self.k, self.groups, x.codes.data_ptr(), x.codes.stride(0), x.scales.data_ptr(),
-                          scale_row, scale_block, self.codes.data_ptr(), self.scales.data_ptr(), offsets, out.data_ptr(),
-                          out.stride(0), out_dtype, self._status.data_ptr(), _raw_stream(index, stream))
+        rc = self._matmul(rows, n, k, self.groups, x.codes.data_ptr(), x.codes.stride(0), x.scales.data_ptr(), scale_row,
+                          scale_block, self.codes.data_ptr(), self.scales.data_ptr(), offsets, out.data_ptr(), out_stride,
+                          out_dtype, self._status.data_ptr(), _raw_stream(index, stream))
         if rc != 0:
             raise _lib.MoeError("moe_fp8_matmul", rc)
         return out
@@ -227,30 +242,27 @@ def token_logprobs(logits, tokens, top=0, scale=1.0, stream=None):
     """Log probabilities of tokens [rows, n] or [rows] int32 under the softmax of scale * logits [rows, vocab] (float32,
     bfloat16 or float16; consecutive columns), with every row's log-sum-exp, entropy and its `top` best tokens (equal
     logits: the lower id first).  A token outside the vocabulary has log probability -infinity (moe_token_logprobs)."""
-    dtype = _DTYPES.get(logits.dtype)
-    index = logits.get_device()
-    if dtype is None or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1) or index < 0:
+    dtype, index = _DTYPES.get(logits.dtype), logits.get_device()
+    if dtype is None or logits.dim() != 2 or index < 0 or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits: [rows, vocab] of float32, bfloat16 or float16 on a CUDA device with consecutive columns")
     rows, vocab = logits.shape
-    if tokens.dtype is not torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != rows or \
-            tokens.get_device() != index or (tokens.dim() == 2 and tokens.shape[1] > 1 and tokens.stride(1) != 1):
+    shape, strides = tokens.shape, tokens.stride()
+    n = shape[1] if len(shape) == 2 else 1
+    if tokens.dtype is not torch.int32 or not 1 <= len(shape) <= 2 or shape[0] != rows or tokens.get_device() != index or \
+            (len(shape) == 2 and strides[1] != 1 and n > 1):
         raise ValueError(f"tokens: [{rows}, n] or [{rows}] of int32 on cuda:{index} with consecutive columns")
-    n = tokens.shape[1] if tokens.dim() == 2 else 1
-    top = int(top)
-    device = logits.device
-    logprobs = _empty(tokens.shape, torch.float32, device, stream)
-    lse = _empty((rows,), torch.float32, device, stream)
-    entropy = _empty((rows,), torch.float32, device, stream)
-    top_ids = _empty((rows, top), torch.int32, device, stream) if top > 0 else None
-    top_logprobs = _empty((rows, top), torch.float32, device, stream) if top > 0 else None
+    device, f32 = logits.device, torch.float32
+    logprobs, lse, entropy = _empty(shape, f32, device, stream), _empty(rows, f32, device, stream), _empty(rows, f32, device, stream)
+    ids = best = ids_ptr = best_ptr = None
+    if top > 0:
+        ids, best = _empty((rows, top), torch.int32, device, stream), _empty((rows, top), f32, device, stream)
+        ids_ptr, best_ptr = ids.data_ptr(), best.data_ptr()
     rc = _lib.lib().moe_token_logprobs(rows, vocab, dtype, logits.data_ptr(), logits.stride(0), scale, tokens.data_ptr(), n,
-                                       tokens.stride(0), top, logprobs.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
-                                       None if top_ids is None else top_ids.data_ptr(),
-                                       None if top_logprobs is None else top_logprobs.data_ptr(),
-                                       _raw_stream(index, stream))
+                                       strides[0], top, logprobs.data_ptr(), lse.data_ptr(), entropy.data_ptr(), ids_ptr,
+                                       best_ptr, _raw_stream(index, stream))
     if rc != 0:
         raise _lib.MoeError("moe_token_logprobs", rc)
-    return TokenLogprobs(logprobs, lse, entropy, top_ids, top_logprobs)
+    return TokenLogprobs(logprobs, lse, entropy, ids, best)
 
 
 def selftest_fp8_matmul(linear, x, out, stuck, wait_limit_cycles, offsets=None, stream=None):

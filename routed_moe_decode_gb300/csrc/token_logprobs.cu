@@ -6,8 +6,10 @@
 //
 // Alternatives are keys: the logit's order-preserving bits above the complement of its id, so that equal logits are in
 // the order of their ids and no two keys are equal.  A warp keeps its best 32 sorted over its lanes.  What cannot be
-// among the best is told from the maximum of a thread's values, which the sums need anyway, against a threshold: the
-// warp's own last place, or the smallest of all warps' ceil(top / 8)-th places (together they have `top` better ones).
+// among the best is told from the maximum of a thread's values, which the sums need anyway, against a threshold: each
+// warp shows its four best logits, and the top-th of those 32 is not above the row's.  The first step's
+// maxima of the lanes fill the 32 places at once, so that few values are ever looked at one by one (with every value of a
+// hit step looked at, and the smallest of the warps' own places as the threshold, 60 % of the instructions went there).
 //
 // A row is one CTA's, or a cluster's of up to eight where there are few rows; the parts join through distributed shared
 // memory in a fixed order.
@@ -20,6 +22,7 @@ namespace dense {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kVecs = 4;  // 16-byte vectors of a thread's step
+constexpr int kShown = 32 / kWarps;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 typedef unsigned long long Key;
@@ -66,96 +69,149 @@ __device__ __forceinline__ Key merge(Key a, Key b, int lane) {
   return k;
 }
 
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+
+// A 16-byte vector: its values in pairs, and the largest value of a step's.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void get(uint4 r, float* v) {
-    v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
-  }
-  static __device__ __forceinline__ float one(const float* p) { return __ldcg(p); }
   static constexpr uint32_t kLowest = 0xff800000u;
+  static __device__ __forceinline__ void get(uint4 r, float2* v) {
+    v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+  }
+  static __device__ __forceinline__ float most(const uint4 (&)[kVecs], const float2 (&v)[kVecs * N / 2]) {
+    float m = fmaxf(v[0].x, v[0].y);
+#pragma unroll
+    for (int i = 1; i < kVecs * N / 2; ++i) m = fmaxf(m, fmaxf(v[i].x, v[i].y));
+    return m;
+  }
 };
+template <typename P>
+__device__ __forceinline__ P most_pair(const uint4 (&r)[kVecs]) {
+  P m = *reinterpret_cast<const P*>(&r[0].x);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    if (j) m = __hmax2(m, *reinterpret_cast<const P*>(&r[j].x));
+    m = __hmax2(m, *reinterpret_cast<const P*>(&r[j].y));
+    m = __hmax2(m, *reinterpret_cast<const P*>(&r[j].z));
+    m = __hmax2(m, *reinterpret_cast<const P*>(&r[j].w));
+  }
+  return m;
+}
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void get(uint4 r, float* v) {
+  static constexpr uint32_t kLowest = 0xff80ff80u;
+  static __device__ __forceinline__ void get(uint4 r, float2* v) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  static constexpr uint32_t kLowest = 0xff80ff80u;
+  static __device__ __forceinline__ float most(const uint4 (&r)[kVecs], const float2 (&)[kVecs * N / 2]) {
+    const float2 m = __bfloat1622float2(most_pair<__nv_bfloat162>(r));
+    return fmaxf(m.x, m.y);
+  }
 };
 template <>
 struct Vec<__half> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void get(uint4 r, float* v) {
+  static constexpr uint32_t kLowest = 0xfc00fc00u;
+  static __device__ __forceinline__ void get(uint4 r, float2* v) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = p.x;
-      v[2 * i + 1] = p.y;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
   }
-  static __device__ __forceinline__ float one(const __half* p) { return __half2float(*p); }
-  static constexpr uint32_t kLowest = 0xfc00fc00u;
+  static __device__ __forceinline__ float most(const uint4 (&r)[kVecs], const float2 (&)[kVecs * N / 2]) {
+    const float2 m = __half22float2(most_pair<__half2>(r));
+    return fmaxf(m.x, m.y);
+  }
 };
 
 struct Shared {
+  uint4 values[kWarps][kVecs][32];  // of a step whose values are looked at one by one
   Key lists[kWarps][32];
   Sums sums[kWarps];
-  float level[kWarps];  // a warp's ceil(top / 8)-th best logit, -infinity before it has as many
-  // a cluster's parts, at its first CTA
-  Key part_lists[8][32];
-  Sums part_sums[8];
+  uint32_t shown[kWarps * kShown];  // each warp's best logits, or some below them, as float_key has them
+  uint32_t version;                 // of `shown`
+  // a cluster's parts read these
+  Key part_list[32];
+  Sums part_sums;
 };
 
-// A warp's best keys.
-struct Best {
-  Key list;     // lane i: the i-th best, 0 where there is none
-  float floor;  // the warp's `top`-th best logit
-};
-template <int N>
-__device__ __forceinline__ void offer(Best& b, const float (&v)[N], const int (&id0)[kVecs], const int (&valid)[kVecs],
-                                      int top, int place, float bar, volatile float* level, int lane) {
+__device__ __forceinline__ float value_of(uint32_t key) { return logit_of(static_cast<Key>(key) << 32); }
+
+// Lanes' keys into a warp's list (0: none).
+__device__ __forceinline__ Key insert(Key list, Key k, int top, int lane) {
+  k = k > __shfl_sync(kAll, list, top - 1) ? k : 0;
+  uint32_t want = __ballot_sync(kAll, k != 0);
+  if (__popc(want) > 6) {  // as costly as a sort: bitonic, descending over the lanes
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    constexpr int PER = N / kVecs;
-    const float l = v[i];
-    Key k = 0;
-    if (i % PER < valid[i / PER] && !(l < bar)) k = key_of(l, id0[i / PER] + i % PER);
-    const Key last = __shfl_sync(kAll, b.list, top - 1);
-    uint32_t want = __ballot_sync(kAll, k > last);
-    while (want) {
-      const int src = __ffs(want) - 1;
-      want &= want - 1;
-      const Key c = __shfl_sync(kAll, k, src);
-      const int at = __popc(__ballot_sync(kAll, b.list > c));
-      const Key up = __shfl_up_sync(kAll, b.list, 1);
-      if (lane == at) b.list = c;
-      else if (lane > at) b.list = up;
-    }
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+      for (int o = size >> 1; o > 0; o >>= 1) {
+        const Key p = shfl_xor(k, o);
+        const bool larger = ((lane & o) == 0) == ((lane & size) == 0);
+        k = larger == (k > p) ? k : p;
+      }
+    return merge(list, k, lane);
   }
-  const Key last = __shfl_sync(kAll, b.list, top - 1), at = __shfl_sync(kAll, b.list, place - 1);
-  b.floor = last ? logit_of(last) : -INFINITY;
-  if (lane == 0) *level = at ? logit_of(at) : -INFINITY;
+  while (want) {
+    const Key c = __shfl_sync(kAll, k, __ffs(want) - 1);
+    want &= want - 1;
+    const int at = __popc(__ballot_sync(kAll, list > c));
+    const Key up = __shfl_up_sync(kAll, list, 1);
+    list = lane < at ? list : lane == at ? c : up;
+  }
+  return list;
+}
+
+// The top-th largest of the lanes' keys.
+__device__ __forceinline__ uint32_t nth(uint32_t k, int top, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int o = size >> 1; o > 0; o >>= 1) {
+      const uint32_t p = __shfl_xor_sync(kAll, k, o);
+      k = ((lane & o) == 0) == ((lane & size) == 0) ? max(k, p) : min(k, p);
+    }
+  return __shfl_sync(kAll, k, top - 1);
+}
+
+// The warp's lists into the first warp's.
+template <bool TOP>
+__device__ __forceinline__ Key best_of_warps(Shared& sh, Key list, int warp, int lane) {
+  if constexpr (TOP) {
+    for (int n = kWarps / 2; n > 0; n >>= 1) {
+      if (warp >= n && warp < 2 * n) sh.lists[warp][lane] = list;
+      __syncthreads();
+      if (warp < n) list = merge(list, sh.lists[warp + n][lane], lane);
+    }
+  } else {
+    __syncthreads();
+  }
+  return list;
+}
+// With the sums of the lane `o` away, in the same order on both sides.
+__device__ __forceinline__ Sums joined(Sums a, int o, int lane) {
+  const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.s, o), __shfl_xor_sync(kAll, a.u, o)};
+  return (lane & o) ? join(b, a) : join(a, b);
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(const LogprobArgs a) {
   typedef Vec<T> V;
   constexpr int N = kVecs * V::N;
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = static_cast<int>(cluster_size()), part = static_cast<int>(cluster_rank());
-  if (TOP && lane == 0) sh.level[warp] = -INFINITY;
-  __syncthreads();
+  if (TOP && tid < kWarps * kShown) sh.shown[tid] = 0;
+  if (TOP && tid == 0) sh.version = 0;
+  if (TOP) __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   const int64_t row = blockIdx.x / parts;
@@ -168,13 +224,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
   const int v1 = static_cast<int>(static_cast<int64_t>(vecs) * (part + 1) / parts);
 
   Sums mine{-FLT_MAX, 0.f, 0.f};
-  Best best{0, -INFINITY};
-  const int place = (a.top + kWarps - 1) / kWarps;
+  Key list = 0;
+  uint32_t seen = ~0u;
+  float bar = -INFINITY;
+  const float2 scale = make_float2(a.scale, a.scale), log2e = make_float2(kLog2e, kLog2e);
 
-  auto take = [&](const float (&v)[N], const int (&id0)[kVecs], const int (&valid)[kVecs]) {
-    float most = v[0];
+  auto load = [&](uint4 (&raw)[kVecs], int at) {
 #pragma unroll
-    for (int i = 1; i < N; ++i) most = fmaxf(most, v[i]);
+    for (int j = 0; j < kVecs; ++j) {
+      const int i = at + j * kThreads + tid;
+      raw[j] = i < v1 ? __ldcs(xv + i) : make_uint4(V::kLowest, V::kLowest, V::kLowest, V::kLowest);
+    }
+  };
+  auto add = [&](const float2 (&v)[N / 2], float most) {
     const float m = fmaxf(mine.m, most * a.scale);
     if (m > mine.m) {
       const float d = fmaxf(mine.m - m, -1e30f), f = exp2_of(d * kLog2e);
@@ -182,89 +244,119 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
       mine.s *= f;
       mine.m = m;
     }
-    float2 s = make_float2(0.f, 0.f), u = s;
+    const float2 down = make_float2(-m, -m);
+    float2 s[2], u[2];
+    s[0] = s[1] = u[0] = u[1] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float d0 = fmaf(v[i], a.scale, -m), d1 = fmaf(v[i + 1], a.scale, -m);
-      const float e0 = exp2_of(d0 * kLog2e), e1 = exp2_of(d1 * kLog2e);
-      s.x += e0; s.y += e1;
-      u = fma2(make_float2(e0, e1), make_float2(fmaxf(d0, -FLT_MAX), fmaxf(d1, -FLT_MAX)), u);
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 d = fma2(v[i], scale, down), t = mul2(d, log2e);
+      const float2 e = make_float2(exp2_of(t.x), exp2_of(t.y));
+      s[i & 1] = add2(s[i & 1], e);
+      u[i & 1] = fma2(e, make_float2(fmaxf(d.x, -FLT_MAX), fmaxf(d.y, -FLT_MAX)), u[i & 1]);
     }
-    mine.s += s.x + s.y;
-    mine.u += u.x + u.y;
-    if constexpr (TOP) {
-      float bar = *const_cast<volatile float*>(&sh.level[0]);
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) bar = fminf(bar, *const_cast<volatile float*>(&sh.level[w]));
-      bar = fmaxf(bar, best.floor);
-      // a NaN ranks as -infinity, and so does a maximum of NaNs alone
-      if (__any_sync(kAll, !(most < bar))) offer<N>(best, v, id0, valid, a.top, place, bar, &sh.level[warp], lane);
-    }
+    mine.s += (s[0].x + s[0].y) + (s[1].x + s[1].y);
+    mine.u += (u[0].x + u[0].y) + (u[1].x + u[1].y);
   };
 
+  uint4 raw[kVecs];
+  if (v0 < v1) load(raw, v0);
   for (int at = v0; at < v1; at += kVecs * kThreads) {
-    uint4 raw[kVecs];
-    int id0[kVecs], valid[kVecs];
+    uint4 next[kVecs];
+    const bool more = at + kVecs * kThreads < v1;
+    if (more) load(next, at + kVecs * kThreads);
+    float2 v[N / 2];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int i = at + j * kThreads + tid;
-      raw[j] = i < v1 ? __ldcs(xv + i) : make_uint4(V::kLowest, V::kLowest, V::kLowest, V::kLowest);
-      id0[j] = head + i * V::N;
-      valid[j] = i < v1 ? V::N : 0;
+    for (int j = 0; j < kVecs; ++j) V::get(raw[j], v + j * (V::N / 2));
+    const float most = V::most(raw, v);
+    add(v, most);
+    if constexpr (TOP) {
+      if (at == v0) {  // the same for the whole CTA
+        uint32_t k = float_key(most == most ? most : -INFINITY);
+#pragma unroll
+        for (int p = 0; p < kShown; ++p) {
+          const uint32_t w = __reduce_max_sync(kAll, k);
+          if (lane == p) sh.shown[warp * kShown + p] = w;
+          if (lane == __ffs(__ballot_sync(kAll, k == w)) - 1) k = 0;
+        }
+        __syncthreads();
+      }
+      const uint32_t version = *const_cast<volatile uint32_t*>(&sh.version);
+      if (__any_sync(kAll, version != seen)) {
+        seen = __shfl_sync(kAll, version, 0);
+        bar = value_of(nth(*const_cast<volatile uint32_t*>(&sh.shown[lane]), a.top, lane));
+      }
+      // a NaN ranks as -infinity, and so does a maximum of NaNs alone
+      if (__any_sync(kAll, !(most < bar))) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          if (!(v[i].x < bar)) mask |= 1u << (2 * i);
+          if (!(v[i].y < bar)) mask |= 2u << (2 * i);
+        }
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+          sh.values[warp][j][lane] = raw[j];
+          if (at + j * kThreads + tid >= v1) mask &= ~(((1u << (V::N - 1)) * 2 - 1) << (j * V::N));
+        }
+        __syncwarp();
+        const Key old = list;
+        for (uint32_t left = __reduce_or_sync(kAll, mask); left; left &= left - 1) {
+          const int i = __ffs(left) - 1, j = i / V::N, e = i % V::N;
+          const float l = to_float(reinterpret_cast<const T*>(&sh.values[warp][j][lane])[e]);
+          list = insert(list, (mask >> i) & 1 ? key_of(l, head + (at + j * kThreads + tid) * V::N + e) : 0, a.top, lane);
+        }
+        if (__any_sync(kAll, list != old)) {
+          const uint32_t k = static_cast<uint32_t>(list >> 32);
+          volatile uint32_t* shown = &sh.shown[warp * kShown];
+          if (lane < kShown && k > shown[lane]) shown[lane] = k;
+          __syncwarp();
+          if (lane == 0) atomicAdd(&sh.version, 1u);
+        }
+        __syncwarp();
+      }
     }
-    float v[N];
+    if (more) {
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) V::get(raw[j], v + j * V::N);
-    take(v, id0, valid);
+      for (int j = 0; j < kVecs; ++j) raw[j] = next[j];
+    }
   }
   if (part == 0 && head + rest > 0 && warp == 0) {  // at most 14 elements
-    float v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = -INFINITY;
     const int id = lane < head ? lane : a.vocab - rest + lane - head;
     const bool there = lane < head + rest;
-    if (there) v[0] = V::one(x + id);
-    const int id0[kVecs] = {id, 0, 0, 0}, valid[kVecs] = {there ? 1 : 0, 0, 0, 0};
-    take(v, id0, valid);
+    float2 v[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) v[i] = make_float2(-INFINITY, -INFINITY);
+    if (there) v[0].x = to_float(x[id]);
+    add(v, v[0].x);
+    if constexpr (TOP) list = insert(list, there ? key_of(v[0].x, id) : 0, a.top, lane);
   }
 
   // the CTA's sums and lists
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(kAll, mine.m, o);
-    b.s = __shfl_xor_sync(kAll, mine.s, o);
-    b.u = __shfl_xor_sync(kAll, mine.u, o);
-    // the same order on both sides
-    mine = (lane & o) ? join(b, mine) : join(mine, b);
-  }
+  for (int o = 16; o > 0; o >>= 1) mine = joined(mine, o, lane);
   if (lane == 0) sh.sums[warp] = mine;
-  if constexpr (TOP) {
-    for (int n = kWarps / 2; n > 0; n >>= 1) {
-      sh.lists[warp][lane] = best.list;
-      __syncthreads();
-      if (warp < n) best.list = merge(best.list, sh.lists[warp + n][lane], lane);
-      __syncthreads();
-    }
-  } else {
-    __syncthreads();
-  }
+  list = best_of_warps<TOP>(sh, list, warp, lane);
   if (warp == 0) {
-    mine = sh.sums[0];
-    for (int w = 1; w < kWarps; ++w) mine = join(mine, sh.sums[w]);
+    mine = sh.sums[lane & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) mine = joined(mine, o, lane);
   }
   if (parts > 1) {
     if (warp == 0) {
-      if (TOP) sh.part_lists[0][lane] = best.list;
-      if (lane == 0) sh.part_sums[0] = mine;
+      if (TOP) sh.part_list[lane] = list;
+      if (lane == 0) sh.part_sums = mine;
     }
     __syncwarp();
     cluster_sync();
-    if (part == 0 && warp == 0) {
-      for (int p = 1; p < parts; ++p) {
-        const uint32_t at = mapa(smem_addr(&sh.part_sums[0]), p);
-        mine = join(mine, Sums{ld_cluster(at), ld_cluster(at + 4), ld_cluster(at + 8)});
-        if (TOP) best.list = merge(best.list, ld_cluster_u64(mapa(smem_addr(&sh.part_lists[0][lane]), p)), lane);
+    if (part == 0) {  // a warp has a part's list, a lane a part's sums
+      if (TOP) {
+        list = warp < parts ? ld_cluster_u64(mapa(smem_addr(&sh.part_list[lane]), warp)) : 0;
+        list = best_of_warps<TOP>(sh, list, warp, lane);
+      }
+      if (warp == 0) {
+        const uint32_t at = mapa(smem_addr(&sh.part_sums), lane & (parts - 1));
+        mine = Sums{ld_cluster(at), ld_cluster(at + 4), ld_cluster(at + 8)};
+        for (int o = parts / 2; o > 0; o >>= 1) mine = joined(mine, o, lane);
       }
     }
     __syncwarp();
@@ -281,13 +373,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
   if (a.logprobs) {
     for (int j = lane; j < a.n_tokens; j += 32) {
       const int t = a.tokens[row * a.token_stride + j];
-      a.logprobs[row * a.n_tokens + j] = logprob(t >= 0 && t < a.vocab ? V::one(x + t) : -INFINITY);
+      a.logprobs[row * a.n_tokens + j] = logprob(t >= 0 && t < a.vocab ? to_float(x[t]) : -INFINITY);
     }
   }
   if (TOP && lane < a.top) {
-    const int id = static_cast<int>(~static_cast<uint32_t>(best.list));
+    const int id = static_cast<int>(~static_cast<uint32_t>(list));
     if (a.top_ids) a.top_ids[row * a.top + lane] = id;
-    if (a.top_logprobs) a.top_logprobs[row * a.top + lane] = logprob(logit_of(best.list));
+    if (a.top_logprobs) a.top_logprobs[row * a.top + lane] = logprob(logit_of(list));
   }
 }
 
