@@ -37,7 +37,7 @@ struct NormArgs {
   FastDiv inner;
   uint32_t rows;
   int d, dtype, weight_dtype;
-  float eps, add;  // add: 1 where the norm multiplies by 1 + weight
+  float eps, inv_d, add;  // inv_d: 1 / d; add: 1 where the norm multiplies by 1 + weight
   bool vec;        // every row can be read and written 16 bytes (weights: 8 elements) at a time
   bool vec_codes;  // codes can be written 8 bytes at a time
 };

@@ -128,7 +128,7 @@ int moe_rms_norm(int outer, int inner, int d, int dtype, const void* x, int64_t 
   a.r_stride = residual_stride; a.ro_stride = residual_out_stride; a.code_stride = code_stride;
   a.scale_row = scale_row; a.scale_block = scale_block;
   a.inner = moe::dense::fast_div(static_cast<uint32_t>(inner));
-  a.rows = static_cast<uint32_t>(rows); a.d = d; a.dtype = dtype; a.weight_dtype = weight_dtype; a.eps = eps;
+  a.rows = static_cast<uint32_t>(rows); a.d = d; a.dtype = dtype; a.weight_dtype = weight_dtype; a.eps = eps; a.inv_d = 1.f / static_cast<float>(d);
   a.add = one_plus ? 1.f : 0.f;
   a.vec = d % 8 == 0 && rows_vec(x, x_outer, x_inner, size) && rows_vec(residual, residual_stride, 0, size) &&
           rows_vec(residual_out, residual_out_stride, 0, size) && rows_vec(normed, normed_outer, normed_inner, size) &&

@@ -6,6 +6,7 @@
 // Both kernels read every input and write every output once; memory bounds them from some hundred rows on, and below that
 // the launch and one trip to memory.  A thread has 8 consecutive values (16 bytes of a 16-bit type), so 16 neighbouring
 // lanes have a block, whose maximum takes four shuffles.
+#include <algorithm>
 #include "dense.cuh"
 
 namespace moe {
@@ -63,6 +64,43 @@ __device__ __forceinline__ void load8(const T* row, int c, int d, float (&v)[8])
     for (int i = 0; i < 8; ++i) v[i] = c + i < d ? to_float<T>(row[c + i]) : 0.f;
   }
 }
+// The same, converted when they are needed.
+template <typename T, bool VEC>
+struct Raw8 {
+  uint4 r[VEC ? sizeof(T) / 2 : 1];
+  float f[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const T* row, int c, int d) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+        r[i] = c < d ? __ldcs(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c + i < d ? to_float<T>(row[c + i]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 4) {
+            v[4 * i + j] = __uint_as_float(w[j]);
+          } else {
+            const float2 p = pair(w[j], T());
+            v[2 * j] = p.x;
+            v[2 * j + 1] = p.y;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = f[i];
+    }
+  }
+};
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* row, int c, int d, const float (&v)[8]) {
   if constexpr (VEC && sizeof(T) == 4) {
@@ -78,10 +116,15 @@ __device__ __forceinline__ void store8(T* row, int c, int d, const float (&v)[8]
   }
 }
 
-// (lo, hi) as two E4M3 codes, to nearest even, at most 448.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+// Four values as E4M3 codes, to nearest even, at most 448.
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
@@ -89,11 +132,11 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(two & 0xffffu)));
 }
 
-// The quotients' errors are below 2^-23 (a rounded reciprocal and a rounded product), so codes of quotients 2^-22
+// The quotients' errors are below 2^-22 (an approximate reciprocal and two rounded products), so codes of quotients 2^-21
 // smaller and larger are the same unless a border between two codes lies next to the quotient.  There the exact
 // quotient decides: |v| against border * scale, by the sign of one fused multiply-add; on the border the even code.
-// (Rows of 16-bit types meet borders often: v / s is then a fraction of small numbers.  Dividing each value by the
-// scale instead cost a gated chunk of 8192 rows of 4096 as much as its memory.)
+// (Rows of 16-bit types meet borders often: v / s is then a fraction of small numbers.  A rounded division costs 87 cycles
+// of a quarter of the SM's warp slots, as much as all else of eight values.)
 __device__ __noinline__ uint32_t settle(uint32_t less, uint32_t more, float v0, float v1, float v2, float v3, float s) {
   const float v[4] = {v0, v1, v2, v3};
   uint32_t codes = 0;
@@ -111,38 +154,48 @@ __device__ __noinline__ uint32_t settle(uint32_t less, uint32_t more, float v0, 
   return codes;
 }
 
+// The largest magnitude of three; a NaN stays one.
+__device__ __forceinline__ float most_of(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Codes of a thread's 8 values; 16 neighbouring lanes have a block.  All lanes of the warp take part.
 __device__ __forceinline__ uint2 quantize8(float (&v)[8], float* scale) {
-  uint32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
-    most = m > most ? m : most;
-  }
+  float most = most_of(most_of(v[0], v[1], v[2]), most_of(v[3], v[4], v[5]), most_of(v[6], v[7], v[7]));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
-    const uint32_t m = __shfl_xor_sync(kAll, most, o);
-    most = m > most ? m : most;
+    const float m = __shfl_xor_sync(kAll, most, o);
+    most = most_of(most, m, m);
   }
-  if (most >= 0x7f800000u) {  // an infinity or a NaN
-    *scale = __uint_as_float(0x7fc00000u);
-    return make_uint2(0, 0);
-  }
-  float s = __fdiv_rn(__uint_as_float(most), 448.f);
-  *scale = s;
-  if (s < 0x1p-90f) {  // the same quotients, with a reciprocal and border products inside FP32's range
+  // most / 448, rounded: a product and one correction by its residual (Markstein), exact steps above 2^-80
+  float s = most * (1.f / 448.f);
+  s = fmaf(fmaf(-s, 448.f, most), 1.f / 448.f, s);
+  if (!(most >= 0x1p-80f && most < INFINITY)) {
+    if (!(most < INFINITY)) {  // an infinity or a NaN
+      *scale = __uint_as_float(0x7fc00000u);
+      return make_uint2(0, 0);
+    }
+    s = __fdiv_rn(most, 448.f);
+    *scale = s;
+    if (s == 0.f) return make_uint2(0, 0);
+    // the same quotients, with a reciprocal and border products inside FP32's range
     s *= 0x1p64f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= 0x1p64f;
+  } else {
+    *scale = s;
   }
-  if (s == 0.f) return make_uint2(0, 0);
-  const float inv = __fdiv_rn(1.f, s);
-  const float down = inv * (1.f - 0x1p-22f), up = inv * (1.f + 0x1p-22f);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
   uint32_t less[2], more[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    less[h] = e4m3x2(v[4 * h] * down, v[4 * h + 1] * down) | (e4m3x2(v[4 * h + 2] * down, v[4 * h + 3] * down) << 16);
-    more[h] = e4m3x2(v[4 * h] * up, v[4 * h + 1] * up) | (e4m3x2(v[4 * h + 2] * up, v[4 * h + 3] * up) << 16);
+    const float2 a = make_float2(v[4 * h], v[4 * h + 1]), b = make_float2(v[4 * h + 2], v[4 * h + 3]);
+    less[h] = e4m3x4(mul2(a, make_float2(down, down)), mul2(b, make_float2(down, down)));
+    more[h] = e4m3x4(mul2(a, make_float2(up, up)), mul2(b, make_float2(up, up)));
     if (less[h] != more[h]) less[h] = settle(less[h], more[h], v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3], s);
   }
   return make_uint2(less[0], less[1]);
@@ -167,7 +220,7 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    v = lane < TPR / 32 ? red[lane] : 0.f;
+    v = lane < TPR / 32 ? red[(warp & ~(TPR / 32 - 1)) + lane] : 0.f;
 #pragma unroll
     for (int o = TPR / 64; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     v = __shfl_sync(kAll, v, 0);
@@ -237,31 +290,40 @@ __device__ __forceinline__ void finish(const NormArgs& a, const RowPtrs<T>& p, i
   }
 }
 
+// 1 / sqrt(mean + eps): the approximate root's reciprocal (2 units) and a step of Newton's iteration.
 __device__ __forceinline__ float norm_factor(float squares, const NormArgs& a) {
-  return __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(squares, static_cast<float>(a.d)) + a.eps));
+  const float m = fmaf(squares, a.inv_d, a.eps), f = rsqrtf(m);
+  return fmaf(0.5f * f, fmaf(-m * f, f, 1.f), f);
 }
 
 // A row's channels in the registers of TPR threads, VPT times 8 each.
 template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(256) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(256, VPT == 1 ? 8 : VPT == 2 ? 4 : 3) norm_kernel(const NormArgs a) {
   __shared__ float red[8];
   pdl_wait();
   const uint32_t row0 = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
   const bool live = row0 < a.rows;
   const RowPtrs<T> p = row_of<T>(a, live ? row0 : a.rows - 1);
   const int t = threadIdx.x % TPR;
+  Raw8<T, true> x[VPT], r[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = 8 * (t + j * TPR);
+    x[j].load(p.x, c, a.d);
+    if (p.r) r[j].load(p.r, c, a.d);
+  }
+  pdl_launch_dependents();
   float h[VPT][8];
   float squares = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int c = 8 * (t + j * TPR);
+    x[j].get(h[j]);
+    if (p.r) {
+      float v[8];
+      r[j].get(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[j][i] = 0.f;
-    if (live && c < a.d) load_h<T, true>(a, p, c, h[j]);
-  }
-  pdl_launch_dependents();
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
+      for (int i = 0; i < 8; ++i) h[j][i] = to_float<T>(from_float<T>(h[j][i] + v[i]));
+    }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(h[j][i], h[j][i], s);
@@ -325,7 +387,7 @@ cudaError_t run_norm_long(const NormArgs& a, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t norm_of(const NormArgs& a, int sms, cudaStream_t stream) {
+cudaError_t norm_of(const NormArgs& a, cudaStream_t stream) {
   if (!a.vec) return a.d <= 1024 ? run_norm_long<T, 32, false>(a, stream) : run_norm_long<T, 256, false>(a, stream);
   if (a.d <= 128) return run_norm<T, 16, 1>(a, stream);
   if (a.d <= 256) return run_norm<T, 32, 1>(a, stream);
@@ -337,39 +399,83 @@ cudaError_t norm_of(const NormArgs& a, int sms, cudaStream_t stream) {
   return run_norm_long<T, 256, true>(a, stream);
 }
 
-// g / (1 + exp(-g)) * u
-__device__ __forceinline__ float gated_value(float g, float u) { return __fdiv_rn(g, 1.f + expf(-g)) * u; }
+// g / (1 + exp(-g)) * u, with exp(-|g|) (0 below 2^-126) so that nothing overflows: g or g exp(-|g|) over 1 + exp(-|g|).  The
+// exponential's argument is a product and its rounding error (Dekker's exact product, by a fused multiply-add), the quotient
+// a product corrected once by its residual (Markstein): errors of a unit or two, as with expf and a rounded division,
+// which took a gated chunk 47 us instead of the 33 of this.
+__device__ __forceinline__ float2 gated_pair(float2 g, float2 u) {
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925962991e-08f, kLn2 = 0.693147180559945f;  // log2(e) = kHi + kLo
+  const float2 hi = make_float2(kHi, kHi), minus = make_float2(-1.f, -1.f), one = make_float2(1.f, 1.f);
+  const float2 a = make_float2(fmaxf(-fabsf(g.x), -200.f), fmaxf(-fabsf(g.y), -200.f));  // below: 0 all the same
+  const float2 t = mul2(a, hi);
+  const float2 low = fma2(a, make_float2(kLo, kLo), fma2(a, hi, mul2(t, minus)));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = fma2(e, mul2(low, make_float2(kLn2, kLn2)), e);
+  const float2 den = add2(one, e), less = mul2(g, e);
+  const float2 num = make_float2(g.x < 0.f ? less.x : g.x, g.y < 0.f ? less.y : g.y);
+  float both;  // one reciprocal for two: both denominators are within [1, 2]
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(both) : "f"(den.x * den.y));
+  const float2 r = mul2(make_float2(both, both), make_float2(den.y, den.x));
+  const float2 q = mul2(num, r);
+  return mul2(fma2(fma2(mul2(q, minus), den, num), r, q), u);
+}
+
+// A group of 16 lanes takes a block, then the block as many further as there are groups; the next one's loads are under
+// way meanwhile.
+constexpr int kQuantCtas = 6;  // of an SM
 
 template <typename T, bool GATED, bool VEC>
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(256, kQuantCtas) quantize_kernel(const QuantArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t block = blockIdx.x * 16 + threadIdx.x / 16;
-  const bool live = block < a.blocks;
-  const uint32_t row = div(a.nblocks, live ? block : a.blocks - 1);
-  const uint32_t b = (live ? block : a.blocks - 1) - row * a.nblocks.d;
-  const int c = static_cast<int>(b) * kBlock + 8 * (threadIdx.x & 15);
-  const bool in = live && c < a.d;
-  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (in) {
-    load8<T, VEC>(x, c, a.d, v);
+  const int lane = threadIdx.x & 15;
+  Raw8<T, VEC> next, next_up;
+  uint32_t row = 0, b = 0;
+  auto load = [&](uint32_t block) {
+    block = min(block, a.blocks - 1);
+    row = div(a.nblocks, block);
+    b = block - row * a.nblocks.d;
+    const int c = static_cast<int>(b) * kBlock + 8 * lane;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    next.load(x, c, a.d);
+    if constexpr (GATED) next_up.load(x + a.d, c, a.d);
+  };
+  const uint32_t step = gridDim.x * 16;
+  // a warp's two groups stay together: they share the shuffles
+  const uint32_t begin = blockIdx.x * 16 + threadIdx.x / 16, warp_begin = begin & ~1u;
+  load(begin);
+  for (uint32_t at = 0; warp_begin + at < a.blocks; at += step) {
+    const uint32_t block = begin + at, r = row, k = b;
+    const int c = static_cast<int>(k) * kBlock + 8 * lane;
+    float v[8];
+    next.get(v);
     if constexpr (GATED) {
       float u[8];
-      load8<T, VEC>(x + a.d, c, a.d, u);
+      next_up.get(u);
+      if (warp_begin + at + step < a.blocks) load(block + step);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = gated_value(v[i], u[i]);
+      for (int i = 0; i < 8; i += 2) {
+        const float2 p = gated_pair(make_float2(v[i], v[i + 1]), make_float2(u[i], u[i + 1]));
+        v[i] = p.x;
+        v[i + 1] = p.y;
+      }
+    } else {
+      if (warp_begin + at + step < a.blocks) load(block + step);
     }
+    float scale;
+    const uint2 codes = quantize8(v, &scale);
+    if (block >= a.blocks) continue;
+    if (c < a.d) store_codes(a.codes + r * a.code_stride, c, a.d, codes, a.vec_codes);
+    if (lane == 0) a.scales[r * a.scale_row + k * a.scale_block] = scale;
   }
-  float scale;
-  const uint2 codes = quantize8(v, &scale);
-  if (in) store_codes(a.codes + row * a.code_stride, c, a.d, codes, a.vec_codes);
-  if (live && (threadIdx.x & 15) == 0) a.scales[row * a.scale_row + b * a.scale_block] = scale;
 }
 
 template <typename T>
-cudaError_t quantize_of(const QuantArgs& a, cudaStream_t stream) {
-  const dim3 grid((a.blocks + 15) / 16), block(256);
+cudaError_t quantize_of(const QuantArgs& a, int sms, cudaStream_t stream) {
+  const uint32_t most = static_cast<uint32_t>(sms) * kQuantCtas;
+  const dim3 grid(std::min((a.blocks + 15) / 16, most)), block(256);
   if (a.gated)
     return a.vec ? launch_ready<quantize_kernel<T, true, true>>(grid, block, 0, stream, a)
                  : launch_ready<quantize_kernel<T, true, false>>(grid, block, 0, stream, a);
@@ -380,15 +486,15 @@ cudaError_t quantize_of(const QuantArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t stream) {
-  if (a.dtype == MOE_DENSE_FP32) return norm_of<float>(a, sms, stream);
-  if (a.dtype == MOE_DENSE_BF16) return norm_of<__nv_bfloat16>(a, sms, stream);
-  return norm_of<__half>(a, sms, stream);
+  if (a.dtype == MOE_DENSE_FP32) return norm_of<float>(a, stream);
+  if (a.dtype == MOE_DENSE_BF16) return norm_of<__nv_bfloat16>(a, stream);
+  return norm_of<__half>(a, stream);
 }
 
 cudaError_t launch_quantize(const QuantArgs& a, int sms, cudaStream_t stream) {
-  if (a.dtype == MOE_DENSE_FP32) return quantize_of<float>(a, stream);
-  if (a.dtype == MOE_DENSE_BF16) return quantize_of<__nv_bfloat16>(a, stream);
-  return quantize_of<__half>(a, stream);
+  if (a.dtype == MOE_DENSE_FP32) return quantize_of<float>(a, sms, stream);
+  if (a.dtype == MOE_DENSE_BF16) return quantize_of<__nv_bfloat16>(a, sms, stream);
+  return quantize_of<__half>(a, sms, stream);
 }
 
 }  // namespace dense
