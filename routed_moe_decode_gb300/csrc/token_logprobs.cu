@@ -202,8 +202,12 @@ __device__ __forceinline__ Sums joined(Sums a, int o, int lane) {
   return (lane & o) ? join(b, a) : join(a, b);
 }
 
+// CTAs of an SM: with alternatives, 16-bit types (32 values a step) would spill at four.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(const LogprobArgs a) {
+constexpr int ctas() { return TOP && sizeof(T) == 2 ? 3 : 4; }
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads, ctas<T, TOP>()) logprobs_kernel(const LogprobArgs a) {
   typedef Vec<T> V;
   constexpr int N = kVecs * V::N;
   __shared__ Shared sh;
@@ -280,13 +284,17 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(const L
         }
         __syncthreads();
       }
-      const uint32_t version = *const_cast<volatile uint32_t*>(&sh.version);
-      if (__any_sync(kAll, version != seen)) {
-        seen = __shfl_sync(kAll, version, 0);
-        bar = value_of(nth(*const_cast<volatile uint32_t*>(&sh.shown[lane]), a.top, lane));
-      }
       // a NaN ranks as -infinity, and so does a maximum of NaNs alone
-      if (__any_sync(kAll, !(most < bar))) {
+      bool some = __any_sync(kAll, !(most < bar));
+      if (some) {  // against the threshold as it is now
+        const uint32_t version = *const_cast<volatile uint32_t*>(&sh.version);
+        if (__any_sync(kAll, version != seen)) {
+          seen = __shfl_sync(kAll, version, 0);
+          bar = value_of(nth(*const_cast<volatile uint32_t*>(&sh.shown[lane]), a.top, lane));
+          some = __any_sync(kAll, !(most < bar));
+        }
+      }
+      if (some) {
         uint32_t mask = 0;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
@@ -387,7 +395,8 @@ template <typename T>
 cudaError_t run(const LogprobArgs& a, int sms, cudaStream_t stream) {
   // parts of a row: while all CTAs are resident together, and a part is worth a CTA
   int parts = 1;
-  while (parts < 8 && static_cast<int64_t>(a.rows) * parts * 2 <= 4 * sms && a.vocab / (parts * 2) >= 2048) parts *= 2;
+  const int64_t most = static_cast<int64_t>(a.top > 0 ? ctas<T, true>() : ctas<T, false>()) * sms;
+  while (parts < 8 && static_cast<int64_t>(a.rows) * parts * 2 <= most && a.vocab / (parts * 2) >= 2048) parts *= 2;
   const dim3 grid(static_cast<unsigned>(a.rows) * parts), block(kThreads);
   return a.top > 0 ? launch_cluster<logprobs_kernel<T, true>>(parts, grid, block, 0, stream, a)
                    : launch_cluster<logprobs_kernel<T, false>>(parts, grid, block, 0, stream, a);
