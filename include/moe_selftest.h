@@ -116,9 +116,9 @@ MOE_API int moe_selftest_kv4_attend(const moe_kv4_cache* cache, int layer, const
                                     int max_rows, float scale, void* out, int stuck, long long wait_limit_cycles,
                                     moe_stream_t stream);
 
-/* moe_fp8_matmul with every wait of its kernels limited to wait_limit_cycles SM cycles.  With stuck 1 the waits for
- * copies expect an arrival that nothing makes, so that they run out; with 0 a wait gives up where what it waits
- * for is not there within the limit (0: at once).  A wait that gives up sets MOE_DENSE_TIMEOUT; what is in flight
+/* moe_fp8_matmul with every wait of its kernels limited to wait_limit_cycles SM cycles (after the time that the
+ * hardware's own try takes).  With stuck 1 the waits for copies expect an arrival that nothing makes, so that they
+ * run out; with 0 a wait gives up where what it waits for is not there within the limit.  A wait that gives up sets MOE_DENSE_TIMEOUT; what is in flight
  * lands, tensor memory is released, the launch completes and the output is undefined. */
 MOE_API int moe_selftest_fp8_matmul(int rows, int n, int k, int groups, const uint8_t* codes, int64_t code_stride,
                                     const float* scales, int64_t scale_row, int64_t scale_block,

@@ -205,7 +205,8 @@ int moe_selftest_fp8_matmul(int rows, int n, int k, int groups, const uint8_t* c
                             const float* w_scales, const int32_t* offsets, void* out, int64_t out_stride, int out_dtype,
                             uint32_t* status, int stuck, long long wait_limit_cycles, moe_stream_t stream) {
   if (stuck < 0 || stuck > 1 || wait_limit_cycles < 0) return MOE_ERR_INVALID_ARG;
-  const uint32_t limit = static_cast<uint32_t>(wait_limit_cycles < 0xffffffffll ? wait_limit_cycles : 0xffffffffll);
+  // 0 would say that a wait has given up already
+  const uint32_t limit = static_cast<uint32_t>(wait_limit_cycles < 1 ? 1 : wait_limit_cycles < 0xffffffffll ? wait_limit_cycles : 0xffffffffll);
   return matmul(rows, n, k, groups, codes, code_stride, scales, scale_row, scale_block, w_codes, w_scales, offsets, out,
                 out_stride, out_dtype, status, limit, 1 + stuck, stream);
 }

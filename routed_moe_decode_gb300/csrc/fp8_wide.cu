@@ -25,7 +25,7 @@ constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScal
 constexpr int kTileRows = 256, kTileCh = 256, kCols = 1024 / kSumWarps;  // kCols: sums of a thread
 constexpr uint32_t kDrainCycles = 1u << 24, kLandCycles = 1u << 20;
 constexpr int kStages = 4, kStage = 2 * 128 * 128, kBufs = 2;
-constexpr int kBatch = 4, kSlot = 132;  // blocks whose scales come together; floats of one: 128 rows', the weight's two
+constexpr int kBatch = 4, kSlot = 132;  // blocks whose scales come together; floats of one: 128 rows', the weight's two, two of the tile's
 constexpr int kBox = 32 * 128;  // bytes of a box of outputs: 32 rows of 128 bytes, in swizzled lines
 
 struct Layout {
@@ -199,8 +199,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (elect_one()) commit_pair(end);
         __syncwarp();
       }
-      // products in flight end before their memory is given back
-      warp_wait(end, 0, &s_drain, a.status);
     } else {
       // rows r and r + 64 of this CTA's 128, and a half's weight scales
       const int second = warp - kScaleWarp, r = second * 32 + lane;
@@ -232,6 +230,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             to[j * kSlot + r + 64] = x1[j];
           }
           if (lane < kBatch) to[lane * kSlot + 128 + second] = w;
+          if (kb0 == 0 && second == 0 && lane == 0) {  // the tile, for the warps that add up
+            to[130] = __int_as_float(t.row0);
+            to[131] = __int_as_float(t.c0);
+            to[kSlot + 130] = __int_as_float(t.rows);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(scaled + 8 * (bt & 1));
         }
@@ -247,8 +250,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t it = 0, bt = 0;
     bool ok = true;
     for (int id = blockIdx.x / 2; ok && id < tiles; id += stride) {
-      const Tile t = tile_of<kTileRows, kTileCh, false>(a, id, ctiles, kblocks, gs);
-      const int ch = t.c0 + half * kCols, live = min(32, t.rows - slice);
+      ok = warp_wait(scaled + 8 * (bt & 1), (bt >> 1) & 1, limit, a.status);
+      const float* tile = scales + (bt & 1) * (kBatch * kSlot);
+      const int row0 = __float_as_int(tile[130]) + slice, ch = __float_as_int(tile[131]) + half * kCols;
+      const int live = min(32, __float_as_int(tile[kSlot + 130]) - slice);
       const bool work = live > 0 && ch < a.n;
       const uint32_t mine = tmem + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
       float2 acc[kCols / 2];
@@ -257,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const uint32_t b = it % kBufs, from = mine + b * 256;
         const bool turn = kb % kBatch == kBatch - 1 || kb == kblocks - 1;  // of the scales' buffer
-        if (kb % kBatch == 0) ok = warp_wait(scaled + 8 * (bt & 1), (bt >> 1) & 1, limit, a.status);
+        if (kb % kBatch == 0 && kb) ok = warp_wait(scaled + 8 * (bt & 1), (bt >> 1) & 1, limit, a.status);
         const float* slot = scales + ((bt & 1) * kBatch + kb % kBatch) * kSlot;
         const float s = slot[quarter * 32 + lane] * slot[128 + half];
         ok = ok && warp_wait(done + 8 * b, (it / kBufs) & 1, limit, a.status);
@@ -288,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (!work) continue;
       constexpr int PER = 128 / sizeof(T), EL = 16 / sizeof(T);  // channels of a box, of 16 bytes
-      T* out = static_cast<T*>(a.out) + static_cast<int64_t>(t.row0 + slice) * a.out_stride + ch;
+      T* out = static_cast<T*>(a.out) + static_cast<int64_t>(row0) * a.out_stride + ch;
 #pragma unroll
       for (int c = 0; c < kCols; c += PER) {
         const int left = a.n - ch - c;
@@ -306,16 +311,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) {
             asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&maps.out),
-                         "r"(ch + c), "r"(t.row0 + slice), "r"(smem_addr(box))
+                         "r"(ch + c), "r"(row0), "r"(smem_addr(box))
                          : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {  // rows behind these are not to be written, or addresses that bulk copies do not take
           __syncwarp();
-          for (int i = lane; i < PER && i < left; i += 32)
-            for (int r = 0; r < live; ++r)
-              out[r * a.out_stride + c + i] =
-                  *reinterpret_cast<const T*>(box + r * 128 + (((i / EL) ^ (r & 7)) << 4) + (i % EL) * sizeof(T));
+          if (maps.store && left >= PER) {
+            for (int r = lane >> 3; r < live; r += 4)
+              *reinterpret_cast<uint4*>(out + r * a.out_stride + c + (lane & 7) * EL) =
+                  *reinterpret_cast<const uint4*>(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          } else {
+            for (int i = lane; i < PER && i < left; i += 32)
+              for (int r = 0; r < live; ++r)
+                out[r * a.out_stride + c + i] =
+                    *reinterpret_cast<const T*>(box + r * 128 + (((i / EL) ^ (r & 7)) << 4) + (i % EL) * sizeof(T));
+          }
           __syncwarp();
         }
       }
@@ -323,6 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_wait_ld();
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
+  __syncthreads();
+  if (warp == kMmaWarp) warp_wait(end, 0, &s_drain, a.status);  // products in flight end before their memory is given back
   __syncwarp();
   tc_fence_before();
   cluster_sync();
