@@ -71,7 +71,11 @@ struct MatmulArgs {
   uint32_t wait_cycles;
   int copy_arrivals;  // arrivals that a stage's barrier waits for beside its bytes
 };
-cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, int split, cudaStream_t stream);
+// Parts of k for that kernel, 1 where the rows' tiles keep the SMs busy as they are.
+int fp8_stream_split(const MatmulArgs& a, int sms);
+// Rows of x in a tile of that kernel, at most, for so many rows (of a group, on average).
+constexpr int kFewRows = 32, kSomeRows = 128;
 cudaError_t launch_fp8_wide(const MatmulArgs& a, int sms, cudaStream_t stream);
 // Map of a matrix of size-byte elements, copied in boxes of 128 bytes x box_rows rows with the 128-byte swizzle; stride in bytes.
 int encode_rows_map(CUtensorMap* map, const void* base, int size, uint64_t cols, uint64_t rows, uint64_t stride,
@@ -188,6 +192,14 @@ __device__ __forceinline__ uint32_t mapa(uint32_t local, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
   return r;
 }
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -197,6 +209,36 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
   unsigned long long v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// Clusters of `cluster` CTAs of a kernel that are resident together on the current device (0: it cannot be said).
+template <auto Kernel>
+int resident_clusters(int cluster, dim3 block, size_t smem) {
+  constexpr int kMost = 8;
+  static std::atomic<int> known[64][kMost + 1];  // 1 + the number
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64 || cluster > kMost) return 0;
+  int n = known[dev][cluster].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int most = 0;
+    if (cudaOccupancyMaxActiveClusters(&most, Kernel, &cfg) != cudaSuccess) most = 0;
+    known[dev][cluster].store(n = 1 + most, std::memory_order_relaxed);
+  }
+  return n - 1;
 }
 
 // launch_ready for clusters of `cluster` CTAs along x.

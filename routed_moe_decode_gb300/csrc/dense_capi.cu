@@ -65,6 +65,25 @@ bool rows_vec(const void* p, int64_t s0, int64_t s1, int size) {
   return !p || (aligned(p, 16) && s0 % per == 0 && s1 % per == 0);
 }
 
+// Whether CTA pairs (256 rows x 256 channels a tile) take the product, rather than the kernel with up to 128 rows x 128
+// channels a tile and k in parts.  Estimates of both in us, fitted to measured products (us, pairs / the others): a block of 128 k
+// takes a pair 0.41 and a CTA 0.28 + n / 800 for n rows of x.
+//   rows 256: 5120 x 2048 11.0 / 11.6, 2048 x 8192 29.5 / 14.9, 8192 x 8192 30.1 / 29.2, 16384 x 4096 18.5 / 31.9
+//   rows 512: 5120 x 2048 11.6 / 19.9, 2048 x 8192 29.7 / 22.8, 8192 x 8192 31.0 / 54.9
+// Groups: by their rows on average, as the numbers of each are on the device.
+bool wide(const MatmulArgs& a, int sms, int split) {
+  if (a.offsets) return (a.rows + a.groups - 1) / a.groups > 64;
+  if (a.rows <= moe::dense::kSomeRows) return false;
+  const double kblocks = static_cast<double>(blocks(a.k));
+  const int64_t row_tiles = (a.rows + 127) / 128;
+  const double rows = static_cast<double>(a.rows) / row_tiles;
+  const int64_t pair_turns = ((a.rows + 255) / 256 * ((a.n + 255) / 256) + sms / 2 - 1) / (sms / 2);
+  const int64_t turns = (row_tiles * blocks(a.n) * split + sms - 1) / sms;
+  const double pairs_us = 4.5 + pair_turns * (1.8 + kblocks * 0.41);
+  const double others_us = 4.0 + (split > 1 ? 2.0 : 0.0) + turns * std::ceil(kblocks / split) * (0.28 + rows / 800);
+  return pairs_us < others_us;
+}
+
 int matmul(int rows, int n, int k, int groups, const uint8_t* codes, int64_t code_stride, const float* scales,
            int64_t scale_row, int64_t scale_block, const uint8_t* w_codes, const float* w_scales, const int32_t* offsets,
            void* out, int64_t out_stride, int out_dtype, uint32_t* status, uint32_t wait_cycles, int copy_arrivals,
@@ -90,9 +109,9 @@ int matmul(int rows, int n, int k, int groups, const uint8_t* codes, int64_t cod
   a.x_stride = rows > 1 ? code_stride : (k + 15) / 16 * 16; a.scale_row = scale_row; a.scale_block = scale_block; a.out_stride = out_stride;
   a.rows = rows; a.n = n; a.k = k; a.groups = groups ? groups : 1; a.out_dtype = out_dtype;
   a.wait_cycles = wait_cycles; a.copy_arrivals = copy_arrivals;
-  const int64_t average = (rows + a.groups - 1) / a.groups;
-  const bool wide = average > (groups ? 64 : 128);
-  return done("product launch", wide ? moe::dense::launch_fp8_wide(a, sms, stream) : moe::dense::launch_fp8_stream(a, sms, stream));
+  const int split = moe::dense::fp8_stream_split(a, sms);
+  return done("product launch", wide(a, sms, split) ? moe::dense::launch_fp8_wide(a, sms, stream)
+                                                    : moe::dense::launch_fp8_stream(a, sms, split, stream));
 }
 
 }  // namespace

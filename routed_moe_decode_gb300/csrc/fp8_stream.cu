@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarps = 2, kScaleWarp = 10, kThreads = 32 * 12;
 constexpr uint32_t kDrainCycles = 1u << 24;
+constexpr int kMostParts = 8;  // of k, the CTAs of a cluster
 constexpr int kSlab = 16;      // rows of x whose sums are staged for writing at a time
 constexpr int kPrefetch = 4;  // blocks of scales that are under way in a scale warp's registers
 
@@ -61,6 +62,16 @@ __device__ __forceinline__ void store4(const MatmulArgs& a, int64_t row, int c, 
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (c + i < a.n) store_one(a, row, c + i, f[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void load_scales(float2 (&f)[N], const float* s) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(s + 2 * i);
+    f[i] = make_float2(v.x, v.y);
+    f[i + 1] = make_float2(v.z, v.w);
+  }
 }
 
 template <int NT>
@@ -227,25 +238,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < H / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int kb = k0; kb < k1; ++kb, ++it) {
         const uint32_t b = it % L::kBufs, phase = (it / L::kBufs) & 1;
-        ok = warp_wait(scaled + 8 * b, phase, limit, a.status) && warp_wait(done + 8 * b, phase, limit, a.status);
+        // a step's scales are in registers before its products are there (or are read from tensor memory)
+        constexpr int STEP = H < 32 ? H : 32;
+        float2 f[STEP / 2];
+        const float* s = scales + b * NT + first;
+        ok = warp_wait(scaled + 8 * b, phase, limit, a.status);
+        load_scales(f, s);
+        ok = ok && warp_wait(done + 8 * b, phase, limit, a.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t from = tmem + b * NT + first + (static_cast<uint32_t>(quarter * 32) << 16);
-        const float* s = scales + b * NT + first;
 #pragma unroll
-        for (int c = 0; c < H; c += 16) {
-          if (c >= mine) break;
-          uint32_t v[16];
-          tmem_ld_x16(from + c, v);
+        for (int c = 0; c < H; c += STEP) {
+          if (c >= mine) break;  // (columns past `mine` in its last step are added up and not used)
+          uint32_t v[STEP];
+          if constexpr (STEP == 32) tmem_ld_x32(from + c, v);
+          else tmem_ld_x16(from + c, v);
+          if (c) load_scales(f, s + c);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(s + c + i);
-            float2& p = acc[(c + i) / 2];
-            float2& q = acc[(c + i) / 2 + 1];
-            p = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(f.x, f.y), p);
-            q = fma2(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), make_float2(f.z, f.w), q);
-          }
+          for (int i = 0; i < STEP; i += 2)
+            acc[(c + i) / 2] = fma2_in_order(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f[i / 2],
+                                             acc[(c + i) / 2]);
         }
         tc_fence_before();
         __syncwarp();
@@ -291,14 +305,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int id = blockIdx.x / split;
     if (id < tiles && s_limit) {
       const Tile t = tile_of<NT, 128, true>(a, id, ctiles, kblocks, gs);
-      const int ch = tid & 127;
-      // three groups of 128 threads, every CTA a row of its own
-      for (int r = part + split * (tid >> 7); r < t.rows; r += 3 * split) {
-        float v = 0.f;
-        for (int p = 0; p < split; ++p) v += ld_cluster(mapa(base + (r * 128 + ch) * 4, p));
-        if (t.c0 + ch < a.n) store_one(a, t.row0 + r, t.c0 + ch, v);
+      // a warp takes a row, a lane four channels of it; the parts' loads are under way together and added in order
+      const int size = a.out_dtype == MOE_DENSE_FP32 ? 4 : 2;
+      const bool vec = reinterpret_cast<uintptr_t>(a.out) % (4 * size) == 0 && a.out_stride % 4 == 0;
+      for (int r = part + split * warp; r < t.rows; r += split * (kThreads / 32)) {
+        float4 v[kMostParts];
+#pragma unroll
+        for (int p = 0; p < kMostParts; ++p)
+          if (p < split) v[p] = ld_cluster4(mapa(base + (r * 128 + lane * 4) * 4, p));
+#pragma unroll
+        for (int p = 1; p < kMostParts; ++p)
+          if (p < split) v[0] = make_float4(v[0].x + v[p].x, v[0].y + v[p].y, v[0].z + v[p].z, v[0].w + v[p].w);
+        store4(a, t.row0 + r, t.c0 + lane * 4, v[0], vec);
       }
     }
+    __syncwarp();
     cluster_sync();
   }
   tc_fence_before();
@@ -314,28 +335,43 @@ cudaError_t run(const Maps& maps, const MatmulArgs& a, int split, int grid, cuda
   return launch_cluster<fp8_stream_kernel<NT>>(split, dim3(grid), dim3(kThreads), Shape<NT>::kTotal, stream, maps, a);
 }
 
+// Few rows: 32 at most in a tile (groups: 16 on average), else 128.
+bool few_rows(const MatmulArgs& a) {
+  return a.offsets ? (a.rows + a.groups - 1) / a.groups <= 16 : a.rows <= kFewRows;
+}
+
 }  // namespace
 
-cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, cudaStream_t stream) {
+int fp8_stream_split(const MatmulArgs& a, int sms) {
+  if (a.offsets) return 1;
+  const bool few = few_rows(a);
+  const int nt = few ? kFewRows : kSomeRows, kblocks = (a.k + 127) / 128;
+  const int64_t tiles = static_cast<int64_t>((a.n + 127) / 128) * ((a.rows + nt - 1) / nt);
+  // clusters that would not all be resident take twice the time (16 of 8 CTAs: 12.2 us, of 6: 7.7, 8192 k x 2048 channels)
+  for (int split = kMostParts; split > 1; --split) {
+    if (split > kblocks || tiles * split > sms) continue;
+    const int most = few ? resident_clusters<fp8_stream_kernel<kFewRows>>(split, dim3(kThreads), Shape<kFewRows>::kTotal)
+                         : resident_clusters<fp8_stream_kernel<kSomeRows>>(split, dim3(kThreads), Shape<kSomeRows>::kTotal);
+    if (tiles <= most) return split;
+  }
+  return 1;
+}
+
+cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, int split, cudaStream_t stream) {
   Maps maps;
   const int64_t groups = a.offsets ? a.groups : 1;
   if (encode_fp8_map(&maps.w, a.w, a.k, groups * a.n, a.k, 128) != MOE_OK ||
       encode_fp8_map(&maps.x16, a.x, a.k, a.rows, a.x_stride, 16) != MOE_OK ||
       encode_fp8_map(&maps.x64, a.x, a.k, a.rows, a.x_stride, 64) != MOE_OK)
     return cudaErrorInvalidValue;
-  const int64_t average = (a.rows + groups - 1) / groups;
-  const bool few = average <= (a.offsets ? 16 : 32);
-  const int nt = few ? 32 : 128;
-  int split = 1, grid = sms;
-  const int ctiles = (a.n + 127) / 128, kblocks = (a.k + 127) / 128;
+  const bool few = few_rows(a);
+  int grid = sms;
   if (!a.offsets) {
-    const int64_t tiles = static_cast<int64_t>(ctiles) * ((a.rows + nt - 1) / nt);
-    if (tiles < sms) {
-      while (split < 8 && tiles * (split + 1) <= sms && split + 1 <= kblocks) ++split;
-      grid = static_cast<int>(tiles) * split;
-    }
+    const int nt = few ? kFewRows : kSomeRows;
+    const int64_t tiles = static_cast<int64_t>((a.n + 127) / 128) * ((a.rows + nt - 1) / nt);
+    if (tiles * split < sms || split > 1) grid = static_cast<int>(tiles) * split;
   }
-  return few ? run<32>(maps, a, split, grid, stream) : run<128>(maps, a, split, grid, stream);
+  return few ? run<kFewRows>(maps, a, split, grid, stream) : run<kSomeRows>(maps, a, split, grid, stream);
 }
 
 }  // namespace dense
