@@ -8,7 +8,7 @@
 // few rows the weights' bytes bound the product, with many rows the tensor cores and the sums.
 //
 // Roles: warps 0-7 add up (a lane of tensor memory is a channel; two groups of four warps take half of the rows
-// each), a warp copies tiles into a ring, a warp issues the MMAs, two warps bring xs * ws of a block's rows into shared memory.
+// each), a warp copies tiles into a ring, a warp issues the MMAs, two warps bring a block's scales into shared memory.
 // CTAs take tiles statically, one after the other; the ring runs on across tiles.  Where one row of x tiles would leave
 // SMs idle, a cluster's CTAs take a part of k each and add up through distributed shared memory, in order.
 #include "fp8_tiles.cuh"
@@ -21,7 +21,6 @@ constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarps = 2, kScal
 constexpr uint32_t kDrainCycles = 1u << 24;
 constexpr int kMostParts = 8;  // of k, the CTAs of a cluster
 constexpr int kSlab = 16;      // rows of x whose sums are staged for writing at a time
-constexpr int kPrefetch = 4;  // blocks of scales that are under way in a scale warp's registers
 
 template <int NT>
 struct Shape {
@@ -29,10 +28,11 @@ struct Shape {
   static constexpr int kStages = NT == 128 ? 6 : 9;
   static constexpr int kBufs = NT == 128 ? 4 : 8;  // products in tensor memory
   static constexpr int kCols = NT * kBufs;
-  static constexpr int kScales = kStage * kStages;                 // [kBufs][NT] floats
-  static constexpr int kStaged = kScales + 4 * NT * kBufs;         // [2][kSlab][128] floats
+  static constexpr int kSlots = NT == 128 ? 8 : 32, kSlot = NT + 4;  // blocks' scales: of the rows, the weight's
+  static constexpr int kScales = kStage * kStages;                   // [kSlots][kSlot] floats
+  static constexpr int kStaged = kScales + 4 * kSlots * kSlot;       // [2][kSlab][128] floats
   static constexpr int kBars = kStaged + 4 * 2 * kSlab * 128;
-  static constexpr int kNumBars = 2 * kStages + 3 * kBufs + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 2 * kSlots + 1;
   static constexpr int kGroups = kBars + 8 * kNumBars;
   static constexpr int kTotal = kGroups + static_cast<int>(sizeof(Groups)) + 1024;
   static_assert(kTotal <= 227 * 1024);
@@ -65,13 +65,17 @@ __device__ __forceinline__ void store4(const MatmulArgs& a, int64_t row, int c, 
 }
 
 template <int N>
-__device__ __forceinline__ void load_scales(float2 (&f)[N], const float* s) {
+__device__ __forceinline__ void load_scales(float2 (&f)[N], const float* s, float ws) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float4 v = *reinterpret_cast<const float4*>(s + 2 * i);
-    f[i] = make_float2(v.x, v.y);
-    f[i + 1] = make_float2(v.z, v.w);
+    f[i] = mul2(make_float2(v.x, v.y), make_float2(ws, ws));
+    f[i + 1] = mul2(make_float2(v.z, v.w), make_float2(ws, ws));
   }
+}
+// Four bytes, or zeros, asynchronously into shared memory.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
 template <int NT>
@@ -85,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = smem_addr(smem);
   Groups& gs = *reinterpret_cast<Groups*>(smem + L::kGroups);
   const uint32_t full = base + L::kBars, empty = full + 8 * L::kStages, done = empty + 8 * L::kStages,
-                 freed = done + 8 * L::kBufs, scaled = freed + 8 * L::kBufs, end = scaled + 8 * L::kBufs;
+                 freed = done + 8 * L::kBufs, scaled = freed + 8 * L::kBufs, used = scaled + 8 * L::kSlots, end = used + 8 * L::kSlots;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
@@ -95,7 +99,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < L::kBufs; ++i) {
       mbar_init(done + 8 * i, 1);
       mbar_init(freed + 8 * i, kSumWarps);
-      mbar_init(scaled + 8 * i, kScaleWarps);
+    }
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(scaled + 8 * i, 32 * kScaleWarps);
+      mbar_init(used + 8 * i, kSumWarps);
     }
     mbar_init(end, 1);
     s_limit = a.wait_cycles;
@@ -184,43 +191,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     warp_wait(end, 0, &s_drain_mma, a.status);
   } else if (warp >= kScaleWarp) {
-    // rows r0, r0 + 64, ...: their scales of the next kPrefetch blocks in registers
-    constexpr int PER = (NT + 63) / 64;
+    // scales of rows r0 and r0 + 64, and of the weight, kSlots blocks ahead, across tiles (four blocks ahead in
+    // registers, 256 groups of 8 rows took 113 us instead of the 89 of this)
     const int r0 = (warp - kScaleWarp) * 32 + lane;
-    float* out = reinterpret_cast<float*>(smem + L::kScales);
+    const uint32_t out = base + L::kScales;
     uint32_t it = 0;
     bool ok = true;
     for (int id = blockIdx.x / split; ok && id < tiles; id += stride) {
       const Tile t = tile_of<NT, 128, true>(a, id, ctiles, kblocks, gs);
-      float x[kPrefetch][PER], w[kPrefetch];
-      auto load = [&](int j, int kb) {
-        w[j] = kb < k1 ? __ldcg(t.ws + kb) : 0.f;
+      const float* xs = a.xs + static_cast<int64_t>(t.row0 + r0) * a.scale_row;
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const uint32_t slot = it % L::kSlots, to = out + slot * (L::kSlot * 4);
+        if (!(ok = warp_wait(used + 8 * slot, ((it / L::kSlots) & 1) ^ 1, limit, a.status))) break;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int r = r0 + 64 * i;
-          x[j][i] = kb < k1 && r < t.rows ? __ldcg(a.xs + (t.row0 + r) * a.scale_row + kb * a.scale_block) : 0.f;
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < kPrefetch; ++j) load(j, k0 + j);
-      for (int kb0 = k0; ok && kb0 < k1; kb0 += kPrefetch) {
-#pragma unroll
-        for (int j = 0; j < kPrefetch; ++j) {
-          const int kb = kb0 + j;
-          if (!ok || kb >= k1) continue;
-          const uint32_t b = it % L::kBufs;
-          ok = warp_wait(freed + 8 * b, ((it / L::kBufs) & 1) ^ 1, limit, a.status);
-          if (!ok) continue;
-          ++it;
-#pragma unroll
-          for (int i = 0; i < PER; ++i)
-            if (r0 + 64 * i < NT) out[b * NT + r0 + 64 * i] = x[j][i] * w[j];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(scaled + 8 * b);
-          load(j, kb + kPrefetch);
-        }
+        for (int r = r0; r < NT; r += 64)
+          copy4(to + 4 * r, r < t.rows ? xs + (r - r0) * a.scale_row + kb * a.scale_block : a.xs, r < t.rows);
+        if (r0 == 0) copy4(to + 4 * NT, t.ws + kb, true);
+        cp_async_arrive_noinc(scaled + 8 * slot);
       }
     }
+    cp_async_wait_all();
   } else {
     constexpr int H = NT / 2;
     const int half = warp >> 2, quarter = warp & 3;
@@ -241,9 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a step's scales are in registers before its products are there (or are read from tensor memory)
         constexpr int STEP = H < 32 ? H : 32;
         float2 f[STEP / 2];
-        const float* s = scales + b * NT + first;
-        ok = warp_wait(scaled + 8 * b, phase, limit, a.status);
-        load_scales(f, s);
+        const uint32_t slot = it % L::kSlots;
+        const float* s = scales + slot * L::kSlot + first;
+        ok = warp_wait(scaled + 8 * slot, (it / L::kSlots) & 1, limit, a.status);
+        const float ws = scales[slot * L::kSlot + NT];
+        load_scales(f, s, ws);
         ok = ok && warp_wait(done + 8 * b, phase, limit, a.status);
         if (!ok) break;
         tc_fence_after();
@@ -254,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[STEP];
           if constexpr (STEP == 32) tmem_ld_x32(from + c, v);
           else tmem_ld_x16(from + c, v);
-          if (c) load_scales(f, s + c);
+          if (c) load_scales(f, s + c, ws);
           tc_wait_ld();
 #pragma unroll
           for (int i = 0; i < STEP; i += 2)
@@ -263,7 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(freed + 8 * b);
+        if (lane == 0) {
+          mbar_arrive(freed + 8 * b);
+          mbar_arrive(used + 8 * slot);
+        }
       }
       // the four warps of a half write together, so they go on or give up together
       ok = named_bar_and(1 + half, 128, ok);
