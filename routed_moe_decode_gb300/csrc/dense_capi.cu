@@ -67,7 +67,7 @@ bool rows_vec(const void* p, int64_t s0, int64_t s1, int size) {
 
 // Whether CTA pairs (256 rows x 256 channels a tile) take the product, rather than the kernel with up to 128 rows x 128
 // channels a tile and k in parts.  Estimates of both in us, fitted to measured products (us, pairs / the others): a block of 128 k
-// takes a pair 0.41 and a CTA 0.28 + n / 800 for n rows of x.
+// takes a pair 0.375 and a CTA 0.28 + n / 800 for n rows of x.
 //   rows 256: 5120 x 2048 11.0 / 11.6, 2048 x 8192 29.5 / 14.9, 8192 x 8192 30.1 / 29.2, 16384 x 4096 18.5 / 31.9
 //   rows 512: 5120 x 2048 11.6 / 19.9, 2048 x 8192 29.7 / 22.8, 8192 x 8192 31.0 / 54.9
 // Groups: by their rows on average, as the numbers of each are on the device.
@@ -79,7 +79,7 @@ bool wide(const MatmulArgs& a, int sms, int split) {
   const double rows = static_cast<double>(a.rows) / row_tiles;
   const int64_t pair_turns = ((a.rows + 255) / 256 * ((a.n + 255) / 256) + sms / 2 - 1) / (sms / 2);
   const int64_t turns = (row_tiles * blocks(a.n) * split + sms - 1) / sms;
-  const double pairs_us = 4.5 + pair_turns * (1.8 + kblocks * 0.41);
+  const double pairs_us = 4.5 + pair_turns * (1.8 + kblocks * 0.375);
   const double others_us = 4.0 + (split > 1 ? 2.0 : 0.0) + turns * std::ceil(kblocks / split) * (0.28 + rows / 800);
   return pairs_us < others_us;
 }

@@ -73,10 +73,6 @@ __device__ __forceinline__ void load_scales(float2 (&f)[N], const float* s, floa
     f[i + 1] = mul2(make_float2(v.z, v.w), make_float2(ws, ws));
   }
 }
-// Four bytes, or zeros, asynchronously into shared memory.
-__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -80,6 +80,11 @@ __device__ __forceinline__ Tile tile_of(const MatmulArgs& a, int id, int ctiles,
   return t;
 }
 
+// Four bytes, or zeros, asynchronously into shared memory.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ T rounded(float v);
 template <>
