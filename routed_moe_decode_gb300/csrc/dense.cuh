@@ -241,7 +241,7 @@ int resident_clusters(int cluster, dim3 block, size_t smem) {
   return n - 1;
 }
 
-// launch_ready for clusters of `cluster` CTAs along x.
+// launch_ready for clusters of `cluster` CTAs along x (and the SM's memory divided as by default: loads under way need L1).
 template <auto Kernel, typename... Args>
 cudaError_t launch_cluster(int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
   static std::atomic<unsigned long long> ready{0};

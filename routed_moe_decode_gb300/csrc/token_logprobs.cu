@@ -5,15 +5,17 @@
 // rescaled when m rises; joined over a row, lse = m + log s and entropy = log s - u / s.
 //
 // Alternatives are keys: the logit's order-preserving bits above the complement of its id, so that equal logits are in
-// the order of their ids and no two keys are equal.  A warp keeps its best 32 sorted over its lanes.  What cannot be
-// among the best is told from the maximum of a thread's values, which the sums need anyway, against a threshold: each
-// warp shows its four best logits, and the top-th of those 32 is not above the row's.  The first step's
-// maxima of the lanes fill the 32 places at once, so that few values are ever looked at one by one (with every value of a
-// hit step looked at, and the smallest of the warps' own places as the threshold, 60 % of the instructions went there).
+// the order of their ids and no two keys are equal.  The pass keeps only the largest logit of every thread's step (or of a
+// few), which the sums need anyway, in shared memory.  At its end each warp shows its threads' four largest logits; the
+// top-th of these 32 is a threshold that at least `top` logits reach.  Only the steps whose largest reaches it, about `top`
+// of them, are read again, and what reaches it there is put into lists that the warps keep sorted over their lanes.  (With lists
+// kept during the pass, 20 alternatives cost 53 us beside 96 without any for 2048 rows of 131072, and 13 beside 11 for 127 of 100003.)
+// Where very many reach the threshold (nothing but masks, equal logits) the row is read again as a whole.
 //
 // A row is one CTA's, or a cluster's of up to eight where there are few rows; the parts join through distributed shared
 // memory in a fixed order.
 #include <cfloat>
+#include <type_traits>
 
 #include "dense.cuh"
 
@@ -132,21 +134,27 @@ struct Vec<__half> {
   }
 };
 
-struct Shared {
-  uint4 values[kWarps][kVecs][32];  // of a step whose values are looked at one by one
+constexpr int kGroups = 8, kPairs = 1024;  // steps, or groups of them, whose largest logits are kept; of those read again
+
+struct Sorted {
+  float largest[kGroups][kThreads];
+  uint16_t pairs[kPairs];  // thread, group << 8
+  int npairs;
   Key lists[kWarps][32];
+  uint32_t shown[kWarps * kShown];  // logits of each warp, as float_key has them
+  Key part_list[32];                // a cluster's parts read this
+};
+struct None {};
+template <bool TOP>
+struct Shared : std::conditional_t<TOP, Sorted, None> {
   Sums sums[kWarps];
-  uint32_t shown[kWarps * kShown];  // each warp's best logits, or some below them, as float_key has them
-  uint32_t version;                 // of `shown`
-  // a cluster's parts read these
-  Key part_list[32];
-  Sums part_sums;
+  Sums part_sums;  // a cluster's parts read this
 };
 
 __device__ __forceinline__ float value_of(uint32_t key) { return logit_of(static_cast<Key>(key) << 32); }
 
 // Lanes' keys into a warp's list (0: none).
-__device__ __forceinline__ Key insert(Key list, Key k, int top, int lane) {
+__device__ __noinline__ Key insert(Key list, Key k, int top, int lane) {
   k = k > __shfl_sync(kAll, list, top - 1) ? k : 0;
   uint32_t want = __ballot_sync(kAll, k != 0);
   if (__popc(want) > 6) {  // as costly as a sort: bitonic, descending over the lanes
@@ -184,7 +192,7 @@ __device__ __forceinline__ uint32_t nth(uint32_t k, int top, int lane) {
 
 // The warp's lists into the first warp's.
 template <bool TOP>
-__device__ __forceinline__ Key best_of_warps(Shared& sh, Key list, int warp, int lane) {
+__device__ __forceinline__ Key best_of_warps(Shared<TOP>& sh, Key list, int warp, int lane) {
   if constexpr (TOP) {
     for (int n = kWarps / 2; n > 0; n >>= 1) {
       if (warp >= n && warp < 2 * n) sh.lists[warp][lane] = list;
@@ -202,20 +210,18 @@ __device__ __forceinline__ Sums joined(Sums a, int o, int lane) {
   return (lane & o) ? join(b, a) : join(a, b);
 }
 
-// CTAs of an SM: with alternatives, 16-bit types (32 values a step) would spill at four.
-template <typename T, bool TOP>
-constexpr int ctas() { return TOP && sizeof(T) == 2 ? 3 : 4; }
+constexpr int kCtas = 4;  // of an SM
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, ctas<T, TOP>()) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a) {
   typedef Vec<T> V;
   constexpr int N = kVecs * V::N;
-  __shared__ Shared sh;
+  __shared__ Shared<TOP> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = static_cast<int>(cluster_size()), part = static_cast<int>(cluster_rank());
-  if (TOP && tid < kWarps * kShown) sh.shown[tid] = 0;
-  if (TOP && tid == 0) sh.version = 0;
-  if (TOP) __syncthreads();
+  if constexpr (TOP) {
+    if (tid == 0) sh.npairs = 0;
+  }
   pdl_wait();
   pdl_launch_dependents();
   const int64_t row = blockIdx.x / parts;
@@ -229,8 +235,11 @@ __global__ void __launch_bounds__(kThreads, ctas<T, TOP>()) logprobs_kernel(cons
 
   Sums mine{-FLT_MAX, 0.f, 0.f};
   Key list = 0;
-  uint32_t seen = ~0u;
-  float bar = -INFINITY;
+  float best = -INFINITY, group_best = -INFINITY;  // of this thread; of its steps in the group at hand
+  // steps, in groups of 2^shift
+  const int steps = (v1 - v0 + kVecs * kThreads - 1) / (kVecs * kThreads);
+  int shift = 0;
+  while (((steps - 1) >> shift) >= kGroups) ++shift;
   const float2 scale = make_float2(a.scale, a.scale), log2e = make_float2(kLog2e, kLog2e);
 
   auto load = [&](uint4 (&raw)[kVecs], int at) {
@@ -274,53 +283,12 @@ __global__ void __launch_bounds__(kThreads, ctas<T, TOP>()) logprobs_kernel(cons
     const float most = V::most(raw, v);
     add(v, most);
     if constexpr (TOP) {
-      if (at == v0) {  // the same for the whole CTA
-        uint32_t k = float_key(most == most ? most : -INFINITY);
-#pragma unroll
-        for (int p = 0; p < kShown; ++p) {
-          const uint32_t w = __reduce_max_sync(kAll, k);
-          if (lane == p) sh.shown[warp * kShown + p] = w;
-          if (lane == __ffs(__ballot_sync(kAll, k == w)) - 1) k = 0;
-        }
-        __syncthreads();
-      }
-      // a NaN ranks as -infinity, and so does a maximum of NaNs alone
-      bool some = __any_sync(kAll, !(most < bar));
-      if (some) {  // against the threshold as it is now
-        const uint32_t version = *const_cast<volatile uint32_t*>(&sh.version);
-        if (__any_sync(kAll, version != seen)) {
-          seen = __shfl_sync(kAll, version, 0);
-          bar = value_of(nth(*const_cast<volatile uint32_t*>(&sh.shown[lane]), a.top, lane));
-          some = __any_sync(kAll, !(most < bar));
-        }
-      }
-      if (some) {
-        uint32_t mask = 0;
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          if (!(v[i].x < bar)) mask |= 1u << (2 * i);
-          if (!(v[i].y < bar)) mask |= 2u << (2 * i);
-        }
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-          sh.values[warp][j][lane] = raw[j];
-          if (at + j * kThreads + tid >= v1) mask &= ~(((1u << (V::N - 1)) * 2 - 1) << (j * V::N));
-        }
-        __syncwarp();
-        const Key old = list;
-        for (uint32_t left = __reduce_or_sync(kAll, mask); left; left &= left - 1) {
-          const int i = __ffs(left) - 1, j = i / V::N, e = i % V::N;
-          const float l = to_float(reinterpret_cast<const T*>(&sh.values[warp][j][lane])[e]);
-          list = insert(list, (mask >> i) & 1 ? key_of(l, head + (at + j * kThreads + tid) * V::N + e) : 0, a.top, lane);
-        }
-        if (__any_sync(kAll, list != old)) {
-          const uint32_t k = static_cast<uint32_t>(list >> 32);
-          volatile uint32_t* shown = &sh.shown[warp * kShown];
-          if (lane < kShown && k > shown[lane]) shown[lane] = k;
-          __syncwarp();
-          if (lane == 0) atomicAdd(&sh.version, 1u);
-        }
-        __syncwarp();
+      group_best = fmaxf(group_best, most);
+      const int step = (at - v0) / (kVecs * kThreads);
+      if (!more || ((step + 1) & ((1 << shift) - 1)) == 0) {
+        sh.largest[step >> shift][tid] = group_best;
+        best = fmaxf(best, group_best);
+        group_best = -INFINITY;
       }
     }
     if (more) {
@@ -339,6 +307,50 @@ __global__ void __launch_bounds__(kThreads, ctas<T, TOP>()) logprobs_kernel(cons
     if constexpr (TOP) list = insert(list, there ? key_of(v[0].x, id) : 0, a.top, lane);
   }
 
+  if constexpr (TOP) {
+    uint32_t k = float_key(best);
+#pragma unroll
+    for (int p = 0; p < kShown; ++p) {
+      const uint32_t w = __reduce_max_sync(kAll, k);
+      if (lane == p) sh.shown[warp * kShown + p] = w;
+      if (lane == __ffs(__ballot_sync(kAll, k == w)) - 1) k = 0;
+    }
+    __syncthreads();
+    const float bar = value_of(nth(sh.shown[lane], a.top, lane));
+    // a NaN ranks as -infinity: a group of nothing else has that as its largest
+    for (int g = 0; g <= (steps - 1) >> shift && steps; ++g) {
+      if (!(sh.largest[g][tid] < bar)) {
+        const int at = atomicAdd(&sh.npairs, 1);
+        if (at < kPairs) sh.pairs[at] = static_cast<uint16_t>(tid | g << 8);
+      }
+    }
+    __syncthreads();
+    // vector i, or none: its values into the list
+    auto look = [&](int i, bool there) {
+      const uint4 r = there ? __ldcg(xv + i) : make_uint4(0, 0, 0, 0);
+      float2 v[V::N / 2];
+      V::get(r, v);
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) {
+        const float l = e & 1 ? v[e / 2].y : v[e / 2].x;
+        const bool good = there && !(l < bar);
+        if (__any_sync(kAll, good)) list = insert(list, good ? key_of(l, head + i * V::N + e) : 0, a.top, lane);
+      }
+    };
+    const int pairs = sh.npairs;
+    if (pairs <= kPairs) {
+      const int per = kVecs << shift, log = 31 - __clz(per);
+      for (int n0 = warp * 32; n0 < pairs << log; n0 += kThreads) {
+        const int n = n0 + lane, pair = n < pairs << log ? sh.pairs[n >> log] : 0, sub = n & (per - 1);
+        const int step = ((pair >> 8) << shift) + sub / kVecs;
+        const int i = v0 + (step * kVecs + sub % kVecs) * kThreads + (pair & 255);
+        look(i, n < pairs << log && i < v1);
+      }
+    } else {
+      for (int i0 = v0 + warp * 32; i0 < v1; i0 += kThreads) look(i0 + lane, i0 + lane < v1);
+    }
+  }
+
   // the CTA's sums and lists
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine = joined(mine, o, lane);
@@ -351,13 +363,13 @@ __global__ void __launch_bounds__(kThreads, ctas<T, TOP>()) logprobs_kernel(cons
   }
   if (parts > 1) {
     if (warp == 0) {
-      if (TOP) sh.part_list[lane] = list;
+      if constexpr (TOP) sh.part_list[lane] = list;
       if (lane == 0) sh.part_sums = mine;
     }
     __syncwarp();
     cluster_sync();
     if (part == 0) {  // a warp has a part's list, a lane a part's sums
-      if (TOP) {
+      if constexpr (TOP) {
         list = warp < parts ? ld_cluster_u64(mapa(smem_addr(&sh.part_list[lane]), warp)) : 0;
         list = best_of_warps<TOP>(sh, list, warp, lane);
       }
@@ -395,7 +407,7 @@ template <typename T>
 cudaError_t run(const LogprobArgs& a, int sms, cudaStream_t stream) {
   // parts of a row: while all CTAs are resident together, and a part is worth a CTA
   int parts = 1;
-  const int64_t most = static_cast<int64_t>(a.top > 0 ? ctas<T, true>() : ctas<T, false>()) * sms;
+  const int64_t most = static_cast<int64_t>(kCtas) * sms;
   while (parts < 8 && static_cast<int64_t>(a.rows) * parts * 2 <= most && a.vocab / (parts * 2) >= 2048) parts *= 2;
   const dim3 grid(static_cast<unsigned>(a.rows) * parts), block(kThreads);
   return a.top > 0 ? launch_cluster<logprobs_kernel<T, true>>(parts, grid, block, 0, stream, a)

@@ -455,6 +455,19 @@ def test_logprobs(moe, rows, vocab, dtype):
         check_logprobs(got, logits, tokens, top, scale)
 
 
+@pytest.mark.parametrize("rows", [2, 700])
+def test_logprobs_of_a_large_vocabulary(moe, rows):
+    """Many steps a thread: one CTA a row where there are many rows, parts of a cluster where there are few."""
+    g = gen(rows)
+    vocab = 400003
+    logits = rand(g, rows, vocab, dtype=BF16, scale=2.0)
+    logits[0, ::2] = logits[0, 1]
+    tokens = torch.randint(0, vocab, (rows, 2), generator=g, device="cuda").to(torch.int32)
+    got = moe.token_logprobs(logits, tokens, top=32)
+    few = [0, rows - 1]
+    check_logprobs(moe.TokenLogprobs(*(t[few] for t in got)), logits[few], tokens[few], 32, 1.0)
+
+
 def test_logprobs_masks_ties_and_bad_tokens(moe):
     g = gen(77)
     inf = math.inf
