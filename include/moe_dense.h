@@ -23,7 +23,7 @@
  * Conventions are those of moe.h: device pointers owned by the caller, asynchronous calls that can
  * be captured in a CUDA graph, host-detected errors returned before anything is enqueued, nothing
  * kept between calls, and no workspace: calls on different streams do not meet.  Outputs do not
- * overlap inputs or each other unless a call says so.  The products OR device-detected conditions into the
+ * overlap inputs or each other unless a call says so, and an output's rows lie apart.  The products OR device-detected conditions into the
  * caller's status word (moe_dense_read_status).
  */
 #ifndef ROUTED_MOE_DENSE_H
@@ -90,7 +90,7 @@ MOE_API int moe_fp8_matmul(int rows, int n, int k, int groups, const uint8_t* co
  * of the last two are null where top is 0.  n_tokens <= 1024, top <= 32, top <= vocab.
  * A logit of -infinity has probability 0 and log probability -infinity; so has a token outside
  * [0, vocab).  A row of nothing else has lse -infinity, log probabilities -infinity and entropy 0.
- * A row with a NaN or +infinity has NaN for them; its alternatives are ordered as if the NaNs were
+ * A row with a NaN or +infinity (also where scale * logit is that in FP32) has NaN for them; its alternatives are ordered as if the NaNs were
  * -infinity. */
 MOE_API int moe_token_logprobs(int rows, int vocab, int dtype, const void* logits, int64_t row_stride, float scale,
                                const int32_t* tokens, int n_tokens, int64_t token_stride, int top, float* logprobs,

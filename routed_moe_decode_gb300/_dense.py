@@ -9,6 +9,8 @@ import torch
 from . import _lib
 from ._routing import _DTYPES, _raw_stream
 
+_quantize_rows = _token_logprobs = None  # the library's functions, looked up at the first call
+
 DENSE_BAD_OFFSETS = 0x1
 DENSE_TIMEOUT = 0x2
 
@@ -45,8 +47,11 @@ class Fp8Rows:
             with torch.cuda.stream(stream):
                 return cls.empty(rows, k, device)
         self = object.__new__(cls)
-        codes = torch.empty((rows, -(-k // 16) * 16), dtype=_E4M3, device=device)
-        self.codes = codes[:, :k] if k % 16 else codes
+        if k % 16:
+            codes = torch.empty((rows, -(-k // 16) * 16), dtype=_E4M3, device=device)
+            self.codes = codes[:, :k]
+        else:
+            self.codes = codes = torch.empty((rows, k), dtype=_E4M3, device=device)
         self.scales = torch.empty_strided((rows, -(-k // 128)), (1, rows), dtype=torch.float32, device=device)
         self.device, self._index = codes.device, codes.get_device()
         return self
@@ -102,7 +107,8 @@ class RmsNorm:
                 raise ValueError(f"residual: of x's type and shape, which is [rows, {d}], with consecutive channels")
             residual_ptr, r_stride = residual.data_ptr(), residual.stride(0)
             if residual_out is None:
-                residual_out, ro_stride = _empty(shape, x.dtype, x.device, stream), d
+                residual_out, ro_stride = torch.empty(shape, dtype=x.dtype, device=x.device) if stream is None else \
+                    _empty(shape, x.dtype, x.device, stream), d
                 sum_ptr = residual_out.data_ptr()
             elif residual_out is False:
                 residual_out = None
@@ -118,7 +124,8 @@ class RmsNorm:
         else:
             residual_out = None
         if normed is True:
-            normed, n_outer, n_inner = _empty(shape, x.dtype, x.device, stream), inner * d, d
+            normed, n_outer, n_inner = torch.empty(shape, dtype=x.dtype, device=x.device) if stream is None else \
+                _empty(shape, x.dtype, x.device, stream), inner * d, d
             normed_ptr = normed.data_ptr()
         elif normed is False or normed is None:
             normed = None
@@ -154,11 +161,13 @@ def quantize_rows(x, gated=False, out=None, stream=None):
                          "consecutive channels")
     if gated:
         d //= 2
+    global _quantize_rows
+    if _quantize_rows is None:
+        _quantize_rows = _lib.lib().moe_quantize_rows
     out = Fp8Rows.empty(rows, d, x.device, stream) if out is None else _rows_to_write(out, rows, d, index)
     scale_row, scale_block = out.scales.stride()
-    rc = _lib.lib().moe_quantize_rows(rows, d, 1 if gated else 0, dtype, x.data_ptr(), row, out.codes.data_ptr(),
-                                      out.codes.stride(0), out.scales.data_ptr(), scale_row, scale_block,
-                                      _raw_stream(index, stream))
+    rc = _quantize_rows(rows, d, 1 if gated else 0, dtype, x.data_ptr(), row, out.codes.data_ptr(),
+                        out.codes.stride(0), out.scales.data_ptr(), scale_row, scale_block, _raw_stream(index, stream))
     if rc != 0:
         raise _lib.MoeError("moe_quantize_rows", rc)
     return out
@@ -197,7 +206,8 @@ class Fp8Linear:
         if k != self.k or x._index != index:
             raise ValueError(f"x: [rows, {self.k}] on cuda:{index}")
         if out is None:
-            out, out_stride = _empty((rows, n), dtype, self.device, stream), n
+            out, out_stride = torch.empty((rows, n), dtype=dtype, device=self.device) if stream is None else \
+                _empty((rows, n), dtype, self.device, stream), n
         else:
             out_stride, channel = out.stride() if out.dim() == 2 else (0, 0)
             if out.shape != (rows, n) or (channel != 1 and n > 1) or out.get_device() != index:
@@ -251,15 +261,25 @@ def token_logprobs(logits, tokens, top=0, scale=1.0, stream=None):
     if tokens.dtype is not torch.int32 or not 1 <= len(shape) <= 2 or shape[0] != rows or tokens.get_device() != index or \
             (len(shape) == 2 and strides[1] != 1 and n > 1):
         raise ValueError(f"tokens: [{rows}, n] or [{rows}] of int32 on cuda:{index} with consecutive columns")
+    global _token_logprobs
+    if _token_logprobs is None:
+        _token_logprobs = _lib.lib().moe_token_logprobs
     device, f32 = logits.device, torch.float32
-    logprobs, lse, entropy = _empty(shape, f32, device, stream), _empty(rows, f32, device, stream), _empty(rows, f32, device, stream)
     ids = best = ids_ptr = best_ptr = None
+    if stream is None:
+        empty = torch.empty
+        logprobs, lse, entropy = empty(shape, dtype=f32, device=device), empty(rows, dtype=f32, device=device), \
+            empty(rows, dtype=f32, device=device)
+        if top > 0:
+            ids, best = empty((rows, top), dtype=torch.int32, device=device), empty((rows, top), dtype=f32, device=device)
+    else:
+        logprobs, lse, entropy = _empty(shape, f32, device, stream), _empty(rows, f32, device, stream), _empty(rows, f32, device, stream)
+        if top > 0:
+            ids, best = _empty((rows, top), torch.int32, device, stream), _empty((rows, top), f32, device, stream)
     if top > 0:
-        ids, best = _empty((rows, top), torch.int32, device, stream), _empty((rows, top), f32, device, stream)
         ids_ptr, best_ptr = ids.data_ptr(), best.data_ptr()
-    rc = _lib.lib().moe_token_logprobs(rows, vocab, dtype, logits.data_ptr(), logits.stride(0), scale, tokens.data_ptr(), n,
-                                       strides[0], top, logprobs.data_ptr(), lse.data_ptr(), entropy.data_ptr(), ids_ptr,
-                                       best_ptr, _raw_stream(index, stream))
+    rc = _token_logprobs(rows, vocab, dtype, logits.data_ptr(), logits.stride(0), scale, tokens.data_ptr(), n, strides[0], top,
+                         logprobs.data_ptr(), lse.data_ptr(), entropy.data_ptr(), ids_ptr, best_ptr, _raw_stream(index, stream))
     if rc != 0:
         raise _lib.MoeError("moe_token_logprobs", rc)
     return TokenLogprobs(logprobs, lse, entropy, ids, best)

@@ -65,6 +65,15 @@ bool rows_vec(const void* p, int64_t s0, int64_t s1, int size) {
   return !p || (aligned(p, 16) && s0 % per == 0 && s1 % per == 0);
 }
 
+// Whether outer x inner pieces of `size` elements, so far apart, lie apart.
+bool apart(int64_t outer, int64_t outer_stride, int64_t inner, int64_t inner_stride, int64_t size) {
+  if (outer <= 1) return inner <= 1 || inner_stride >= size;
+  if (inner <= 1) return outer_stride >= size;
+  if (outer_stride < size || inner_stride < size) return false;
+  return outer_stride >= inner_stride ? (outer_stride - size) / (inner - 1) >= inner_stride
+                                      : (inner_stride - size) / (outer - 1) >= outer_stride;
+}
+
 // Whether CTA pairs (256 rows x 256 channels a tile) take the product, rather than the kernel with up to 128 rows x 128
 // channels a tile and k in parts.  Estimates of both in us, fitted to measured products (us, pairs / the others): a block of 128 k
 // takes a pair 0.375 and a CTA 0.28 + n / 800 for n rows of x.
@@ -136,7 +145,10 @@ int moe_rms_norm(int outer, int inner, int d, int dtype, const void* x, int64_t 
       !aligned(weight, wsize) || !aligned(scales, 4))
     return MOE_ERR_INVALID_ARG;
   if (normed && normed == residual_out) return MOE_ERR_INVALID_ARG;
-  if (codes && rows > 1 && code_stride < d) return MOE_ERR_INVALID_ARG;
+  if (residual_out && !apart(rows, residual_out_stride, 1, 0, d)) return MOE_ERR_INVALID_ARG;
+  if (normed && !apart(outer, normed_outer, inner, normed_inner, d)) return MOE_ERR_INVALID_ARG;
+  if (codes && (!apart(rows, code_stride, 1, 0, d) || !apart(rows, scale_row, blocks(d), scale_block, 1)))
+    return MOE_ERR_INVALID_ARG;
   int sms = 0;
   const int rc = moe::device_sms(&sms);
   if (rc != MOE_OK) return rc;
@@ -163,7 +175,8 @@ int moe_quantize_rows(int rows, int d, int gated, int dtype, const void* x, int6
   const int64_t all = static_cast<int64_t>(rows) * blocks(d);
   if (all > 0x7fffffffll || d > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   const int size = size_of(dtype);
-  if (!x || !codes || !scales || !aligned(x, size) || !aligned(scales, 4) || (rows > 1 && code_stride < d))
+  if (!x || !codes || !scales || !aligned(x, size) || !aligned(scales, 4) || !apart(rows, code_stride, 1, 0, d) ||
+      !apart(rows, scale_row, blocks(d), scale_block, 1))
     return MOE_ERR_INVALID_ARG;
   int sms = 0;
   const int rc = moe::device_sms(&sms);

@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
     cluster_sync();
   }
   if (part != 0 || warp != 0) return;
+  if (!(mine.m < INFINITY)) mine.s = __int_as_float(0x7fc00000);  // scale * logit is +infinity, of a finite logit too
   const bool none = mine.s == 0.f;
   const float logs = logf(mine.s);
   if (lane == 0) {

@@ -66,7 +66,11 @@ def test_norm_refuses_bad_arguments(L):
         ({7: None, 13: None, 15: None, 18: None, 20: None}, INV),  # nothing to write
         ({20: None}, INV), ({18: None}, INV),   # codes and scales go together
         ({15: P0}, INV),                        # normed in residual_out's place
-        ({19: 255}, INV), ({0: 1 << 20, 1: 1 << 20}, UNS), ({2: 1 << 25, 19: 1 << 25}, UNS)])
+        ({19: 255}, INV), ({0: 1 << 20, 1: 1 << 20}, UNS), ({2: 1 << 25, 19: 1 << 25}, UNS),
+        # rows of an output on top of each other
+        ({14: 255}, INV), ({16: 0}, INV), ({21: 0}, INV), ({22: 0}, INV), ({22: 3}, INV), ({22: 1}, INV),
+        ({1: 3, 6: 256, 5: 768, 17: 256, 16: 767, 7: None, 13: None, 18: None, 20: None}, INV),
+        ({1: 3, 6: 256, 5: 768, 17: 1023, 16: 256, 7: None, 13: None, 18: None, 20: None}, INV)])
 
 
 def test_quantize_refuses_bad_arguments(L):
@@ -75,7 +79,8 @@ def test_quantize_refuses_bad_arguments(L):
     INV, UNS = L.MOE_ERR_INVALID_ARG, L.MOE_ERR_UNSUPPORTED
     refused(L, "moe_quantize_rows", good, [
         ({0: 0}, L.MOE_OK), ({0: -1}, INV), ({1: 0}, INV), ({3: 9}, INV), ({4: None}, INV), ({6: None}, INV), ({8: None}, INV),
-        ({4: P0 + 1}, INV), ({8: P0 + 1}, INV), ({7: 200}, INV), ({0: 1 << 30, 1: 1 << 20, 7: 1 << 20}, UNS), ({1: 1 << 25}, UNS)])
+        ({4: P0 + 1}, INV), ({8: P0 + 1}, INV), ({7: 200}, INV), ({0: 1 << 30, 1: 1 << 20, 7: 1 << 20}, UNS), ({1: 1 << 25}, UNS),
+        ({9: 0}, INV), ({10: 0}, INV), ({10: 3}, INV), ({10: 1}, INV)])
 
 
 def test_matmul_refuses_bad_arguments(L):

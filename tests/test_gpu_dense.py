@@ -153,6 +153,9 @@ def test_norm_zeros_infinities_and_refusals(moe):
     with pytest.raises(ValueError):  # in x's place with other strides
         big = rand(gen(2), 8, 256)
         norm(big[:4], normed=big[::2])
+    for bad in (dict(normed=y[:1].clone().expand(4, 256)), dict(residual=y, residual_out=y[:1].clone().expand(4, 256))):
+        with pytest.raises(moe.MoeError):  # rows on top of each other
+            norm(y, **bad)
     with pytest.raises(moe.MoeError):
         norm(y, normed=False)
     with pytest.raises(moe.MoeError):
@@ -296,9 +299,10 @@ def test_product_of_one_hot_rows_is_the_weight(moe):
         assert ((out.double() - want[:rows]).abs() <= want[:rows].abs() * 4 * U).all()
 
 
-def test_product_strides_types_and_places(moe):
+@pytest.mark.parametrize("rows", [50, 700])
+def test_product_strides_types_and_places(moe, rows):
     g = gen(4)
-    rows, n, k = 50, 200, 160
+    n, k = 200, 160
     wide = (rand(g, rows, 320) * 50).to(torch.float8_e4m3fn)
     x = moe.Fp8Rows(wide[:, 128:288], torch.rand(rows, 6, generator=g, device="cuda")[:, 1:5:3])
     codes, scales = make_weight(g, n, k)
@@ -384,6 +388,17 @@ def test_grouped_product(moe, counts, n, k, dtype):
     for i, (a, b) in enumerate(zip(edges, edges[1:])):
         if b > a:
             check_product(out[a:b], moe.Fp8Rows(x.codes[a:b], x.scales[a:b]), codes[i], scales[i])
+
+
+@pytest.mark.parametrize("rows", [20, 1000])
+def test_grouped_product_of_no_rows(moe, rows):
+    g = gen(14)
+    x = make_rows(moe, g, rows, 128)
+    linear = moe.Fp8Linear(*make_weight(g, 3, 128, 128))
+    for at in (0, 7, rows):
+        out = torch.full((rows, 128), 7.0, device="cuda")
+        linear(x, offsets=torch.full((4,), at, dtype=torch.int32, device="cuda"), out=out)
+        assert (out == 7).all() and linear.status() == 0
 
 
 def test_grouped_product_bad_offsets(moe):
@@ -494,6 +509,11 @@ def test_logprobs_masks_ties_and_bad_tokens(moe):
     zero[:, 1::2] = -0.0
     got = moe.token_logprobs(zero, tokens[:2], top=32)
     assert got.top_ids.tolist() == [list(range(32))] * 2
+    big = torch.full((1, 300), 1e38, device="cuda")  # finite, but not times the scale
+    got = moe.token_logprobs(big, tokens[:1], top=2, scale=5.0)
+    assert math.isnan(got.lse[0]) and math.isnan(got.entropy[0]) and torch.isnan(got.logprobs).all() and got.top_ids.tolist() == [[0, 1]]
+    got = moe.token_logprobs(-big, tokens[:1], top=2, scale=5.0)
+    assert got.lse[0] == -inf and got.entropy[0] == 0 and (got.logprobs == -inf).all()
     few = torch.full((1, 5000), -inf, device="cuda")
     few[0, [4000, 17, 2500]] = torch.tensor([1.0, 1.0, 2.0], device="cuda")
     got = moe.token_logprobs(few, tokens[:1], top=6)
