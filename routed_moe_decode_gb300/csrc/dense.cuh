@@ -49,7 +49,7 @@ struct QuantArgs {
   float* scales;
   int64_t x_stride, code_stride, scale_row, scale_block;
   FastDiv nblocks;  // blocks of a row
-  uint32_t blocks;  // of all rows
+  uint32_t rows, rows_step;
   int d, dtype;
   bool gated, vec, vec_codes;
 };

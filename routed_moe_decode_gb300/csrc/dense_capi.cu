@@ -185,7 +185,7 @@ int moe_quantize_rows(int rows, int d, int gated, int dtype, const void* x, int6
   a.x = x; a.codes = codes; a.scales = scales; a.x_stride = x_stride; a.code_stride = code_stride;
   a.scale_row = scale_row; a.scale_block = scale_block;
   a.nblocks = moe::dense::fast_div(static_cast<uint32_t>(blocks(d)));
-  a.blocks = static_cast<uint32_t>(all); a.d = d; a.dtype = dtype; a.gated = gated != 0;
+  a.rows = static_cast<uint32_t>(rows); a.d = d; a.dtype = dtype; a.gated = gated != 0;
   a.vec = d % 8 == 0 && rows_vec(x, x_stride, 0, size);
   a.vec_codes = aligned(codes, 8) && code_stride % 8 == 0;
   return done("quantize launch", moe::dense::launch_quantize(a, sms, stream));

@@ -7,6 +7,7 @@
 // the launch and one trip to memory.  A thread has 8 consecutive values (16 bytes of a 16-bit type), so 16 neighbouring
 // lanes have a block, whose maximum takes four shuffles.
 #include <algorithm>
+
 #include "dense.cuh"
 
 namespace moe {
@@ -162,6 +163,8 @@ __device__ __forceinline__ float most_of(float a, float b, float c) {
 }
 
 // Codes of a thread's 8 values; 16 neighbouring lanes have a block.  All lanes of the warp take part.
+// MINUS: of the values' negatives.
+template <bool MINUS = false>
 __device__ __forceinline__ uint2 quantize8(float (&v)[8], float* scale) {
   float most = most_of(most_of(v[0], v[1], v[2]), most_of(v[3], v[4], v[5]), most_of(v[6], v[7], v[7]));
 #pragma unroll
@@ -188,7 +191,7 @@ __device__ __forceinline__ uint2 quantize8(float (&v)[8], float* scale) {
     *scale = s;
   }
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(MINUS ? -s : s));
   const float down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
   uint32_t less[2], more[2];
 #pragma unroll
@@ -399,31 +402,30 @@ cudaError_t norm_of(const NormArgs& a, cudaStream_t stream) {
   return run_norm_long<T, 256, true>(a, stream);
 }
 
-// g / (1 + exp(-g)) * u, with exp(-|g|) (0 below 2^-126) so that nothing overflows: g or g exp(-|g|) over 1 + exp(-|g|).  The
-// exponential's argument is a product and its rounding error (Dekker's exact product, by a fused multiply-add), the quotient
-// a product corrected once by its residual (Markstein): errors of a unit or two, as with expf and a rounded division,
-// which took a gated chunk 47 us instead of the 33 of this.
+// -g / (1 + exp(-g)) * u (its sign is turned when it is quantised), with e = exp(-|g|) (0 below 2^-126) so that nothing
+// overflows: the larger of g and g e, over 1 + e.  The exponential's argument is a product and its rounding error (Dekker's
+// exact product, by a fused multiply-add), the quotient a product corrected once by its residual (Markstein): errors
+// of a unit or two, as with expf and a rounded division, which took a gated chunk 47 us.
 __device__ __forceinline__ float2 gated_pair(float2 g, float2 u) {
   constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925962991e-08f, kLn2 = 0.693147180559945f;  // log2(e) = kHi + kLo
-  const float2 hi = make_float2(kHi, kHi), minus = make_float2(-1.f, -1.f), one = make_float2(1.f, 1.f);
+  const float2 one = make_float2(1.f, 1.f);
   const float2 a = make_float2(fmaxf(-fabsf(g.x), -200.f), fmaxf(-fabsf(g.y), -200.f));  // below: 0 all the same
-  const float2 t = mul2(a, hi);
-  const float2 low = fma2(a, make_float2(kLo, kLo), fma2(a, hi, mul2(t, minus)));
+  const float2 minus_t = mul2(a, make_float2(-kHi, -kHi));
+  const float2 low = fma2(a, make_float2(kLo, kLo), fma2(a, make_float2(kHi, kHi), minus_t));
   float2 e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(-minus_t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(-minus_t.y));
   e = fma2(e, mul2(low, make_float2(kLn2, kLn2)), e);
   const float2 den = add2(one, e), less = mul2(g, e);
-  const float2 num = make_float2(g.x < 0.f ? less.x : g.x, g.y < 0.f ? less.y : g.y);
+  const float2 num = make_float2(fmaxf(g.x, less.x), fmaxf(g.y, less.y));
   float both;  // one reciprocal for two: both denominators are within [1, 2]
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(both) : "f"(den.x * den.y));
-  const float2 r = mul2(make_float2(both, both), make_float2(den.y, den.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(both) : "f"(-(den.x * den.y)));
+  const float2 r = mul2(make_float2(both, both), make_float2(den.y, den.x));  // -1 / den
   const float2 q = mul2(num, r);
-  return mul2(fma2(fma2(mul2(q, minus), den, num), r, q), u);
+  return mul2(fma2(fma2(q, den, num), r, q), u);
 }
 
-// A group of 16 lanes takes a block, then the block as many further as there are groups; the next one's loads are under
-// way meanwhile.
+// A group of 16 lanes has one block of the rows, every a.rows_step-th of them; the next row's loads are under way meanwhile.
 constexpr int kQuantCtas = 6;  // of an SM
 
 template <typename T, bool GATED, bool VEC>
@@ -431,30 +433,33 @@ __global__ void __launch_bounds__(256, kQuantCtas) quantize_kernel(const QuantAr
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 15;
+  const uint32_t group = blockIdx.x * 16 + threadIdx.x / 16, row0 = div(a.nblocks, group), b = group - row0 * a.nblocks.d;
+  const bool mine = row0 < a.rows_step;  // the last groups may have no row
+  uint32_t left = mine && row0 < a.rows ? (a.rows - row0 + a.rows_step - 1) / a.rows_step : 0;
+  // a warp's two groups go on together: they share the shuffles
+  uint32_t turns = max(left, __shfl_xor_sync(kAll, left, 16));
+  const int c = static_cast<int>(b) * kBlock + 8 * lane;
+  const T* x = static_cast<const T*>(a.x) + row0 * a.x_stride;
+  uint8_t* codes = a.codes + row0 * a.code_stride;
+  float* scales = a.scales + row0 * a.scale_row + b * a.scale_block;
+  const int64_t x_step = a.rows_step * a.x_stride, code_step = a.rows_step * a.code_stride, scale_step = a.rows_step * a.scale_row;
   Raw8<T, VEC> next, next_up;
-  uint32_t row = 0, b = 0;
-  auto load = [&](uint32_t block) {
-    block = min(block, a.blocks - 1);
-    row = div(a.nblocks, block);
-    b = block - row * a.nblocks.d;
-    const int c = static_cast<int>(b) * kBlock + 8 * lane;
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    next.load(x, c, a.d);
-    if constexpr (GATED) next_up.load(x + a.d, c, a.d);
+  auto load = [&] {
+    const int d = left ? a.d : 0;
+    next.load(x, c, d);
+    if constexpr (GATED) next_up.load(x + a.d, c, d);
+    x += x_step;
   };
-  const uint32_t step = gridDim.x * 16;
-  // a warp's two groups stay together: they share the shuffles
-  const uint32_t begin = blockIdx.x * 16 + threadIdx.x / 16, warp_begin = begin & ~1u;
-  load(begin);
-  for (uint32_t at = 0; warp_begin + at < a.blocks; at += step) {
-    const uint32_t block = begin + at, r = row, k = b;
-    const int c = static_cast<int>(k) * kBlock + 8 * lane;
+  load();
+  for (; turns; --turns) {
     float v[8];
     next.get(v);
+    const bool live = left != 0;
+    if (live) --left;
     if constexpr (GATED) {
       float u[8];
       next_up.get(u);
-      if (warp_begin + at + step < a.blocks) load(block + step);
+      load();
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const float2 p = gated_pair(make_float2(v[i], v[i + 1]), make_float2(u[i], u[i + 1]));
@@ -462,20 +467,25 @@ __global__ void __launch_bounds__(256, kQuantCtas) quantize_kernel(const QuantAr
         v[i + 1] = p.y;
       }
     } else {
-      if (warp_begin + at + step < a.blocks) load(block + step);
+      load();
     }
     float scale;
-    const uint2 codes = quantize8(v, &scale);
-    if (block >= a.blocks) continue;
-    if (c < a.d) store_codes(a.codes + r * a.code_stride, c, a.d, codes, a.vec_codes);
-    if (lane == 0) a.scales[r * a.scale_row + k * a.scale_block] = scale;
+    const uint2 eight = quantize8<GATED>(v, &scale);
+    if (live) {
+      if (c < a.d) store_codes(codes, c, a.d, eight, a.vec_codes);
+      if (lane == 0) *scales = scale;
+      codes += code_step;
+      scales += scale_step;
+    }
   }
 }
 
 template <typename T>
-cudaError_t quantize_of(const QuantArgs& a, int sms, cudaStream_t stream) {
-  const uint32_t most = static_cast<uint32_t>(sms) * kQuantCtas;
-  const dim3 grid(std::min((a.blocks + 15) / 16, most)), block(256);
+cudaError_t quantize_of(QuantArgs a, int sms, cudaStream_t stream) {
+  // a multiple of a row's blocks, as far as there are rows for them
+  const uint32_t nb = a.nblocks.d, groups = std::max(nb, static_cast<uint32_t>(sms) * kQuantCtas * 16);
+  a.rows_step = std::min(groups / nb, a.rows);
+  const dim3 grid((a.rows_step * nb + 15) / 16), block(256);
   if (a.gated)
     return a.vec ? launch_ready<quantize_kernel<T, true, true>>(grid, block, 0, stream, a)
                  : launch_ready<quantize_kernel<T, true, false>>(grid, block, 0, stream, a);
