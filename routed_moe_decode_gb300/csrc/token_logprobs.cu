@@ -6,14 +6,22 @@
 //
 // Alternatives are keys: the logit's order-preserving bits above the complement of its id, so that equal logits are in
 // the order of their ids and no two keys are equal.  The pass keeps only the largest logit of every thread's step (or of a
-// few), which the sums need anyway, in shared memory.  At its end each warp shows its threads' four largest logits; the
-// top-th of these 32 is a threshold that at least `top` logits reach.  Only the steps whose largest reaches it, about `top`
-// of them, are read again, and what reaches it there is put into lists that the warps keep sorted over their lanes.  (With lists
-// kept during the pass, 20 alternatives cost 53 us beside 96 without any for 2048 rows of 131072, and 13 beside 11 for 127 of 100003.)
-// Where very many reach the threshold (nothing but masks, equal logits) the row is read again as a whole.
+// few), which the sums need anyway, in shared memory.  At its end the largest logits of groups of threads, as many groups as
+// alternatives or more, give a threshold that at least `top` logits reach: the smallest of eight warps', or the top-th of 32
+// groups of eight threads.  Only the steps whose largest reaches it are read again, and what reaches it there, some 20
+// logits, is sorted by counting.  (With lists kept during the pass, 20 alternatives cost 53 us beside 96 without any for 2048 rows of
+// 131072.)  Where very many reach the threshold (nothing but masks, equal logits) each warp keeps a list sorted over its
+// lanes, and the row is read again as a whole if need be.
 //
 // A row is one CTA's, or a cluster's of up to eight where there are few rows; the parts join through distributed shared
 // memory in a fixed order.
+//
+// Measured: 2048 rows of 131072 BF16 logits with 5 alternatives 96 us (5.6 TB/s), without any 96; the same in FP32 183 and 165
+// (6.5 TB/s); 127 rows of 100003 in FP32 with 20 alternatives 17.5 us, without 9.6; 4 rows of 131072 with 8, 7.9, without 3.9.
+// The end of a row is a chain of trips through shared memory and back to the logits, 3 to 4 us that other CTAs hide where
+// there are more rows than CTAs fit.  The pass is close to the limit of its registers (64 of a thread; see kCtas): how the
+// second reading is written moved 2048 rows from 96 to 113 us by what it left for the pass.
+#include <algorithm>
 #include <cfloat>
 #include <type_traits>
 
@@ -24,7 +32,7 @@ namespace dense {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kVecs = 4;  // 16-byte vectors of a thread's step
-constexpr int kShown = 32 / kWarps;
+constexpr int kParts = 8;  // of a row, at most
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 typedef unsigned long long Key;
@@ -47,23 +55,12 @@ __device__ __forceinline__ Key shfl_xor(Key k, int o) { return __shfl_xor_sync(k
 struct Sums {
   float m, s, u;
 };
-__device__ __forceinline__ Sums join(Sums a, Sums b) {
-  if (b.m > a.m) { const Sums t = a; a = b; b = t; }
-  const float d = fmaxf(b.m - a.m, -1e30f), f = exp2_of(d * kLog2e);
-  if (b.s != 0.f && f != 0.f) {
-    a.u += (b.u + b.s * d) * f;
-    a.s += b.s * f;
-  } else if (b.s != b.s) {
-    a.s = b.s;
-  }
-  return a;
-}
 
 // Sorted descending over the lanes: the 32 best of two such lists.
 __device__ __forceinline__ Key merge(Key a, Key b, int lane) {
   const Key other = __shfl_sync(kAll, b, 31 - lane);
   Key k = a > other ? a : other;
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
     const Key p = shfl_xor(k, o);
     k = ((lane & o) == 0) == (k > p) ? k : p;
@@ -82,6 +79,11 @@ template <>
 struct Vec<float> {
   static constexpr int N = 4;
   static constexpr uint32_t kLowest = 0xff800000u;
+  static __device__ __forceinline__ float first(uint4& r) {  // and the others move up
+    const float v = __uint_as_float(r.x);
+    r = make_uint4(r.y, r.z, r.w, 0);
+    return v;
+  }
   static __device__ __forceinline__ void get(uint4 r, float2* v) {
     v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
     v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
@@ -109,6 +111,11 @@ template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
   static constexpr uint32_t kLowest = 0xff80ff80u;
+  static __device__ __forceinline__ float first(uint4& r) {
+    const float v = __uint_as_float(r.x << 16);
+    r = make_uint4(__funnelshift_r(r.x, r.y, 16), __funnelshift_r(r.y, r.z, 16), __funnelshift_r(r.z, r.w, 16), r.w >> 16);
+    return v;
+  }
   static __device__ __forceinline__ void get(uint4 r, float2* v) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -123,6 +130,11 @@ template <>
 struct Vec<__half> {
   static constexpr int N = 8;
   static constexpr uint32_t kLowest = 0xfc00fc00u;
+  static __device__ __forceinline__ float first(uint4& r) {
+    const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(r.x & 0xffffu)));
+    r = make_uint4(__funnelshift_r(r.x, r.y, 16), __funnelshift_r(r.y, r.z, 16), __funnelshift_r(r.z, r.w, 16), r.w >> 16);
+    return v;
+  }
   static __device__ __forceinline__ void get(uint4 r, float2* v) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -135,20 +147,25 @@ struct Vec<__half> {
 };
 
 constexpr int kGroups = 8, kPairs = 1024;  // steps, or groups of them, whose largest logits are kept; of those read again
+constexpr int kFound = 256;                // logits that reach the threshold, sorted by one warp
 
 struct Sorted {
   float largest[kGroups][kThreads];
   uint16_t pairs[kPairs];  // thread, group << 8
-  int npairs;
-  Key lists[kWarps][32];
-  uint32_t shown[kWarps * kShown];  // logits of each warp, as float_key has them
-  Key part_list[32];                // a cluster's parts read this
+  int npairs[2], nfound[2];  // of even and odd rows
+  union {
+    Key found[kFound + 4];
+    Key lists[kWarps][32];  // where more than that reach it
+  };
+  Key result[32];
+  Key incoming[kParts][32];               // the best of a cluster's parts
+  alignas(16) uint32_t shown[32];         // the largest logit of eight threads, as float_key has it
 };
 struct None {};
 template <bool TOP>
 struct Shared : std::conditional_t<TOP, Sorted, None> {
-  Sums sums[kWarps];
-  Sums part_sums;  // a cluster's parts read this
+  Sums sums[2][kWarps];  // of even and odd rows: the first warp may still read one row's when another has the next's
+  Sums whole, incoming_sums[kParts];
 };
 
 __device__ __forceinline__ float value_of(uint32_t key) { return logit_of(static_cast<Key>(key) << 32); }
@@ -158,9 +175,9 @@ __device__ __noinline__ Key insert(Key list, Key k, int top, int lane) {
   k = k > __shfl_sync(kAll, list, top - 1) ? k : 0;
   uint32_t want = __ballot_sync(kAll, k != 0);
   if (__popc(want) > 6) {  // as costly as a sort: bitonic, descending over the lanes
-#pragma unroll
+#pragma unroll 1
     for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
+#pragma unroll 1
       for (int o = size >> 1; o > 0; o >>= 1) {
         const Key p = shfl_xor(k, o);
         const bool larger = ((lane & o) == 0) == ((lane & size) == 0);
@@ -178,39 +195,40 @@ __device__ __noinline__ Key insert(Key list, Key k, int top, int lane) {
   return list;
 }
 
-// The top-th largest of the lanes' keys.
-__device__ __forceinline__ uint32_t nth(uint32_t k, int top, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int o = size >> 1; o > 0; o >>= 1) {
-      const uint32_t p = __shfl_xor_sync(kAll, k, o);
-      k = ((lane & o) == 0) == ((lane & size) == 0) ? max(k, p) : min(k, p);
-    }
-  return __shfl_sync(kAll, k, top - 1);
+// The top-th largest of 32 keys.
+__device__ __forceinline__ uint32_t nth(const uint32_t (&keys)[32], int top, int lane) {
+  const uint32_t k = keys[lane];
+  int before = 0;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) before += keys[i] > k - (i < lane);  // no key is 0
+  return __shfl_sync(kAll, k, __ffs(__ballot_sync(kAll, before == top - 1)) - 1);
 }
 
 // The warp's lists into the first warp's.
-template <bool TOP>
-__device__ __forceinline__ Key best_of_warps(Shared<TOP>& sh, Key list, int warp, int lane) {
-  if constexpr (TOP) {
-    for (int n = kWarps / 2; n > 0; n >>= 1) {
-      if (warp >= n && warp < 2 * n) sh.lists[warp][lane] = list;
-      __syncthreads();
-      if (warp < n) list = merge(list, sh.lists[warp + n][lane], lane);
-    }
-  } else {
+__device__ __forceinline__ Key best_of_warps(Sorted& sh, Key list, int warp, int lane) {
+  for (int n = kWarps / 2; n > 0; n >>= 1) {
+    if (warp >= n && warp < 2 * n) sh.lists[warp][lane] = list;
     __syncthreads();
+    if (warp < n) list = merge(list, sh.lists[warp + n][lane], lane);
   }
   return list;
 }
-// With the sums of the lane `o` away, in the same order on both sides.
-__device__ __forceinline__ Sums joined(Sums a, int o, int lane) {
-  const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.s, o), __shfl_xor_sync(kAll, a.u, o)};
-  return (lane & o) ? join(b, a) : join(a, b);
+// The lanes' sums, in an order that does not change: all have the result.
+__device__ __noinline__ Sums joined(Sums a) {
+  const float m = value_of(__reduce_max_sync(kAll, float_key(a.m)));
+  const float d = fmaxf(a.m - m, -1e30f), f = exp2_of(d * kLog2e);
+  a.u = a.s != 0.f && f != 0.f ? (a.u + a.s * d) * f : 0.f;
+  a.s = f != 0.f || a.s != a.s ? a.s * f : 0.f;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(kAll, a.s, o);
+    a.u += __shfl_xor_sync(kAll, a.u, o);
+  }
+  a.m = m;
+  return a;
 }
 
-constexpr int kCtas = 4;  // of an SM
+constexpr int kCtas = 4;  // of an SM: 3, with more registers, take 112 us for 2048 rows of 131072 with 5 alternatives (104 at that time)
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a) {
@@ -218,28 +236,28 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
   constexpr int N = kVecs * V::N;
   __shared__ Shared<TOP> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int parts = static_cast<int>(cluster_size()), part = static_cast<int>(cluster_rank());
+  const int parts = static_cast<int>(cluster_size()), log_parts = 31 - __clz(parts), part = static_cast<int>(cluster_rank());
   if constexpr (TOP) {
-    if (tid == 0) sh.npairs = 0;
+    if (tid < 2) sh.npairs[tid] = sh.nfound[tid] = 0;
   }
+  if (parts > 1) cluster_arrive();
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row = blockIdx.x / parts;
-  const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-  // elements before the first 16-byte boundary, whole vectors, the rest
-  const int head = min(a.vocab, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
-  const int vecs = (a.vocab - head) / V::N, rest = a.vocab - head - vecs * V::N;
-  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-  const int v0 = static_cast<int>(static_cast<int64_t>(vecs) * part / parts);
-  const int v1 = static_cast<int>(static_cast<int64_t>(vecs) * (part + 1) / parts);
-
-  Sums mine{-FLT_MAX, 0.f, 0.f};
-  Key list = 0;
-  float best = -INFINITY, group_best = -INFINITY;  // of this thread; of its steps in the group at hand
-  // steps, in groups of 2^shift
-  const int steps = (v1 - v0 + kVecs * kThreads - 1) / (kVecs * kThreads);
-  int shift = 0;
-  while (((steps - 1) >> shift) >= kGroups) ++shift;
+  // of the row at hand: elements before the first 16-byte boundary, whole vectors (this part's from v0 to v1), the rest
+  const T* x;
+  const uint4* xv;
+  int head, rest, v0, v1;
+  auto go_to = [&](uint32_t row) {
+    x = static_cast<const T*>(a.logits) + row * a.row_stride;
+    head = min(a.vocab, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
+    const int vecs = (a.vocab - head) / V::N;
+    rest = a.vocab - head - vecs * V::N;
+    xv = reinterpret_cast<const uint4*>(x + head);
+    v0 = static_cast<int>(static_cast<uint32_t>(vecs) * part >> log_parts);  // below 2^29 * 8
+    v1 = static_cast<int>(static_cast<uint32_t>(vecs) * (part + 1u) >> log_parts);
+  };
+  const Sums kNoSums{-FLT_MAX, 0.f, 0.f};
+  Sums mine;
   const float2 scale = make_float2(a.scale, a.scale), log2e = make_float2(kLog2e, kLog2e);
 
   auto load = [&](uint4 (&raw)[kVecs], int at) {
@@ -272,135 +290,222 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
   };
 
   uint4 raw[kVecs];
-  if (v0 < v1) load(raw, v0);
-  for (int at = v0; at < v1; at += kVecs * kThreads) {
-    uint4 next[kVecs];
-    const bool more = at + kVecs * kThreads < v1;
-    if (more) load(next, at + kVecs * kThreads);
-    float2 v[N / 2];
+  const uint32_t rows = a.rows, row_step = gridDim.x >> log_parts;
+  uint32_t row = blockIdx.x >> log_parts;
+  int buffer = 0;
+  go_to(row);
+  load(raw, v0);
+  for (;; buffer ^= 1) {
+    mine = kNoSums;
+    Key list = 0;
+    float best = -INFINITY, group_best = -INFINITY;  // of this thread; of its steps in the group at hand
+    // steps, in groups of 2^shift
+    const int steps = (v1 - v0 + kVecs * kThreads - 1) / (kVecs * kThreads);
+    int shift = 0;
+    while (((steps - 1) >> shift) >= kGroups) ++shift;
+    const bool finishes = part == 0 && warp == 0;
+    int token = -1;
+    if (finishes && a.logprobs && lane < a.n_tokens) token = a.tokens[row * a.token_stride + lane];
+    for (int at = v0; at < v1; at += kVecs * kThreads) {
+      uint4 next[kVecs];
+      const bool more = at + kVecs * kThreads < v1;
+      if (more) load(next, at + kVecs * kThreads);
+      float2 v[N / 2];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) V::get(raw[j], v + j * (V::N / 2));
-    const float most = V::most(raw, v);
-    add(v, most);
-    if constexpr (TOP) {
-      group_best = fmaxf(group_best, most);
-      const int step = (at - v0) / (kVecs * kThreads);
-      if (!more || ((step + 1) & ((1 << shift) - 1)) == 0) {
-        sh.largest[step >> shift][tid] = group_best;
-        best = fmaxf(best, group_best);
-        group_best = -INFINITY;
+      for (int j = 0; j < kVecs; ++j) V::get(raw[j], v + j * (V::N / 2));
+      const float most = V::most(raw, v);
+      add(v, most);
+      if constexpr (TOP) {
+        group_best = fmaxf(group_best, most);
+        const int step = (at - v0) / (kVecs * kThreads);
+        if (!more || ((step + 1) & ((1 << shift) - 1)) == 0) {
+          sh.largest[step >> shift][tid] = group_best;
+          best = fmaxf(best, group_best);
+          group_best = -INFINITY;
+        }
+      }
+      if (more) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) raw[j] = next[j];
       }
     }
-    if (more) {
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) raw[j] = next[j];
-    }
-  }
-  if (part == 0 && head + rest > 0 && warp == 0) {  // at most 14 elements
+    const float token_logit = token >= 0 && token < a.vocab ? to_float(x[token]) : -INFINITY;
+    // elements that are in no vector, 14 at most
+    const bool there = finishes && lane < head + rest;
     const int id = lane < head ? lane : a.vocab - rest + lane - head;
-    const bool there = lane < head + rest;
-    float2 v[N / 2];
+    const float single = there ? to_float(x[id]) : -INFINITY;
+    if (finishes && head + rest > 0) {
+      float2 v[N / 2];
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) v[i] = make_float2(-INFINITY, -INFINITY);
-    if (there) v[0].x = to_float(x[id]);
-    add(v, v[0].x);
-    if constexpr (TOP) list = insert(list, there ? key_of(v[0].x, id) : 0, a.top, lane);
-  }
+      for (int i = 0; i < N / 2; ++i) v[i] = make_float2(-INFINITY, -INFINITY);
+      v[0].x = single;
+      add(v, single);
+    }
+    // what the end of the row needs, before the next row's loads
+    const T* const row_x = x;
+    const uint4* const row_xv = xv;
+    const int row_head = head, row_v0 = v0, row_v1 = v1;
+    const uint32_t next_row = row + row_step;
+    if (next_row < rows) {
+      go_to(next_row);
+      load(raw, v0);
+    }
 
-  if constexpr (TOP) {
-    uint32_t k = float_key(best);
+    mine = joined(mine);
+    if (lane == 0) sh.sums[buffer][warp] = mine;
+    if constexpr (TOP) {
+    float most = best;
 #pragma unroll
-    for (int p = 0; p < kShown; ++p) {
-      const uint32_t w = __reduce_max_sync(kAll, k);
-      if (lane == p) sh.shown[warp * kShown + p] = w;
-      if (lane == __ffs(__ballot_sync(kAll, k == w)) - 1) k = 0;
-    }
-    __syncthreads();
-    const float bar = value_of(nth(sh.shown[lane], a.top, lane));
-    // a NaN ranks as -infinity: a group of nothing else has that as its largest
-    for (int g = 0; g <= (steps - 1) >> shift && steps; ++g) {
-      if (!(sh.largest[g][tid] < bar)) {
-        const int at = atomicAdd(&sh.npairs, 1);
-        if (at < kPairs) sh.pairs[at] = static_cast<uint16_t>(tid | g << 8);
-      }
-    }
-    __syncthreads();
-    // vector i, or none: its values into the list
-    auto look = [&](int i, bool there) {
-      const uint4 r = there ? __ldcg(xv + i) : make_uint4(0, 0, 0, 0);
-      float2 v[V::N / 2];
-      V::get(r, v);
+      for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+      if (a.top > kWarps) {
+        if ((lane & 7) == 0) sh.shown[tid >> 3] = float_key(most);
+      } else {
 #pragma unroll
-      for (int e = 0; e < V::N; ++e) {
-        const float l = e & 1 ? v[e / 2].y : v[e / 2].x;
-        const bool good = there && !(l < bar);
-        if (__any_sync(kAll, good)) list = insert(list, good ? key_of(l, head + i * V::N + e) : 0, a.top, lane);
+        for (int o = 8; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+        if (lane == 0) sh.shown[warp] = float_key(most);
       }
-    };
-    const int pairs = sh.npairs;
-    if (pairs <= kPairs) {
-      const int per = kVecs << shift, log = 31 - __clz(per);
-      for (int n0 = warp * 32; n0 < pairs << log; n0 += kThreads) {
-        const int n = n0 + lane, pair = n < pairs << log ? sh.pairs[n >> log] : 0, sub = n & (per - 1);
-        const int step = ((pair >> 8) << shift) + sub / kVecs;
-        const int i = v0 + (step * kVecs + sub % kVecs) * kThreads + (pair & 255);
-        look(i, n < pairs << log && i < v1);
+      __syncthreads();
+      if (warp == kWarps - 1) {
+        const Sums all = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums);
+        if (lane == 0) sh.whole = all;
+      }
+      uint32_t bar_key;
+      if (a.top > kWarps) {
+        bar_key = nth(sh.shown, a.top, lane);
+      } else {
+        bar_key = sh.shown[0];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) bar_key = min(bar_key, sh.shown[i]);
+      }
+      const float bar = value_of(bar_key);
+      // a NaN ranks as -infinity: a group of nothing else has that as its largest
+      uint32_t reach = 0;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) reach |= (sh.largest[g][tid] < bar ? 0u : 1u) << g;
+      reach &= (1u << ((steps + (1 << shift) - 1) >> shift)) - 1;
+      for (; reach; reach &= reach - 1) {
+        const int at = atomicAdd(&sh.npairs[buffer], 1);
+        if (at < kPairs) sh.pairs[at] = static_cast<uint16_t>(tid | (__ffs(reach) - 1) << 8);
+      }
+      __syncthreads();
+      if (warp == 0) sh.result[lane] = 0;
+      const int pairs = sh.npairs[buffer];
+      if (tid == 0) sh.npairs[buffer ^ 1] = sh.nfound[buffer ^ 1] = 0;
+      // the values of vector i, or of none
+      auto look = [&](int i, bool there, auto&& take) {
+        uint4 r = there ? __ldcg(row_xv + i) : make_uint4(0, 0, 0, 0);
+        const int id = row_head + i * V::N;
+#pragma unroll 1
+        for (int e = 0; e < V::N; ++e) {
+          const float l = V::first(r);
+          const bool good = there && !(l < bar);
+          if (__any_sync(kAll, good)) take(l, id + e, good);
+        }
+      };
+      auto look_at_pairs = [&](auto&& take) {
+        const int per = kVecs << shift, log = 31 - __clz(per);
+        for (int n0 = warp * 32; n0 < pairs << log; n0 += kThreads) {
+          const int n = n0 + lane, pair = n < pairs << log ? sh.pairs[n >> log] : 0, sub = n & (per - 1);
+          const int step = ((pair >> 8) << shift) + sub / kVecs;
+          const int i = row_v0 + (step * kVecs + sub % kVecs) * kThreads + (pair & 255);
+          look(i, n < pairs << log && i < row_v1, take);
+        }
+      };
+      auto find = [&](float l, int id, bool good) {
+        if (!good) return;
+        const int at = atomicAdd(&sh.nfound[buffer], 1);
+        if (at < kFound) sh.found[at] = key_of(l, id);
+      };
+      if (pairs <= kPairs) {
+        look_at_pairs(find);
+        find(single, id, there && !(single < bar));
+      } else if (tid == 0) {
+        sh.nfound[buffer] = kFound + 1;
+      }
+      __syncthreads();
+      const int found = sh.nfound[buffer];
+      if (found <= kFound) {
+        if (warp <= (found - 1) >> 5) {
+          if (lane < 4) sh.found[found + lane] = 0;  // each warp for itself
+          __syncwarp();
+        }
+        if (tid < found) {  // a key's place is the number of larger ones
+          const Key k = sh.found[tid];
+          int at = 0;
+#pragma unroll 1
+          for (int i = 0; i < found; i += 4)
+            at += (sh.found[i] > k) + (sh.found[i + 1] > k) + (sh.found[i + 2] > k) + (sh.found[i + 3] > k);
+          if (at < 32) sh.result[at] = k;
+        }
+        __syncthreads();
+        if (warp == 0) list = sh.result[lane];
+      } else {
+        auto keep = [&](float l, int id, bool good) {
+          list = insert(list, good ? key_of(l, id) : 0, a.top, lane);
+        };
+        if (warp == 0) keep(single, id, there);
+        if (pairs <= kPairs) look_at_pairs(keep);
+        else
+          for (int i0 = row_v0 + warp * 32; i0 < row_v1; i0 += kThreads) look(i0 + lane, i0 + lane < row_v1, keep);
+        list = best_of_warps(sh, list, warp, lane);
       }
     } else {
-      for (int i0 = v0 + warp * 32; i0 < v1; i0 += kThreads) look(i0 + lane, i0 + lane < v1);
+      __syncthreads();
     }
-  }
-
-  // the CTA's sums and lists
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine = joined(mine, o, lane);
-  if (lane == 0) sh.sums[warp] = mine;
-  list = best_of_warps<TOP>(sh, list, warp, lane);
-  if (warp == 0) {
-    mine = sh.sums[lane & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) mine = joined(mine, o, lane);
-  }
-  if (parts > 1) {
     if (warp == 0) {
-      if constexpr (TOP) sh.part_list[lane] = list;
-      if (lane == 0) sh.part_sums = mine;
+      if constexpr (TOP) mine = sh.whole;
+      else mine = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums);
     }
-    __syncwarp();
-    cluster_sync();
-    if (part == 0) {  // a warp has a part's list, a lane a part's sums
-      if constexpr (TOP) {
-        list = warp < parts ? ld_cluster_u64(mapa(smem_addr(&sh.part_list[lane]), warp)) : 0;
-        list = best_of_warps<TOP>(sh, list, warp, lane);
-      }
+    if (parts > 1) {  // of one row: see the launch
+      cluster_wait();  // all of them have started
       if (warp == 0) {
-        const uint32_t at = mapa(smem_addr(&sh.part_sums), lane & (parts - 1));
-        mine = Sums{ld_cluster(at), ld_cluster(at + 4), ld_cluster(at + 8)};
-        for (int o = parts / 2; o > 0; o >>= 1) mine = joined(mine, o, lane);
+        if constexpr (TOP) {
+          st_cluster(mapa(smem_addr(&sh.incoming[part][lane]), 0), list);
+        }
+        if (lane == 0) {
+          const uint32_t to = mapa(smem_addr(&sh.incoming_sums[part]), 0);
+          st_cluster(to, mine.m);
+          st_cluster(to + 4, mine.s);
+          st_cluster(to + 8, mine.u);
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+      if (part != 0) return;
+      if (warp == (TOP ? kWarps - 1 : 0)) {
+        mine = joined(lane < parts ? sh.incoming_sums[lane] : kNoSums);
+        if (lane == 0) sh.whole = mine;
+      }
+      if constexpr (TOP) {
+        list = best_of_warps(sh, warp < parts ? sh.incoming[warp][lane] : 0, warp, lane);
+        if (warp == 0) mine = sh.whole;
       }
     }
-    __syncwarp();
-    cluster_sync();
-  }
-  if (part != 0 || warp != 0) return;
-  if (!(mine.m < INFINITY)) mine.s = __int_as_float(0x7fc00000);  // scale * logit is +infinity, of a finite logit too
-  const bool none = mine.s == 0.f;
-  const float logs = logf(mine.s);
-  if (lane == 0) {
-    if (a.lse) a.lse[row] = none ? -INFINITY : mine.m + logs;
-    if (a.entropy) a.entropy[row] = none ? 0.f : logs - mine.u / mine.s;
-  }
-  auto logprob = [&](float l) { return none ? -INFINITY : fmaf(l, a.scale, -mine.m) - logs; };
-  if (a.logprobs) {
-    for (int j = lane; j < a.n_tokens; j += 32) {
-      const int t = a.tokens[row * a.token_stride + j];
-      a.logprobs[row * a.n_tokens + j] = logprob(t >= 0 && t < a.vocab ? to_float(x[t]) : -INFINITY);
+    if (finishes) {
+      if (!(mine.m < INFINITY)) mine.s = __int_as_float(0x7fc00000);  // scale * logit is +infinity, of a finite logit too
+      const bool none = mine.s == 0.f;
+      const float logs = logf(mine.s);
+      if (lane == 0) {
+        if (a.lse) a.lse[row] = none ? -INFINITY : mine.m + logs;
+        if (a.entropy) a.entropy[row] = none ? 0.f : logs - mine.u / mine.s;
+      }
+      auto logprob = [&](float l) { return none ? -INFINITY : fmaf(l, a.scale, -mine.m) - logs; };
+      if (a.logprobs) {
+        float* const to = a.logprobs + static_cast<int64_t>(row) * a.n_tokens;
+        if (lane < a.n_tokens) to[lane] = logprob(token_logit);
+        for (int j = lane + 32; j < a.n_tokens; j += 32) {
+          const int t = a.tokens[row * a.token_stride + j];
+          to[j] = logprob(t >= 0 && t < a.vocab ? to_float(row_x[t]) : -INFINITY);
+        }
+      }
+      if (TOP && lane < a.top) {
+        const int64_t at = static_cast<int64_t>(row) * a.top + lane;
+        if (a.top_ids) a.top_ids[at] = static_cast<int>(~static_cast<uint32_t>(list));
+        if (a.top_logprobs) a.top_logprobs[at] = logprob(logit_of(list));
+      }
     }
-  }
-  if (TOP && lane < a.top) {
-    const int id = static_cast<int>(~static_cast<uint32_t>(list));
-    if (a.top_ids) a.top_ids[row * a.top + lane] = id;
-    if (a.top_logprobs) a.top_logprobs[row * a.top + lane] = logprob(logit_of(list));
+    if (next_row >= rows) return;
+    row = next_row;
   }
 }
 
@@ -409,8 +514,13 @@ cudaError_t run(const LogprobArgs& a, int sms, cudaStream_t stream) {
   // parts of a row: while all CTAs are resident together, and a part is worth a CTA
   int parts = 1;
   const int64_t most = static_cast<int64_t>(kCtas) * sms;
-  while (parts < 8 && static_cast<int64_t>(a.rows) * parts * 2 <= most && a.vocab / (parts * 2) >= 2048) parts *= 2;
-  const dim3 grid(static_cast<unsigned>(a.rows) * parts), block(kThreads);
+  while (parts < kParts && static_cast<int64_t>(a.rows) * parts * 2 <= most && a.vocab / (parts * 2) >= 2048) parts *= 2;
+  // CTAs of short rows go on from row to row, with the next row's first loads under way at the end of one: 8192 rows of 8000
+  // BF16 logits take 42 us, with a CTA for each row 55.  Of rows of more steps the hardware's own order is better: 2048 of 131072
+  // 96 us, with CTAs that go on 102.
+  const bool keep = a.vocab <= 8 * kVecs * kThreads * Vec<T>::N;
+  const int64_t ctas = static_cast<int64_t>(a.rows) * parts;
+  const dim3 grid(static_cast<unsigned>(keep ? std::min(ctas, most) : ctas)), block(kThreads);
   return a.top > 0 ? launch_cluster<logprobs_kernel<T, true>>(parts, grid, block, 0, stream, a)
                    : launch_cluster<logprobs_kernel<T, false>>(parts, grid, block, 0, stream, a);
 }

@@ -483,6 +483,25 @@ def test_logprobs_of_a_large_vocabulary(moe, rows):
     check_logprobs(moe.TokenLogprobs(*(t[few] for t in got)), logits[few], tokens[few], 32, 1.0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_logprobs_of_many_short_rows(moe, dtype):
+    """A CTA takes several rows, of every alignment; among them rows of masks, equal logits and NaN."""
+    g = gen(79)
+    rows, vocab = 1900, 2503
+    logits = rand(g, rows, vocab + 3, dtype=dtype, scale=2.0)[:, 1:vocab + 1]
+    logits[3::11] = -math.inf
+    logits[5::13] = 0.25
+    logits[7::17, ::2] = -math.inf
+    logits[9::19, 100:700] = math.nan
+    tokens = torch.randint(0, vocab, (rows, 40), generator=g, device="cuda").to(torch.int32)
+    for top in (0, 3, 32):
+        got = moe.token_logprobs(logits, tokens, top=top)
+        check_logprobs(got, logits, tokens, top, 1.0)
+        again = moe.token_logprobs(logits, tokens, top=top)
+        for a, b in zip(got, again):
+            assert a is None and b is None or torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
 def test_logprobs_masks_ties_and_bad_tokens(moe):
     g = gen(77)
     inf = math.inf
