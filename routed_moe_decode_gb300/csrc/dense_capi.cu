@@ -79,7 +79,9 @@ bool apart(int64_t outer, int64_t outer_stride, int64_t inner, int64_t inner_str
 // takes a pair 0.375 and a CTA 0.28 + n / 800 for n rows of x.
 //   rows 256: 5120 x 2048 11.0 / 11.6, 2048 x 8192 29.5 / 14.9, 8192 x 8192 30.1 / 29.2, 16384 x 4096 18.5 / 31.9
 //   rows 512: 5120 x 2048 11.6 / 19.9, 2048 x 8192 29.7 / 22.8, 8192 x 8192 31.0 / 54.9
-// Groups: by their rows on average, as the numbers of each are on the device.
+// Groups: by their rows on average, as the numbers of each are on the device.  256 weights of 1024 x 2048 (us, pairs / the others):
+// 48 rows each 110.0 / 93.6, 64: 114.8 / 110.2, 96: 117.2 / 116.0, 128: 122.3 / 188.3, 256: 169.7 / 309.0.  Between 64 and 96 they are
+// alike; groups are never equal in practice, and those above 128 cost the others twice.
 bool wide(const MatmulArgs& a, int sms, int split) {
   if (a.offsets) return (a.rows + a.groups - 1) / a.groups > 64;
   if (a.rows <= moe::dense::kSomeRows) return false;

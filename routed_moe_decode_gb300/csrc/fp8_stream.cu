@@ -11,6 +11,11 @@
 // each), a warp copies tiles into a ring, a warp issues the MMAs, two warps bring a block's scales into shared memory.
 // CTAs take tiles statically, one after the other; the ring runs on across tiles.  Where one row of x tiles would leave
 // SMs idle, a cluster's CTAs take a part of k each and add up through distributed shared memory, in order.
+//
+// Measured: 16 rows x 131072 x 2048 into FP32 47 us (5.9 TB/s of what has to move, 0.87 of the measured copy); 256 weights of
+// 1024 x 2048 with 8 rows each 88 us (6.2 TB/s); 4 rows x 5120 x 2048 6.1 us, of which ~2 are the launch and the first trip to
+// memory and ~1.5 the parts' join.  What bounds the long ones is memory and the start: the tensor cores are 4 % busy, the issue
+// slots 26 %.  Scales come by asynchronous copies, far ahead: loaded into registers they held 256 weights at 113 us.
 #include "fp8_tiles.cuh"
 
 namespace moe {
@@ -326,7 +331,8 @@ cudaError_t run(const Maps& maps, const MatmulArgs& a, int split, int grid, cuda
   return launch_cluster<fp8_stream_kernel<NT>>(split, dim3(grid), dim3(kThreads), Shape<NT>::kTotal, stream, maps, a);
 }
 
-// Few rows: 32 at most in a tile (groups: 16 on average), else 128.
+// Few rows: 32 at most in a tile (groups: 16 on average), else 128.  256 weights of 1024 x 2048 (us, tiles of 32 / 128 rows): 16 rows
+// each 89.8 / 89.6, 32 (some above) 116.2 / 92.5; 16 weights of 4096 x 4096: 8 rows each 49.9 / 51.4, 32: 62.6 / 53.2.
 bool few_rows(const MatmulArgs& a) {
   return a.offsets ? (a.rows + a.groups - 1) / a.groups <= 16 : a.rows <= kFewRows;
 }

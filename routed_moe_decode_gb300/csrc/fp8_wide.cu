@@ -14,7 +14,9 @@
 //
 // What bounds it: a block takes ~750 cycles against 512 of the MMAs, the chain of a product's end, the 256 x 128
 // multiply-adds of an SM (256 cycles of its FP32 lanes, ~450 with the reads of tensor memory) and the barriers between.
-// Measured: 8192 x 8192 x 4096: 206 us, 2.66 PFLOP/s, 1.38 of the measured bf16 rate.
+// A tile costs another ~2500 cycles, mostly its first and last products.  Measured: 8192 x 8192 x 4096: 194 to 206 us, 2.7 to
+// 2.84 PFLOP/s (1.4 to 1.48 of the measured bf16 rate; the tensor cores are busy 60 % of the time); 512 weights of 1024 x 2048
+// with 160 rows each, unequal, 229 us (185 us of bytes).
 #include "fp8_tiles.cuh"
 
 namespace moe {
