@@ -12,9 +12,12 @@
 // Whole slices of 32 rows leave as bulk tensor stores of boxes of 128 bytes a row, while the next tile is under way; written
 // by their threads they held up the warps 5000 cycles a tile.
 //
-// What bounds it: a block takes ~750 cycles against 512 of the MMAs, the chain of a product's end, the 256 x 128
-// multiply-adds of an SM (256 cycles of its FP32 lanes, ~450 with the reads of tensor memory) and the barriers between.
-// A tile costs another ~2500 cycles, mostly its first and last products.  Measured: 8192 x 8192 x 4096: 194 to 206 us, 2.7 to
+// What bounds it: the warps that add up.  A block takes ~765 cycles against 512 of the MMAs and ~560 of its copies (57 bytes a
+// cycle and SM from L2): 256 x 128 multiply-adds of an SM are 256 cycles of its FP32 lanes, and the reads of tensor memory
+// overlap with them only in part.  8192 x 8192 x 4096 takes 196 us, with the sums and reads left out (and their waits kept) 134,
+// without the multiply-adds 167, without the reads 174, with buffers given back before they are read 201.  Reads of 8 columns,
+// or ahead of the multiply-adds, 207 to 211; of 32 columns in two sets of registers, with more of them for these warps, 202.
+// A tile's outputs cost another ~1400 cycles.  Measured: 8192 x 8192 x 4096: 194 to 206 us, 2.7 to
 // 2.84 PFLOP/s (1.4 to 1.48 of the measured bf16 rate; the tensor cores are busy 60 % of the time); 512 weights of 1024 x 2048
 // with 160 rows each, unequal, 229 us (185 us of bytes).
 #include "fp8_tiles.cuh"
