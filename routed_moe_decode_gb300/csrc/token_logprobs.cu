@@ -16,8 +16,8 @@
 // A row is one CTA's, or a cluster's of up to eight where there are few rows; the parts join through distributed shared
 // memory in a fixed order.
 //
-// Measured: 2048 rows of 131072 BF16 logits with 5 alternatives 96 us (5.6 TB/s), without any 96; the same in FP32 183 and 165
-// (6.5 TB/s); 127 rows of 100003 in FP32 with 20 alternatives 17.5 us, without 9.6; 4 rows of 131072 with 8, 7.9, without 3.9.
+// Measured: 2048 rows of 131072 BF16 logits with 5 alternatives 96 us (5.6 TB/s), without any 96; the same in FP32 180 and 165
+// (6.5 TB/s); 127 rows of 100003 in FP32 with 20 alternatives 16.0 us, without 9.5; 4 rows of 131072 with 8, 7.9, without 3.9.
 // The end of a row is a chain of trips through shared memory and back to the logits, 3 to 4 us that other CTAs hide where
 // there are more rows than CTAs fit.  The pass is close to the limit of its registers (64 of a thread; see kCtas): how the
 // second reading is written moved 2048 rows from 96 to 113 us by what it left for the pass.
@@ -154,12 +154,13 @@ struct Sorted {
   uint16_t pairs[kPairs];  // thread, group << 8
   int npairs[2], nfound[2];  // of even and odd rows
   union {
-    Key found[kFound + 4];
+    Key found[kFound];
     Key lists[kWarps][32];  // where more than that reach it
   };
   Key result[32];
   Key incoming[kParts][32];               // the best of a cluster's parts
   alignas(16) uint32_t shown[32];         // the largest logit of eight threads, as float_key has it
+  uint32_t bar;                           // the top-th of them
 };
 struct None {};
 template <bool TOP>
@@ -195,18 +196,22 @@ __device__ __noinline__ Key insert(Key list, Key k, int top, int lane) {
   return list;
 }
 
-// The top-th largest of 32 keys.
-__device__ __forceinline__ uint32_t nth(const uint32_t (&keys)[32], int top, int lane) {
-  const uint32_t k = keys[lane];
-  int before = 0;
-#pragma unroll 8
-  for (int i = 0; i < 32; ++i) before += keys[i] > k - (i < lane);  // no key is 0
-  return __shfl_sync(kAll, k, __ffs(__ballot_sync(kAll, before == top - 1)) - 1);
+// How many of 32 keys are before the CTA's key number tid / 8, equal ones by their places: four are compared by each of eight
+// threads.
+__device__ __forceinline__ int before(const uint32_t (&keys)[32], int tid) {
+  const int at = tid >> 3, first = 4 * (tid & 7);
+  const uint32_t k = keys[at];
+  int n = 0;
+#pragma unroll
+  for (int i = first; i < first + 4; ++i) n += keys[i] > k - (i < at);  // no key is 0
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(kAll, n, o);
+  return n;
 }
 
-// The warp's lists into the first warp's.
-__device__ __forceinline__ Key best_of_warps(Sorted& sh, Key list, int warp, int lane) {
-  for (int n = kWarps / 2; n > 0; n >>= 1) {
+// The lists of the first `lists` warps into the first one's.
+__device__ __forceinline__ Key best_of_warps(Sorted& sh, Key list, int lists, int warp, int lane) {
+  for (int n = lists / 2; n > 0; n >>= 1) {
     if (warp >= n && warp < 2 * n) sh.lists[warp][lane] = list;
     __syncthreads();
     if (warp < n) list = merge(list, sh.lists[warp + n][lane], lane);
@@ -365,17 +370,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
         if (lane == 0) sh.shown[warp] = float_key(most);
       }
       __syncthreads();
-      if (warp == kWarps - 1) {
-        const Sums all = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums);
-        if (lane == 0) sh.whole = all;
-      }
       uint32_t bar_key;
       if (a.top > kWarps) {
-        bar_key = nth(sh.shown, a.top, lane);
+        if (before(sh.shown, tid) == a.top - 1) sh.bar = sh.shown[tid >> 3];
+        __syncthreads();
+        bar_key = sh.bar;
       } else {
         bar_key = sh.shown[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) bar_key = min(bar_key, sh.shown[i]);
+      }
+      if (warp == kWarps - 1) {
+        const Sums all = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums);
+        if (lane == 0) sh.whole = all;
       }
       const float bar = value_of(bar_key);
       // a NaN ranks as -infinity: a group of nothing else has that as its largest
@@ -425,17 +432,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       __syncthreads();
       const int found = sh.nfound[buffer];
       if (found <= kFound) {
-        if (warp <= (found - 1) >> 5) {
-          if (lane < 4) sh.found[found + lane] = 0;  // each warp for itself
-          __syncwarp();
-        }
-        if (tid < found) {  // a key's place is the number of larger ones
-          const Key k = sh.found[tid];
+        for (int n0 = 0; n0 < found; n0 += kThreads / 8) {  // a key's place is the number of larger ones: eight threads count
+          const int n = n0 + (tid >> 3);
+          const Key k = sh.found[min(n, kFound - 1)];
           int at = 0;
-#pragma unroll 1
-          for (int i = 0; i < found; i += 4)
-            at += (sh.found[i] > k) + (sh.found[i + 1] > k) + (sh.found[i + 2] > k) + (sh.found[i + 3] > k);
-          if (at < 32) sh.result[at] = k;
+          for (int i = tid & 7; i < found; i += 8) at += sh.found[i] > k;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) at += __shfl_xor_sync(kAll, at, o);
+          if (n < found && at < 32) sh.result[at] = k;
         }
         __syncthreads();
         if (warp == 0) list = sh.result[lane];
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
         if (pairs <= kPairs) look_at_pairs(keep);
         else
           for (int i0 = row_v0 + warp * 32; i0 < row_v1; i0 += kThreads) look(i0 + lane, i0 + lane < row_v1, keep);
-        list = best_of_warps(sh, list, warp, lane);
+        list = best_of_warps(sh, list, kWarps, warp, lane);
       }
     } else {
       __syncthreads();
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
         if (lane == 0) sh.whole = mine;
       }
       if constexpr (TOP) {
-        list = best_of_warps(sh, warp < parts ? sh.incoming[warp][lane] : 0, warp, lane);
+        list = best_of_warps(sh, warp < parts ? sh.incoming[warp][lane] : 0, parts, warp, lane);
         if (warp == 0) mine = sh.whole;
       }
     }
