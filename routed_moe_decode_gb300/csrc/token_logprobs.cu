@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       else mine = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums);
     }
     if (parts > 1) {  // of one row: see the launch
+      __syncwarp();
       cluster_wait();  // all of them have started
       if (warp == 0) {
         if constexpr (TOP) {
