@@ -87,7 +87,7 @@ MOE_API int moe_fp8_matmul(int rows, int n, int k, int groups, const uint8_t* co
  * and the `top` best tokens by logit (equal logits: the lower id first; -0 equals 0), with their log probabilities.
  * tokens [rows][n_tokens] int32 (row stride token_stride); logprobs [rows][n_tokens], lse [rows],
  * entropy [rows], top_ids and top_logprobs [rows][top], all contiguous; any output may be null, both
- * of the last two are null where top is 0.  n_tokens <= 1024, top <= 32, top <= vocab.
+ * of the last two are null where top is 0.  n_tokens <= 1024, top <= 32, top <= vocab, 2^-80 <= scale <= 2^80.
  * A logit of -infinity has probability 0 and log probability -infinity; so has a token outside
  * [0, vocab).  A row of nothing else has lse -infinity, log probabilities -infinity and entropy 0.
  * A row with a NaN or +infinity (also where scale * logit is that in FP32) has NaN for them; its alternatives are ordered as if the NaNs were

@@ -94,7 +94,7 @@ struct LogprobArgs {
   int* top_ids;
   float* top_logprobs;
   int64_t row_stride, token_stride;
-  float scale;
+  float scale, exp_scale;  // exp_scale: scale * log2(e)
   int rows, vocab, n_tokens, top, dtype;
 };
 cudaError_t launch_logprobs(const LogprobArgs& a, int sms, cudaStream_t stream);

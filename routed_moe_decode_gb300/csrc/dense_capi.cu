@@ -207,7 +207,7 @@ int moe_token_logprobs(int rows, int vocab, int dtype, const void* logits, int64
   if (rows < 0 || vocab <= 0 || !dtype_ok(dtype) || !(scale > 0.f) || !std::isfinite(scale) || n_tokens < 0 || top < 0 ||
       top > vocab)
     return MOE_ERR_INVALID_ARG;
-  if (top > 32 || n_tokens > 1024 || vocab > (1 << 30) || rows > (1 << 28)) return MOE_ERR_UNSUPPORTED;
+  if (top > 32 || n_tokens > 1024 || vocab > (1 << 30) || rows > (1 << 28) || scale < 0x1p-80f || scale > 0x1p80f) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!logits || !aligned(logits, size_of(dtype)) || !aligned(tokens, 4) || !aligned(logprobs, 4) || !aligned(lse, 4) ||
       !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
@@ -219,6 +219,7 @@ int moe_token_logprobs(int rows, int vocab, int dtype, const void* logits, int64
   moe::dense::LogprobArgs a{};
   a.logits = logits; a.tokens = tokens; a.logprobs = logprobs; a.lse = lse; a.entropy = entropy; a.top_ids = top_ids;
   a.top_logprobs = top_logprobs; a.row_stride = row_stride; a.token_stride = token_stride; a.scale = scale;
+  a.exp_scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.rows = rows; a.vocab = vocab; a.n_tokens = n_tokens; a.top = top; a.dtype = dtype;
   return done("log probabilities launch", moe::dense::launch_logprobs(a, sms, stream));
 }

@@ -1,8 +1,10 @@
 // Log probabilities of given tokens, log-sum-exp, entropy and the best alternatives of rows of logits
 // (include/moe_dense.h), in one pass over them.
 //
-// A thread keeps a running maximum m of x = scale * logit, s = sum exp(x - m) and u = sum exp(x - m) (x - m), each
-// rescaled when m rises; joined over a row, lse = m + log s and entropy = log s - u / s.
+// A thread keeps a running maximum m of the logits l, s = sum exp(scale (l - m)) and u = sum exp(scale (l - m)) (l - m), each
+// rescaled when m rises; joined over a row, lse = scale m + log s and entropy = log s - scale u / s.  The difference comes
+// before the scale, so that the largest logit's own term is exactly 1: next to a rounded scale * m, what the rounding left of a
+// large logit (half a unit of 1e10 is 512) would be its exponent.
 //
 // Alternatives are keys: the logit's order-preserving bits above the complement of its id, so that equal logits are in
 // the order of their ids and no two keys are equal.  The pass keeps only the largest logit of every thread's step (or of a
@@ -34,7 +36,6 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kVecs = 4;  // 16-byte vectors of a thread's step
 constexpr int kParts = 8;  // of a row, at most
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr float kLog2e = 1.44269504088896340736f;
 typedef unsigned long long Key;
 
 __device__ __forceinline__ float exp2_of(float x) {
@@ -55,6 +56,8 @@ __device__ __forceinline__ Key shfl_xor(Key k, int o) { return __shfl_xor_sync(k
 struct Sums {
   float m, s, u;
 };
+// Differences of a rescaled sum: no further down, so that s times one is finite; exp of the smallest scale times this is 0.
+constexpr float kFarDown = -1e28f;
 
 // Sorted descending over the lanes: the 32 best of two such lists.
 __device__ __forceinline__ Key merge(Key a, Key b, int lane) {
@@ -219,9 +222,9 @@ __device__ __forceinline__ Key best_of_warps(Sorted& sh, Key list, int lists, in
   return list;
 }
 // The lanes' sums, in an order that does not change: all have the result.
-__device__ __noinline__ Sums joined(Sums a) {
+__device__ __noinline__ Sums joined(Sums a, float exp_scale) {
   const float m = value_of(__reduce_max_sync(kAll, float_key(a.m)));
-  const float d = fmaxf(a.m - m, -1e30f), f = exp2_of(d * kLog2e);
+  const float d = fmaxf(a.m - m, kFarDown), f = exp2_of(d * exp_scale);
   a.u = a.s != 0.f && f != 0.f ? (a.u + a.s * d) * f : 0.f;
   a.s = f != 0.f || a.s != a.s ? a.s * f : 0.f;
 #pragma unroll 1
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
   };
   const Sums kNoSums{-FLT_MAX, 0.f, 0.f};
   Sums mine;
-  const float2 scale = make_float2(a.scale, a.scale), log2e = make_float2(kLog2e, kLog2e);
+  const float2 exp_scale = make_float2(a.exp_scale, a.exp_scale);
 
   auto load = [&](uint4 (&raw)[kVecs], int at) {
 #pragma unroll
@@ -273,9 +276,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
     }
   };
   auto add = [&](const float2 (&v)[N / 2], float most) {
-    const float m = fmaxf(mine.m, most * a.scale);
+    const float m = fmaxf(mine.m, most);
     if (m > mine.m) {
-      const float d = fmaxf(mine.m - m, -1e30f), f = exp2_of(d * kLog2e);
+      const float d = fmaxf(mine.m - m, kFarDown), f = exp2_of(d * a.exp_scale);
       mine.u = (mine.u + mine.s * d) * f;
       mine.s *= f;
       mine.m = m;
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
     s[0] = s[1] = u[0] = u[1] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const float2 d = fma2(v[i], scale, down), t = mul2(d, log2e);
+      const float2 d = add2(v[i], down), t = mul2(d, exp_scale);
       const float2 e = make_float2(exp2_of(t.x), exp2_of(t.y));
       s[i & 1] = add2(s[i & 1], e);
       u[i & 1] = fma2(e, make_float2(fmaxf(d.x, -FLT_MAX), fmaxf(d.y, -FLT_MAX)), u[i & 1]);
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       load(raw, v0);
     }
 
-    mine = joined(mine);
+    mine = joined(mine, a.exp_scale);
     if (lane == 0) sh.sums[buffer][warp] = mine;
     if constexpr (TOP) {
     float most = best;
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
         for (int i = 1; i < kWarps; ++i) bar_key = min(bar_key, sh.shown[i]);
       }
       if (warp == kWarps - 1) {
-        const Sums all = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums);
+        const Sums all = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums, a.exp_scale);
         if (lane == 0) sh.whole = all;
       }
       const float bar = value_of(bar_key);
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
     }
     if (warp == 0) {
       if constexpr (TOP) mine = sh.whole;
-      else mine = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums);
+      else mine = joined(lane < kWarps ? sh.sums[buffer][lane] : kNoSums, a.exp_scale);
     }
     if (parts > 1) {  // of one row: see the launch
       __syncwarp();
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       cluster_sync();
       if (part != 0) return;
       if (warp == (TOP ? kWarps - 1 : 0)) {
-        mine = joined(lane < parts ? sh.incoming_sums[lane] : kNoSums);
+        mine = joined(lane < parts ? sh.incoming_sums[lane] : kNoSums, a.exp_scale);
         if (lane == 0) sh.whole = mine;
       }
       if constexpr (TOP) {
@@ -487,14 +490,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       }
     }
     if (finishes) {
-      if (!(mine.m < INFINITY)) mine.s = __int_as_float(0x7fc00000);  // scale * logit is +infinity, of a finite logit too
-      const bool none = mine.s == 0.f;
+      const float most = mine.m * a.scale;
+      if (!(most < INFINITY)) mine.s = __int_as_float(0x7fc00000);  // scale * logit is +infinity, of a finite logit too
+      const bool none = mine.s == 0.f || most == -INFINITY;
       const float logs = logf(mine.s);
       if (lane == 0) {
-        if (a.lse) a.lse[row] = none ? -INFINITY : mine.m + logs;
-        if (a.entropy) a.entropy[row] = none ? 0.f : logs - mine.u / mine.s;
+        if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(mine.m, a.scale, logs);
+        if (a.entropy) a.entropy[row] = none ? 0.f : logs - a.scale * (mine.u / mine.s);
       }
-      auto logprob = [&](float l) { return none ? -INFINITY : fmaf(l, a.scale, -mine.m) - logs; };
+      auto logprob = [&](float l) {
+        const float d = l - mine.m;  // -infinity also where two finite logits are too far apart for their difference
+        return none ? -INFINITY : d >= -FLT_MAX ? fmaf(d, a.scale, -logs) : fmaf(l, a.scale, -most) - logs;
+      };
       if (a.logprobs) {
         float* const to = a.logprobs + static_cast<int64_t>(row) * a.n_tokens;
         if (lane < a.n_tokens) to[lane] = logprob(token_logit);

@@ -128,3 +128,8 @@ def test_tensors_of_the_host_are_refused(L):
         moe.quantize_rows(torch.zeros(4, 32))
     with pytest.raises(ValueError):
         moe.token_logprobs(torch.zeros(4, 32), torch.zeros(4, dtype=torch.int32))
+
+
+def test_logprobs_refuse_scales_far_from_one(L):
+    good = [4, 500, 0, P0, 500, 1.0, P0, 1, 1, 8, P0, P0, P0, P0, P0]
+    refused(L, "moe_token_logprobs", good, [({5: 2.0 ** -81}, L.MOE_ERR_UNSUPPORTED), ({5: 2.0 ** 81}, L.MOE_ERR_UNSUPPORTED)])

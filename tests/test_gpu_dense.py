@@ -539,6 +539,51 @@ def test_logprobs_masks_ties_and_bad_tokens(moe):
     assert got.top_ids.tolist() == [[2500, 17, 4000, 0, 1, 2]]
 
 
+@pytest.mark.parametrize("rows", [1, 700])
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+def test_logprobs_of_large_logits_with_a_scale(moe, dtype, rows):
+    """Rows whose scaled logits FP32 does not hold exactly: nothing but masks of any kind, and differences far below their size."""
+    lowest = torch.finfo(dtype).min
+    v, large = 5003, min(1e10, -lowest)
+    g = gen(79 + rows)
+    kinds = [torch.full((v,), lowest), torch.full((v,), -large), torch.full((v,), large), torch.full((v,), lowest),
+             torch.full((v,), -large), torch.randint(0, 20, (v,), generator=torch.Generator().manual_seed(rows)) - 1e7]
+    kinds[3][torch.tensor([17, 2500, 4999])] = torch.tensor([0.25, -1.0, 2.0])
+    kinds[4][4321] = 3.0
+    if dtype is not FP32:
+        kinds.pop()  # their steps are larger than 1 there
+    x = torch.stack(kinds).to(dtype).cuda()
+    if rows > 1:
+        x = x[torch.randint(0, len(kinds), (rows,), generator=g, device="cuda")]
+    tokens = torch.randint(0, v, (x.shape[0], 3), generator=g, device="cuda").to(torch.int32)
+    tokens[:, 0] = 2500
+    for scale in (0.699999988079071044921875, 1.2999999523162841796875):  # values of FP32
+        for i in range(x.shape[0] if rows == 1 else 0):  # a row in parts of a cluster
+            one(moe, x[i:i + 1], tokens[i:i + 1], scale)
+        one(moe, x, tokens, scale)
+
+
+def one(moe, x, tokens, scale):
+    got = moe.token_logprobs(x, tokens, top=4, scale=scale)
+    seen = {}
+    for i, row in enumerate(x):
+        key = (row[0].item(), row[2500].item(), row[4321].item())
+        if key not in seen:
+            seen[key] = P.logprobs(row[None], torch.arange(x.shape[1])[None], 4, scale)[0]
+        lps, lse, ent, ids, tops, spread = seen[key]
+        if lse < -torch.finfo(FP32).max:  # FP32 has -infinity for all of them
+            assert got.lse[i] == -math.inf and got.entropy[i] == 0 and (got.logprobs[i] == -math.inf).all()
+            continue
+        # the sums as in check_logprobs; the difference of two logits, its product and one addition round to FP32
+        assert abs(float(got.lse[i]) - lse) <= 1e-5 + 4 * U * abs(lse)
+        assert abs(float(got.entropy[i]) - ent) <= 2e-5 * (1 + spread)
+        for a, b in zip(got.logprobs[i].tolist() + got.top_logprobs[i].tolist(), [lps[t] for t in tokens[i].tolist()] + tops):
+            if b < -(2 - 2.0 ** -24) * 2.0 ** 127:  # its nearest FP32 value (the lowest mask times 1.3 is -4.4e38)
+                b = -math.inf
+            assert a == b or abs(a - b) <= 1e-5 + 4 * U * abs(b), (i, a, b)
+        assert got.top_ids[i].tolist() == ids
+
+
 def test_logprobs_strides(moe):
     g = gen(78)
     for dtype in (FP32, BF16):
