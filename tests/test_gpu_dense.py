@@ -584,6 +584,86 @@ def one(moe, x, tokens, scale):
         assert got.top_ids[i].tolist() == ids
 
 
+def check_sure(got, x, tokens, scale, steps):
+    """Rows in which one token has nearly all the probability, by relative errors.  With x = scale * (logit - largest) and r the sum
+    of exp(x) over the other tokens: lse - max = log1p(r) is the sure token's log probability (negated), entropy = log1p(r) +
+    sum exp(x) |x| / (1 + r).  A term's exponent has three roundings (the difference, scale * log2(e), their product), in parts that add up to
+    |x|: 3 U |x| of the term, so that of r 3 U times the mean of |x| under the terms, that of the entropy with |x| times the terms as
+    weights.  Every exponential (of the term; of its thread's, warp's and part's largest; of a step that finds a larger one) is
+    good to 4 U; additions one after the other: 10 in a step, one a step, 15 in joins; logarithm, quotient and product 6."""
+    f = x.double()
+    most, at = f.max(-1)
+    d = (f - most[:, None]) * scale
+    d[torch.arange(len(x)), at] = -math.inf
+    e = d.exp()
+    size = torch.where(e > 0, -d, torch.zeros_like(d))
+    r = e.sum(-1)
+    mean, mean2 = (e * size).sum(-1) / r, (e * size * size).sum(-1) / (e * size).sum(-1)
+    want = -torch.log1p(r)
+    entropy = torch.log1p(r) + (e * size).sum(-1) / (1 + r)
+    terms = 10 + 15 + 4 * 4 + 6 + 6 * steps
+    sure = got.logprobs[:, 0].double()
+    assert (tokens[:, 0] == at).all() and (got.top_ids is None or (got.top_ids[:, 0] == at).all())
+    assert ((sure - want).abs() <= -want * U * (3 * mean + terms)).all(), float(((sure - want) / want).abs().max())
+    assert got.top_logprobs is None or torch.equal(got.top_logprobs[:, 0], got.logprobs[:, 0])
+    assert ((got.entropy.double() - entropy).abs() <= entropy * U * (3 * torch.maximum(mean, mean2) + terms)).all(), \
+        float(((got.entropy.double() - entropy) / entropy).abs().max())
+    # the others: a difference, its product and one addition
+    other = (f.gather(1, tokens[:, 1:].long()) - most[:, None]) * scale + want[:, None]
+    assert ((got.logprobs[:, 1:].double() - other).abs() <= 4 * U * other.abs() + 1e-5 * r[:, None].clamp(max=1)).all()
+    lse = most * scale + torch.log1p(r)
+    assert ((got.lse.double() - lse).abs() <= 4 * U * lse.abs() + 1e-5 * r).all()
+
+
+RESTS = [10.0 ** -(i / 2) for i in range(0, 17)]  # 1 to 1e-8
+
+
+@pytest.mark.parametrize("rows,vocab,steps", [(2, 60, 1), (1, 131072, 4), (5, 50001, 2), (300, 3001, 2), (640, 20011, 6), (640, 70001, 18)])
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+def test_logprobs_of_sure_tokens(moe, dtype, rows, vocab, steps):
+    """One CTA for each row, several rows a CTA, parts of a cluster; the sure token anywhere, outside all vectors too."""
+    g = gen(vocab)
+    for turn, (top, scale) in enumerate(((0, 1.0), (3, 1.0), (20, 0.699999988079071044921875), (0, 2.5))):
+        x = rand(g, rows, vocab + 9, dtype=dtype)[:, 1 + turn:1 + turn + vocab]
+        targets = torch.tensor([RESTS[i % len(RESTS)] for i in range(turn, turn + rows)], dtype=torch.float64, device="cuda")
+        total = (x.double() * scale).exp().sum(-1)
+        sure = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+        edge = torch.tensor([0, vocab - 1, 1, vocab - 2], device="cuda")
+        sure[::3] = edge[torch.arange(len(sure[::3]), device="cuda") % 4]
+        x[torch.arange(rows, device="cuda"), sure] = ((total / targets).log() / scale).to(dtype)
+        tokens = torch.randint(0, vocab, (rows, 3), generator=g, device="cuda")
+        tokens = torch.cat([sure[:, None], torch.where(tokens == sure[:, None], (tokens + 1) % vocab, tokens)], 1).to(torch.int32)
+        got = moe.token_logprobs(x, tokens, top=top, scale=scale)
+        check_sure(got, x, tokens, scale, steps)
+        again = moe.token_logprobs(x, tokens, top=top, scale=scale)
+        assert torch.equal(got.entropy, again.entropy) and torch.equal(got.logprobs, again.logprobs)
+
+
+@pytest.mark.parametrize("rows", [3, 900])
+def test_logprobs_of_sure_tokens_with_few_others(moe, rows):
+    """Everything else masked but one token, or all of it: the rest is one term, or nothing."""
+    vocab = 40009
+    g = gen(rows)
+    for mask in (-math.inf, torch.finfo(FP32).min, -1e10):
+        x = torch.full((rows, vocab), mask, device="cuda")
+        pair = torch.stack([torch.randperm(vocab, generator=g, device="cuda")[:2] for _ in range(rows)])
+        at = torch.arange(rows, device="cuda")
+        x[at, pair[:, 0]] = 3.25
+        x[at, pair[:, 1]] = 3.25 - torch.linspace(0.5, 18.5, rows, device="cuda")
+        for top in (0, 2):
+            check_sure(moe.token_logprobs(x, pair.to(torch.int32), top=top), x, pair, 1.0, 10)
+        x[at, pair[:, 1]] = mask
+        for top in (0, 1):
+            got = moe.token_logprobs(x, pair.to(torch.int32), top=top)
+            assert (got.logprobs[:, 0] == 0).all() and (got.entropy == 0).all() and (got.lse == 3.25).all()
+            assert top == 0 or ((got.top_logprobs == 0).all() and torch.equal(got.top_ids[:, 0], pair[:, 0].to(torch.int32)))
+    # two of the same: each has a half
+    x[at, pair[:, 1]] = 3.25
+    for top in (0, 2):
+        got = moe.token_logprobs(x, pair.to(torch.int32), top=top)
+        assert ((got.logprobs.double() + math.log(2)).abs() <= 8 * U).all() and ((got.entropy.double() - math.log(2)).abs() <= 8 * U).all()
+
+
 def test_logprobs_strides(moe):
     g = gen(78)
     for dtype in (FP32, BF16):
