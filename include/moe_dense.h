@@ -53,7 +53,9 @@ extern "C" {
  * normed likewise (heads of a fused projection's rows); residual, residual_out and the codes have
  * one stride.  residual, residual_out (needs residual), normed and codes (with scales) may be null,
  * but something is written.  residual_out may be x or residual; normed may be x or residual; with the same strides.
- * Sums and statistics in FP32.  Any d >= 1; rows of 16-byte aligned starts and lengths are faster.
+ * Sums and statistics in FP32; a row whose mean square (with eps) FP32 does not hold as a normal value is
+ * summed times a power of two.  In a row with an infinity what is finite becomes 0 and the infinity NaN.
+ * Any d >= 1; rows of 16-byte aligned starts and lengths are faster.
  * dtype, weight_dtype: MOE_DENSE_*. */
 MOE_API int moe_rms_norm(int outer, int inner, int d, int dtype, const void* x, int64_t x_outer, int64_t x_inner,
                          const void* residual, int64_t residual_stride, const void* weight, int weight_dtype,

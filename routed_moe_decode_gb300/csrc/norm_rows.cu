@@ -12,6 +12,7 @@
 // slots as memory leaves.  Norm rows that a persistent grid fetches ahead, 64 channels a lane with a warp to a row (66 us), or
 // other numbers of CTAs (28.9 to 29.6 us) are no faster.
 #include <algorithm>
+#include <cfloat>
 
 #include "dense.cuh"
 
@@ -296,10 +297,26 @@ __device__ __forceinline__ void finish(const NormArgs& a, const RowPtrs<T>& p, i
   }
 }
 
-// 1 / sqrt(mean + eps): the approximate root's reciprocal (2 units) and a step of Newton's iteration.
-__device__ __forceinline__ float norm_factor(float squares, const NormArgs& a) {
-  const float m = fmaf(squares, a.inv_d, a.eps), f = rsqrtf(m);
+// 1 / sqrt(m): the approximate root's reciprocal (2 units) and a step of Newton's iteration.
+__device__ __forceinline__ float root(float m) {
+  const float f = rsqrtf(m);
   return fmaf(0.5f * f, fmaf(-m * f, f, 1.f), f);
+}
+
+// Rows whose mean square (with eps) is beyond FP32 or below its normal values, where squares lose their digits: their squares are
+// added up again of h * far_scale.  Large ones (an element is 2^52 or more; scaled, at most 2^48, so 2^24 squares are finite) and
+// small ones (elements at most 2^-51; the smallest, 2^-149, has a normal square, and one in 2^24 a normal mean).
+__device__ __forceinline__ bool is_far(float m) { return !(m >= 0x1p-126f && m <= FLT_MAX); }
+__device__ __forceinline__ float far_scale(float m) { return m < 1.f ? 0x1p100f : 0x1p-80f; }
+// n = h * before * after * w * factor.  A large row's h meets the factor before the scale: its small elements stay normal, and the
+// product is at most 2^92.
+struct Far {
+  float before, after, factor;
+};
+__device__ __forceinline__ Far far_row(float squares, float scale, const NormArgs& a) {
+  const float m = fmaf(squares, a.inv_d, a.eps * scale * scale);
+  const float f = m <= FLT_MAX || m != m ? root(m) : 0.f;  // an infinite element: finite ones become 0
+  return scale < 1.f ? Far{f, scale, 1.f} : Far{scale, 1.f, f};
 }
 
 // A row's channels in the registers of TPR threads, VPT times 8 each.
@@ -337,7 +354,25 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 8 : VPT == 2 ? (sizeof(T) == 4
     const int c = 8 * (t + j * TPR);
     if (p.ro && live && c < a.d) store8<T, true>(p.ro, c, a.d, h[j]);
   }
-  const float factor = norm_factor(row_sum<TPR>(squares, red), a);
+  const float m = fmaf(row_sum<TPR>(squares, red), a.inv_d, a.eps);
+  float factor = root(m);
+  if (__any_sync(kAll, is_far(m))) {  // all threads of a row, and of a warp
+    if constexpr (TPR > 32) __syncthreads();
+    const float scale = far_scale(m);
+    squares = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) squares = fmaf(h[j][i] * scale, h[j][i] * scale, squares);
+    const Far far = far_row(row_sum<TPR>(squares, red), scale, a);
+    if (is_far(m)) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * far.before * far.after;
+      factor = far.factor;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int c = 8 * (t + j * TPR);
@@ -368,14 +403,38 @@ __global__ void __launch_bounds__(256) norm_long_kernel(const NormArgs a) {
     squares += s;
     if (p.ro) store8<T, VEC>(p.ro, c, a.d, h);
   }
-  const float factor = norm_factor(row_sum<TPR>(squares, red), a);
+  auto again = [&](int c, float (&h)[8]) {
+    if (p.ro) load8<T, VEC>(p.ro, c, a.d, h);
+    else load_h<T, VEC>(a, p, c, h);
+  };
+  const float m = fmaf(row_sum<TPR>(squares, red), a.inv_d, a.eps);
+  Far far = {1.f, 1.f, root(m)};
+  if (__any_sync(kAll, is_far(m))) {  // all threads of a row, and of a warp
+    if constexpr (TPR > 32) __syncthreads();
+    const float scale = far_scale(m);
+    squares = 0.f;
+    for (int j = 0; j < steps; ++j) {
+      const int c = 8 * (t + j * TPR);
+      if (!live || c >= a.d) continue;
+      float h[8];
+      again(c, h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) squares = fmaf(h[i] * scale, h[i] * scale, squares);
+    }
+    const Far f = far_row(row_sum<TPR>(squares, red), scale, a);
+    if (is_far(m)) far = f;
+  }
+  const float factor = far.factor;
   for (int j = 0; j < steps; ++j) {
     const int c = 8 * (t + j * TPR);
     const bool in = live && c < a.d;
     float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (in) {
-      if (p.ro) load8<T, VEC>(p.ro, c, a.d, h);
-      else load_h<T, VEC>(a, p, c, h);
+      again(c, h);
+      if (is_far(m)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = h[i] * far.before * far.after;
+      }
     }
     finish<T, VEC>(a, p, c, in, h, factor);
   }

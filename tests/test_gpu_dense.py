@@ -165,6 +165,54 @@ def test_norm_zeros_infinities_and_refusals(moe):
     assert norm(e)[0].shape == (0, 256)
 
 
+@pytest.mark.parametrize("d", [1, 64, 100, 250, 512, 1000, 1030, 2048, 4096, 5000, 8192, 20000])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_norm_of_rows_whose_squares_leave_fp32(moe, d, dtype):
+    """Rows of every size that the type has, alone and beside ordinary ones of the same warp: the norm is of size 1."""
+    g = gen(d)
+    sizes = [1e30, 1.0, 1e-30, 1e18, 1e19, 3e37, 1e-18, 1e-20, 1e-23, 1e-36, 3e-39, 1e-40, 1e-10, 1.0, 1e25, 3e-38, 2.0 ** -133]
+    x = torch.stack([rand(g, d) * 1.0 for _ in sizes]).clamp(-8, 8) * torch.tensor(sizes, device="cuda")[:, None]
+    x[1::4, d // 2] *= 2.0 ** -40  # far below the rest of its row
+    x[:, 0] = torch.tensor(sizes, device="cuda")  # no row of zeros
+    x = x.to(dtype)
+    r = (x.flip(1).float() * 0.5).to(dtype)
+    w = (1 + rand(g, d, scale=0.2)).to(FP32)
+    for eps in (0.0, 1e-6, 1e-42, 1e-30):
+        norm = moe.RmsNorm(w, eps=eps)
+        eps32 = float(torch.tensor(eps, dtype=FP32))
+        for residual, quantize, place in ((False, False, False), (True, True, False), (False, True, True), (True, False, True)):
+            if quantize and d % 16 and d > 1030:
+                continue
+            a, b = x.clone(), r.clone()
+            h = (x.float() + r.float()).to(dtype) if residual else x
+            want = P.rms_norm(h, w, eps32, False)
+            n, ro, q = norm(a, residual=b if residual else None, residual_out=None if residual and not place else False,
+                            normed=a if place else True, quantize=quantize)
+            assert ro is None or torch.equal(ro, h)
+            # the scaled row's products round as often as the others'; without a scale, an h * w below FP32's normal values is off by
+            # 2^-150, times the factor
+            mean = h.double().square().mean(-1, keepdim=True) + eps32
+            plain = mean >= 2.0 ** -126
+            low = torch.where(plain, 2.0 ** -150 / mean.sqrt(), torch.zeros_like(mean))
+            assert ((n.double() - want).abs() <= half_step(want, dtype) * (1 + 2.0 ** -8) + want.abs() * NORM_REL + low).all()
+            if quantize:
+                keep = ~plain[:, 0] | (h.double().abs().amax(-1) >= 2.0 ** -110)
+                check_quantized(moe.Fp8Rows(q.codes[keep], q.scales[keep]), want[keep], NORM_REL)
+
+
+@pytest.mark.parametrize("d", [100, 256, 2048, 9000])
+def test_norm_of_infinite_rows(moe, d):
+    """h / sqrt(infinity): 0 for what is finite and NaN for the infinities, block by block in 8 bits."""
+    x = rand(gen(d), 5, d) + 3.0
+    x[1, 70], x[3, 5] = math.inf, -math.inf
+    n, _, q = moe.RmsNorm(torch.ones(d, device="cuda"))(x, quantize=True)
+    assert torch.isfinite(n[0::2]).all() and torch.isfinite(q.scales[0::2]).all()
+    for row, at in ((1, 70), (3, 5)):
+        rest = torch.arange(d, device="cuda") != at
+        assert torch.isnan(n[row, at]) and (n[row, rest] == 0).all()
+        assert torch.isnan(q.scales[row, 0]) and (q.scales[row, 1:] == 0).all() and (q.codes[row].float() == 0).all()
+
+
 # ---- quantised rows ----
 
 @pytest.mark.parametrize("rows,d", [(1, 1), (1, 16), (3, 100), (5, 128), (2, 136), (33, 4096), (7, 1000), (4, 131), (300, 640)])
