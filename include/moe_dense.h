@@ -36,8 +36,9 @@ extern "C" {
 #endif
 
 /* Status bits of a product. */
-#define MOE_DENSE_BAD_OFFSETS 0x1u /* a group's offsets decrease or leave [0, rows]: they are cut to
-                                      that range, and a group that would end before it begins has no rows */
+#define MOE_DENSE_BAD_OFFSETS 0x1u /* a group's offsets decrease or leave [0, rows]: they are cut to that
+                                      range, a group begins where those before it have ended at the
+                                      earliest, and one that would end before it begins has no rows */
 #define MOE_DENSE_TIMEOUT 0x2u     /* a bounded wait gave up: the product's results are not valid */
 
 /* Element types. */

@@ -11,6 +11,19 @@ struct Groups {
   int first[kMaxGroups], rows[kMaxGroups], before[kMaxGroups + 1];
 };
 
+// Behind offsets that decrease a group begins where those before it have ended, so that every row has one writer and there are no
+// more row tiles than the host has allowed for.  (A function of its own: in place it cost calls without groups 0.2 us.)
+static __device__ __noinline__ void part_groups(Groups& gs, int groups) {
+  int end = 0;
+#pragma unroll 1
+  for (int g = 0; g < groups; ++g) {
+    const int b = gs.first[g], e = b + gs.rows[g], from = max(b, end);
+    gs.first[g] = from;
+    gs.rows[g] = max(e - from, 0);
+    end = max(end, gs.rows[g] > 0 ? e : 0);
+  }
+}
+
 // By all WARPS warps of the CTA; tiles of ROWS rows.  scan: WARPS ints.
 template <int WARPS, int ROWS>
 __device__ __forceinline__ void make_groups(const MatmulArgs& a, Groups& gs, int* scan) {
@@ -18,6 +31,7 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, Groups& gs, int
   const int per = (a.groups + 32 * WARPS - 1) / (32 * WARPS);
   const int g0 = min(tid * per, a.groups), g1 = min(g0 + per, a.groups);
   int mine = 0;
+  bool back = false;
   for (int g = g0; g < g1; ++g) {
     int b = 0, e = a.rows;
     if (a.offsets) {
@@ -25,11 +39,17 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, Groups& gs, int
       b = min(max(rb, 0), a.rows);
       e = min(max(re, 0), a.rows);
       if (blockIdx.x == 0 && (b != rb || e != re || re < rb)) atomicOr(a.status, MOE_DENSE_BAD_OFFSETS);
+      back |= re < rb;
     }
-    const int n = max(e - b, 0);
     gs.first[g] = b;
-    gs.rows[g] = n;
-    mine += (n + ROWS - 1) / ROWS;
+    gs.rows[g] = max(e - b, 0);
+    mine += (gs.rows[g] + ROWS - 1) / ROWS;
+  }
+  if (a.offsets && __syncthreads_or(back)) {
+    if (tid == 0) part_groups(gs, a.groups);
+    __syncthreads();
+    mine = 0;
+    for (int g = g0; g < g1; ++g) mine += (gs.rows[g] + ROWS - 1) / ROWS;
   }
   int sum = mine;
 #pragma unroll

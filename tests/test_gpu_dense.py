@@ -473,6 +473,40 @@ def test_grouped_product_bad_offsets(moe):
         linear(x, offsets=torch.zeros(5, dtype=torch.int64, device="cuda"))
 
 
+def spans_of(edges, rows):
+    """(group, first row, end) by the header's rule for offsets out of order."""
+    end, spans = 0, []
+    for i, (a, b) in enumerate(zip(edges, edges[1:])):
+        a, b = max(min(max(a, 0), rows), end), min(max(b, 0), rows)
+        if b > a:
+            spans.append((i, a, b))
+            end = b
+    return spans
+
+
+@pytest.mark.parametrize("rows,edges", [(20, [0, 10, 5, 15]), (20, [3, 18, 0, 19, 1, 40]), (1000, [0, 600, 100, 900, 200, 1000]),
+                                        (900, [0, 900] * 5), (700, [0, 700] * 512 + [0]), (64, [30, 20, 40, 10, 64])])
+def test_grouped_product_overlapping_offsets(moe, rows, edges):
+    """Offsets that decrease give no row to two groups: the first group that has it multiplies it, every time."""
+    g = gen(rows)
+    n, k = 136, 144
+    x = make_rows(moe, g, rows, k)
+    codes, scales = make_weight(g, len(edges) - 1, n, k)
+    linear = moe.Fp8Linear(codes, scales)
+    offsets = torch.tensor(edges, dtype=torch.int32, device="cuda")
+    outs = []
+    for _ in range(3):
+        out = torch.full((rows, n), 7.0, device="cuda")
+        linear(x, offsets=offsets, out=out)
+        assert linear.status() == moe.DENSE_BAD_OFFSETS
+        outs.append(out)
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    for i, a, b in spans_of(edges, rows):
+        check_product(outs[0][a:b], moe.Fp8Rows(x.codes[a:b], x.scales[a:b]), codes[i], scales[i])
+        rest[a:b] = False
+    assert (outs[0][rest] == 7).all() and torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 def test_grouped_rows_do_not_depend_on_the_others(moe):
     """A group's rows have the bits of the same rows alone under the same kernel (order of sums fixed by k alone)."""
     g = gen(13)
