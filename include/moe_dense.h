@@ -100,8 +100,9 @@ MOE_API int moe_token_logprobs(int rows, int vocab, int dtype, const void* logit
                                float* lse, float* entropy, int32_t* top_ids, float* top_logprobs,
                                moe_stream_t stream);
 
-/* The product's status word: blocking copy on `stream`, cleared when `clear` is non-zero.  MOE_OK if no bit
- * is set, MOE_ERR_DEVICE if any is. */
+/* The product's status word: read on `stream`, with `clear` non-zero exchanged for 0 in the same step, and waited for.  It has the
+ * bits of the products that are ordered before this call on `stream`, and of others that ran by then; a bit that a product of
+ * another stream sets meanwhile is in this result or stays for the next.  MOE_OK if no bit is set, MOE_ERR_DEVICE if any is. */
 MOE_API int moe_dense_read_status(uint32_t* status, int clear, uint32_t* status_bits, moe_stream_t stream);
 
 #ifdef __cplusplus

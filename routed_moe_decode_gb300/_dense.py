@@ -231,7 +231,8 @@ class Fp8Linear:
         return out
 
     def status(self, clear=True, stream=None):
-        """The status bits of the products so far (DENSE_*); waits for the stream."""
+        """The status bits (DENSE_*) of the products that are ordered before this call on the stream, and of others that ran by then;
+        waits for the stream.  A bit that a product of another stream sets meanwhile is in this result or in the next."""
         bits = ctypes.c_uint32(0)
         rc = _lib.lib().moe_dense_read_status(self._status.data_ptr(), 1 if clear else 0, ctypes.byref(bits),
                                               _raw_stream(self._index, stream))

@@ -48,6 +48,8 @@ namespace {
 
 using moe::dense::MatmulArgs;
 
+__global__ void take_status(uint32_t* status, uint32_t* bits) { *bits = atomicExch(status, 0u); }
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool dtype_ok(int d) { return d == MOE_DENSE_FP32 || d == MOE_DENSE_BF16 || d == MOE_DENSE_FP16; }
 int size_of(int dtype) { return dtype == MOE_DENSE_FP32 ? 4 : 2; }
@@ -226,10 +228,22 @@ int moe_token_logprobs(int rows, int vocab, int dtype, const void* logits, int64
 
 int moe_dense_read_status(uint32_t* status, int clear, uint32_t* status_bits, moe_stream_t stream) {
   if (!status || !aligned(status, 4) || !status_bits) return MOE_ERR_INVALID_ARG;
-  uint32_t bits = 0;
-  cudaError_t e = cudaMemcpyAsync(&bits, status, sizeof bits, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess && clear) e = cudaMemsetAsync(status, 0, sizeof bits, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  // Cleared by the exchange that reads it: a product of another stream may set a bit at any time, which this read or a later one has.
+  uint32_t bits = 0, *taken = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (clear) {
+    e = cudaMallocAsync(reinterpret_cast<void**>(&taken), sizeof bits, stream);
+    if (e != cudaSuccess) return done("status", e);
+    take_status<<<1, 1, 0, stream>>>(status, taken);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&bits, clear ? taken : status, sizeof bits, cudaMemcpyDeviceToHost, stream);
+  if (taken) {
+    const cudaError_t freed = cudaFreeAsync(taken, stream);
+    if (e == cudaSuccess) e = freed;
+  }
+  const cudaError_t waited = cudaStreamSynchronize(stream);  // `bits` is written until then
+  if (e == cudaSuccess) e = waited;
   if (e != cudaSuccess) return done("status", e);
   *status_bits = bits;
   return bits ? MOE_ERR_DEVICE : MOE_OK;

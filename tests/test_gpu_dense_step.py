@@ -147,6 +147,32 @@ def test_eager_calls_between_two_streams(moe):  # noqa: F811
     assert same(got[0], want[0]) and same(got[1], want[1])
 
 
+def test_a_status_bit_is_read_once_whatever_the_streams(moe):  # noqa: F811
+    """A product of one stream sets its bit at any moment of a read on another: one of two reads has it."""
+    g = gen(10)
+    x = moe.quantize_rows(rand(g, 20, 128))
+    linear = moe.Fp8Linear(*make_weight(g, 4, 128, 128))
+    bad = torch.tensor([0, 5, 5, 25, 30], dtype=torch.int32, device="cuda")
+    out = torch.zeros(20, 128, device="cuda")
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    both = 0
+    for i in range(4000):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1 + 100 * (i % 500))  # moments up to 25 us apart
+        linear(x, offsets=bad, out=out, stream=side)
+        first = linear.status(stream=main)
+        side.synchronize()
+        second = linear.status(stream=main)
+        assert first | second == moe.DENSE_BAD_OFFSETS, i
+        both += first == second
+    assert both == 0 and linear.status(stream=main) == 0
+    # a read that does not clear leaves the bit
+    linear(x, offsets=bad, out=out, stream=main)
+    assert linear.status(clear=False, stream=main) == linear.status(stream=main) == moe.DENSE_BAD_OFFSETS
+    assert linear.status(clear=False, stream=main) == 0
+
+
 # ---- past 32 bits: the last rows of arrays of more than 2^31 elements equal the same rows alone ----
 
 def test_many_logits(moe):  # noqa: F811
