@@ -192,6 +192,8 @@ class Fp8Linear:
             raise ValueError("no groups")
         self.codes, self.scales, self.device, self._index = codes, scales, codes.device, codes.get_device()
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        if not torch.cuda.is_current_stream_capturing():  # products of other streams may set it from now on
+            torch.cuda.current_stream(self.device).synchronize()
         self._matmul = _lib.lib().moe_fp8_matmul
         # an empty product: what the library thinks of the sizes
         _lib._check("moe_fp8_matmul", self._matmul(0, self.n, self.k, self.groups, None, 0, None, 0, 0, None, None, None,

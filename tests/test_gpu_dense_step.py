@@ -173,6 +173,25 @@ def test_a_status_bit_is_read_once_whatever_the_streams(moe):  # noqa: F811
     assert linear.status(clear=False, stream=main) == 0
 
 
+def test_a_new_weight_on_a_busy_stream(moe):  # noqa: F811
+    """The status word is clear before a product of another stream can set it."""
+    g = gen(11)
+    x = moe.quantize_rows(rand(g, 20, 128))
+    codes, scales = make_weight(g, 4, 128, 128)
+    bad = torch.tensor([0, 5, 5, 25, 30], dtype=torch.int32, device="cuda")
+    out = torch.zeros(20, 128, device="cuda")
+    side, busy = torch.cuda.Stream(), torch.cuda.Stream()
+    moe.Fp8Linear(codes, scales)(x, offsets=bad, out=out)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(100_000_000)  # ~50 ms
+        linear = moe.Fp8Linear(codes, scales)
+    linear(x, offsets=bad, out=out, stream=side)
+    side.synchronize()
+    busy.synchronize()
+    assert linear.status(stream=side) == moe.DENSE_BAD_OFFSETS
+
+
 # ---- past 32 bits: the last rows of arrays of more than 2^31 elements equal the same rows alone ----
 
 def test_many_logits(moe):  # noqa: F811
