@@ -73,7 +73,7 @@ MOE_API int moe_quantize_rows(int rows, int d, int gated, int dtype, const void*
 /* out[t][c] = sum over blocks b of scales[t][b] * w_scales[c / 128][b] *
  *             (sum over the block's channels k of codes[t][k] * w_codes[c][k]),
  * sums in FP32, rounded once to out_dtype.  k a multiple of 16; codes, w_codes 16-byte aligned, code_stride
- * a multiple of 16; out rows out_stride elements apart, channels consecutive.
+ * a multiple of 16 (of one row it says nothing); out rows out_stride elements apart, channels consecutive.
  *
  * groups > 0: w_codes [groups][n][k] (w_scales likewise), and rows offsets[g] .. offsets[g + 1] - 1
  * meet weight g (offsets on the device, [groups + 1], non-decreasing, within [0, rows]; empty groups

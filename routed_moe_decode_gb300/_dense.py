@@ -64,8 +64,9 @@ def _rows_to_write(out, rows, k, index):
 
 
 def _same_place(out, out_strides, of, of_strides):
-    """An output in an input's place has its strides."""
-    if of is not None and out.data_ptr() == of.data_ptr() and out_strides != of_strides:
+    """An output in an input's place has its strides (those of a dimension of one element say nothing)."""
+    if of is not None and out_strides != of_strides and out.data_ptr() == of.data_ptr() and out.numel() and \
+            any(n > 1 and a != b for n, a, b in zip(out.shape, out_strides, of_strides)):
         raise ValueError("an output in an input's place has its strides")
 
 

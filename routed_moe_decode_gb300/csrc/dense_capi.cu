@@ -109,11 +109,11 @@ int matmul(int rows, int n, int k, int groups, const uint8_t* codes, int64_t cod
   if (!aligned(codes, 16) || !aligned(w_codes, 16) || !aligned(scales, 4) || !aligned(w_scales, 4) ||
       !aligned(offsets, 4) || !aligned(out, size_of(out_dtype)) || !aligned(status, 4))
     return MOE_ERR_INVALID_ARG;
-  if ((rows > 1 && code_stride < k) || code_stride % 16 || (rows > 1 && out_stride < n)) return MOE_ERR_INVALID_ARG;
+  if (rows > 1 && (code_stride < k || code_stride % 16 || out_stride < n)) return MOE_ERR_INVALID_ARG;  // one row has no stride
   const int64_t wrows = static_cast<int64_t>(groups ? groups : 1) * n;
   // row tiles times channel tiles, and rows of the weights, are ints
   if (wrows > 0x7fffff00ll || (blocks(rows) * 4 + groups) * blocks(n) > 0x7fffffffll || rows > 0x7fffff00) return MOE_ERR_UNSUPPORTED;
-  if (code_stride >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+  if (rows > 1 && code_stride >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
   int sms = 0;
   const int rc = moe::device_sms(&sms);
   if (rc != MOE_OK) return rc;

@@ -370,6 +370,34 @@ def test_product_strides_types_and_places(moe, rows):
     assert torch.equal(linear(x2, dtype=FP32), base[::2])
 
 
+@pytest.mark.parametrize("groups", [0, 2])
+def test_product_of_one_row_of_any_stride(moe, groups):
+    g = gen(5)
+    n, k = 200, 160
+    codes, scales = make_weight(g, *((groups,) if groups else ()), n, k)
+    linear = moe.Fp8Linear(codes, scales)
+    x = make_rows(moe, g, 1, k)
+    offsets = torch.tensor([0, 0, 1], dtype=torch.int32, device="cuda") if groups else None
+    want = linear(x, offsets=offsets, dtype=FP32)
+    for stride in (1, 7, k, k + 8, 1 << 41):
+        one = moe.Fp8Rows(x.codes.as_strided((1, k), (stride, 1)), x.scales.as_strided((1, 2), (stride, x.scales.stride(1))))
+        out = torch.zeros(1, n, device="cuda").as_strided((1, n), (stride, 1))
+        assert torch.equal(linear(one, offsets=offsets, out=out), want)
+
+
+def test_norm_of_one_row_in_place_whatever_its_stride(moe):
+    g = gen(6)
+    w = torch.ones(256, device="cuda")
+    norm = moe.RmsNorm(w)
+    for shape in ((1, 256), (3, 1, 256), (1, 3, 256)):
+        x = rand(g, *shape)
+        want = norm(x)[0]
+        other = x.as_strided(shape, tuple(999 if n == 1 else s for n, s in zip(shape, x.stride())))
+        assert norm(x, normed=other)[0] is other and torch.equal(x, want)
+    empty = torch.empty(0, 512, device="cuda")
+    assert norm(empty[:, :256], normed=torch.empty(0, 256, device="cuda"))[0].shape == (0, 256)
+
+
 def test_product_nan_rows_stay_alone(moe):
     g = gen(6)
     v = rand(g, 40, 512)
