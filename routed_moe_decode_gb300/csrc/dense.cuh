@@ -71,6 +71,8 @@ struct MatmulArgs {
   uint32_t wait_cycles;
   int copy_arrivals;  // arrivals that a stage's barrier waits for beside its bytes
 };
+// Rows of a group on average, rounded up.
+inline int64_t rows_of_a_group(const MatmulArgs& a) { return (static_cast<int64_t>(a.rows) + a.groups - 1) / a.groups; }
 cudaError_t launch_fp8_stream(const MatmulArgs& a, int sms, int split, cudaStream_t stream);
 // Parts of k for that kernel, 1 where the rows' tiles keep the SMs busy as they are.
 int fp8_stream_split(const MatmulArgs& a, int sms);

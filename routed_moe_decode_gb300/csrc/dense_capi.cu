@@ -85,7 +85,7 @@ bool apart(int64_t outer, int64_t outer_stride, int64_t inner, int64_t inner_str
 // 48 rows each 110.0 / 93.6, 64: 114.8 / 110.2, 96: 117.2 / 116.0, 128: 122.3 / 188.3, 256: 169.7 / 309.0.  Between 64 and 96 they are
 // alike; groups are never equal in practice, and those above 128 cost the others twice.
 bool wide(const MatmulArgs& a, int sms, int split) {
-  if (a.offsets) return (a.rows + a.groups - 1) / a.groups > 64;
+  if (a.offsets) return moe::dense::rows_of_a_group(a) > 64;
   if (a.rows <= moe::dense::kSomeRows) return false;
   const double kblocks = static_cast<double>(blocks(a.k));
   const int64_t row_tiles = (a.rows + 127) / 128;

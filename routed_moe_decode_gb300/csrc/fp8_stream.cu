@@ -334,7 +334,7 @@ cudaError_t run(const Maps& maps, const MatmulArgs& a, int split, int grid, cuda
 // Few rows: 32 at most in a tile (groups: 16 on average), else 128.  256 weights of 1024 x 2048 (us, tiles of 32 / 128 rows): 16 rows
 // each 89.8 / 89.6, 32 (some above) 116.2 / 92.5; 16 weights of 4096 x 4096: 8 rows each 49.9 / 51.4, 32: 62.6 / 53.2.
 bool few_rows(const MatmulArgs& a) {
-  return a.offsets ? (a.rows + a.groups - 1) / a.groups <= 16 : a.rows <= kFewRows;
+  return a.offsets ? rows_of_a_group(a) <= 16 : a.rows <= kFewRows;
 }
 
 }  // namespace

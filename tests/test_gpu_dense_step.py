@@ -235,6 +235,27 @@ def test_many_outputs(moe, groups):  # noqa: F811
     del out
 
 
+def test_as_many_grouped_rows_as_there_can_be(moe):  # noqa: F811
+    """Rows and groups whose sum passes 2^31 (81 GB; only the last rows hold anything)."""
+    rows, n, k, groups = 0x7fffff00, 8, 16, 1024
+    g = gen(4)
+    codes, scales = make_weight(g, groups, n, k)
+    linear = moe.Fp8Linear(codes, scales)
+    few = moe.quantize_rows(rand(g, 300, k))
+    x = moe.Fp8Rows.empty(rows, k)
+    x.codes[-300:], x.scales[-300:] = few.codes, few.scales
+    edges = torch.linspace(0, rows, groups + 1, dtype=torch.float64).to(torch.int32)
+    edges[-1], edges[-2] = rows, rows - 300
+    out = torch.empty(rows, n + 1, dtype=BF16, device="cuda")
+    out[-300:] = 7
+    linear(x, offsets=edges.cuda(), out=out[:, :n])
+    assert linear.status() == 0
+    check_product(out[-300:, :n], few, codes[-1], scales[-1])
+    assert (out[-300:, n:] == 7).all()
+    del x, out
+    torch.cuda.empty_cache()
+
+
 def test_example_with_the_dense_path_in_8_bits():
     spec = importlib.util.spec_from_file_location("verify_step", os.path.join(ROOT, "examples", "verify_step.py"))
     m = importlib.util.module_from_spec(spec)
