@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
       const float most = all.m * a.scale;
       if (!(most < INFINITY)) all.rest = __int_as_float(0x7fc00000);  // scale * logit is +infinity, of a finite logit too
       const float sum = all.s + all.rest;
-      const bool none = sum == 0.f || most == -INFINITY;
+      const bool none = sum == 0.f || (most == -INFINITY && sum == sum);  // a NaN beside what has no probability is one
       const float logs = all.at < 0 ? log1pf(all.rest) : logf(sum);
       if (lane == 0) {
         if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(all.m, a.scale, logs);

@@ -694,6 +694,20 @@ def one(moe, x, tokens, scale):
         assert got.top_ids[i].tolist() == ids
 
 
+@pytest.mark.parametrize("rows", [2, 800])
+def test_logprobs_of_nan_beside_values_whose_scaled_ones_are_minus_infinity(moe, rows):
+    for dtype in (FP32, BF16):
+        x = torch.full((rows, 3001), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+        x[0, 77], x[1] = math.nan, math.nan
+        tokens = torch.zeros(rows, 2, dtype=torch.int32, device="cuda")
+        for top in (0, 3):
+            got = moe.token_logprobs(x, tokens, top=top, scale=5.0)
+            for t in got:
+                if t is not None and t.dtype is FP32:
+                    assert torch.isnan(t[:2]).all() and not torch.isnan(t[2:]).any()
+            assert (got.lse[2:] == -math.inf).all() and (got.entropy[2:] == 0).all()
+
+
 def check_sure(got, x, tokens, scale, steps):
     """Rows in which one token has nearly all the probability, by relative errors.  With x = scale * (logit - largest) and r the sum
     of exp(x) over the other tokens: lse - max = log1p(r) is the sure token's log probability (negated), entropy = log1p(r) +
