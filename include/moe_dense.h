@@ -65,7 +65,7 @@ MOE_API int moe_rms_norm(int outer, int inner, int d, int dtype, const void* x, 
                          float* scales, int64_t scale_row, int64_t scale_block, moe_stream_t stream);
 
 /* rows of d values in 8 bits; gated: x has 2 d values a row, gate then up, and what is quantised is
- * gate / (1 + exp(-gate)) * up (FP32). */
+ * gate / (1 + exp(-gate)) * up (FP32; a gate below -87.3, where exp(gate) is no normal value, counts as 0). */
 MOE_API int moe_quantize_rows(int rows, int d, int gated, int dtype, const void* x, int64_t x_stride,
                               uint8_t* codes, int64_t code_stride, float* scales, int64_t scale_row,
                               int64_t scale_block, moe_stream_t stream);

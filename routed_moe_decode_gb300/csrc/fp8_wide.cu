@@ -17,9 +17,10 @@
 // overlap with them only in part.  8192 x 8192 x 4096 takes 196 us, with the sums and reads left out (and their waits kept) 134,
 // without the multiply-adds 167, without the reads 174, with buffers given back before they are read 201.  Reads of 8 columns,
 // or ahead of the multiply-adds, 207 to 211; of 32 columns in two sets of registers, with more of them for these warps, 202.
-// A tile's outputs cost another ~1400 cycles.  Measured: 8192 x 8192 x 4096: 194 to 206 us, 2.7 to
-// 2.84 PFLOP/s (1.4 to 1.48 of the measured bf16 rate; the tensor cores are busy 60 % of the time); 512 weights of 1024 x 2048
-// with 160 rows each, unequal, 229 us (185 us of bytes).
+// A tile's outputs cost another ~1400 cycles.  Measured in graph replays, codes of normal values, clocks left alone, on several machines:
+// 8192 x 8192 x 4096 194 to 206 us, 2.7 to 2.84 PFLOP/s (1.4 to 1.48 of the measured bf16 rate; the tensor cores are busy
+// 60 % of the time); 512 weights of 1024 x 2048 with 160 rows each, unequal, 229 to 236 us (185 us of bytes).  Single calls one after
+// the other, with a new output each, take 215 to 224 and 256 to 262.
 #include "fp8_tiles.cuh"
 
 namespace moe {

@@ -7,8 +7,8 @@
 // the launch and one trip to memory (4 rows of 2048 channels: 2 us).  A thread has 8 consecutive values (16 bytes of
 // a 16-bit type), so 16 neighbouring lanes have a block, whose maximum takes four shuffles.
 //
-// Measured: 8192 rows of 2048 BF16 channels with a residual, normed and in 8 bits, 29 us (5.2 TB/s of what has to move); 8192
-// gated rows of 4096, 36.3 us (4.7 TB/s), where the exponentials, quotients and conversions take as many instruction
+// Measured: 8192 rows of 2048 BF16 channels with a residual, normed and in 8 bits, 29 to 30 us (5.1 TB/s of what has to move); 8192
+// gated rows of 4096, 36.3 us (4.7 TB/s; 38.5 where each call has an output of its own), where the exponentials, quotients and conversions take as many instruction
 // slots as memory leaves.  Norm rows that a persistent grid fetches ahead, 64 channels a lane with a warp to a row (66 us), or
 // other numbers of CTAs (28.9 to 29.6 us) are no faster.
 #include <algorithm>

@@ -28,7 +28,8 @@
 // Measured (graph replays; in brackets where the model is sure of every row's token or of most): 2048 rows of 131072 BF16 logits
 // with 5 alternatives 100 us [101] (5.4 TB/s), without any 101 [103]; the same in FP32 181 [186] and 172 [170] (6.2 TB/s); 127 rows of
 // 100003 in FP32 with 20 alternatives 17.5 [17.5], without 13.1 [14.0]; 4 rows of 131072 with 8, 8.6 [8.5], without 5.5 [6.3];
-// inputs from memory, as many in turn as are larger than L2.
+// inputs from memory, as many in turn as are larger than L2.  Where masks leave fewer logits than there are groups to give the threshold,
+// every logit reaches it and the lists below work for 4 rows of 131072 with 8 alternatives 50 us, for 127 of 100003 with 20, 64.
 // The end of a row is a chain of trips through shared memory and back to the logits, 3 to 4 us that other CTAs hide where
 // there are more rows than CTAs fit.  The pass is close to the limit of its registers (64 of a thread; see kCtas): how the
 // second reading is written moved 2048 rows from 96 to 113 us by what it left for the pass.

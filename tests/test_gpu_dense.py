@@ -279,6 +279,15 @@ def test_quantize_gated(moe, rows, d, dtype):
         moe.quantize_rows(x[:, :-1], gated=True)
 
 
+def test_quantize_gates_far_below_zero(moe):
+    """exp(gate) is no normal FP32 value below -87.34: such gates count as 0, those above do not."""
+    x = torch.ones(3, 256, device="cuda")
+    x[0, :128], x[1, :128], x[2, :128] = -87.5, -200.0, -87.0
+    q = moe.quantize_rows(x, gated=True)
+    assert (q.scales[:2] == 0).all() and (q.codes[:2].float() == 0).all()
+    check_quantized(moe.Fp8Rows(q.codes[2:], q.scales[2:]), torch.full((1, 128), -87.0 * math.exp(-87.0), dtype=torch.float64, device="cuda"), 8 * U)
+
+
 def test_quantize_strides_and_places(moe):
     g = gen(5)
     x = rand(g, 20, 300, dtype=BF16)
